@@ -306,6 +306,156 @@ COLIBRI_API int colibri_moe_ep_experts(colibri_moe_t* ctx, const void* recv_rows
  * slots of gate * y_back[row], in slot order in fp32 (m.nxbn.cn 3.3), T from the last ep_dispatch. */
 COLIBRI_API int colibri_moe_ep_combine(colibri_moe_t* ctx, const float* y_back, void* out, void* stream);
 
+/* ======================================================================================
+ * Operators of the block around the expert layer, and experts in 8-bit integers.
+ *
+ * No context: every pointer is the caller's, on the CURRENT device, every call is asynchronous on
+ * `stream`, allocates nothing and can be captured into a graph.  Row strides (ld*) count elements
+ * between the first elements of neighbouring rows; outputs without a stride are contiguous.  A
+ * workspace is scratch of the size the call's _workspace function gives, 256-byte aligned; its
+ * contents need no initialisation, and calls that may overlap on the GPU need one each.  Sums, norm
+ * statistics and scores are fp32 or wider; a value is rounded to bf16 once, when it is stored.
+ * Errors: COLIBRI_ERR_INVALID_ARG (NULL or host pointers, sizes or strides out of range, overlapping
+ * inputs and outputs, a workspace too small), COLIBRI_ERR_UNSUPPORTED (sizes this build does not
+ * run, as listed), COLIBRI_ERR_CUDA.  Nothing is enqueued when a call fails its checks.
+ * ====================================================================================== */
+
+/* ---- norms before and after a block, with its gate and the residual scale ----
+ *   z  = norm_after(y) * after_weight + after_bias          (after: none, RMS or layer)
+ *   x1 = residual_scale * x + block_scale * gate * z        (no gate: 1)
+ *   p  = norm_before(x1) * before_weight + before_bias      (before: the next block's norm, or none)
+ * RMS: v / sqrt(mean(v^2) + eps); layer: (v - mean) / sqrt(mean((v - mean)^2) + eps).
+ * norm_before reads x1 as stored (rounded to `dtype`). */
+#define COLIBRI_NORM_NONE 0
+#define COLIBRI_NORM_RMS 1
+#define COLIBRI_NORM_LAYER 2
+
+typedef struct {
+  int32_t d_model;        /* 1..16384                                                             */
+  int32_t dtype;          /* COLIBRI_DTYPE_* of the stream: x, x1, p and their gradients          */
+  int32_t block_dtype;    /* of y and d_y                                                          */
+  int32_t param_dtype;    /* of the weights, biases and the gate                                   */
+  int32_t after, before;  /* COLIBRI_NORM_*                                                        */
+  int64_t rows_per_gate;  /* > 0 with a gate: row t uses gate row t / rows_per_gate                */
+  float residual_scale, block_scale, eps;
+} colibri_moe_norm_config_t;
+
+/* [d_model] vectors of param_dtype, gate [ceil(T / rows_per_gate), d_model]; a weight is required
+ * iff its norm is there, biases only with a layer norm (NULL: none), gate may be NULL. */
+typedef struct {
+  const void *after_weight, *after_bias, *before_weight, *before_bias, *gate;
+} colibri_moe_norm_params_t;
+
+/* Gradients of the same vectors, fp32 (sums over up to all rows); NULL where not wanted, except gate,
+ * which is required iff the block has one. */
+typedef struct {
+  float *after_weight, *after_bias, *before_weight, *before_bias, *gate;
+} colibri_moe_norm_grads_t;
+
+/* x [T, d], y [T, d] -> x1 [T, d], p [T, d].  y and x1 may both be NULL (a norm before a block alone:
+ * p = norm_before(x)), p is NULL iff before is none.  x1 may be x itself when ldx == d_model.  T == 0 is
+ * a no-op. */
+COLIBRI_API int colibri_moe_block_norm(const colibri_moe_norm_config_t* cfg, const colibri_moe_norm_params_t* params,
+                                       const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t T, void* x1,
+                                       void* p, void* stream);
+
+COLIBRI_API int colibri_moe_block_norm_backward_workspace(const colibri_moe_norm_config_t* cfg, int32_t T,
+                                                          size_t* bytes);
+
+/* The gradients, from those of x1 (d_x1; NULL: none, where there is a next norm) and of p (d_p; NULL
+ * iff before is none), and from x1 (read iff there is a next norm) and y as the forward call left them.
+ * Writes d_x [T, d] in dtype, d_y [T, d] in block_dtype (NULL iff y is) and the parameters' gradients.
+ * Deterministic: column sums are added in a fixed order.  T == 0 zeroes the gradients of the vectors. */
+COLIBRI_API int colibri_moe_block_norm_backward(const colibri_moe_norm_config_t* cfg,
+                                                const colibri_moe_norm_params_t* params, const void* d_x1,
+                                                int64_t ld_dx1, const void* d_p, int64_t ld_dp, const void* x1,
+                                                int64_t ldx1, const void* y, int64_t ldy, int32_t T, void* d_x,
+                                                void* d_y, const colibri_moe_norm_grads_t* grads, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/* ---- routing to many experts ----
+ *   s      = softmax(logits) over the experts, or 1 / (1 + exp(-logit)) of each
+ *   key_e  = s_e + bias_e; without a bias the experts are ranked by their logits
+ *   groups: the experts in `groups` equal runs; a group's score is the sum of its group_top largest s_e +
+ *           bias_e (group_top 1 without a bias: its largest logit); the top_groups best groups are kept
+ *   idx    = the top_k experts of the kept groups by (key descending, index ascending), groups likewise
+ *   gate   = scale * s_idx, divided by the sum of the chosen s if renormalize (0 / 0 gives 0)
+ * The ranking is that of the keys evaluated in 64 bits.  An expert whose logit or bias is -inf or NaN
+ * is masked: it is never chosen (a NaN logit counts as -inf).  A token with fewer than top_k experts
+ * left gets idx -1, gate 0, row_of -1 in its last slots.
+ * Dispatch: rows grouped by expert, ascending tokens inside each, no padding: counts [E], offsets
+ * [E + 1], row_of [T, k] and token_of_row [T * k] (-1 at rows from offsets[E] on). */
+#define COLIBRI_SCORE_SOFTMAX 0
+#define COLIBRI_SCORE_SIGMOID 1
+
+typedef struct {
+  int32_t num_experts;  /* E, 1..512                                           */
+  int32_t top_k;        /* 1..32, at most top_groups * E / groups               */
+  int32_t score;        /* COLIBRI_SCORE_*                                      */
+  int32_t groups;       /* 1..32, divides E                                     */
+  int32_t top_groups;   /* 1..groups                                            */
+  int32_t group_top;    /* 1 or 2                                               */
+  int32_t renormalize;  /* 0 or 1                                               */
+  int32_t logits_dtype; /* COLIBRI_DTYPE_*                                      */
+  float scale;
+} colibri_moe_route_config_t;
+
+COLIBRI_API int colibri_moe_route_experts_workspace(const colibri_moe_route_config_t* cfg, int32_t T, size_t* bytes);
+
+/* logits [T, E] with row stride ld, bias [E] fp32 or NULL; T * top_k < 2^31.  T == 0 zeroes counts and
+ * offsets. */
+COLIBRI_API int colibri_moe_route_experts(const colibri_moe_route_config_t* cfg, const void* logits, int64_t ld,
+                                          const float* bias, int32_t T, int32_t* idx, float* gate, int32_t* counts,
+                                          int32_t* offsets, int32_t* row_of, int32_t* token_of_row, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* d_logits [T, E] (row stride ld_d, the logits' type) from the gradient of gate: the choice idx [T, k] is
+ * constant, slots with an index outside 0..E-1 contribute nothing, masked experts get 0.  The bias takes no
+ * gradient: it does not enter the gates.  groups, top_groups and group_top are not used. */
+COLIBRI_API int colibri_moe_route_experts_backward(const colibri_moe_route_config_t* cfg, const void* logits,
+                                                   int64_t ld, const int32_t* idx, const float* d_gate, int32_t T,
+                                                   void* d_logits, int64_t ld_d, void* stream);
+
+/* ---- experts in 8-bit integers: a scale for each row of activations and each output channel ----
+ *   scale_t = max_k |x[t, k]| / 127,  q[t, k] = round(x[t, k] / scale_t)      (fp32, ties to even)
+ *   v[r, n] = scale_t * w_scale[e, n] * sum_k q[t, k] * w[e, n, k],           t = rows[r], r in segment e
+ *   y[r, n] = v[r, n],  or with w3:  silu(v[r, n]) * v3[r, n]
+ * A row of zeros gives zeros; a row that holds an infinity or a NaN gives NaN. */
+typedef struct {
+  int32_t in_features;   /* K, 16..65536, a multiple of 16                                         */
+  int32_t out_features;  /* N, 1..131072 (channels of y; with w3, of each projection)              */
+  int32_t num_experts;   /* E, 1..512 (1: a plain linear layer)                                     */
+  int32_t dtype;         /* COLIBRI_DTYPE_* of x                                                    */
+  int32_t out_dtype;     /* COLIBRI_DTYPE_* of y                                                    */
+} colibri_moe_int8_config_t;
+
+/* q [n, K] int8 and scale [n] fp32 of x [n, K] (row stride ldx): activations, or weights once ahead of
+ * time (a row of a weight matrix is an output channel).  A row with an infinity or a NaN gets scale NaN
+ * and q 0.  Uses cfg's in_features and dtype. */
+COLIBRI_API int colibri_moe_int8_quantize(const colibri_moe_int8_config_t* cfg, const void* x, int64_t ldx, int32_t n,
+                                          int8_t* q, float* scale, void* stream);
+
+COLIBRI_API int colibri_moe_int8_experts_workspace(const colibri_moe_int8_config_t* cfg, int32_t n_tokens, int32_t R,
+                                                   size_t* bytes);
+
+/* x [n_tokens, K] (row stride ldx), w [E, N, K] int8 (16-byte aligned), w_scale [E, N] fp32, w3 and
+ * w3_scale likewise or both NULL; offsets [E + 1] int32, as routing writes them (offsets[e] .. offsets[e +
+ * 1] are expert e's rows; values outside 0..R are clamped); rows [R] int32 gives the token of each row
+ * (outside 0..n_tokens-1: a row of zeros), or NULL: row r is token r (R <= n_tokens).  y [R, N]: rows from
+ * offsets[E] on are not written.  R == 0 is a no-op. */
+COLIBRI_API int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, const void* x, int64_t ldx,
+                                         int32_t n_tokens, const int32_t* rows, int32_t R, const int32_t* offsets,
+                                         const int8_t* w, const float* w_scale, const int8_t* w3,
+                                         const float* w3_scale, void* y, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/* out[t] = sum over s < k of gate[t, s] * y[row_of[t, s]] in slot order in fp32, slots with a row outside
+ * 0..R-1 left out (their gates multiply nothing): the combine for any number of experts, k 1..32, d >= 1.
+ * y [R, d] contiguous in y_dtype, out [T, d] in out_dtype. */
+COLIBRI_API int colibri_moe_combine_rows(const void* y, int32_t y_dtype, int32_t R, const int32_t* row_of,
+                                         const float* gate, int32_t T, int32_t k, int32_t d, void* out,
+                                         int32_t out_dtype, void* stream);
+
 /* Frees everything the context owns (the articles' colibri_free, the release call every program
  * must make once it is done: zskr.cn 4.3, m.nxbn.cn 4.3).  NULL-safe. */
 COLIBRI_API void colibri_moe_destroy(colibri_moe_t* ctx);

@@ -9,7 +9,8 @@ if the library is missing or cannot run, calls raise.
     out = layer.forward(x)                              # x: [T, d] CUDA tensor
 
 The C functions keep their names (``colibri_moe_*``); ``lib()`` returns the
-loaded ``ctypes.CDLL`` for direct calls.
+loaded ``ctypes.CDLL`` for direct calls.  ``ops`` holds the operators of the block around the
+layer (norms, routing to many experts) and experts in 8-bit integers.
 """
 from __future__ import annotations
 
@@ -38,7 +39,10 @@ EXPORTED = ("colibri_moe_create", "colibri_moe_load_weights", "colibri_moe_forwa
             "colibri_moe_last_kernel_count", "colibri_moe_last_gemm", "colibri_moe_set_stage_events", "colibri_moe_device_status",
             "colibri_moe_probe_wait_timeout", "colibri_moe_route_noalloc",
             "colibri_moe_ep_create", "colibri_moe_ep_dispatch", "colibri_moe_ep_experts", "colibri_moe_ep_combine",
-            "colibri_moe_destroy", "colibri_moe_strerror")
+            "colibri_moe_block_norm", "colibri_moe_block_norm_backward_workspace", "colibri_moe_block_norm_backward",
+            "colibri_moe_route_experts_workspace", "colibri_moe_route_experts", "colibri_moe_route_experts_backward",
+            "colibri_moe_int8_quantize", "colibri_moe_int8_experts_workspace", "colibri_moe_int8_experts",
+            "colibri_moe_combine_rows", "colibri_moe_destroy", "colibri_moe_strerror")
 
 
 class ColibriError(RuntimeError):
@@ -52,6 +56,30 @@ class Config(ctypes.Structure):
                 ("top_k", ctypes.c_int32), ("max_tokens", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("act", ctypes.c_int32), ("has_router_bias", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("gate_mode", ctypes.c_int32), ("has_shared_expert", ctypes.c_int32)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("d_model", ctypes.c_int32), ("dtype", ctypes.c_int32), ("block_dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("after", ctypes.c_int32), ("before", ctypes.c_int32),
+                ("rows_per_gate", ctypes.c_int64), ("residual_scale", ctypes.c_float),
+                ("block_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class NormVectors(ctypes.Structure):
+    """Both colibri_moe_norm_params_t and colibri_moe_norm_grads_t: five pointers."""
+    _fields_ = [("after_weight", ctypes.c_void_p), ("after_bias", ctypes.c_void_p),
+                ("before_weight", ctypes.c_void_p), ("before_bias", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
+
+
+class RouteConfig(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("logits_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class Int8Config(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 class Weights(ctypes.Structure):
@@ -94,6 +122,19 @@ def lib() -> ctypes.CDLL:
             "colibri_moe_ep_dispatch": ([vp, vp, i32, vp, vp, vp], ctypes.c_int),
             "colibri_moe_ep_experts": ([vp, vp, vp, vp, vp], ctypes.c_int),
             "colibri_moe_ep_combine": ([vp, vp, vp, vp], ctypes.c_int),
+            "colibri_moe_block_norm": ([vp, vp, vp, i64, vp, i64, i32, vp, vp, vp], ctypes.c_int),
+            "colibri_moe_block_norm_backward_workspace": ([vp, i32, vp], ctypes.c_int),
+            "colibri_moe_block_norm_backward": ([vp, vp, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, vp,
+                                                 ctypes.c_size_t, vp], ctypes.c_int),
+            "colibri_moe_route_experts_workspace": ([vp, i32, vp], ctypes.c_int),
+            "colibri_moe_route_experts": ([vp, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+                                          ctypes.c_int),
+            "colibri_moe_route_experts_backward": ([vp, vp, i64, vp, vp, i32, vp, i64, vp], ctypes.c_int),
+            "colibri_moe_int8_quantize": ([vp, vp, i64, i32, vp, vp, vp], ctypes.c_int),
+            "colibri_moe_int8_experts_workspace": ([vp, i32, i32, vp], ctypes.c_int),
+            "colibri_moe_int8_experts": ([vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+                                         ctypes.c_int),
+            "colibri_moe_combine_rows": ([vp, i32, i32, vp, vp, i32, i32, i32, vp, i32, vp], ctypes.c_int),
             "colibri_moe_destroy": ([vp], None),
             "colibri_moe_strerror": ([ctypes.c_int], ctypes.c_char_p),
         }

@@ -1,0 +1,617 @@
+// Norms before and after a block, fused with the block's gate and the residual scale.
+//
+//   z  = norm_after(y) * w_a + b_a            (y: the block's output; norm none, RMS or layer)
+//   x1 = residual_scale * x + block_scale * gate * z
+//   p  = norm_before(x1) * w_b + b_b          (the next block's input; from x1 as stored)
+//   RMS:   norm(v) = v / sqrt(mean(v^2) + eps)
+//   layer: norm(v) = (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps)
+//
+// The backward pass, with D the gradient of x1 from both of its uses, n = norm(v), r = 1 / deviation:
+//   d_v = r (d_n - n mean(d_n n) [- mean(d_n), layer])     d_n = d_out * w
+//   D   = d_x1 + (d_v of norm_before at x1),  d_x = residual_scale * D,  d_z = block_scale * gate * D
+//   d_y = d_v of norm_after at y,  and column sums over the rows for w_a, b_a, w_b, b_b and the gate.
+//
+// HBM-bound: each of x, y read once, x1, p written once; a row stays in registers between the loads
+// and the stores, so both norms cost no second pass.  All statistics and sums are fp32, the variance is
+// taken about the mean in a second sum over the registers (no E[v^2] - mean^2 cancellation).
+#include <algorithm>
+
+#include "ops_common.cuh"
+
+namespace colibri {
+namespace {
+
+struct NormArgs {
+  const void *x, *y, *wa, *ba, *wb, *bb, *gate;
+  void *x1, *p;                    // forward outputs
+  const void *dx1, *dp;            // backward inputs
+  void *dx, *dy;                   // backward outputs
+  float* part;                     // backward: [blocks][kSlots][d] column sums of each block
+  float* dgate;                    // backward: [gates][d]; groups inside one block's rows go straight here
+  int64_t ldx, ldy, lddx1, lddp;   // row strides, elements
+  int64_t rpg;                     // rows per gate row
+  int T, d, after, before, param_bf16;
+  int rows_per_block;              // backward
+  float alpha, beta, eps;
+};
+
+// Column-sum slots of a block: the four parameter vectors, the gate row that began in an earlier block
+// and the one that goes on in the next.
+enum { kSumWb, kSumBb, kSumWa, kSumBa, kSumGateFirst, kSumGateLast, kSlots };
+
+// How a thread's 8 * C values lie in a row: VEC, chunks of 8 consecutive columns (16-byte accesses; d,
+// row strides and addresses are multiples of 16 bytes); else single columns a block width apart.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load_cols(const T* row, int c, int d, float (&v)[8]) {
+  if constexpr (VEC) {
+    const int col = (c * blockDim.x + threadIdx.x) * 8;
+    if (col < d) {
+      load8(row + col, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = (c * 8 + j) * blockDim.x + threadIdx.x;
+      v[j] = col < d ? to_float(row[col]) : 0.f;
+    }
+  }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void store_cols(T* row, int c, int d, const float (&v)[8]) {
+  if constexpr (VEC) {
+    const int col = (c * blockDim.x + threadIdx.x) * 8;
+    if (col < d) store8(row + col, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = (c * 8 + j) * blockDim.x + threadIdx.x;
+      if (col < d) row[col] = from_float<T>(v[j]);
+    }
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ bool col_in(int c, int j, int d) {
+  return (VEC ? (c * (int)blockDim.x + (int)threadIdx.x) * 8 + j : (c * 8 + j) * (int)blockDim.x + (int)threadIdx.x) < d;
+}
+template <bool VEC>
+__device__ __forceinline__ void load_param(const void* p, int bf16, int64_t row, int c, int d, float (&v)[8]) {
+  if (bf16)
+    load_cols<VEC>(static_cast<const __nv_bfloat16*>(p) + row * d, c, d, v);
+  else
+    load_cols<VEC>(static_cast<const float*>(p) + row * d, c, d, v);
+}
+
+// Subtracts the row's mean (layer); the values past d stay zero.
+template <bool VEC, int C>
+__device__ __forceinline__ void center(float (&v)[C][8], float mean, int d) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[c][j] = col_in<VEC>(c, j, d) ? v[c][j] - mean : 0.f;
+}
+template <int C>
+__device__ __forceinline__ float sum_of(const float (&v)[C][8]) {
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s += v[c][j];
+  return s;
+}
+template <int C>
+__device__ __forceinline__ float dot_of(const float (&v)[C][8], const float (&w)[C][8]) {
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = fmaf(v[c][j], w[c][j], s);
+  return s;
+}
+
+// v <- (v [- mean]) and returns 1 / deviation.
+template <bool VEC, int C>
+__device__ __forceinline__ float norm_stats(float (&v)[C][8], int kind, int d, float eps, float* buf, int& turn) {
+  if (kind == COLIBRI_NORM_LAYER) {
+    float s[1] = {sum_of(v)};
+    block_sum(s, buf, turn);
+    center<VEC>(v, s[0] / d, d);
+  }
+  float s[1] = {dot_of(v, v)};
+  block_sum(s, buf, turn);
+  return rsqrtf(s[0] / d + eps);
+}
+
+template <typename S, typename Y, bool VEC, int C, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_norm_kernel(NormArgs a) {
+  __shared__ float buf[kSumBuf];
+  int turn = 0;
+  pdl_wait();
+  for (int row = blockIdx.x; row < a.T; row += gridDim.x) {
+    float x[C][8];
+    const S* px = static_cast<const S*>(a.x) + row * a.ldx;
+#pragma unroll
+    for (int c = 0; c < C; ++c) load_cols<VEC>(px, c, a.d, x[c]);
+    if (a.y) {
+      float z[C][8], w[8];
+      const Y* py = static_cast<const Y*>(a.y) + row * a.ldy;
+#pragma unroll
+      for (int c = 0; c < C; ++c) load_cols<VEC>(py, c, a.d, z[c]);
+      if (a.after) {
+        const float r = norm_stats<VEC, C>(z, a.after, a.d, a.eps, buf, turn);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          load_param<VEC>(a.wa, a.param_bf16, 0, c, a.d, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[c][j] *= r * w[j];
+          if (a.ba) {
+            load_param<VEC>(a.ba, a.param_bf16, 0, c, a.d, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[c][j] += w[j];
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (a.gate) {
+          load_param<VEC>(a.gate, a.param_bf16, row / a.rpg, c, a.d, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[c][j] *= w[j];
+        }
+        // the next norm reads x1 as it is stored, rounded to the stream's type
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[c][j] = to_float(from_float<S>(fmaf(a.beta, z[c][j], a.alpha * x[c][j])));
+        store_cols<VEC>(static_cast<S*>(a.x1) + (int64_t)row * a.d, c, a.d, x[c]);
+      }
+    }
+    if (a.before) {
+      const float r = norm_stats<VEC, C>(x, a.before, a.d, a.eps, buf, turn);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float w[8];
+        load_param<VEC>(a.wb, a.param_bf16, 0, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[c][j] *= r * w[j];
+        if (a.bb) {
+          load_param<VEC>(a.bb, a.param_bf16, 0, c, a.d, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[c][j] += w[j];
+        }
+        store_cols<VEC>(static_cast<S*>(a.p) + (int64_t)row * a.d, c, a.d, x[c]);
+      }
+    }
+  }
+}
+
+// The gate row of group g lies in [g * rpg, (g + 1) * rpg); block b owns rows [b * R, (b + 1) * R).
+// A group inside one block is written by it; one that crosses blocks leaves a partial sum in slot
+// kSumGateLast of the block where it begins and kSumGateFirst of every later one.
+template <bool VEC, int C>
+__device__ __forceinline__ void flush_gate(const NormArgs& a, int64_t g, int r0, int r1, float (&acc)[C][8]) {
+  const int64_t first = g * a.rpg, last = min((g + 1) * a.rpg, (int64_t)a.T) - 1;
+  float* out = first >= r0 && last < r1
+                   ? a.dgate + g * a.d
+                   : a.part + ((int64_t)blockIdx.x * kSlots + (first < r0 ? kSumGateFirst : kSumGateLast)) * a.d;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    store_cols<VEC>(out, c, a.d, acc[c]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[c][j] = 0.f;
+  }
+}
+
+// A block takes consecutive rows and keeps the column sums of its own columns in registers; the sums
+// of all blocks are added by norm_sums_kernel in block order (no atomics: the same bits every time).
+// BIAS: either norm is a layer norm (two more column sums).
+template <typename S, typename Y, bool VEC, int C, bool BIAS, int MAXT>
+__global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormArgs a) {
+  __shared__ float buf[kSumBuf];
+  int turn = 0;
+  float swb[C][8] = {}, swa[C][8] = {}, sg[C][8] = {};
+  float sbb[BIAS ? C : 1][8] = {}, sba[BIAS ? C : 1][8] = {};
+  const int r0 = blockIdx.x * a.rows_per_block, r1 = min(r0 + a.rows_per_block, a.T);
+  const float inv_d = 1.f / a.d;
+  pdl_wait();
+  int64_t group = a.gate ? r0 / a.rpg : 0;
+  for (int row = r0; row < r1; ++row) {
+    float D[C][8], w[8];
+    if (a.gate && row / a.rpg != group) {
+      flush_gate<VEC, C>(a, group, r0, r1, sg);
+      group = row / a.rpg;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (a.dx1) {
+        load_cols<VEC>(static_cast<const S*>(a.dx1) + row * a.lddx1, c, a.d, D[c]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) D[c][j] = 0.f;
+      }
+    }
+    if (a.before) {
+      float x[C][8], q[C][8];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        load_cols<VEC>(static_cast<const S*>(a.x) + row * a.ldx, c, a.d, x[c]);
+        load_cols<VEC>(static_cast<const S*>(a.dp) + row * a.lddp, c, a.d, q[c]);
+      }
+      if (BIAS && a.before == COLIBRI_NORM_LAYER) {
+        float s[1] = {sum_of(x)};
+        block_sum(s, buf, turn);
+        center<VEC>(x, s[0] * inv_d, a.d);
+      }
+      float t[3] = {dot_of(x, x), 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        load_param<VEC>(a.wb, a.param_bf16, 0, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float dn = q[c][j] * w[j];
+          t[1] = fmaf(dn, x[c][j], t[1]);
+          t[2] += dn;
+        }
+      }
+      block_sum(t, buf, turn);
+      const float r = rsqrtf(t[0] * inv_d + a.eps);
+      // x becomes n = x r; sum(dn n) = r sum(dn x)
+      const float m1 = t[1] * inv_d * r, m0 = BIAS && a.before == COLIBRI_NORM_LAYER ? t[2] * inv_d : 0.f;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        load_param<VEC>(a.wb, a.param_bf16, 0, c, a.d, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float n = x[c][j] * r, dn = q[c][j] * w[j];
+          swb[c][j] = fmaf(q[c][j], n, swb[c][j]);
+          if constexpr (BIAS) sbb[c][j] += q[c][j];
+          D[c][j] = fmaf(r, dn - n * m1 - m0, D[c][j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = a.alpha * D[c][j];
+      store_cols<VEC>(static_cast<S*>(a.dx) + (int64_t)row * a.d, c, a.d, o);
+    }
+    if (a.y) {
+      float y[C][8];
+#pragma unroll
+      for (int c = 0; c < C; ++c) load_cols<VEC>(static_cast<const Y*>(a.y) + row * a.ldy, c, a.d, y[c]);
+      float r = 1.f;
+      if (a.after) r = norm_stats<VEC, C>(y, a.after, a.d, a.eps, buf, turn);
+      float t[2] = {0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float wa[8];
+        if (a.after) {
+          load_param<VEC>(a.wa, a.param_bf16, 0, c, a.d, wa);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[c][j] *= r;  // now n
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) D[c][j] *= a.beta;
+        if (a.gate) {
+          float z[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[j] = a.after ? y[c][j] * wa[j] : y[c][j];
+          if (BIAS && a.ba) {
+            load_param<VEC>(a.ba, a.param_bf16, 0, c, a.d, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] += w[j];
+          }
+          load_param<VEC>(a.gate, a.param_bf16, group, c, a.d, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            sg[c][j] = fmaf(D[c][j], z[j], sg[c][j]);
+            D[c][j] *= w[j];
+          }
+        }
+        if (a.after) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            swa[c][j] = fmaf(D[c][j], y[c][j], swa[c][j]);
+            if constexpr (BIAS) sba[c][j] += D[c][j];
+            D[c][j] *= wa[j];  // now d_n
+            t[0] = fmaf(D[c][j], y[c][j], t[0]);
+            t[1] += D[c][j];
+          }
+        }
+      }
+      if (a.after) {
+        block_sum(t, buf, turn);
+        const float m1 = t[0] * inv_d, m0 = BIAS && a.after == COLIBRI_NORM_LAYER ? t[1] * inv_d : 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) D[c][j] = r * (D[c][j] - y[c][j] * m1 - m0);
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) store_cols<VEC>(static_cast<Y*>(a.dy) + (int64_t)row * a.d, c, a.d, D[c]);
+    }
+  }
+  float* part = a.part + (int64_t)blockIdx.x * kSlots * a.d;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (a.before) store_cols<VEC>(part + (int64_t)kSumWb * a.d, c, a.d, swb[c]);
+    if (a.after) store_cols<VEC>(part + (int64_t)kSumWa * a.d, c, a.d, swa[c]);
+    if constexpr (BIAS) {
+      if (a.before) store_cols<VEC>(part + (int64_t)kSumBb * a.d, c, a.d, sbb[c]);
+      if (a.after) store_cols<VEC>(part + (int64_t)kSumBa * a.d, c, a.d, sba[c]);
+    }
+  }
+  if (a.gate) flush_gate<VEC, C>(a, group, r0, r1, sg);
+}
+
+struct NormSumsArgs {
+  const float* part;
+  float* out[4];       // d_wb, d_bb, d_wa, d_ba (kSumWb..kSumBa), nullptr where not wanted
+  float* dgate;        // [gates][d] or nullptr
+  int64_t rpg;
+  int T, d, blocks, rows_per_block;
+};
+
+constexpr int kSumCols = 32, kSumLanes = 8;
+
+// Adds the blocks' column sums: 32 columns x 8 lanes a block, each lane every eighth partial in order,
+// then the lanes in order.
+__global__ void __launch_bounds__(kSumCols * kSumLanes) norm_sums_kernel(NormSumsArgs a) {
+  __shared__ float red[kSumLanes][kSumCols];
+  const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols;
+  const int col = blockIdx.x * kSumCols + tx;
+  pdl_wait();
+  const int64_t stride = (int64_t)kSlots * a.d;
+  auto total = [&](float mine) {
+    red[ty][tx] = mine;
+    __syncthreads();
+    float s = 0.f;
+    if (ty == 0)
+      for (int i = 0; i < kSumLanes; ++i) s += red[i][tx];
+    __syncthreads();
+    return s;
+  };
+  if (blockIdx.y < 4) {
+    float* out = a.out[blockIdx.y];
+    if (!out) return;
+    float s = 0.f;
+    if (col < a.d) {
+      const float* p = a.part + (int64_t)blockIdx.y * a.d + col;
+#pragma unroll 4
+      for (int b = ty; b < a.blocks; b += kSumLanes) s += p[b * stride];
+    }
+    s = total(s);
+    if (ty == 0 && col < a.d) out[col] = s;
+    return;
+  }
+  if (!a.dgate) return;
+  // the groups that begin in block b and go on past it
+  for (int b = 0; b + 1 < a.blocks; ++b) {
+    const int64_t r0 = (int64_t)b * a.rows_per_block, r1 = r0 + a.rows_per_block;
+    const int64_t g = (r1 - 1) / a.rpg, first = g * a.rpg, last = min((g + 1) * a.rpg, (int64_t)a.T) - 1;
+    if (first < r0 || last < r1) continue;
+    const int end = (int)(last / a.rows_per_block);
+    float s = 0.f;
+    if (col < a.d) {
+      const float* p = a.part + col;
+      if (ty == 0) s = p[b * stride + (int64_t)kSumGateLast * a.d];
+#pragma unroll 4
+      for (int i = b + 1 + ty; i <= end; i += kSumLanes) s += p[i * stride + (int64_t)kSumGateFirst * a.d];
+    }
+    s = total(s);
+    if (ty == 0 && col < a.d) a.dgate[g * a.d + col] = s;
+  }
+}
+
+constexpr int kNormMaxD = 16384;
+
+int norm_threads(int d) { return std::min(1024, ((d + 7) / 8 + 31) / 32 * 32); }
+
+template <typename S, typename Y, bool VEC>
+cudaError_t launch_forward(const NormArgs& a, int sms, cudaStream_t s) {
+  const int threads = norm_threads(a.d);
+  const dim3 grid(std::min<int64_t>(a.T, (int64_t)sms * std::max(1, 2048 / threads)));
+  if (a.d > 8 * 1024)
+    return pdl_launch(block_norm_kernel<S, Y, VEC, 2, 1024>, grid, dim3(threads), 0, s, a);
+  if (threads > 512)
+    return pdl_launch(block_norm_kernel<S, Y, VEC, 1, 1024>, grid, dim3(threads), 0, s, a);
+  return pdl_launch(block_norm_kernel<S, Y, VEC, 1, 512>, grid, dim3(threads), 0, s, a);
+}
+
+// Blocks of the backward pass: enough to fill the SMs at about 512 threads each, and at least 8 rows a
+// block where the batch allows, so that the partial column sums stay small beside the rows.
+int backward_blocks(int T, int d, int sms, int* rows_per_block) {
+  const int want = std::min(sms * std::max(1, 512 / norm_threads(d)), std::max(sms, T / 8));
+  *rows_per_block = (T + want - 1) / want;
+  return (T + *rows_per_block - 1) / *rows_per_block;
+}
+
+template <typename S, typename Y, bool VEC, bool BIAS>
+cudaError_t launch_backward_t(const NormArgs& a, int blocks, cudaStream_t s) {
+  const int threads = norm_threads(a.d);
+  if (a.d > 8 * 1024)
+    return pdl_launch(block_norm_backward_kernel<S, Y, VEC, 2, BIAS, 1024>, dim3(blocks), dim3(threads), 0, s, a);
+  if (threads > 512)
+    return pdl_launch(block_norm_backward_kernel<S, Y, VEC, 1, BIAS, 1024>, dim3(blocks), dim3(threads), 0, s, a);
+  return pdl_launch(block_norm_backward_kernel<S, Y, VEC, 1, BIAS, 512>, dim3(blocks), dim3(threads), 0, s, a);
+}
+
+template <typename S, typename Y, bool VEC>
+cudaError_t launch_backward(const NormArgs& a, int blocks, cudaStream_t s) {
+  if (a.after == COLIBRI_NORM_LAYER || a.before == COLIBRI_NORM_LAYER)
+    return launch_backward_t<S, Y, VEC, true>(a, blocks, s);
+  return launch_backward_t<S, Y, VEC, false>(a, blocks, s);
+}
+
+template <typename F>
+cudaError_t by_type(int dtype, int block_dtype, bool vec, F f) {
+  using B = __nv_bfloat16;
+  if (dtype == COLIBRI_DTYPE_F32)
+    return block_dtype == COLIBRI_DTYPE_F32 ? f(float{}, float{}, vec) : f(float{}, B{}, vec);
+  return block_dtype == COLIBRI_DTYPE_F32 ? f(B{}, float{}, vec) : f(B{}, B{}, vec);
+}
+
+bool norm_kind(int32_t k) { return k == COLIBRI_NORM_NONE || k == COLIBRI_NORM_RMS || k == COLIBRI_NORM_LAYER; }
+
+// The checks that need no device.
+int check_norm_config(const colibri_moe_norm_config_t* c, const colibri_moe_norm_params_t* w, bool block, int32_t T) {
+  if (!c || !w || T < 0) return COLIBRI_ERR_INVALID_ARG;
+  if (c->d_model <= 0 || !ops_dtype(c->dtype) || !ops_dtype(c->block_dtype) || !ops_dtype(c->param_dtype) ||
+      !norm_kind(c->after) || !norm_kind(c->before) || !(c->eps >= 0.f))
+    return COLIBRI_ERR_INVALID_ARG;
+  if (c->d_model > kNormMaxD) return COLIBRI_ERR_UNSUPPORTED;
+  // without a block output there is nothing to norm after, to gate or to add
+  if (!block && (c->after != COLIBRI_NORM_NONE || w->gate || c->before == COLIBRI_NORM_NONE))
+    return COLIBRI_ERR_INVALID_ARG;
+  if ((c->after != COLIBRI_NORM_NONE) != (w->after_weight != nullptr) ||
+      (c->before != COLIBRI_NORM_NONE) != (w->before_weight != nullptr))
+    return COLIBRI_ERR_INVALID_ARG;
+  if ((w->after_bias && c->after != COLIBRI_NORM_LAYER) || (w->before_bias && c->before != COLIBRI_NORM_LAYER))
+    return COLIBRI_ERR_INVALID_ARG;
+  if (w->gate && c->rows_per_gate <= 0) return COLIBRI_ERR_INVALID_ARG;
+  return COLIBRI_OK;
+}
+
+bool stride_ok(int64_t ld, int32_t d) { return ld >= d; }
+
+// [p, p + bytes) as compared for overlap.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool spans_overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.bytes <= 0 || b.bytes <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+int64_t span_of(int32_t T, int64_t ld, int32_t d, int elem) { return T ? ((int64_t)(T - 1) * ld + d) * elem : 0; }
+
+}  // namespace
+}  // namespace colibri
+
+using namespace colibri;
+
+extern "C" int colibri_moe_block_norm(const colibri_moe_norm_config_t* cfg, const colibri_moe_norm_params_t* w,
+                                      const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t T, void* x1,
+                                      void* p, void* stream) {
+  int rc = check_norm_config(cfg, w, y != nullptr || T == 0, T);  // no rows: y may be NULL either way
+  if (rc) return rc;
+  const int d = cfg->d_model;
+  const bool next = cfg->before != COLIBRI_NORM_NONE;
+  if (T == 0) return COLIBRI_OK;
+  if (!x || !stride_ok(ldx, d) || (y && !stride_ok(ldy, d)) || (y != nullptr) != (x1 != nullptr) || next != (p != nullptr))
+    return COLIBRI_ERR_INVALID_ARG;
+  const int es = ops_elem(cfg->dtype), ey = ops_elem(cfg->block_dtype);
+  const Span sx{x, span_of(T, ldx, d, es)}, sy{y, span_of(T, ldy, d, ey)};
+  const Span o1{x1, (int64_t)T * d * es}, op{p, (int64_t)T * d * es};
+  // x1 may be x itself (the stream updated in place): a row is read before it is written
+  if ((spans_overlap(sx, o1) && !(x1 == x && ldx == d)) || spans_overlap(sy, o1) || spans_overlap(sx, op) ||
+      spans_overlap(sy, op) || spans_overlap(o1, op))
+    return COLIBRI_ERR_INVALID_ARG;
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  for (const void* q : {x, y, w->after_weight, w->after_bias, w->before_weight, w->before_bias, w->gate,
+                        (const void*)x1, (const void*)p})
+    if (q && !ops_on_device(q, device)) return COLIBRI_ERR_INVALID_ARG;
+  NormArgs a = {};
+  a.x = x, a.y = y, a.wa = w->after_weight, a.ba = w->after_bias, a.wb = w->before_weight, a.bb = w->before_bias;
+  a.gate = w->gate, a.x1 = x1, a.p = p, a.ldx = ldx, a.ldy = ldy, a.rpg = cfg->rows_per_gate, a.T = T, a.d = d;
+  a.after = cfg->after, a.before = cfg->before, a.param_bf16 = cfg->param_dtype == COLIBRI_DTYPE_BF16;
+  a.alpha = cfg->residual_scale, a.beta = cfg->block_scale, a.eps = cfg->eps;
+  bool vec = d % 8 == 0 && ldx % 8 == 0 && (!y || ldy % 8 == 0);
+  for (const void* q : {x, y, a.wa, a.ba, a.wb, a.bb, a.gate, (const void*)x1, (const void*)p}) vec = vec && ops_aligned16(q);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = by_type(cfg->dtype, cfg->block_dtype, vec, [&](auto st, auto yt, bool v) {
+    using S = decltype(st);
+    using Y = decltype(yt);
+    return v ? launch_forward<S, Y, true>(a, sms, s) : launch_forward<S, Y, false>(a, sms, s);
+  });
+  return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+extern "C" int colibri_moe_block_norm_backward_workspace(const colibri_moe_norm_config_t* cfg, int32_t T,
+                                                         size_t* bytes) {
+  if (!cfg || !bytes || T < 0 || cfg->d_model <= 0) return COLIBRI_ERR_INVALID_ARG;
+  if (cfg->d_model > kNormMaxD) return COLIBRI_ERR_UNSUPPORTED;
+  int device = 0, sms = 0, rows = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  *bytes = T ? (size_t)backward_blocks(T, cfg->d_model, sms, &rows) * kSlots * cfg->d_model * sizeof(float) : 0;
+  return COLIBRI_OK;
+}
+
+extern "C" int colibri_moe_block_norm_backward(const colibri_moe_norm_config_t* cfg,
+                                               const colibri_moe_norm_params_t* w, const void* d_x1, int64_t ld_dx1,
+                                               const void* d_p, int64_t ld_dp, const void* x1, int64_t ldx1,
+                                               const void* y, int64_t ldy, int32_t T, void* d_x, void* d_y,
+                                               const colibri_moe_norm_grads_t* grads, void* workspace,
+                                               size_t workspace_bytes, void* stream) {
+  int rc = check_norm_config(cfg, w, y != nullptr || T == 0, T);  // no rows: y may be NULL either way
+  if (rc) return rc;
+  if (!grads) return COLIBRI_ERR_INVALID_ARG;
+  const int d = cfg->d_model;
+  const bool next = cfg->before != COLIBRI_NORM_NONE;
+  // a gradient can be asked for only where the parameter is
+  if ((grads->after_weight && !w->after_weight) || (grads->after_bias && cfg->after != COLIBRI_NORM_LAYER) ||
+      (grads->before_weight && !w->before_weight) || (grads->before_bias && cfg->before != COLIBRI_NORM_LAYER) ||
+      (grads->gate != nullptr) != (w->gate != nullptr))
+    return COLIBRI_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (next != (d_p != nullptr) || (next && !x1) || (!next && !d_x1) || !d_x || (y != nullptr) != (d_y != nullptr))
+      return COLIBRI_ERR_INVALID_ARG;
+    if ((d_x1 && !stride_ok(ld_dx1, d)) || (d_p && !stride_ok(ld_dp, d)) || (next && !stride_ok(ldx1, d)) ||
+        (y && !stride_ok(ldy, d)))
+      return COLIBRI_ERR_INVALID_ARG;
+    const int es = ops_elem(cfg->dtype), ey = ops_elem(cfg->block_dtype);
+    const Span in[] = {{d_x1, span_of(T, ld_dx1, d, es)},
+                       {d_p, span_of(T, ld_dp, d, es)},
+                       {next ? x1 : nullptr, span_of(T, ldx1, d, es)},
+                       {y, span_of(T, ldy, d, ey)}};
+    const Span ox{d_x, (int64_t)T * d * es}, oy{d_y, (int64_t)T * d * ey};
+    for (const Span& q : in)
+      if (spans_overlap(q, ox) || spans_overlap(q, oy)) return COLIBRI_ERR_INVALID_ARG;
+    if (spans_overlap(ox, oy)) return COLIBRI_ERR_INVALID_ARG;
+  }
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  for (const void* q : {d_x1, d_p, next ? x1 : nullptr, y, w->after_weight, w->after_bias, w->before_weight,
+                        w->before_bias, w->gate, (const void*)d_x, (const void*)d_y, (const void*)grads->after_weight,
+                        (const void*)grads->after_bias, (const void*)grads->before_weight,
+                        (const void*)grads->before_bias, (const void*)grads->gate, (const void*)workspace})
+    if (q && !ops_on_device(q, device)) return COLIBRI_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {  // no rows: the column sums are zero (there is no gate row to sum into)
+    for (float* g : {grads->after_weight, grads->after_bias, grads->before_weight, grads->before_bias})
+      if (g && cudaMemsetAsync(g, 0, d * sizeof(float), s) != cudaSuccess) {
+        cudaGetLastError();
+        return COLIBRI_ERR_CUDA;
+      }
+    return COLIBRI_OK;
+  }
+  int rows = 0;
+  const int blocks = backward_blocks(T, d, sms, &rows);
+  if (!workspace || workspace_bytes < (size_t)blocks * kSlots * d * sizeof(float) || !ops_aligned16(workspace))
+    return COLIBRI_ERR_INVALID_ARG;
+  NormArgs a = {};
+  a.x = x1, a.y = y, a.wa = w->after_weight, a.ba = w->after_bias, a.wb = w->before_weight, a.bb = w->before_bias;
+  a.gate = w->gate, a.dx1 = d_x1, a.dp = d_p, a.dx = d_x, a.dy = d_y, a.part = static_cast<float*>(workspace);
+  a.dgate = grads->gate, a.ldx = ldx1, a.ldy = ldy, a.lddx1 = ld_dx1, a.lddp = ld_dp, a.rpg = cfg->rows_per_gate;
+  a.T = T, a.d = d, a.after = cfg->after, a.before = cfg->before, a.rows_per_block = rows;
+  a.param_bf16 = cfg->param_dtype == COLIBRI_DTYPE_BF16;
+  a.alpha = y ? cfg->residual_scale : 1.f, a.beta = cfg->block_scale, a.eps = cfg->eps;
+  bool vec = d % 8 == 0 && (!d_x1 || ld_dx1 % 8 == 0) && (!next || (ldx1 % 8 == 0 && ld_dp % 8 == 0)) && (!y || ldy % 8 == 0);
+  for (const void* q : {d_x1, d_p, next ? x1 : nullptr, y, a.wa, a.ba, a.wb, a.bb, a.gate, (const void*)d_x,
+                        (const void*)d_y, (const void*)grads->gate})
+    vec = vec && ops_aligned16(q);
+  cudaError_t e = by_type(cfg->dtype, cfg->block_dtype, vec, [&](auto st, auto yt, bool v) {
+    using S = decltype(st);
+    using Y = decltype(yt);
+    return v ? launch_backward<S, Y, true>(a, blocks, s) : launch_backward<S, Y, false>(a, blocks, s);
+  });
+  if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
+  NormSumsArgs q = {a.part,
+                    {grads->before_weight, grads->before_bias, grads->after_weight, grads->after_bias},
+                    grads->gate, cfg->rows_per_gate, T, d, blocks, rows};
+  e = pdl_launch(norm_sums_kernel, dim3((d + kSumCols - 1) / kSumCols, 5), dim3(kSumCols * kSumLanes), 0, s, q);
+  return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}

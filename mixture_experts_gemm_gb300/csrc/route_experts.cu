@@ -1,0 +1,652 @@
+// Routing to many experts: scores, a balance bias, expert groups, top-k, gates and the dispatch order.
+//
+//   s_e = softmax(l)_e or 1 / (1 + exp(-l_e)),   key_e = s_e + b_e   (without a bias: rank by l_e)
+//   group score = sum of the group_top largest keys of the group; the top_groups best groups are kept
+//   e_1..e_k = the experts of the kept groups ranked first by (key descending, index ascending)
+//   gate_i = scale * s_{e_i} [/ sum_j s_{e_j}]         (the bias decides who is chosen, not the weight)
+//   rows: expert segments in order, ascending tokens inside each: row_of, token_of_row, counts, offsets
+// An expert whose logit or bias is -inf or NaN is masked: never chosen.  A token with fewer than k
+// experts left gets index -1, gate 0 and row -1 in its last slots.
+//
+// The choice is that of the keys in 64 bits: scores are fp32, with a bound on their error beside them;
+// where a choice is not decided by more than the bounds (about one token in a thousand on normal
+// logits), the warp ranks that token again with 64-bit keys.  So which experts serve a token does not
+// hang on the rounding of one exp.  Two slots that hold the same logit and bias are equal, not close:
+// the lower index is right without a second look.
+//
+// One warp a token, the experts over its lanes (expert = lane + 32 slot); k rounds of a warp-wide
+// maximum.  Ranks inside a chunk of 32 tokens come from one 32-bit token mask per expert.
+#include <algorithm>
+
+#include "ops_common.cuh"
+
+namespace colibri {
+namespace {
+
+constexpr int kRouteMaxE = 512, kRouteMaxK = 32, kRouteMaxGroups = 32;
+constexpr int kRouteTokens = 32;  // tokens of a chunk: the bits of an expert's token mask
+constexpr int kRouteWarps = 16;
+
+struct RouteManyArgs {
+  const void* logits;
+  int64_t ld;
+  const float* bias;
+  int T, E, k, groups, per_group, top_groups, group_top, softmax, renorm;
+  float scale;
+  int32_t *idx, *counts, *offsets, *row_of, *token_of_row;
+  float* gate;
+  int32_t* hist;  // [E][chunks]: a chunk's tokens per expert, then the tokens of earlier chunks
+  int chunks;
+};
+
+// Floats as unsigned numbers in the same order (no NaN).
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);  // -0 becomes +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+__device__ __forceinline__ float warp_max(float v) { return unordered(__reduce_max_sync(~0u, ordered(v))); }
+__device__ __forceinline__ float warp_min(float v) { return unordered(__reduce_min_sync(~0u, ordered(v))); }
+
+template <typename T>
+__device__ __forceinline__ bool before(T va, int ia, T vb, int ib) {
+  return va > vb || (va == vb && ia < ib);
+}
+
+// Best (value, index) of the warp, in every lane.
+__device__ __forceinline__ void warp_best(double& v, int& i) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double w = __shfl_xor_sync(~0u, v, o);
+    const int j = __shfl_xor_sync(~0u, i, o);
+    if (before(w, j, v, i)) v = w, i = j;
+  }
+}
+
+// The selection in 64 bits: sets lane i's `sel` (i < k) to the i-th expert, or -1.
+template <typename L, int NS>
+__device__ __noinline__ void select_exact(const RouteManyArgs& a, int t, int& sel) {
+  const int lane = threadIdx.x & 31;
+  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
+  const double none = -INFINITY;
+  double score[NS], key[NS];
+  double m = none;
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    const int e = lane + 32 * j;
+    double l = none;
+    if (e < a.E) {
+      const float f = to_float(row[e]);
+      if (f > -INFINITY && (!a.bias || a.bias[e] > -INFINITY)) l = f;
+    }
+    score[j] = l;
+    // the softmax runs over every expert with a logit, its key masked or not
+    if (e < a.E && to_float(row[e]) > -INFINITY) m = fmax(m, (double)to_float(row[e]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(~0u, m, o));
+  if (a.softmax) {
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const int e = lane + 32 * j;
+      const double l = e < a.E ? (double)to_float(row[e]) : none;
+      const double z = l == m ? 1.0 : (l > none ? exp(l - m) : 0.0);
+      sum += z;
+      key[j] = z;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) key[j] = score[j] > none ? (sum > 0.0 ? key[j] / sum : 0.0) : none;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) key[j] = score[j] > none ? 1.0 / (1.0 + exp(-score[j])) : none;
+  }
+  // key: the score with the bias (what groups are ranked by); score: the logit
+#pragma unroll
+  for (int j = 0; j < NS; ++j)
+    if (a.bias && key[j] > none) key[j] += a.bias[lane + 32 * j];
+  uint32_t kept = ~0u;
+  if (a.groups > 1) {
+    double mine = none;
+    for (int g = 0; g < a.groups; ++g) {
+      double total = 0.0;
+      int first = -1;
+      for (int n = 0; n < a.group_top; ++n) {
+        double v = none;
+        int i = kRouteMaxE;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const int e = lane + 32 * j;
+          if (e / a.per_group != g || e == first || key[j] == none) continue;
+          // one expert a group and no bias: the logits rank the groups, as they rank the experts
+          const double r = a.group_top == 1 && !a.bias ? score[j] : key[j];
+          if (before(r, e, v, i)) v = r, i = e;
+        }
+        warp_best(v, i);
+        if (i == kRouteMaxE) {
+          if (n == 0) total = none;
+          break;
+        }
+        total += v;
+        first = i;
+      }
+      if (lane == g) mine = total;
+    }
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const double v = __shfl_sync(~0u, mine, g);
+      rank += before(v, g, mine, lane);
+    }
+    kept = __ballot_sync(~0u, lane < a.groups && rank < a.top_groups);
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    const int e = lane + 32 * j;
+    if (key[j] > none && !a.bias) key[j] = score[j];
+    if (e >= a.E || !(kept >> (e / a.per_group) & 1)) key[j] = none;
+  }
+  sel = -1;
+  for (int n = 0; n < a.k; ++n) {
+    double v = none;
+    int i = kRouteMaxE;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      if (key[j] > none && before(key[j], lane + 32 * j, v, i)) v = key[j], i = lane + 32 * j;
+    warp_best(v, i);
+    if (i == kRouteMaxE) break;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      if (lane + 32 * j == i) key[j] = none;
+    if (lane == n) sel = i;
+  }
+}
+
+// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.
+template <typename L, int NS>
+__device__ __forceinline__ void route_token(const RouteManyArgs& a, int t, int& sel, float& s_sel) {
+  const int lane = threadIdx.x & 31;
+  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
+  float l[NS], s[NS], key[NS], err[NS];
+  bool any = false;
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    const int e = lane + 32 * j;
+    l[j] = e < a.E ? to_float(row[e]) : -INFINITY;
+    if (!(l[j] > -INFINITY)) l[j] = -INFINITY;  // NaN
+  }
+  if (a.softmax) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) m = fmaxf(m, l[j]);
+    m = warp_max(m);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      s[j] = l[j] == -INFINITY ? 0.f : (l[j] == m ? 1.f : expf(l[j] - m));
+      sum += s[j];
+    }
+    sum = warp_sum(sum);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      s[j] *= inv;
+      // l - m is rounded to 2^-24 of itself, exp to 2 ulp, the sum (at most 16 + 5 additions) and the
+      // product with 1 / sum to less than 2^-19 together
+      err[j] = s[j] * (0x1p-18f + 0x1p-23f * fminf(m - l[j], 200.f));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      s[j] = l[j] == -INFINITY ? 0.f : 1.f / (1.f + expf(-l[j]));
+      err[j] = s[j] * 0x1p-21f;  // exp 2 ulp, the sum and the quotient half an ulp each
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    key[j] = l[j] == -INFINITY ? -INFINITY : s[j];
+    if (a.bias && l[j] > -INFINITY) {
+      const float b = a.bias[lane + 32 * j];
+      key[j] = b > -INFINITY ? s[j] + b : -INFINITY;
+    }
+    // half an ulp of the sum with the bias, and what exp loses below the normal range
+    err[j] += fabsf(key[j] > -INFINITY ? key[j] : 0.f) * 0x1p-23f + 0x1p-120f;
+    any |= key[j] > -INFINITY;
+  }
+  bool unsure = false;
+  uint32_t kept = ~0u;
+  if (a.groups > 1) {
+    const bool by_logit = a.group_top == 1 && !a.bias;
+    float total = -INFINITY, off = 0.f;
+    for (int g = 0; g < a.groups; ++g) {
+      float v = -INFINITY, v2 = -INFINITY, o = 0.f;
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const int e = lane + 32 * j;
+        if (e >= a.E || e / a.per_group != g || key[j] == -INFINITY) continue;
+        const float r = by_logit ? l[j] : key[j];
+        o = fmaxf(o, err[j]);
+        v2 = fmaxf(v2, fminf(v, r));
+        v = fmaxf(v, r);
+      }
+      const float best = warp_max(v);
+      float sum = best;
+      if (a.group_top == 2) {
+        // the second best: the lane that gave the best (the first of equals) offers its next one
+        const uint32_t who = __ballot_sync(~0u, v == best);
+        const float second = warp_max(lane == __ffs(who) - 1 ? v2 : v);
+        if (second > -INFINITY) sum += second;
+      }
+      o = warp_max(o);
+      if (lane == g) total = sum, off = by_logit ? 0.f : 2.f * o + fabsf(sum > -INFINITY ? sum : 0.f) * 0x1p-23f;
+    }
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) rank += before(__shfl_sync(~0u, total, g), g, total, lane);
+    const bool in = lane < a.groups && rank < a.top_groups;
+    kept = __ballot_sync(~0u, in);
+    if (!by_logit && a.top_groups < a.groups) {
+      const float lowest = warp_min(in ? total - off : INFINITY);
+      const float highest = warp_max(lane < a.groups && !in ? total + off : -INFINITY);
+      unsure = !(lowest > highest) && highest > -INFINITY;
+    }
+  }
+  // the experts that are left, by (key, index)
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    const int e = lane + 32 * j;
+    if (key[j] > -INFINITY && !a.bias) key[j] = l[j], err[j] = 0.f;
+    if (e >= a.E || !(kept >> (a.groups > 1 ? e / a.per_group : 0) & 1)) key[j] = -INFINITY;
+  }
+  sel = -1;
+  float mine = -INFINITY, off = 0.f, ml = 0.f;
+  s_sel = 0.f;
+  float best = -INFINITY;
+  int at = 0;
+#pragma unroll
+  for (int j = NS - 1; j >= 0; --j)
+    if (key[j] >= best) best = key[j], at = j;
+  uint32_t taken = 0;
+  for (int n = 0; n < a.k; ++n) {
+    const uint32_t o = ordered(best), top = __reduce_max_sync(~0u, o);
+    if (top == ordered(-INFINITY)) break;
+    const int e = __reduce_min_sync(~0u, o == top ? lane + 32 * at : kRouteMaxE);
+    // the winner's values to lane n
+    float ws = 0.f, wo = 0.f, wl = 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      if (j == at) ws = s[j], wo = err[j], wl = l[j];
+    ws = __shfl_sync(~0u, ws, e & 31), wo = __shfl_sync(~0u, wo, e & 31), wl = __shfl_sync(~0u, wl, e & 31);
+    if (lane == n) sel = e, mine = unordered(top), off = wo, ml = wl, s_sel = ws;
+    if (lane == (e & 31)) {
+      taken |= 1u << at;
+      best = -INFINITY, at = 0;
+#pragma unroll
+      for (int j = NS - 1; j >= 0; --j)
+        if (!(taken >> j & 1) && key[j] >= best) best = key[j], at = j;
+    }
+  }
+  if (a.bias) {
+    const int found = __popc(__ballot_sync(~0u, sel >= 0));
+    // neighbours in the ranking, and the last chosen one against everything that was not
+    const float nv = __shfl_down_sync(~0u, mine, 1), no = __shfl_down_sync(~0u, off, 1), nl = __shfl_down_sync(~0u, ml, 1);
+    const float mb = sel >= 0 ? a.bias[sel] : 0.f, nb = __shfl_down_sync(~0u, mb, 1);
+    if (lane + 1 < found && !(mine - off > nv + no) && !(ml == nl && mb == nb)) unsure = true;
+    if (found == a.k) {
+      const float lo = __shfl_sync(~0u, mine - off, a.k - 1), ll = __shfl_sync(~0u, ml, a.k - 1);
+      const float lb = __shfl_sync(~0u, mb, a.k - 1);
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+        if (!(taken >> j & 1) && key[j] > -INFINITY && !(lo > key[j] + err[j]) &&
+            !(l[j] == ll && a.bias[lane + 32 * j] == lb))
+          unsure = true;
+    }
+  }
+  if (__any_sync(~0u, unsure)) {
+    select_exact<L, NS>(a, t, sel);
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {  // the chosen experts' scores, slot by slot
+      const float w = __shfl_sync(~0u, s[j], max(sel, 0) & 31);
+      if (sel >> 5 == j) v = w;
+    }
+    s_sel = sel >= 0 ? v : 0.f;
+  }
+}
+
+// offsets[e] = rows before expert e, from counts in shared memory, by one warp; returns nothing past it.
+__device__ __forceinline__ void scan_counts(const int* counts, int* offsets, int E) {
+  const int lane = threadIdx.x & 31;
+  const int per = (E + 31) / 32;
+  int sum = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < E) sum += counts[e];
+  }
+  int before_me = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, before_me, o);
+    if (lane >= o) before_me += v;
+  }
+  if (lane == 31) offsets[E] = before_me;
+  before_me -= sum;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < E) {
+      offsets[e] = before_me;
+      before_me += counts[e];
+    }
+  }
+}
+
+// One chunk of 32 tokens a block.  With a single chunk the whole dispatch is done here; else row_of
+// holds ranks inside the chunk and hist the chunk's counts.
+template <typename L, int NS>
+__global__ void __launch_bounds__(32 * kRouteWarps) route_tokens_kernel(RouteManyArgs a) {
+  __shared__ uint32_t mask[NS * 32];
+  __shared__ int count[NS * 32], offset[NS * 32 + 1];
+  __shared__ int16_t chosen[kRouteTokens][kRouteMaxK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  for (int e = threadIdx.x; e < NS * 32; e += blockDim.x) mask[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  const int t0 = blockIdx.x * kRouteTokens, n = min(kRouteTokens, a.T - t0);
+  for (int i = warp; i < n; i += warps) {
+    int sel;
+    float s;
+    route_token<L, NS>(a, t0 + i, sel, s);
+    const float sum = warp_sum(lane < a.k ? s : 0.f);
+    if (lane < a.k) {
+      const int64_t o = (int64_t)(t0 + i) * a.k + lane;
+      a.idx[o] = sel;
+      a.gate[o] = a.renorm ? (sum > 0.f ? a.scale * (s / sum) : 0.f) : a.scale * s;
+      chosen[i][lane] = sel;
+      if (sel >= 0) atomicOr(&mask[sel], 1u << i);  // bits of different tokens: any order gives the same
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    count[e] = __popc(mask[e]);
+    if (a.chunks > 1) a.hist[(int64_t)e * a.chunks + blockIdx.x] = count[e];
+  }
+  if (a.chunks == 1) {
+    __syncthreads();
+    if (warp == 0) scan_counts(count, offset, a.E);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
+      a.offsets[e] = offset[e];
+      if (e < a.E) a.counts[e] = count[e];
+    }
+    for (int i = offset[a.E] + threadIdx.x; i < a.T * a.k; i += blockDim.x) a.token_of_row[i] = -1;
+  }
+  for (int i = threadIdx.x; i < n * a.k; i += blockDim.x) {
+    const int tok = i / a.k, e = chosen[tok][i % a.k];
+    int r = -1;
+    if (e >= 0) {
+      r = __popc(mask[e] & ((1u << tok) - 1));
+      if (a.chunks == 1) {
+        r += offset[e];
+        a.token_of_row[r] = tok;
+      }
+    }
+    a.row_of[(int64_t)t0 * a.k + i] = r;
+  }
+}
+
+// hist[e][c] becomes the tokens of e in chunks before c; counts[e] their total.  One warp an expert.
+__global__ void __launch_bounds__(256) route_scan_kernel(RouteManyArgs a) {
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  pdl_wait();
+  if (e >= a.E) return;
+  int32_t* h = a.hist + (int64_t)e * a.chunks;
+  int carry = 0;
+  for (int c0 = 0; c0 < a.chunks; c0 += 32) {
+    const int v = c0 + lane < a.chunks ? h[c0 + lane] : 0;
+    int run = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(~0u, run, o);
+      if (lane >= o) run += w;
+    }
+    if (c0 + lane < a.chunks) h[c0 + lane] = carry + run - v;
+    carry += __shfl_sync(~0u, run, 31);
+  }
+  if (lane == 0) a.counts[e] = carry;
+}
+
+// Ranks inside the chunks become rows.
+__global__ void __launch_bounds__(256) route_rows_many_kernel(RouteManyArgs a) {
+  __shared__ int count[kRouteMaxE], offset[kRouteMaxE + 1];
+  pdl_wait();
+  for (int e = threadIdx.x; e < a.E; e += 256) count[e] = a.counts[e];
+  __syncthreads();
+  if (threadIdx.x < 32) scan_counts(count, offset, a.E);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= a.E; e += 256) a.offsets[e] = offset[e];
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = (int64_t)a.T * a.k;
+  if (i >= n) return;
+  const int e = a.idx[i];
+  if (e >= 0) {
+    const int t = (int)(i / a.k);
+    const int r = a.row_of[i] + a.hist[(int64_t)e * a.chunks + t / kRouteTokens] + offset[e];
+    a.row_of[i] = r;
+    a.token_of_row[r] = t;
+  }
+  if (i >= offset[a.E]) a.token_of_row[i] = -1;
+}
+
+struct RouteBackArgs {
+  const void* logits;
+  int64_t ld, ldd;
+  const int32_t* idx;
+  const float* d_gate;
+  void* d_logits;
+  int T, E, k, softmax, renorm;
+  float scale;
+};
+
+// d_logits of one token a warp.  With q_i = s_i / sum_j s_j over the chosen experts:
+//   renormalised: softmax  d_l = scale q_i (g_i - sum q g)           (the softmax's own sum drops out)
+//                 sigmoid  d_l = scale q_i (g_i - sum q g) (1 - s_i)
+//   else:         softmax  d_l = scale s_e (g_e - sum s g), g_e = 0 where e was not chosen
+//                 sigmoid  d_l = scale g_i s_i (1 - s_i)
+template <typename L, int NS>
+__global__ void __launch_bounds__(256) route_backward_kernel(RouteBackArgs a) {
+  __shared__ float dense[8][NS * 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* mine = dense[warp];
+  pdl_wait();
+  for (int t = blockIdx.x * 8 + warp; t < a.T; t += gridDim.x * 8) {
+    const L* row = static_cast<const L*>(a.logits) + t * a.ld;
+    int e = -1;
+    float g = 0.f, l = -INFINITY;
+    if (lane < a.k) {
+      e = a.idx[(int64_t)t * a.k + lane];
+      if (e < 0 || e >= a.E) e = -1;
+      if (e >= 0) {
+        g = a.d_gate[(int64_t)t * a.k + lane];
+        l = to_float(row[e]);
+        if (!(l > -INFINITY)) e = -1, g = 0.f;  // masked: its score is 0 and stays it
+      }
+    }
+    for (int i = lane; i < NS * 32; i += 32) mine[i] = 0.f;
+    __syncwarp();
+    float v[NS], common = 0.f;
+    if (a.softmax) {
+      float m = -INFINITY;
+      if (a.renorm) {
+        m = warp_max(e >= 0 ? l : -INFINITY);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          v[j] = lane + 32 * j < a.E ? to_float(row[lane + 32 * j]) : -INFINITY;
+          if (!(v[j] > -INFINITY)) v[j] = -INFINITY;
+          m = fmaxf(m, v[j]);
+        }
+        m = warp_max(m);
+      }
+      float sum = 0.f;
+      float s = e < 0 ? 0.f : (l == m ? 1.f : expf(l - m));
+      if (a.renorm) {
+        sum = s;
+      } else {
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          v[j] = v[j] == -INFINITY ? 0.f : (v[j] == m ? 1.f : expf(v[j] - m));
+          sum += v[j];
+        }
+      }
+      sum = warp_sum(sum);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      s *= inv;
+      common = warp_sum(s * g);
+      if (a.renorm) {
+        if (e >= 0) mine[e] = a.scale * s * (g - common);
+      } else {
+        if (e >= 0) mine[e] = g;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) v[j] *= inv;
+      }
+    } else if (e >= 0) {
+      // s (1 - s) from exp(-|l|): no cancellation where s is near 1
+      const float x = expf(-fabsf(l)), inv = 1.f / (1.f + x);
+      const float small = x * inv, big = inv;  // the smaller and the larger of s and 1 - s
+      v[0] = l >= 0.f ? big : small;           // s
+      common = l >= 0.f ? small : big;         // 1 - s
+    }
+    if (!a.softmax) {
+      if (a.renorm) {
+        const float s = e >= 0 ? v[0] : 0.f, sum = warp_sum(s), q = sum > 0.f ? s / sum : 0.f;
+        const float mean = warp_sum(q * g);
+        if (e >= 0) mine[e] = a.scale * q * (g - mean) * common;
+      } else if (e >= 0) {
+        mine[e] = a.scale * g * v[0] * common;
+      }
+    }
+    __syncwarp();
+    const bool full = a.softmax && !a.renorm;
+    L* out = static_cast<L*>(a.d_logits) + t * a.ldd;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const int i = lane + 32 * j;
+      if (i < a.E) out[i] = from_float<L>(full ? a.scale * v[j] * (mine[i] - common) : mine[i]);
+    }
+    __syncwarp();
+  }
+}
+
+// f(L{}, slots as a constant) by the logits' type and the experts' number.
+template <typename F>
+cudaError_t by_experts(int dtype, int E, F f) {
+  auto with = [&](auto l) {
+    if (E <= 32) return f(l, std::integral_constant<int, 1>{});
+    if (E <= 64) return f(l, std::integral_constant<int, 2>{});
+    if (E <= 128) return f(l, std::integral_constant<int, 4>{});
+    if (E <= 256) return f(l, std::integral_constant<int, 8>{});
+    return f(l, std::integral_constant<int, 16>{});
+  };
+  return dtype == COLIBRI_DTYPE_F32 ? with(float{}) : with(__nv_bfloat16{});
+}
+
+int check_route_config(const colibri_moe_route_config_t* c, int32_t T, int64_t ld) {
+  if (!c || T < 0) return COLIBRI_ERR_INVALID_ARG;
+  if (c->num_experts < 1 || c->top_k < 1 || c->top_k > c->num_experts || !ops_dtype(c->logits_dtype) ||
+      (c->score != COLIBRI_SCORE_SOFTMAX && c->score != COLIBRI_SCORE_SIGMOID) || (c->renormalize & ~1))
+    return COLIBRI_ERR_INVALID_ARG;
+  if (c->groups < 1 || c->num_experts % c->groups || c->top_groups < 1 || c->top_groups > c->groups ||
+      c->group_top < 1 || c->group_top > 2 || c->top_k > c->top_groups * (c->num_experts / c->groups))
+    return COLIBRI_ERR_INVALID_ARG;
+  if (c->num_experts > kRouteMaxE || c->top_k > kRouteMaxK || c->groups > kRouteMaxGroups) return COLIBRI_ERR_UNSUPPORTED;
+  if (ld < c->num_experts) return COLIBRI_ERR_INVALID_ARG;
+  if ((int64_t)T * c->top_k > INT32_MAX) return COLIBRI_ERR_INVALID_ARG;
+  return COLIBRI_OK;
+}
+
+int route_chunks(int T) { return (T + kRouteTokens - 1) / kRouteTokens; }
+
+}  // namespace
+}  // namespace colibri
+
+using namespace colibri;
+
+extern "C" int colibri_moe_route_experts_workspace(const colibri_moe_route_config_t* cfg, int32_t T, size_t* bytes) {
+  if (!bytes) return COLIBRI_ERR_INVALID_ARG;
+  const int rc = check_route_config(cfg, T, cfg ? cfg->num_experts : 0);
+  if (rc) return rc;
+  const int chunks = route_chunks(T);
+  *bytes = chunks > 1 ? (size_t)chunks * cfg->num_experts * sizeof(int32_t) : 0;
+  return COLIBRI_OK;
+}
+
+extern "C" int colibri_moe_route_experts(const colibri_moe_route_config_t* cfg, const void* logits, int64_t ld,
+                                         const float* bias, int32_t T, int32_t* idx, float* gate, int32_t* counts,
+                                         int32_t* offsets, int32_t* row_of, int32_t* token_of_row, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  const int rc = check_route_config(cfg, T, ld);
+  if (rc) return rc;
+  if (!counts || !offsets || (T > 0 && (!logits || !idx || !gate || !row_of || !token_of_row)))
+    return COLIBRI_ERR_INVALID_ARG;
+  const int chunks = route_chunks(T);
+  if (chunks > 1 && (!workspace || workspace_bytes < (size_t)chunks * cfg->num_experts * sizeof(int32_t)))
+    return COLIBRI_ERR_INVALID_ARG;
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  for (const void* p : {logits, (const void*)bias, (const void*)idx, (const void*)gate, (const void*)counts,
+                        (const void*)offsets, (const void*)row_of, (const void*)token_of_row,
+                        (const void*)(chunks > 1 ? workspace : nullptr)})
+    if (p && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int E = cfg->num_experts;
+  if (T == 0) {
+    if (cudaMemsetAsync(counts, 0, E * sizeof(int32_t), s) != cudaSuccess ||
+        cudaMemsetAsync(offsets, 0, (E + 1) * sizeof(int32_t), s) != cudaSuccess) {
+      cudaGetLastError();
+      return COLIBRI_ERR_CUDA;
+    }
+    return COLIBRI_OK;
+  }
+  RouteManyArgs a = {};
+  a.logits = logits, a.ld = ld, a.bias = bias, a.T = T, a.E = E, a.k = cfg->top_k, a.groups = cfg->groups;
+  a.per_group = E / cfg->groups, a.top_groups = cfg->top_groups;
+  a.group_top = std::min(cfg->group_top, a.per_group), a.softmax = cfg->score == COLIBRI_SCORE_SOFTMAX;
+  a.renorm = cfg->renormalize, a.scale = cfg->scale, a.idx = idx, a.gate = gate, a.counts = counts;
+  a.offsets = offsets, a.row_of = row_of, a.token_of_row = token_of_row, a.hist = static_cast<int32_t*>(workspace);
+  a.chunks = chunks;
+  cudaError_t e = by_experts(cfg->logits_dtype, E, [&](auto l, auto ns) {
+    return pdl_launch(route_tokens_kernel<decltype(l), decltype(ns)::value>, dim3(chunks),
+                      dim3(32 * std::min(kRouteWarps, T)), 0, s, a);
+  });
+  if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
+  if (chunks > 1) {
+    e = pdl_launch(route_scan_kernel, dim3((E + 7) / 8), dim3(256), 0, s, a);
+    if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
+    e = pdl_launch(route_rows_many_kernel, dim3((unsigned)(((int64_t)T * a.k + 255) / 256)), dim3(256), 0, s, a);
+    if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
+  }
+  return COLIBRI_OK;
+}
+
+extern "C" int colibri_moe_route_experts_backward(const colibri_moe_route_config_t* cfg, const void* logits, int64_t ld,
+                                                  const int32_t* idx, const float* d_gate, int32_t T, void* d_logits,
+                                                  int64_t ld_d, void* stream) {
+  const int rc = check_route_config(cfg, T, ld);
+  if (rc) return rc;
+  if (T == 0) return COLIBRI_OK;
+  if (!logits || !idx || !d_gate || !d_logits || ld_d < cfg->num_experts) return COLIBRI_ERR_INVALID_ARG;
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  for (const void* p : {logits, (const void*)idx, (const void*)d_gate, (const void*)d_logits})
+    if (!ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
+  RouteBackArgs a = {logits, ld, ld_d, idx, d_gate, d_logits, T, cfg->num_experts, cfg->top_k,
+                     cfg->score == COLIBRI_SCORE_SOFTMAX, cfg->renormalize, cfg->scale};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = by_experts(cfg->logits_dtype, cfg->num_experts, [&](auto l, auto ns) {
+    return pdl_launch(route_backward_kernel<decltype(l), decltype(ns)::value>, dim3(std::min((T + 7) / 8, sms * 8)),
+                      dim3(256), 0, s, a);
+  });
+  return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}

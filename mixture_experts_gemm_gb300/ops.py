@@ -1,0 +1,353 @@
+"""Operators of the block around the expert layer, and experts in 8-bit integers.
+
+The counterparts of the context-free calls of ``include/colibri_moe.h``: norms before and after a
+block with its gate and residual scale (``block_norm``), routing to many experts with the dispatch
+order (``route``), experts in 8-bit integers (``int8_experts``) and their combine (``combine``), with
+the backward passes of the norms and of the routing.  Every call runs on CUDA tensors, asynchronously
+on ``stream`` (default: the current stream), allocates its outputs and workspace from torch, and can be
+captured into a CUDA graph.  Errors raise ``ColibriError`` (checks of the library) or ``ValueError``
+(shapes and types that cannot be passed on).
+
+    x1, p = block_norm(x, y, after="rms", after_weight=w_a, before="rms", before_weight=w_b)
+    r = route(logits, 8, score="sigmoid", bias=b, groups=8, top_groups=4, group_top=2, scale=2.5)
+    h = int8_experts(p, w1, s1, r.offsets, rows=r.token_of_row, w3=w3, w3_scale=s3)
+    o = combine(int8_experts(h, w2, s2, r.offsets), r.row_of, r.gate)
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import (DTYPE_BF16, DTYPE_F32, ColibriError, Int8Config, NormConfig, NormVectors, RouteConfig, _check, lib)
+
+__all__ = ["block_norm", "block_norm_backward", "pre_norm", "route", "route_backward", "Routing", "int8_quantize",
+           "int8_experts", "combine", "ColibriError"]
+
+_DTYPE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+_NORMS = {"none": 0, "rms": 1, "layer": 2}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _dtype(t, name: str) -> int:
+    try:
+        return _DTYPE[t]
+    except KeyError:
+        raise ValueError(f"{name}: float32 or bfloat16, not {t}") from None
+
+
+def _kind(table, key, name: str) -> int:
+    try:
+        return table[key]
+    except KeyError:
+        raise ValueError(f"{name}: one of {', '.join(table)}, not {key!r}") from None
+
+
+def _matrix(t, name: str, rows: Optional[int] = None, cols: Optional[int] = None, dtype=None):
+    """(address, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{'n' if rows is None else rows}, "
+                         f"{'d' if cols is None else cols}]")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} expected, not {t.dtype}")
+    n, d = t.shape
+    s0, s1 = t.stride()
+    if d > 1 and s1 != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), (s0 if n > 1 else max(d, 1))
+
+
+def _vector(t, name: str, shape, dtype):
+    """Address of a contiguous CUDA tensor of the given shape and type, or None for None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: a contiguous CUDA tensor {tuple(shape)} of {dtype} expected, not "
+                         f"{tuple(t.shape)} of {t.dtype}")
+    return t.data_ptr()
+
+
+class _on:
+    """Makes the tensors' device current for the call, and their stream the caller's.
+
+    Outputs and workspace come from torch's allocator on the stream that the kernels run on, so a block
+    freed after the call is handed out again only behind them on that stream."""
+    __slots__ = ("guard", "stream", "handle")
+
+    def __init__(self, t, stream):
+        dev = t.device.index
+        self.guard = torch.cuda.device(dev) if dev != torch.cuda.current_device() else None
+        if stream is None:
+            self.stream = None
+            self.handle = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=t.device)
+            self.stream = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _workspace(n: int, device):
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+# ------------------------------------------------------------------------------------------- norms
+@functools.lru_cache(maxsize=256)
+def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gate, residual_scale, block_scale, eps):
+    c = NormConfig(d, dtype, block_dtype, param_dtype, _kind(_NORMS, after, "after"), _kind(_NORMS, before, "before"),
+                   rows_per_gate, residual_scale, block_scale, eps)
+    return c, ctypes.addressof(c)
+
+
+def _norm_setup(T, d, dtype, block_dtype, after, after_weight, after_bias, before, before_weight, before_bias, gate,
+                rows_per_gate, residual_scale, block_scale, eps):
+    params = [p for p in (after_weight, after_bias, before_weight, before_bias, gate) if p is not None]
+    pt = params[0].dtype if params else torch.float32
+    rpg, n_gates = 0, 0
+    if gate is not None:
+        if gate.dim() == 1:
+            gate = gate.unsqueeze(0)
+        rpg = max(T, 1) if rows_per_gate is None else int(rows_per_gate)
+        if rpg <= 0:
+            raise ValueError("rows_per_gate must be positive")
+        n_gates = -(-T // rpg)
+        if T == 0:
+            n_gates = gate.shape[0]
+    v = NormVectors(_vector(after_weight, "after_weight", (d,), pt), _vector(after_bias, "after_bias", (d,), pt),
+                    _vector(before_weight, "before_weight", (d,), pt), _vector(before_bias, "before_bias", (d,), pt),
+                    _vector(gate, "gate", (n_gates, d), pt))
+    c = _norm_config(d, _dtype(dtype, "x"), _dtype(block_dtype, "y"), _dtype(pt, "the parameters"), after, before, rpg,
+                     float(residual_scale), float(block_scale), float(eps))
+    return c, v, n_gates
+
+
+def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, before="none", before_weight=None,
+               before_bias=None, gate=None, rows_per_gate=None, residual_scale=1.0, block_scale=1.0, eps=1e-6,
+               stream=None):
+    """Norms before and after a block, with its gate and the residual scale, in one pass:
+
+        z  = norm_after(y) * after_weight + after_bias
+        x1 = residual_scale * x + block_scale * gate * z
+        p  = norm_before(x1) * before_weight + before_bias
+
+    x [T, d] is the residual stream, y [T, d] the block's output (its own type: the expert layer gives
+    fp32 beside a bf16 stream); after and before are "none", "rms" or "layer"; gate is [d] (every token)
+    or [ceil(T / rows_per_gate), d].  Returns (x1, p); p is None without a next norm, and without y
+    x1 is None (a norm before a block alone)."""
+    T, d = x.shape if x.dim() == 2 else (None, None)
+    px, ldx = _matrix(x, "x")
+    py, ldy = _matrix(y, "y", T, d) if y is not None else (None, 0)
+    (_, c), v, _ = _norm_setup(T, d, x.dtype, y.dtype if y is not None else x.dtype, after, after_weight, after_bias,
+                               before, before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
+    with _on(x, stream) as s:
+        x1 = torch.empty((T, d), dtype=x.dtype, device=x.device) if y is not None else None
+        p = torch.empty((T, d), dtype=x.dtype, device=x.device) if before != "none" else None
+        _check(lib().colibri_moe_block_norm(c, ctypes.addressof(v), px, ldx, py, ldy, T, _at(x1), _at(p), s),
+               "colibri_moe_block_norm")
+    return x1, p
+
+
+def pre_norm(x, weight, bias=None, *, kind="rms", eps=1e-6, stream=None):
+    """norm(x) * weight (+ bias): the norm before a block, alone."""
+    return block_norm(x, before=kind, before_weight=weight, before_bias=bias, eps=eps, stream=stream)[1]
+
+
+def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=None, after_bias=None, before="none",
+                        before_weight=None, before_bias=None, gate=None, rows_per_gate=None, residual_scale=1.0,
+                        block_scale=1.0, eps=1e-6, stream=None):
+    """Gradients of block_norm from those of its results, as a dict: d_x, d_y, and in fp32 d_wa, d_ba
+    (after), d_wb, d_bb (before), d_g, whichever the call has.  x1 and y are the forward call's (x1: x
+    itself without y); d_x1 may be None where there is a next norm, d_p is None where there is none."""
+    ref = d_x1 if d_x1 is not None else d_p
+    if ref is None:
+        raise ValueError("one of d_x1 and d_p is needed")
+    T, d = ref.shape if ref.dim() == 2 else (None, None)
+    dt = ref.dtype
+    p1, ld1 = _matrix(d_x1, "d_x1", T, d, dt) if d_x1 is not None else (None, 0)
+    pp, ldp = _matrix(d_p, "d_p", T, d, dt) if d_p is not None else (None, 0)
+    px, ldx = _matrix(x1, "x1", T, d, dt) if x1 is not None else (None, 0)
+    py, ldy = _matrix(y, "y", T, d) if y is not None else (None, 0)
+    (cfg, c), v, n_gates = _norm_setup(T, d, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
+                                       before, before_weight, before_bias, gate, rows_per_gate, residual_scale,
+                                       block_scale, eps)
+    with _on(ref, stream) as s:
+        new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=ref.device)  # noqa: E731
+        out = dict(d_x=torch.empty((T, d), dtype=dt, device=ref.device))
+        if y is not None:
+            out["d_y"] = torch.empty((T, d), dtype=y.dtype, device=ref.device)
+        for name, param in (("d_wa", after_weight), ("d_ba", after_bias), ("d_wb", before_weight),
+                            ("d_bb", before_bias)):
+            if param is not None:
+                out[name] = new(d)
+        if gate is not None:
+            out["d_g"] = new(n_gates, d) if T else torch.zeros((n_gates, d), dtype=torch.float32, device=ref.device)
+        g = NormVectors(*[_at(out.get(n)) for n in ("d_wa", "d_ba", "d_wb", "d_bb", "d_g")])
+        n = ctypes.c_size_t()
+        _check(lib().colibri_moe_block_norm_backward_workspace(c, T, ctypes.addressof(n)), "colibri_moe_block_norm_backward")
+        ws = _workspace(n.value, ref.device)
+        _check(lib().colibri_moe_block_norm_backward(c, ctypes.addressof(v), p1, ld1, pp, ldp, px, ldx, py, ldy, T,
+                                                     _at(out["d_x"]), _at(out.get("d_y")), ctypes.addressof(g),
+                                                     _at(ws), n.value, s), "colibri_moe_block_norm_backward")
+    return out
+
+
+# ----------------------------------------------------------------------------------------- routing
+class Routing(NamedTuple):
+    """Experts and gates of every token, and the dispatch order (rows grouped by expert, tokens ascending)."""
+    idx: torch.Tensor           # [T, k] int32, best first; -1: none left
+    gate: torch.Tensor          # [T, k] fp32
+    counts: torch.Tensor        # [E] int32
+    offsets: torch.Tensor       # [E + 1] int32
+    row_of: torch.Tensor        # [T, k] int32, -1 where idx is
+    token_of_row: torch.Tensor  # [T * k] int32, -1 from offsets[E] on
+
+
+@functools.lru_cache(maxsize=256)
+def _route_config(E, k, score, groups, top_groups, group_top, renormalize, dtype, scale):
+    c = RouteConfig(E, k, _kind(_SCORES, score, "score"), groups, top_groups, group_top, int(bool(renormalize)), dtype,
+                    scale)
+    return c, ctypes.addressof(c)
+
+
+def route(logits, top_k: int, *, score="softmax", bias=None, groups=1, top_groups=1, group_top=1, renormalize=True,
+          scale=1.0, stream=None) -> Routing:
+    """Routes every row of logits [T, E] (fp32 or bf16, rows may be strided) to top_k of E experts.
+
+    Scores are a softmax over the experts or sigmoids; bias [E] (fp32) is added for the choice only;
+    with groups > 1 only the experts of the top_groups best of `groups` equal runs compete, a group
+    being worth the sum of its group_top (1 or 2) largest biased scores.  Gates are the chosen scores
+    without the bias, divided by their sum if renormalize, times scale.  Ties go to the lowest index; an
+    expert with a logit or bias of -inf or NaN is never chosen."""
+    pl, ld = _matrix(logits, "logits")
+    T, E = logits.shape
+    pb = _vector(bias, "bias", (E,), torch.float32)
+    _, c = _route_config(E, int(top_k), score, int(groups), int(top_groups), int(group_top), renormalize,
+                         _dtype(logits.dtype, "logits"), float(scale))
+    with _on(logits, stream) as s:
+        n = ctypes.c_size_t()
+        _check(lib().colibri_moe_route_experts_workspace(c, T, ctypes.addressof(n)), "colibri_moe_route_experts")
+        dev, i32 = logits.device, torch.int32
+        k = int(top_k)
+        r = Routing(torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
+                    torch.empty(E, dtype=i32, device=dev), torch.empty(E + 1, dtype=i32, device=dev),
+                    torch.empty((T, k), dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev))
+        ws = _workspace(n.value, dev)
+        _check(lib().colibri_moe_route_experts(c, pl, ld, pb, T, r.idx.data_ptr(), r.gate.data_ptr(),
+                                               r.counts.data_ptr(), r.offsets.data_ptr(), r.row_of.data_ptr(),
+                                               r.token_of_row.data_ptr(), _at(ws), n.value, s),
+               "colibri_moe_route_experts")
+    return r
+
+
+def route_backward(logits, idx, d_gate, *, score="softmax", renormalize=True, scale=1.0, stream=None):
+    """d_logits [T, E] (the logits' type) from the gradient of the gates, the choice idx [T, k] held constant."""
+    pl, ld = _matrix(logits, "logits")
+    T, E = logits.shape
+    if idx.dim() != 2:
+        raise ValueError("idx: [T, k] expected")
+    k = idx.shape[1]
+    pi = _vector(idx, "idx", (T, k), torch.int32)
+    pg = _vector(d_gate, "d_gate", (T, k), torch.float32)
+    _, c = _route_config(E, k, score, 1, 1, 1, renormalize, _dtype(logits.dtype, "logits"), float(scale))
+    with _on(logits, stream) as s:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        _check(lib().colibri_moe_route_experts_backward(c, pl, ld, pi, pg, T, out.data_ptr(), E, s),
+               "colibri_moe_route_experts_backward")
+    return out
+
+
+# ----------------------------------------------------------------------------------- 8-bit experts
+@functools.lru_cache(maxsize=256)
+def _int8_config(K, N, E, dtype, out_dtype):
+    c = Int8Config(K, N, E, dtype, out_dtype)
+    return c, ctypes.addressof(c)
+
+
+def int8_quantize(x, stream=None):
+    """(q int8, scale fp32) of the rows of x [..., K]: scale = max |x| / 127, q = round(x / scale).  Rows of
+    activations, or the output channels of weights [E, N, K] once ahead of time."""
+    K = x.shape[-1]
+    flat = x.reshape(-1, K)
+    px, ldx = _matrix(flat, "x")
+    _, c = _int8_config(K, 1, 1, _dtype(x.dtype, "x"), DTYPE_F32)
+    with _on(x, stream) as s:
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        _check(lib().colibri_moe_int8_quantize(c, px, ldx, flat.shape[0], q.data_ptr(), scale.data_ptr(), s),
+               "colibri_moe_int8_quantize")
+    return q, scale
+
+
+def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, out_dtype=None, stream=None):
+    """y [R, N]: the rows of every expert times its 8-bit weights.
+
+    x [n, K] (fp32 or bf16) is quantised per row within the call; w [E, N, K] int8 with w_scale [E, N]
+    fp32; offsets [E + 1] int32 bounds every expert's rows and rows [R] int32 gives their tokens
+    (``Routing.offsets`` and ``.token_of_row``), or None: row r is x[r].  With w3 and w3_scale (same
+    shapes) y = silu(v) * v3, the gated pair of projections in one pass.  Rows from offsets[E] on are
+    not written.  out_dtype: fp32 or bf16, default x's."""
+    px, ldx = _matrix(x, "x")
+    if w.dim() != 3 or w.shape[2] != x.shape[1]:
+        raise ValueError(f"w: [E, N, {x.shape[1]}] expected, not {tuple(w.shape)}")
+    E, N, K = w.shape
+    n = x.shape[0]
+    i32 = torch.int32
+    pw = _vector(w, "w", (E, N, K), torch.int8)
+    ps = _vector(w_scale, "w_scale", (E, N), torch.float32)
+    if (w3 is None) != (w3_scale is None):
+        raise ValueError("w3 and w3_scale go together")
+    pw3 = _vector(w3, "w3", (E, N, K), torch.int8)
+    ps3 = _vector(w3_scale, "w3_scale", (E, N), torch.float32)
+    po = _vector(offsets, "offsets", (E + 1,), i32)
+    R = n if rows is None else rows.numel()
+    pr = _vector(rows, "rows", (R,), i32)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    _, c = _int8_config(K, N, E, _dtype(x.dtype, "x"), _dtype(out_dtype, "out_dtype"))
+    with _on(x, stream) as s:
+        size = ctypes.c_size_t()
+        _check(lib().colibri_moe_int8_experts_workspace(c, n, R, ctypes.addressof(size)), "colibri_moe_int8_experts")
+        ws = _workspace(size.value, x.device)
+        y = torch.empty((R, N), dtype=out_dtype, device=x.device)
+        _check(lib().colibri_moe_int8_experts(c, px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws),
+                                              size.value, s), "colibri_moe_int8_experts")
+    return y
+
+
+def combine(y, row_of, gate, *, out_dtype=None, stream=None):
+    """out[t] = sum over a token's slots of gate * y[row_of], in slot order in fp32; rows of -1 are left out."""
+    py, _ = _matrix(y, "y")
+    if not y.is_contiguous():
+        raise ValueError("y: a contiguous tensor expected")
+    if row_of.dim() != 2:
+        raise ValueError("row_of: [T, k] expected")
+    T, k = row_of.shape
+    pr = _vector(row_of, "row_of", (T, k), torch.int32)
+    pg = _vector(gate, "gate", (T, k), torch.float32)
+    out_dtype = y.dtype if out_dtype is None else out_dtype
+    with _on(y, stream) as s:
+        out = torch.empty((T, y.shape[1]), dtype=out_dtype, device=y.device)
+        _check(lib().colibri_moe_combine_rows(py, _dtype(y.dtype, "y"), y.shape[0], pr, pg, T, k, y.shape[1],
+                                              out.data_ptr(), _dtype(out_dtype, "out_dtype"), s),
+               "colibri_moe_combine_rows")
+    return out
