@@ -1,10 +1,11 @@
-// Experts in 8-bit integers: activations quantised per row, weights per output channel.
+// Experts in 8-bit integers: activations quantised per row, weights per output channel; the combine.
 //
 //   scale_t = max |x_t| / 127,  q = round(x / scale_t)  (IEEE fp32 quotients, ties to even)
 //   v[r, n] = scale_{rows[r]} w_scale[e, n] sum_k q[rows[r], k] w[e, n, k]
 //   y = v, or silu(v) * v3 with a second set of weights
 //
-// Sums are exact: 8-bit products added in 32-bit integers (K <= 65536: below 2^30).
+// This file: the quantiser (rows in dispatch order, as fp16 whole numbers that the tensor cores take), the
+// entry points, and the gate-weighted combine.  The products are in int8_mma.cu.
 #include <algorithm>
 
 #include "int8_internal.cuh"
@@ -12,112 +13,104 @@
 namespace colibri {
 namespace {
 
-// One block a row: the largest magnitude, then the quotients.
-template <typename T>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(QuantArgs a) {
-  __shared__ float s_max[8];
-  __shared__ int s_bad[8];
+__device__ __forceinline__ void store_q8(__half* p, const float (&v)[8]) {
+  __half2 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+__device__ __forceinline__ void store_q8(int8_t* p, const float (&v)[8]) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)((int)v[i] & 0xff) << (8 * (i & 3));
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <typename Q>
+__device__ __forceinline__ Q q_value(float v);
+template <>
+__device__ __forceinline__ __half q_value<__half>(float v) {
+  return __float2half_rn(v);
+}
+template <>
+__device__ __forceinline__ int8_t q_value<int8_t>(float v) {
+  return (int8_t)(int)v;
+}
+
+// round(x / scale) as the IEEE quotient gives it.  The product with 1 / scale is within 127 * 2^-22 of the
+// quotient; only where that could cross a half is the division done (about one value in five thousand).
+__device__ __forceinline__ float quotient(float x, float scale, float inv, bool exact) {
+  const float p = x * inv, t = rintf(p);
+  if (exact || fabsf(fabsf(p - t) - 0.5f) < 1e-4f) return fminf(fmaxf(rintf(__fdiv_rn(x, scale)), -127.f), 127.f);
+  return t;
+}
+
+constexpr int kQuantThreads = 256;
+
+// One block a row, held in registers between the maximum and the quotients: C chunks of 8 columns a
+// thread (VEC: 16-byte loads), or read twice (C == 0).  HBM-bound: the row once in, its fp16 once out.
+template <typename T, typename Q, int C>
+__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(QuantArgs a) {
+  __shared__ float s_max[2][8];
+  __shared__ int s_bad[2][8];
   pdl_wait();
+  for (int i = blockIdx.x * kQuantThreads + threadIdx.x; i < a.n_ticket; i += gridDim.x * kQuantThreads) a.ticket[i] = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = blockIdx.x; r < a.n; r += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+  int turn = 0;
+  for (int r = blockIdx.x; r < a.n; r += gridDim.x, turn ^= 1) {
+    int t = r;
+    if (a.rows) t = a.rows[r];
+    const bool real = t >= 0 && t < a.n_tokens;
+    const T* x = static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx;
+    Q* q = static_cast<Q*>(a.q) + (int64_t)r * a.K;
+    float v[C ? C : 1][8];
     float top = 0.f;
     bool bad = false;
-    for (int i = threadIdx.x; i < a.K; i += 256) {
-      const float v = fabsf(to_float(x[i]));
-      bad |= !(v < INFINITY);
-      top = fmaxf(top, v);
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int col = (c * kQuantThreads + threadIdx.x) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
+        if (real && col < a.K) load8(x + col, v[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          bad |= !(fabsf(v[c][j]) < INFINITY);
+          top = fmaxf(top, fabsf(v[c][j]));
+        }
+    } else if (real) {
+      for (int i = threadIdx.x; i < a.K; i += kQuantThreads) {
+        const float m = fabsf(to_float(x[i]));
+        bad |= !(m < INFINITY);
+        top = fmaxf(top, m);
+      }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     bad = __any_sync(~0u, bad);
-    if (lane == 0) s_max[warp] = top, s_bad[warp] = bad;
-    __syncthreads();
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, s_max[i]), bad |= s_bad[i] != 0;
+    if (lane == 0) s_max[turn][warp] = top, s_bad[turn][warp] = bad;
+    __syncthreads();  // one a row: the halves are used in turn
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, s_max[turn][i]), bad |= s_bad[turn][i] != 0;
     const float scale = bad ? NAN : __fdiv_rn(top, 127.f);
     if (threadIdx.x == 0) a.scale[r] = scale;
-    for (int i = threadIdx.x; i < a.K; i += 256) {
-      const float q = scale > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(to_float(x[i]), scale)), -127.f), 127.f) : 0.f;
-      a.q[(int64_t)r * a.K + i] = (int8_t)q;
-    }
-    __syncthreads();
-  }
-}
-
-constexpr int kTile = 64;
-
-// A block computes 64 rows of one expert x 64 channels; K in steps of 64 bytes through shared memory.
-template <typename O, bool SWIGLU>
-__global__ void __launch_bounds__(256) int8_tile_kernel(Int8Args a) {
-  __shared__ int sa[kTile][17], sb[kTile][17], sc[SWIGLU ? kTile : 1][17];
-  __shared__ int s_e, s_r0, s_n;
-  pdl_wait();
-  if (threadIdx.x == 0) {
-    int tile = blockIdx.y;
-    s_e = -1;
-    for (int e = 0; e < a.E; ++e) {
-      const int lo = min(max(a.offsets[e], 0), a.R), hi = min(max(a.offsets[e + 1], lo), a.R);
-      const int tiles = (hi - lo + kTile - 1) / kTile;
-      if (tile < tiles) {
-        s_e = e, s_r0 = lo + tile * kTile, s_n = min(kTile, hi - s_r0);
-        break;
+    const bool live = scale > 0.f, exact = scale < 1e-30f;  // 1 / scale may overflow there
+    const float inv = live ? __frcp_rn(scale) : 0.f;
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int col = (c * kQuantThreads + threadIdx.x) * 8;
+        if (col >= a.K) break;
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = live ? quotient(v[c][j], scale, inv, exact) : 0.f;
+        store_q8(q + col, o);
       }
-      tile -= tiles;
-    }
-  }
-  __syncthreads();
-  const int e = s_e, r0 = s_r0, n = s_n, c0 = blockIdx.x * kTile;
-  if (e < 0) return;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 4;  // this thread's 16 bytes of a tile
-  int64_t tok = -1;
-  if (lr < n) {
-    tok = a.rows ? a.rows[r0 + lr] : r0 + lr;
-    if (tok < 0 || tok >= a.n_tokens) tok = -1;
-  }
-  const bool wc = c0 + lr < a.N;
-  int acc[4][4] = {}, acc3[SWIGLU ? 4 : 1][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += 64) {
-    const bool in = k0 + lc * 4 < a.K;
-    int4 va = make_int4(0, 0, 0, 0), vb = va, vc = va;
-    if (tok >= 0 && in) va = *reinterpret_cast<const int4*>(a.q + tok * a.K + k0 + lc * 4);
-    const int64_t wo = ((int64_t)e * a.N + c0 + lr) * a.K + k0 + lc * 4;
-    if (wc && in) {
-      vb = *reinterpret_cast<const int4*>(a.w + wo);
-      if (SWIGLU) vc = *reinterpret_cast<const int4*>(a.w3 + wo);
-    }
-    __syncthreads();
-    sa[lr][lc] = va.x, sa[lr][lc + 1] = va.y, sa[lr][lc + 2] = va.z, sa[lr][lc + 3] = va.w;
-    sb[lr][lc] = vb.x, sb[lr][lc + 1] = vb.y, sb[lr][lc + 2] = vb.z, sb[lr][lc + 3] = vb.w;
-    if constexpr (SWIGLU) sc[lr][lc] = vc.x, sc[lr][lc + 1] = vc.y, sc[lr][lc + 2] = vc.z, sc[lr][lc + 3] = vc.w;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[i][j] = __dp4a(sa[ty + 16 * i][k], sb[tx + 16 * j][k], acc[i][j]);
-          if constexpr (SWIGLU) acc3[i][j] = __dp4a(sa[ty + 16 * i][k], sc[tx + 16 * j][k], acc3[i][j]);
-        }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty + 16 * i;
-    if (r >= n) continue;
-    int64_t t = a.rows ? a.rows[r0 + r] : r0 + r;
-    const bool real = t >= 0 && t < a.n_tokens;
-    const float sx = real ? a.scale[t] : 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + tx + 16 * j;
-      if (c >= a.N) continue;
-      float v = __int2float_rn(acc[i][j]) * a.w_scale[(int64_t)e * a.N + c] * sx;
-      if constexpr (SWIGLU) {
-        const float u = __int2float_rn(acc3[i][j]) * a.w3_scale[(int64_t)e * a.N + c] * sx;
-        v = v / (1.f + expf(-v)) * u;
-      }
-      static_cast<O*>(a.y)[(int64_t)(r0 + r) * a.N + c] = from_float<O>(v);
+    } else {
+      for (int i = threadIdx.x; i < a.K; i += kQuantThreads)
+        q[i] = q_value<Q>(live ? quotient(to_float(x[i]), scale, inv, exact) : 0.f);
     }
   }
 }
@@ -133,13 +126,42 @@ int check_int8_config(const colibri_moe_int8_config_t* c) {
   return COLIBRI_OK;
 }
 
+template <typename T, typename Q>
+cudaError_t quantize_t(const QuantArgs& q, int sms, cudaStream_t s) {
+  const dim3 grid(std::min(q.n, sms * 8)), block(kQuantThreads);
+  const bool vec = q.ldx % 8 == 0 && ops_aligned16(q.x) && ops_aligned16(q.q);  // K is a multiple of 16
+  const int chunks = (q.K + 8 * kQuantThreads - 1) / (8 * kQuantThreads);
+  if (!vec || chunks > 8) return pdl_launch(quantize_rows_kernel<T, Q, 0>, grid, block, 0, s, q);
+  if (chunks == 1) return pdl_launch(quantize_rows_kernel<T, Q, 1>, grid, block, 0, s, q);
+  if (chunks == 2) return pdl_launch(quantize_rows_kernel<T, Q, 2>, grid, block, 0, s, q);
+  if (chunks <= 4) return pdl_launch(quantize_rows_kernel<T, Q, 4>, grid, block, 0, s, q);
+  return pdl_launch(quantize_rows_kernel<T, Q, 8>, grid, block, 0, s, q);
+}
+
+template <typename Q>
 cudaError_t quantize(int dtype, const QuantArgs& q, int sms, cudaStream_t s) {
-  const dim3 grid(std::min(q.n, sms * 8));
-  return dtype == COLIBRI_DTYPE_F32 ? pdl_launch(quantize_rows_kernel<float>, grid, dim3(256), 0, s, q)
-                                    : pdl_launch(quantize_rows_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, q);
+  return dtype == COLIBRI_DTYPE_F32 ? quantize_t<float, Q>(q, sms, s) : quantize_t<__nv_bfloat16, Q>(q, sms, s);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Few rows an expert on average: tiles of 64 rows, a deeper ring for the weights, and K may be split.
+bool wide_form(int R, int E) { return R > 32 * (int64_t)E; }
+
+// The workspace of a product: the rows' scales and fp16 values, tickets and partial sums of split tiles.
+struct Int8Workspace {
+  size_t scale, q, ticket, partial, bytes;
+  int items;
+};
+Int8Workspace int8_workspace(const colibri_moe_int8_config_t* c, int R, int sms) {
+  Int8Workspace w = {};
+  w.items = wide_form(R, c->num_experts) ? 0 : kInt8SplitWaves * sms;
+  w.q = round256((size_t)R * sizeof(float));
+  w.ticket = w.q + round256((size_t)R * c->in_features * 2);
+  w.partial = w.ticket + round256(w.items * sizeof(uint32_t));
+  w.bytes = w.partial + (size_t)w.items * kInt8NarrowRows * 128 * sizeof(float);
+  return w;
+}
 
 struct CombineManyArgs {
   const void* y;
@@ -182,8 +204,9 @@ extern "C" int colibri_moe_int8_quantize(const colibri_moe_int8_config_t* cfg, c
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
   for (const void* p : {x, (const void*)q, (const void*)scale})
     if (!ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
-  const QuantArgs a = {x, ldx, n, cfg->in_features, q, scale};
-  return quantize(cfg->dtype, a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+  const QuantArgs a = {x, ldx, n, nullptr, n, cfg->in_features, q, scale, nullptr, 0};
+  const cudaError_t e = quantize<int8_t>(cfg->dtype, a, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 
 extern "C" int colibri_moe_int8_experts_workspace(const colibri_moe_int8_config_t* cfg, int32_t n_tokens, int32_t R,
@@ -191,7 +214,9 @@ extern "C" int colibri_moe_int8_experts_workspace(const colibri_moe_int8_config_
   const int rc = check_int8_config(cfg);
   if (rc) return rc;
   if (!bytes || n_tokens < 0 || R < 0) return COLIBRI_ERR_INVALID_ARG;
-  *bytes = round256((size_t)n_tokens * sizeof(float)) + round256((size_t)n_tokens * cfg->in_features);
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  *bytes = R ? int8_workspace(cfg, R, sms).bytes : 0;
   return COLIBRI_OK;
 }
 
@@ -207,34 +232,27 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
   if ((n_tokens > 0 && (!x || ldx < cfg->in_features)) || !offsets || !w || !w_scale || !y || (w3 != nullptr) != (w3_scale != nullptr))
     return COLIBRI_ERR_INVALID_ARG;
   if (!ops_aligned16(w) || !ops_aligned16(w3)) return COLIBRI_ERR_INVALID_ARG;
-  size_t need = 0;
-  colibri_moe_int8_experts_workspace(cfg, n_tokens, R, &need);
-  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
-    return COLIBRI_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return COLIBRI_ERR_INVALID_ARG;
+  if (workspace_bytes < int8_workspace(cfg, R, 0).bytes) return COLIBRI_ERR_INVALID_ARG;  // what any device needs
   int device = 0, sms = 0;
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  const Int8Workspace lay = int8_workspace(cfg, R, sms);
+  if (workspace_bytes < lay.bytes) return COLIBRI_ERR_INVALID_ARG;
   for (const void* p : {n_tokens ? x : nullptr, (const void*)rows, (const void*)offsets, (const void*)w,
                         (const void*)w_scale, (const void*)w3, (const void*)w3_scale, (const void*)y,
                         (const void*)workspace})
     if (p && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  float* scale = reinterpret_cast<float*>(ws);
-  int8_t* q = reinterpret_cast<int8_t*>(ws + round256((size_t)n_tokens * sizeof(float)));
-  if (n_tokens > 0) {
-    const QuantArgs qa = {x, ldx, n_tokens, cfg->in_features, q, scale};
-    if (quantize(cfg->dtype, qa, sms, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
-  }
-  const Int8Args a = {q, scale, rows, offsets, w, w3, w_scale, w3_scale, y, n_tokens, R, cfg->num_experts,
-                      cfg->in_features, cfg->out_features};
-  const dim3 grid((cfg->out_features + kTile - 1) / kTile, R / kTile + std::min(cfg->num_experts, R));
-  cudaError_t e;
-  if (cfg->out_dtype == COLIBRI_DTYPE_F32)
-    e = w3 ? pdl_launch(int8_tile_kernel<float, true>, grid, dim3(256), 0, s, a)
-           : pdl_launch(int8_tile_kernel<float, false>, grid, dim3(256), 0, s, a);
-  else
-    e = w3 ? pdl_launch(int8_tile_kernel<__nv_bfloat16, true>, grid, dim3(256), 0, s, a)
-           : pdl_launch(int8_tile_kernel<__nv_bfloat16, false>, grid, dim3(256), 0, s, a);
+  const bool split = lay.items > 0;
+  const QuantArgs qa = {x, ldx, n_tokens, rows, R, cfg->in_features, ws + lay.q, reinterpret_cast<float*>(ws + lay.scale),
+                        split ? reinterpret_cast<uint32_t*>(ws + lay.ticket) : nullptr, lay.items};
+  CUtensorMap maps[3];
+  if (!int8_tensor_maps(qa.q, R, w, w3, cfg->num_experts, cfg->out_features, cfg->in_features, maps)) return COLIBRI_ERR_CUDA;
+  if (quantize<__half>(cfg->dtype, qa, sms, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
+  const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, split ? reinterpret_cast<float*>(ws + lay.partial) : nullptr,
+                      qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, 2000000000ull};
+  const cudaError_t e = launch_int8_mma(maps, !split, w3 != nullptr, cfg->out_dtype == COLIBRI_DTYPE_BF16, a, device, sms, s);
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 
