@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kSumCols * kSumLanes) norm_sums_kernel(NormSum
     float s = 0.f;
     if (col < a.d) {
       const float* p = a.part + (int64_t)blockIdx.y * a.d + col;
-#pragma unroll 4
+#pragma unroll 8
       for (int b = ty; b < a.blocks; b += kSumLanes) s += p[b * stride];
     }
     s = total(s);
@@ -386,21 +386,25 @@ __global__ void __launch_bounds__(kSumCols * kSumLanes) norm_sums_kernel(NormSum
     return;
   }
   if (!a.dgate) return;
-  // the groups that begin in block b and go on past it
-  for (int b = 0; b + 1 < a.blocks; ++b) {
+  // the groups that begin in block b and go on past it: of each block the one of its last row
+  for (int b = 0; b + 1 < a.blocks;) {
     const int64_t r0 = (int64_t)b * a.rows_per_block, r1 = r0 + a.rows_per_block;
     const int64_t g = (r1 - 1) / a.rpg, first = g * a.rpg, last = min((g + 1) * a.rpg, (int64_t)a.T) - 1;
-    if (first < r0 || last < r1) continue;
     const int end = (int)(last / a.rows_per_block);
+    if (first < r0 || last < r1) {  // began earlier, or ends with the block
+      ++b;
+      continue;
+    }
     float s = 0.f;
     if (col < a.d) {
       const float* p = a.part + col;
       if (ty == 0) s = p[b * stride + (int64_t)kSumGateLast * a.d];
-#pragma unroll 4
+#pragma unroll 8
       for (int i = b + 1 + ty; i <= end; i += kSumLanes) s += p[i * stride + (int64_t)kSumGateFirst * a.d];
     }
     s = total(s);
     if (ty == 0 && col < a.d) a.dgate[g * a.d + col] = s;
+    b = end;  // the next group to cross blocks begins in this group's last one at the earliest
   }
 }
 

@@ -14,8 +14,8 @@
 // hang on the rounding of one exp.  Two slots that hold the same logit and bias are equal, not close:
 // the lower index is right without a second look.
 //
-// One warp a token, the experts over its lanes (expert = lane + 32 slot); k rounds of a warp-wide
-// maximum.  Ranks inside a chunk of 32 tokens come from one 32-bit token mask per expert.
+// One warp a token, runs of experts over its lanes (expert = lane * slots + slot, so that groups are
+// neighbouring lanes and a lane's logits one or two 16-byte loads); k rounds of a warp-wide maximum.  Ranks inside a chunk of 32 tokens come from one 32-bit token mask per expert.
 #include <algorithm>
 
 #include "ops_common.cuh"
@@ -32,6 +32,8 @@ struct RouteManyArgs {
   int64_t ld;
   const float* bias;
   int T, E, k, groups, per_group, top_groups, group_top, softmax, renorm;
+  int lanes_per_group;  // where every group is a run of 1, 2, 4 .. 32 whole lanes, else 0
+  int aligned;          // logits rows start on 16 bytes
   float scale;
   int32_t *idx, *counts, *offsets, *row_of, *token_of_row;
   float* gate;
@@ -65,50 +67,77 @@ __device__ __forceinline__ void warp_best(double& v, int& i) {
   }
 }
 
-// The selection in 64 bits: sets lane i's `sel` (i < k) to the i-th expert, or -1.
-template <typename L, int NS>
-__device__ __noinline__ void select_exact(const RouteManyArgs& a, int t, int& sel) {
-  const int lane = threadIdx.x & 31;
-  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
-  const double none = -INFINITY;
-  double score[NS], key[NS];
-  double m = none;
+// What of a lane's experts does not change from token to token.
+template <int NS>
+struct Lane {
+  int e0;          // its first expert
+  int grp[NS];     // their groups
+  float bias[NS];  // -inf: masked (a NaN too); 0 without a bias
+  __device__ __forceinline__ explicit Lane(const RouteManyArgs& a) {
+    e0 = (threadIdx.x & 31) * NS;
 #pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    const int e = lane + 32 * j;
-    double l = none;
-    if (e < a.E) {
-      const float f = to_float(row[e]);
-      if (f > -INFINITY && (!a.bias || a.bias[e] > -INFINITY)) l = f;
+    for (int j = 0; j < NS; ++j) {
+      grp[j] = a.groups > 1 ? (e0 + j) / a.per_group : 0;
+      bias[j] = 0.f;
+      if (a.bias && e0 + j < a.E) {
+        bias[j] = a.bias[e0 + j];
+        if (!(bias[j] > -INFINITY)) bias[j] = -INFINITY;
+      }
     }
-    score[j] = l;
-    // the softmax runs over every expert with a logit, its key masked or not
-    if (e < a.E && to_float(row[e]) > -INFINITY) m = fmax(m, (double)to_float(row[e]));
+  }
+};
+
+// A lane's logits as fp32; a NaN, and what lies past E, is -inf.
+template <typename L, int NS>
+__device__ __forceinline__ void load_logits(const RouteManyArgs& a, int t, int e0, float (&l)[NS]) {
+  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
+  if constexpr (NS >= 8) {
+    if (a.aligned && e0 + NS <= a.E) {
+#pragma unroll
+      for (int j = 0; j < NS; j += 8) {
+        float v[8];
+        load8(row + e0 + j, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[j + i] = v[i] > -INFINITY ? v[i] : -INFINITY;
+      }
+      return;
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(~0u, m, o));
+  for (int j = 0; j < NS; ++j) {
+    l[j] = e0 + j < a.E ? to_float(row[e0 + j]) : -INFINITY;
+    if (!(l[j] > -INFINITY)) l[j] = -INFINITY;
+  }
+}
+
+// The selection in 64 bits: sets lane i's `sel` (i < k) to the i-th expert, or -1.
+template <int NS>
+__device__ __noinline__ void select_exact(const RouteManyArgs& a, const Lane<NS>& me, const float (&l)[NS], int& sel) {
+  const int lane = threadIdx.x & 31;
+  const double none = -INFINITY;
+  double key[NS];  // the score with the bias: what groups are ranked by
   if (a.softmax) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) m = fmaxf(m, l[j]);
+    m = warp_max(m);
     double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      const int e = lane + 32 * j;
-      const double l = e < a.E ? (double)to_float(row[e]) : none;
-      const double z = l == m ? 1.0 : (l > none ? exp(l - m) : 0.0);
-      sum += z;
-      key[j] = z;
+      key[j] = l[j] == m ? (m > -INFINITY ? 1.0 : 0.0) : (l[j] > -INFINITY ? exp((double)l[j] - (double)m) : 0.0);
+      sum += key[j];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
 #pragma unroll
-    for (int j = 0; j < NS; ++j) key[j] = score[j] > none ? (sum > 0.0 ? key[j] / sum : 0.0) : none;
+    for (int j = 0; j < NS; ++j) key[j] = sum > 0.0 ? key[j] / sum : 0.0;
   } else {
 #pragma unroll
-    for (int j = 0; j < NS; ++j) key[j] = score[j] > none ? 1.0 / (1.0 + exp(-score[j])) : none;
+    for (int j = 0; j < NS; ++j) key[j] = l[j] > -INFINITY ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;
   }
-  // key: the score with the bias (what groups are ranked by); score: the logit
 #pragma unroll
   for (int j = 0; j < NS; ++j)
-    if (a.bias && key[j] > none) key[j] += a.bias[lane + 32 * j];
+    key[j] = l[j] > -INFINITY && me.bias[j] > -INFINITY ? key[j] + (double)me.bias[j] : none;
   uint32_t kept = ~0u;
   if (a.groups > 1) {
     double mine = none;
@@ -120,11 +149,10 @@ __device__ __noinline__ void select_exact(const RouteManyArgs& a, int t, int& se
         int i = kRouteMaxE;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          const int e = lane + 32 * j;
-          if (e / a.per_group != g || e == first || key[j] == none) continue;
+          if (me.grp[j] != g || me.e0 + j == first || key[j] == none) continue;
           // one expert a group and no bias: the logits rank the groups, as they rank the experts
-          const double r = a.group_top == 1 && !a.bias ? score[j] : key[j];
-          if (before(r, e, v, i)) v = r, i = e;
+          const double r = a.group_top == 1 && !a.bias ? (double)l[j] : key[j];
+          if (before(r, me.e0 + j, v, i)) v = r, i = me.e0 + j;
         }
         warp_best(v, i);
         if (i == kRouteMaxE) {
@@ -145,9 +173,8 @@ __device__ __noinline__ void select_exact(const RouteManyArgs& a, int t, int& se
   }
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
-    const int e = lane + 32 * j;
-    if (key[j] > none && !a.bias) key[j] = score[j];
-    if (e >= a.E || !(kept >> (e / a.per_group) & 1)) key[j] = none;
+    if (key[j] > none && !a.bias) key[j] = l[j];
+    if (me.e0 + j >= a.E || !(kept >> me.grp[j] & 1)) key[j] = none;
   }
   sel = -1;
   for (int n = 0; n < a.k; ++n) {
@@ -155,115 +182,122 @@ __device__ __noinline__ void select_exact(const RouteManyArgs& a, int t, int& se
     int i = kRouteMaxE;
 #pragma unroll
     for (int j = 0; j < NS; ++j)
-      if (key[j] > none && before(key[j], lane + 32 * j, v, i)) v = key[j], i = lane + 32 * j;
+      if (key[j] > none && before(key[j], me.e0 + j, v, i)) v = key[j], i = me.e0 + j;
     warp_best(v, i);
     if (i == kRouteMaxE) break;
 #pragma unroll
     for (int j = 0; j < NS; ++j)
-      if (lane + 32 * j == i) key[j] = none;
+      if (me.e0 + j == i) key[j] = none;
     if (lane == n) sel = i;
   }
 }
 
-// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.
-template <typename L, int NS>
-__device__ __forceinline__ void route_token(const RouteManyArgs& a, int t, int& sel, float& s_sel) {
+// The two larger of (a1 >= a2) and (b1 >= b2).
+__device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float b2) {
+  const float lo = fminf(a1, b1);
+  a1 = fmaxf(a1, b1);
+  a2 = fmaxf(lo, fmaxf(a2, b2));
+}
+
+// Which groups compete (a bit each), by the sums of their best keys; `unsure` if the error bounds do not
+// decide it.
+template <int NS>
+__device__ __forceinline__ uint32_t keep_groups(const RouteManyArgs& a, const Lane<NS>& me, const float (&l)[NS],
+                                                const float (&key)[NS], const float (&err)[NS], bool& unsure) {
   const int lane = threadIdx.x & 31;
-  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
-  float l[NS], s[NS], key[NS], err[NS];
-  bool any = false;
-#pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    const int e = lane + 32 * j;
-    l[j] = e < a.E ? to_float(row[e]) : -INFINITY;
-    if (!(l[j] > -INFINITY)) l[j] = -INFINITY;  // NaN
-  }
-  if (a.softmax) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) m = fmaxf(m, l[j]);
-    m = warp_max(m);
-    float sum = 0.f;
+  const bool by_logit = a.group_top == 1 && !a.bias;
+  float best = -INFINITY, second = -INFINITY, off = 0.f;  // of group `lane`, in its lane
+  if (a.lanes_per_group) {
+    // groups are runs of 1, 2, 4 .. 32 lanes: all of them at once, by exchanges inside the runs
+    float v = -INFINITY, v2 = -INFINITY, o = 0.f;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      s[j] = l[j] == -INFINITY ? 0.f : (l[j] == m ? 1.f : expf(l[j] - m));
-      sum += s[j];
+      const float r = key[j] == -INFINITY ? -INFINITY : (by_logit ? l[j] : key[j]);
+      o = fmaxf(o, err[j]);
+      v2 = fmaxf(v2, fminf(v, r));
+      v = fmaxf(v, r);
     }
-    sum = warp_sum(sum);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      s[j] *= inv;
-      // l - m is rounded to 2^-24 of itself, exp to 2 ulp, the sum (at most 16 + 5 additions) and the
-      // product with 1 / sum to less than 2^-19 together
-      err[j] = s[j] * (0x1p-18f + 0x1p-23f * fminf(m - l[j], 200.f));
+    for (int d = 1; d < a.lanes_per_group; d <<= 1) {
+      merge_top2(v, v2, __shfl_xor_sync(~0u, v, d), __shfl_xor_sync(~0u, v2, d));
+      o = fmaxf(o, __shfl_xor_sync(~0u, o, d));
     }
+    const int from = (lane * a.lanes_per_group) & 31;
+    best = __shfl_sync(~0u, v, from), second = __shfl_sync(~0u, v2, from), off = __shfl_sync(~0u, o, from);
   } else {
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      s[j] = l[j] == -INFINITY ? 0.f : 1.f / (1.f + expf(-l[j]));
-      err[j] = s[j] * 0x1p-21f;  // exp 2 ulp, the sum and the quotient half an ulp each
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    key[j] = l[j] == -INFINITY ? -INFINITY : s[j];
-    if (a.bias && l[j] > -INFINITY) {
-      const float b = a.bias[lane + 32 * j];
-      key[j] = b > -INFINITY ? s[j] + b : -INFINITY;
-    }
-    // half an ulp of the sum with the bias, and what exp loses below the normal range
-    err[j] += fabsf(key[j] > -INFINITY ? key[j] : 0.f) * 0x1p-23f + 0x1p-120f;
-    any |= key[j] > -INFINITY;
-  }
-  bool unsure = false;
-  uint32_t kept = ~0u;
-  if (a.groups > 1) {
-    const bool by_logit = a.group_top == 1 && !a.bias;
-    float total = -INFINITY, off = 0.f;
     for (int g = 0; g < a.groups; ++g) {
       float v = -INFINITY, v2 = -INFINITY, o = 0.f;
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        const int e = lane + 32 * j;
-        if (e >= a.E || e / a.per_group != g || key[j] == -INFINITY) continue;
+        if (me.grp[j] != g || key[j] == -INFINITY) continue;
         const float r = by_logit ? l[j] : key[j];
         o = fmaxf(o, err[j]);
         v2 = fmaxf(v2, fminf(v, r));
         v = fmaxf(v, r);
       }
-      const float best = warp_max(v);
-      float sum = best;
-      if (a.group_top == 2) {
-        // the second best: the lane that gave the best (the first of equals) offers its next one
-        const uint32_t who = __ballot_sync(~0u, v == best);
-        const float second = warp_max(lane == __ffs(who) - 1 ? v2 : v);
-        if (second > -INFINITY) sum += second;
-      }
+      const float b = warp_max(v);
+      // the second best: the lane that gave the best (the first of equals) offers its next one
+      const uint32_t who = __ballot_sync(~0u, v == b);
+      const float b2 = a.group_top == 2 ? warp_max(lane == __ffs(who) - 1 ? v2 : v) : -INFINITY;
       o = warp_max(o);
-      if (lane == g) total = sum, off = by_logit ? 0.f : 2.f * o + fabsf(sum > -INFINITY ? sum : 0.f) * 0x1p-23f;
-    }
-    int rank = 0;
-    for (int g = 0; g < a.groups; ++g) rank += before(__shfl_sync(~0u, total, g), g, total, lane);
-    const bool in = lane < a.groups && rank < a.top_groups;
-    kept = __ballot_sync(~0u, in);
-    if (!by_logit && a.top_groups < a.groups) {
-      const float lowest = warp_min(in ? total - off : INFINITY);
-      const float highest = warp_max(lane < a.groups && !in ? total + off : -INFINITY);
-      unsure = !(lowest > highest) && highest > -INFINITY;
+      if (lane == g) best = b, second = b2, off = o;
     }
   }
+  float total = best;
+  if (a.group_top == 2 && second > -INFINITY) total += second;
+  off = by_logit ? 0.f : 2.f * off + fabsf(total > -INFINITY ? total : 0.f) * 0x1p-23f;
+  int rank = 0;
+  for (int g = 0; g < a.groups; ++g) rank += before(__shfl_sync(~0u, total, g), g, total, lane);
+  const bool in = lane < a.groups && rank < a.top_groups;
+  if (!by_logit && a.top_groups < a.groups) {
+    const float lowest = warp_min(in ? total - off : INFINITY);
+    const float highest = warp_max(lane < a.groups && !in ? total + off : -INFINITY);
+    unsure = !(lowest > highest) && highest > -INFINITY;
+  }
+  return __ballot_sync(~0u, in);
+}
+
+// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.
+template <typename L, int NS>
+__device__ __forceinline__ void route_token(const RouteManyArgs& a, const Lane<NS>& me, int t, int& sel, float& s_sel) {
+  const int lane = threadIdx.x & 31;
+  float l[NS], key[NS], err[NS];
+  load_logits<L, NS>(a, t, me.e0, l);
+  float m = 0.f, inv = 0.f;
+  auto raw_score = [&](float v) { return v == -INFINITY ? 0.f : (v == m ? 1.f : expf(v - m)); };
+  if (a.softmax) {
+    m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) m = fmaxf(m, l[j]);
+    m = warp_max(m);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) sum += key[j] = raw_score(l[j]);
+    sum = warp_sum(sum);
+    inv = sum > 0.f ? 1.f / sum : 0.f;
+  }
+  // score of a logit, and a bound on its error.  Softmax: v - m is rounded to 2^-24 of itself, exp to 2 ulp,
+  // the sum (at most 16 + 5 additions) and the product with 1 / sum to less than 2^-19 together.  Sigmoid: exp
+  // 2 ulp, the sum and the quotient half an ulp each.
+  auto error_of = [&](float v, float score) {
+    return a.softmax ? score * (0x1p-18f + 0x1p-23f * fminf(m - v, 200.f)) : score * 0x1p-21f;
+  };
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    const float s = a.softmax ? key[j] * inv : (l[j] == -INFINITY ? 0.f : 1.f / (1.f + expf(-l[j])));
+    key[j] = l[j] > -INFINITY && me.bias[j] > -INFINITY ? s + me.bias[j] : -INFINITY;
+    // half an ulp of the sum with the bias, and what exp loses below the normal range
+    err[j] = error_of(l[j], s) + fabsf(key[j] > -INFINITY ? key[j] : 0.f) * 0x1p-23f + 0x1p-120f;
+  }
+  bool unsure = false;
+  const uint32_t kept = a.groups > 1 ? keep_groups<NS>(a, me, l, key, err, unsure) : ~0u;
   // the experts that are left, by (key, index)
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
-    const int e = lane + 32 * j;
     if (key[j] > -INFINITY && !a.bias) key[j] = l[j], err[j] = 0.f;
-    if (e >= a.E || !(kept >> (a.groups > 1 ? e / a.per_group : 0) & 1)) key[j] = -INFINITY;
+    if (me.e0 + j >= a.E || !(kept >> me.grp[j] & 1)) key[j] = -INFINITY;
   }
   sel = -1;
-  float mine = -INFINITY, off = 0.f, ml = 0.f;
-  s_sel = 0.f;
-  float best = -INFINITY;
+  float mine = -INFINITY, best = -INFINITY;
   int at = 0;
 #pragma unroll
   for (int j = NS - 1; j >= 0; --j)
@@ -272,15 +306,10 @@ __device__ __forceinline__ void route_token(const RouteManyArgs& a, int t, int& 
   for (int n = 0; n < a.k; ++n) {
     const uint32_t o = ordered(best), top = __reduce_max_sync(~0u, o);
     if (top == ordered(-INFINITY)) break;
-    const int e = __reduce_min_sync(~0u, o == top ? lane + 32 * at : kRouteMaxE);
-    // the winner's values to lane n
-    float ws = 0.f, wo = 0.f, wl = 0.f;
-#pragma unroll
-    for (int j = 0; j < NS; ++j)
-      if (j == at) ws = s[j], wo = err[j], wl = l[j];
-    ws = __shfl_sync(~0u, ws, e & 31), wo = __shfl_sync(~0u, wo, e & 31), wl = __shfl_sync(~0u, wl, e & 31);
-    if (lane == n) sel = e, mine = unordered(top), off = wo, ml = wl, s_sel = ws;
-    if (lane == (e & 31)) {
+    const int owner = __ffs(__ballot_sync(~0u, o == top)) - 1;  // lanes in the order of their experts
+    const int e = __shfl_sync(~0u, me.e0 + at, owner);
+    if (lane == n) sel = e, mine = unordered(top);
+    if (lane == owner) {
       taken |= 1u << at;
       best = -INFINITY, at = 0;
 #pragma unroll
@@ -288,8 +317,22 @@ __device__ __forceinline__ void route_token(const RouteManyArgs& a, int t, int& 
         if (!(taken >> j & 1) && key[j] >= best) best = key[j], at = j;
     }
   }
+  // the logit of a chosen expert, in the lane of its rank
+  auto logit_of = [&](int e) {
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const float w = __shfl_sync(~0u, l[j], max(e, 0) / NS);
+      if ((e & (NS - 1)) == j) v = w;
+    }
+    return v;
+  };
+  float ml = logit_of(sel);
+  auto score_of = [&](float v) { return a.softmax ? raw_score(v) * inv : 1.f / (1.f + expf(-v)); };
+  s_sel = sel >= 0 ? score_of(ml) : 0.f;
   if (a.bias) {
     const int found = __popc(__ballot_sync(~0u, sel >= 0));
+    const float off = error_of(ml, s_sel) + fabsf(sel >= 0 ? mine : 0.f) * 0x1p-23f + 0x1p-120f;
     // neighbours in the ranking, and the last chosen one against everything that was not
     const float nv = __shfl_down_sync(~0u, mine, 1), no = __shfl_down_sync(~0u, off, 1), nl = __shfl_down_sync(~0u, ml, 1);
     const float mb = sel >= 0 ? a.bias[sel] : 0.f, nb = __shfl_down_sync(~0u, mb, 1);
@@ -299,20 +342,14 @@ __device__ __forceinline__ void route_token(const RouteManyArgs& a, int t, int& 
       const float lb = __shfl_sync(~0u, mb, a.k - 1);
 #pragma unroll
       for (int j = 0; j < NS; ++j)
-        if (!(taken >> j & 1) && key[j] > -INFINITY && !(lo > key[j] + err[j]) &&
-            !(l[j] == ll && a.bias[lane + 32 * j] == lb))
+        if (!(taken >> j & 1) && key[j] > -INFINITY && !(lo > key[j] + err[j]) && !(l[j] == ll && me.bias[j] == lb))
           unsure = true;
     }
   }
   if (__any_sync(~0u, unsure)) {
-    select_exact<L, NS>(a, t, sel);
-    float v = 0.f;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {  // the chosen experts' scores, slot by slot
-      const float w = __shfl_sync(~0u, s[j], max(sel, 0) & 31);
-      if (sel >> 5 == j) v = w;
-    }
-    s_sel = sel >= 0 ? v : 0.f;
+    select_exact<NS>(a, me, l, sel);
+    ml = logit_of(sel);
+    s_sel = sel >= 0 ? score_of(ml) : 0.f;
   }
 }
 
@@ -354,10 +391,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_tokens_kernel(RouteMan
   __syncthreads();
   pdl_wait();
   const int t0 = blockIdx.x * kRouteTokens, n = min(kRouteTokens, a.T - t0);
+  const Lane<NS> me(a);
   for (int i = warp; i < n; i += warps) {
     int sel;
     float s;
-    route_token<L, NS>(a, t0 + i, sel, s);
+    route_token<L, NS>(a, me, t0 + i, sel, s);
     const float sum = warp_sum(lane < a.k ? s : 0.f);
     if (lane < a.k) {
       const int64_t o = (int64_t)(t0 + i) * a.k + lane;
@@ -616,7 +654,11 @@ extern "C" int colibri_moe_route_experts(const colibri_moe_route_config_t* cfg, 
   a.renorm = cfg->renormalize, a.scale = cfg->scale, a.idx = idx, a.gate = gate, a.counts = counts;
   a.offsets = offsets, a.row_of = row_of, a.token_of_row = token_of_row, a.hist = static_cast<int32_t*>(workspace);
   a.chunks = chunks;
+  a.aligned = ops_aligned16(logits) && ld * ops_elem(cfg->logits_dtype) % 16 == 0;
   cudaError_t e = by_experts(cfg->logits_dtype, E, [&](auto l, auto ns) {
+    constexpr int NS = decltype(ns)::value;
+    const int lanes = a.per_group / NS;
+    a.lanes_per_group = a.per_group % NS == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     return pdl_launch(route_tokens_kernel<decltype(l), decltype(ns)::value>, dim3(chunks),
                       dim3(32 * std::min(kRouteWarps, T)), 0, s, a);
   });
