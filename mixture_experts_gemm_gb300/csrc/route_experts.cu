@@ -57,11 +57,18 @@ __device__ __forceinline__ bool before(T va, int ia, T vb, int ib) {
   return va > vb || (va == vb && ia < ib);
 }
 
+// Doubles (no NaN) as integers in the same order: comparisons run at the integer rate, not the 64-bit one.
+__device__ __forceinline__ int64_t ordered(double v) {
+  const int64_t u = __double_as_longlong(v + 0.0);
+  return u ^ ((u >> 63) & 0x7fffffffffffffffll);
+}
+constexpr int64_t kNoKey = INT64_MIN;  // below every ordered double
+
 // Best (value, index) of the warp, in every lane.
-__device__ __forceinline__ void warp_best(double& v, int& i) {
+__device__ __forceinline__ void warp_best(int64_t& v, int& i) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const double w = __shfl_xor_sync(~0u, v, o);
+    const int64_t w = __shfl_xor_sync(~0u, v, o);
     const int j = __shfl_xor_sync(~0u, i, o);
     if (before(w, j, v, i)) v = w, i = j;
   }
@@ -110,86 +117,113 @@ __device__ __forceinline__ void load_logits(const RouteManyArgs& a, int t, int e
   }
 }
 
-// The selection in 64 bits: sets lane i's `sel` (i < k) to the i-th expert, or -1.
-template <int NS>
-__device__ __noinline__ void select_exact(const RouteManyArgs& a, const Lane<NS>& me, const float (&l)[NS], int& sel) {
-  const int lane = threadIdx.x & 31;
-  const double none = -INFINITY;
-  double key[NS];  // the score with the bias: what groups are ranked by
-  if (a.softmax) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) m = fmaxf(m, l[j]);
-    m = warp_max(m);
-    double sum = 0.0;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      key[j] = l[j] == m ? (m > -INFINITY ? 1.0 : 0.0) : (l[j] > -INFINITY ? exp((double)l[j] - (double)m) : 0.0);
-      sum += key[j];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-#pragma unroll
-    for (int j = 0; j < NS; ++j) key[j] = sum > 0.0 ? key[j] / sum : 0.0;
-  } else {
-#pragma unroll
-    for (int j = 0; j < NS; ++j) key[j] = l[j] > -INFINITY ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;
+// 1 / the softmax's sum in 64 bits over the row's logits, m their maximum (all lanes).
+template <typename L>
+__device__ __forceinline__ double softmax_scale(const RouteManyArgs& a, const L* row, float m) {
+  double sum = 0.0;
+  for (int e = threadIdx.x & 31; e < a.E; e += 32) {
+    const float l = to_float(row[e]);
+    if (l == m)
+      sum += 1.0;
+    else if (l > -INFINITY)
+      sum += exp((double)l - (double)m);
   }
 #pragma unroll
-  for (int j = 0; j < NS; ++j)
-    key[j] = l[j] > -INFINITY && me.bias[j] > -INFINITY ? key[j] + (double)me.bias[j] : none;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+  return sum;
+}
+// The biased score of an admissible logit in 64 bits.
+__device__ __forceinline__ double exact_key(const RouteManyArgs& a, float l, float m, double sum, int e) {
+  const double s = a.softmax ? (l == m ? 1.0 : exp((double)l - (double)m)) / sum : 1.0 / (1.0 + exp(-(double)l));
+  return a.bias ? s + (double)a.bias[e] : s;
+}
+
+// Ranks the listed experts (at most 32, those that can be among the k best) by their 64-bit keys; the list
+// becomes the ranking.  One evaluation a lane.
+template <typename L>
+__device__ __noinline__ void rank_candidates(const RouteManyArgs& a, int t, float m, int16_t* list, int count) {
+  const int lane = threadIdx.x & 31;
+  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
+  const double sum = a.softmax ? softmax_scale(a, row, m) : 1.0;
+  const int e = lane < count ? list[lane] : 0;
+  const int64_t key = lane < count ? ordered(exact_key(a, to_float(row[e]), m, sum, e)) : kNoKey;
+  int rank = 0;
+  for (int i = 0; i < count; ++i) rank += before(__shfl_sync(~0u, key, i), __shfl_sync(~0u, e, i), key, e);
+  __syncwarp();
+  if (lane < count) list[rank] = e;
+  __syncwarp();
+}
+
+// The whole selection, groups and experts, by 64-bit keys: returns lane i's (i < k) expert, or -1.
+template <typename L, int NS>
+__device__ __noinline__ int select_exact(const RouteManyArgs& a, int t, float m) {
+  const int lane = threadIdx.x & 31;
+  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
+  const Lane<NS> me(a);
+  const double sum = a.softmax ? softmax_scale(a, row, m) : 1.0;
+  double key[NS];   // what groups are ranked by
+  int64_t rank_by[NS];
+#pragma unroll
+  for (int j = 0; j < NS; ++j) {
+    const int e = me.e0 + j;
+    const float l = e < a.E ? to_float(row[e]) : -INFINITY;
+    const bool live = l > -INFINITY && me.bias[j] > -INFINITY;
+    key[j] = live ? exact_key(a, l, m, sum, e) : 0.0;
+    rank_by[j] = live ? ordered(a.bias ? key[j] : (double)l) : kNoKey;
+  }
   uint32_t kept = ~0u;
   if (a.groups > 1) {
-    double mine = none;
+    int64_t mine = kNoKey;
     for (int g = 0; g < a.groups; ++g) {
       double total = 0.0;
+      int64_t worth = kNoKey;
       int first = -1;
       for (int n = 0; n < a.group_top; ++n) {
-        double v = none;
+        int64_t v = kNoKey;
         int i = kRouteMaxE;
+        double mine_d = 0.0;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          if (me.grp[j] != g || me.e0 + j == first || key[j] == none) continue;
+          if (me.grp[j] != g || me.e0 + j == first || rank_by[j] == kNoKey) continue;
           // one expert a group and no bias: the logits rank the groups, as they rank the experts
-          const double r = a.group_top == 1 && !a.bias ? (double)l[j] : key[j];
-          if (before(r, me.e0 + j, v, i)) v = r, i = me.e0 + j;
+          const int64_t r = a.group_top == 1 ? rank_by[j] : ordered(key[j]);
+          if (before(r, me.e0 + j, v, i)) v = r, i = me.e0 + j, mine_d = key[j];
         }
+        const int own = i;
         warp_best(v, i);
-        if (i == kRouteMaxE) {
-          if (n == 0) total = none;
-          break;
+        if (i == kRouteMaxE) break;
+        if (a.group_top == 1) {
+          worth = v;
+        } else {
+          total += __shfl_sync(~0u, mine_d, __ffs(__ballot_sync(~0u, own == i)) - 1);
+          worth = ordered(total);
         }
-        total += v;
         first = i;
       }
-      if (lane == g) mine = total;
+      if (lane == g) mine = worth;
     }
     int rank = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const double v = __shfl_sync(~0u, mine, g);
-      rank += before(v, g, mine, lane);
-    }
+    for (int g = 0; g < a.groups; ++g) rank += before(__shfl_sync(~0u, mine, g), g, mine, lane);
     kept = __ballot_sync(~0u, lane < a.groups && rank < a.top_groups);
   }
 #pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    if (key[j] > none && !a.bias) key[j] = l[j];
-    if (me.e0 + j >= a.E || !(kept >> me.grp[j] & 1)) key[j] = none;
-  }
-  sel = -1;
+  for (int j = 0; j < NS; ++j)
+    if (me.e0 + j >= a.E || !(kept >> me.grp[j] & 1)) rank_by[j] = kNoKey;
+  int sel = -1;
   for (int n = 0; n < a.k; ++n) {
-    double v = none;
+    int64_t v = kNoKey;
     int i = kRouteMaxE;
 #pragma unroll
     for (int j = 0; j < NS; ++j)
-      if (key[j] > none && before(key[j], me.e0 + j, v, i)) v = key[j], i = me.e0 + j;
+      if (rank_by[j] != kNoKey && before(rank_by[j], me.e0 + j, v, i)) v = rank_by[j], i = me.e0 + j;
     warp_best(v, i);
     if (i == kRouteMaxE) break;
 #pragma unroll
     for (int j = 0; j < NS; ++j)
-      if (me.e0 + j == i) key[j] = none;
+      if (me.e0 + j == i) rank_by[j] = kNoKey;
     if (lane == n) sel = i;
   }
+  return sel;
 }
 
 // The two larger of (a1 >= a2) and (b1 >= b2).
@@ -256,9 +290,11 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteManyArgs& a, const La
   return __ballot_sync(~0u, in);
 }
 
-// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.
+// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.  `list` is 32
+// entries of shared memory of this warp's own.
 template <typename L, int NS>
-__device__ __forceinline__ void route_token(const RouteManyArgs& a, const Lane<NS>& me, int t, int& sel, float& s_sel) {
+__device__ __forceinline__ void route_token(const RouteManyArgs& a, const Lane<NS>& me, int t, int16_t* list, int& sel,
+                                            float& s_sel) {
   const int lane = threadIdx.x & 31;
   float l[NS], key[NS], err[NS];
   load_logits<L, NS>(a, t, me.e0, l);
@@ -275,21 +311,22 @@ __device__ __forceinline__ void route_token(const RouteManyArgs& a, const Lane<N
     sum = warp_sum(sum);
     inv = sum > 0.f ? 1.f / sum : 0.f;
   }
-  // score of a logit, and a bound on its error.  Softmax: v - m is rounded to 2^-24 of itself, exp to 2 ulp,
+  // A bound on the error of a key: of the score of logit v, half an ulp of the sum with the bias, and what exp
+  // loses below the normal range.  Softmax: v - m is rounded to 2^-24 of itself, exp to 2 ulp,
   // the sum (at most 16 + 5 additions) and the product with 1 / sum to less than 2^-19 together.  Sigmoid: exp
   // 2 ulp, the sum and the quotient half an ulp each.
-  auto error_of = [&](float v, float score) {
-    return a.softmax ? score * (0x1p-18f + 0x1p-23f * fminf(m - v, 200.f)) : score * 0x1p-21f;
+  auto error_at = [&](float v, float score, float k) {
+    return (a.softmax ? score * (0x1p-18f + 0x1p-23f * fminf(m - v, 200.f)) : score * 0x1p-21f) + fabsf(k) * 0x1p-23f +
+           0x1p-120f;
   };
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
     const float s = a.softmax ? key[j] * inv : (l[j] == -INFINITY ? 0.f : 1.f / (1.f + expf(-l[j])));
     key[j] = l[j] > -INFINITY && me.bias[j] > -INFINITY ? s + me.bias[j] : -INFINITY;
-    // half an ulp of the sum with the bias, and what exp loses below the normal range
-    err[j] = error_of(l[j], s) + fabsf(key[j] > -INFINITY ? key[j] : 0.f) * 0x1p-23f + 0x1p-120f;
+    err[j] = error_at(l[j], s, key[j] > -INFINITY ? key[j] : 0.f);
   }
-  bool unsure = false;
-  const uint32_t kept = a.groups > 1 ? keep_groups<NS>(a, me, l, key, err, unsure) : ~0u;
+  bool unsure_groups = false, unsure = false;
+  const uint32_t kept = a.groups > 1 ? keep_groups<NS>(a, me, l, key, err, unsure_groups) : ~0u;
   // the experts that are left, by (key, index)
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
@@ -332,7 +369,7 @@ __device__ __forceinline__ void route_token(const RouteManyArgs& a, const Lane<N
   s_sel = sel >= 0 ? score_of(ml) : 0.f;
   if (a.bias) {
     const int found = __popc(__ballot_sync(~0u, sel >= 0));
-    const float off = error_of(ml, s_sel) + fabsf(sel >= 0 ? mine : 0.f) * 0x1p-23f + 0x1p-120f;
+    const float off = error_at(ml, s_sel, sel >= 0 ? mine : 0.f);
     // neighbours in the ranking, and the last chosen one against everything that was not
     const float nv = __shfl_down_sync(~0u, mine, 1), no = __shfl_down_sync(~0u, off, 1), nl = __shfl_down_sync(~0u, ml, 1);
     const float mb = sel >= 0 ? a.bias[sel] : 0.f, nb = __shfl_down_sync(~0u, mb, 1);
@@ -346,8 +383,32 @@ __device__ __forceinline__ void route_token(const RouteManyArgs& a, const Lane<N
           unsure = true;
     }
   }
-  if (__any_sync(~0u, unsure)) {
-    select_exact<NS>(a, me, l, sel);
+  unsure = __any_sync(~0u, unsure);
+  if (unsure_groups || unsure) {
+    // everything that may be among the best: at or above the least that a chosen one can be
+    const float least = warp_min(sel >= 0 ? mine - (a.bias ? error_at(ml, s_sel, mine) : 0.f) : INFINITY);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) n += key[j] > -INFINITY && !(key[j] + err[j] < least);
+    int to = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(~0u, to, o);
+      if (lane >= o) to += v;
+    }
+    const int count = __shfl_sync(~0u, to, 31);
+    if (unsure_groups || count > 32) {
+      sel = select_exact<L, NS>(a, t, m);
+    } else {
+      to -= n;
+#pragma unroll
+      for (int j = 0; j < NS; ++j)
+        if (key[j] > -INFINITY && !(key[j] + err[j] < least)) list[to++] = me.e0 + j;
+      __syncwarp();
+      rank_candidates<L>(a, t, m, list, count);
+      sel = lane < min(count, a.k) ? list[lane] : -1;
+      __syncwarp();
+    }
     ml = logit_of(sel);
     s_sel = sel >= 0 ? score_of(ml) : 0.f;
   }
@@ -382,7 +443,7 @@ __device__ __forceinline__ void scan_counts(const int* counts, int* offsets, int
 // One chunk of 32 tokens a block.  With a single chunk the whole dispatch is done here; else row_of
 // holds ranks inside the chunk and hist the chunk's counts.
 template <typename L, int NS>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_tokens_kernel(RouteManyArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps) route_tokens_kernel(const __grid_constant__ RouteManyArgs a) {
   __shared__ uint32_t mask[NS * 32];
   __shared__ int count[NS * 32], offset[NS * 32 + 1];
   __shared__ int16_t chosen[kRouteTokens][kRouteMaxK];
@@ -395,7 +456,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_tokens_kernel(RouteMan
   for (int i = warp; i < n; i += warps) {
     int sel;
     float s;
-    route_token<L, NS>(a, me, t0 + i, sel, s);
+    route_token<L, NS>(a, me, t0 + i, chosen[i], sel, s);
     const float sum = warp_sum(lane < a.k ? s : 0.f);
     if (lane < a.k) {
       const int64_t o = (int64_t)(t0 + i) * a.k + lane;
