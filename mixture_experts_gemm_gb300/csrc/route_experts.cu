@@ -26,6 +26,7 @@ namespace {
 constexpr int kRouteMaxE = 512, kRouteMaxK = 32, kRouteMaxGroups = 32;
 constexpr int kRouteTokens = 32;  // tokens of a chunk: the bits of an expert's token mask
 constexpr int kRouteWarps = 16;
+constexpr int64_t kNoKey = INT64_MIN;  // below every ordered double
 
 struct RouteManyArgs {
   const void* logits;
@@ -62,8 +63,6 @@ __device__ __forceinline__ int64_t ordered(double v) {
   const int64_t u = __double_as_longlong(v + 0.0);
   return u ^ ((u >> 63) & 0x7fffffffffffffffll);
 }
-constexpr int64_t kNoKey = INT64_MIN;  // below every ordered double
-
 // Best (value, index) of the warp, in every lane.
 __device__ __forceinline__ void warp_best(int64_t& v, int& i) {
 #pragma unroll
@@ -74,22 +73,18 @@ __device__ __forceinline__ void warp_best(int64_t& v, int& i) {
   }
 }
 
-// What of a lane's experts does not change from token to token.
+// What of the experts does not change from token to token, in shared memory (registers are what bounds the
+// warps at work): biases (-inf: masked, a NaN too; 0 without) and group numbers.
 template <int NS>
-struct Lane {
-  int e0;          // its first expert
-  int grp[NS];     // their groups
-  float bias[NS];  // -inf: masked (a NaN too); 0 without a bias
-  __device__ __forceinline__ explicit Lane(const RouteManyArgs& a) {
-    e0 = (threadIdx.x & 31) * NS;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      grp[j] = a.groups > 1 ? (e0 + j) / a.per_group : 0;
-      bias[j] = 0.f;
-      if (a.bias && e0 + j < a.E) {
-        bias[j] = a.bias[e0 + j];
-        if (!(bias[j] > -INFINITY)) bias[j] = -INFINITY;
-      }
+struct Experts {
+  float bias[NS * 32];
+  uint8_t group[NS * 32];
+  __device__ __forceinline__ void fill(const RouteManyArgs& a) {
+    for (int e = threadIdx.x; e < NS * 32; e += blockDim.x) {
+      float b = 0.f;
+      if (a.bias && e < a.E) b = a.bias[e] > -INFINITY ? a.bias[e] : -INFINITY;
+      bias[e] = b;
+      group[e] = a.groups > 1 && e < a.E ? e / a.per_group : 0;
     }
   }
 };
@@ -156,18 +151,18 @@ __device__ __noinline__ void rank_candidates(const RouteManyArgs& a, int t, floa
 
 // The whole selection, groups and experts, by 64-bit keys: returns lane i's (i < k) expert, or -1.
 template <typename L, int NS>
-__device__ __noinline__ int select_exact(const RouteManyArgs& a, int t, float m) {
+__device__ __noinline__ int select_exact(const RouteManyArgs& a, const Experts<NS>& ex, int t, float m) {
   const int lane = threadIdx.x & 31;
   const L* row = static_cast<const L*>(a.logits) + t * a.ld;
-  const Lane<NS> me(a);
+  const int e0 = lane * NS;
   const double sum = a.softmax ? softmax_scale(a, row, m) : 1.0;
-  double key[NS];   // what groups are ranked by
+  double key[NS];  // what groups are ranked by
   int64_t rank_by[NS];
 #pragma unroll
   for (int j = 0; j < NS; ++j) {
-    const int e = me.e0 + j;
+    const int e = e0 + j;
     const float l = e < a.E ? to_float(row[e]) : -INFINITY;
-    const bool live = l > -INFINITY && me.bias[j] > -INFINITY;
+    const bool live = l > -INFINITY && ex.bias[e] > -INFINITY;
     key[j] = live ? exact_key(a, l, m, sum, e) : 0.0;
     rank_by[j] = live ? ordered(a.bias ? key[j] : (double)l) : kNoKey;
   }
@@ -184,10 +179,10 @@ __device__ __noinline__ int select_exact(const RouteManyArgs& a, int t, float m)
         double mine_d = 0.0;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          if (me.grp[j] != g || me.e0 + j == first || rank_by[j] == kNoKey) continue;
+          if (ex.group[e0 + j] != g || e0 + j == first || rank_by[j] == kNoKey) continue;
           // one expert a group and no bias: the logits rank the groups, as they rank the experts
           const int64_t r = a.group_top == 1 ? rank_by[j] : ordered(key[j]);
-          if (before(r, me.e0 + j, v, i)) v = r, i = me.e0 + j, mine_d = key[j];
+          if (before(r, e0 + j, v, i)) v = r, i = e0 + j, mine_d = key[j];
         }
         const int own = i;
         warp_best(v, i);
@@ -208,19 +203,19 @@ __device__ __noinline__ int select_exact(const RouteManyArgs& a, int t, float m)
   }
 #pragma unroll
   for (int j = 0; j < NS; ++j)
-    if (me.e0 + j >= a.E || !(kept >> me.grp[j] & 1)) rank_by[j] = kNoKey;
+    if (e0 + j >= a.E || !(kept >> ex.group[e0 + j] & 1)) rank_by[j] = kNoKey;
   int sel = -1;
   for (int n = 0; n < a.k; ++n) {
     int64_t v = kNoKey;
     int i = kRouteMaxE;
 #pragma unroll
     for (int j = 0; j < NS; ++j)
-      if (rank_by[j] != kNoKey && before(rank_by[j], me.e0 + j, v, i)) v = rank_by[j], i = me.e0 + j;
+      if (rank_by[j] != kNoKey && before(rank_by[j], e0 + j, v, i)) v = rank_by[j], i = e0 + j;
     warp_best(v, i);
     if (i == kRouteMaxE) break;
 #pragma unroll
     for (int j = 0; j < NS; ++j)
-      if (me.e0 + j == i) rank_by[j] = kNoKey;
+      if (e0 + j == i) rank_by[j] = kNoKey;
     if (lane == n) sel = i;
   }
   return sel;
@@ -236,20 +231,18 @@ __device__ __forceinline__ void merge_top2(float& a1, float& a2, float b1, float
 // Which groups compete (a bit each), by the sums of their best keys; `unsure` if the error bounds do not
 // decide it.
 template <int NS>
-__device__ __forceinline__ uint32_t keep_groups(const RouteManyArgs& a, const Lane<NS>& me, const float (&l)[NS],
-                                                const float (&key)[NS], const float (&err)[NS], bool& unsure) {
+__device__ __forceinline__ uint32_t keep_groups(const RouteManyArgs& a, const Experts<NS>& ex, const float (&key)[NS],
+                                                float err, bool& unsure) {
   const int lane = threadIdx.x & 31;
-  const bool by_logit = a.group_top == 1 && !a.bias;
+  const bool by_logit = a.group_top == 1 && !a.bias;  // keys are logits: exact
   float best = -INFINITY, second = -INFINITY, off = 0.f;  // of group `lane`, in its lane
   if (a.lanes_per_group) {
     // groups are runs of 1, 2, 4 .. 32 lanes: all of them at once, by exchanges inside the runs
-    float v = -INFINITY, v2 = -INFINITY, o = 0.f;
+    float v = -INFINITY, v2 = -INFINITY, o = err;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      const float r = key[j] == -INFINITY ? -INFINITY : (by_logit ? l[j] : key[j]);
-      o = fmaxf(o, err[j]);
-      v2 = fmaxf(v2, fminf(v, r));
-      v = fmaxf(v, r);
+      v2 = fmaxf(v2, fminf(v, key[j]));
+      v = fmaxf(v, key[j]);
     }
     for (int d = 1; d < a.lanes_per_group; d <<= 1) {
       merge_top2(v, v2, __shfl_xor_sync(~0u, v, d), __shfl_xor_sync(~0u, v2, d));
@@ -262,11 +255,10 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteManyArgs& a, const La
       float v = -INFINITY, v2 = -INFINITY, o = 0.f;
 #pragma unroll
       for (int j = 0; j < NS; ++j) {
-        if (me.grp[j] != g || key[j] == -INFINITY) continue;
-        const float r = by_logit ? l[j] : key[j];
-        o = fmaxf(o, err[j]);
-        v2 = fmaxf(v2, fminf(v, r));
-        v = fmaxf(v, r);
+        if (ex.group[lane * NS + j] != g || key[j] == -INFINITY) continue;
+        o = err;
+        v2 = fmaxf(v2, fminf(v, key[j]));
+        v = fmaxf(v, key[j]);
       }
       const float b = warp_max(v);
       // the second best: the lane that gave the best (the first of equals) offers its next one
@@ -290,126 +282,172 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteManyArgs& a, const La
   return __ballot_sync(~0u, in);
 }
 
-// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.  `list` is 32
-// entries of shared memory of this warp's own.
+// A bound on the error of the fp32 key of a logit, besides 2^-120 (what is lost below the normal range): the
+// score's and half an ulp of its sum with the bias.  Softmax: v - m is rounded to 2^-24 of itself, exp to 2
+// ulp, the sum (at most 16 + 5 additions) and the product with 1 / sum to less than 2^-18.5 together.
+// Sigmoid by the fast exp (2 + 1.173 |v| ulp) and the fast quotient (2 ulp).
+__device__ __forceinline__ float key_error(const RouteManyArgs& a, float v, float m, float score, float key) {
+  const float rel = a.softmax ? 0x1p-18f + 0x1p-22f * fminf(m - v, 200.f) : 0x1p-21f + 0x1.4p-23f * fabsf(v);
+  return score * rel + fabsf(key) * 0x1p-23f;
+}
+
+struct RouteScratch {
+  float key[kRouteMaxK];    // a token's candidates
+  int16_t expert[kRouteMaxK];
+};
+
+// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.
 template <typename L, int NS>
-__device__ __forceinline__ void route_token(const RouteManyArgs& a, const Lane<NS>& me, int t, int16_t* list, int& sel,
-                                            float& s_sel) {
+__device__ __forceinline__ void route_token(const RouteManyArgs& a, const Experts<NS>& ex, int t,
+                                            RouteScratch& scratch, int& sel, float& s_sel) {
   const int lane = threadIdx.x & 31;
-  float l[NS], key[NS], err[NS];
-  load_logits<L, NS>(a, t, me.e0, l);
+  const int e0 = lane * NS;
+  float key[NS];
+  load_logits<L, NS>(a, t, e0, key);
   float m = 0.f, inv = 0.f;
   auto raw_score = [&](float v) { return v == -INFINITY ? 0.f : (v == m ? 1.f : expf(v - m)); };
   if (a.softmax) {
     m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NS; ++j) m = fmaxf(m, l[j]);
+    for (int j = 0; j < NS; ++j) m = fmaxf(m, key[j]);
     m = warp_max(m);
     float sum = 0.f;
 #pragma unroll
-    for (int j = 0; j < NS; ++j) sum += key[j] = raw_score(l[j]);
+    for (int j = 0; j < NS; ++j) sum += raw_score(key[j]);
     sum = warp_sum(sum);
     inv = sum > 0.f ? 1.f / sum : 0.f;
   }
-  // A bound on the error of a key: of the score of logit v, half an ulp of the sum with the bias, and what exp
-  // loses below the normal range.  Softmax: v - m is rounded to 2^-24 of itself, exp to 2 ulp,
-  // the sum (at most 16 + 5 additions) and the product with 1 / sum to less than 2^-19 together.  Sigmoid: exp
-  // 2 ulp, the sum and the quotient half an ulp each.
-  auto error_at = [&](float v, float score, float k) {
-    return (a.softmax ? score * (0x1p-18f + 0x1p-23f * fminf(m - v, 200.f)) : score * 0x1p-21f) + fabsf(k) * 0x1p-23f +
-           0x1p-120f;
-  };
-#pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    const float s = a.softmax ? key[j] * inv : (l[j] == -INFINITY ? 0.f : 1.f / (1.f + expf(-l[j])));
-    key[j] = l[j] > -INFINITY && me.bias[j] > -INFINITY ? s + me.bias[j] : -INFINITY;
-    err[j] = error_at(l[j], s, key[j] > -INFINITY ? key[j] : 0.f);
-  }
-  bool unsure_groups = false, unsure = false;
-  const uint32_t kept = a.groups > 1 ? keep_groups<NS>(a, me, l, key, err, unsure_groups) : ~0u;
-  // the experts that are left, by (key, index)
-#pragma unroll
-  for (int j = 0; j < NS; ++j) {
-    if (key[j] > -INFINITY && !a.bias) key[j] = l[j], err[j] = 0.f;
-    if (me.e0 + j >= a.E || !(kept >> me.grp[j] & 1)) key[j] = -INFINITY;
-  }
-  sel = -1;
-  float mine = -INFINITY, best = -INFINITY;
-  int at = 0;
-#pragma unroll
-  for (int j = NS - 1; j >= 0; --j)
-    if (key[j] >= best) best = key[j], at = j;
-  uint32_t taken = 0;
-  for (int n = 0; n < a.k; ++n) {
-    const uint32_t o = ordered(best), top = __reduce_max_sync(~0u, o);
-    if (top == ordered(-INFINITY)) break;
-    const int owner = __ffs(__ballot_sync(~0u, o == top)) - 1;  // lanes in the order of their experts
-    const int e = __shfl_sync(~0u, me.e0 + at, owner);
-    if (lane == n) sel = e, mine = unordered(top);
-    if (lane == owner) {
-      taken |= 1u << at;
-      best = -INFINITY, at = 0;
-#pragma unroll
-      for (int j = NS - 1; j >= 0; --j)
-        if (!(taken >> j & 1) && key[j] >= best) best = key[j], at = j;
-    }
-  }
-  // the logit of a chosen expert, in the lane of its rank
-  auto logit_of = [&](int e) {
-    float v = 0.f;
+  float err = 0.f;  // the largest of this lane's keys
+  if (a.bias || (a.groups > 1 && a.group_top == 2)) {  // else the logits are the keys
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-      const float w = __shfl_sync(~0u, l[j], max(e, 0) / NS);
-      if ((e & (NS - 1)) == j) v = w;
+      const float l = key[j], b = ex.bias[e0 + j];
+      const float s = a.softmax ? raw_score(l) * inv : __fdividef(1.f, 1.f + __expf(-l));
+      const bool live = l > -INFINITY && b > -INFINITY;
+      key[j] = live ? s + b : -INFINITY;
+      if (live) err = fmaxf(err, key_error(a, l, m, s, key[j]));
     }
-    return v;
+    err += 0x1p-120f;
+  }
+  bool unsure_groups = false, unsure = false;
+  // the experts that are left, by (key, index)
+  if (a.groups > 1) {
+    const uint32_t kept = keep_groups<NS>(a, ex, key, err, unsure_groups);
+    if (!a.bias && a.group_top == 2) load_logits<L, NS>(a, t, e0, key);
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      if (!(kept >> ex.group[e0 + j] & 1)) key[j] = -INFINITY;
+  }
+  float best = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NS; ++j) best = fmaxf(best, key[j]);
+  // k lanes have a key at or above the k-th largest of the lanes' best, so the k best keys are among those at
+  // or above it: the candidates, usually a few more than k
+  uint32_t sorted = ordered(best);
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) {  // bitonic, descending
+      const uint32_t other = __shfl_xor_sync(~0u, sorted, d);
+      const bool up = ((lane & d) == 0) == ((lane & size) == 0);
+      sorted = up ? max(sorted, other) : min(sorted, other);
+    }
+  const float least = unordered(__shfl_sync(~0u, sorted, a.k - 1));
+  int n = 0;
+#pragma unroll
+  for (int j = 0; j < NS; ++j) n += key[j] > -INFINITY && key[j] >= least;
+  auto exclusive = [&](int v, int& total) {
+    int to = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(~0u, to, o);
+      if (lane >= o) to += w;
+    }
+    total = __shfl_sync(~0u, to, 31);
+    return to - v;
   };
-  float ml = logit_of(sel);
+  int count, to = exclusive(n, count);
+  float mine = -INFINITY;
+  sel = -1;
+  if (count <= kRouteMaxK) {
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+      if (key[j] > -INFINITY && key[j] >= least) scratch.key[to] = key[j], scratch.expert[to] = e0 + j, ++to;
+    __syncwarp();
+    // the list is in the order of the experts: equal keys rank by their places
+    const float my = lane < count ? scratch.key[lane] : -INFINITY;
+    const int e = scratch.expert[lane];
+    int rank = 0;
+    for (int i = 0; i < count; ++i) {
+      const float o = scratch.key[i];
+      rank += o > my || (o == my && i < lane);
+    }
+    __syncwarp();
+    if (lane < count) scratch.key[rank] = my, scratch.expert[rank] = e;
+    __syncwarp();
+    if (lane < min(count, a.k)) sel = scratch.expert[lane], mine = scratch.key[lane];
+    __syncwarp();
+  } else {  // many equal or few lanes: one at a time
+    uint32_t taken = 0;
+    for (int i = 0; i < a.k; ++i) {
+      float v = -INFINITY;
+      int at = 0;
+#pragma unroll
+      for (int j = NS - 1; j >= 0; --j)
+        if (!(taken >> j & 1) && key[j] >= v) v = key[j], at = j;
+      const uint32_t o = ordered(v), top = __reduce_max_sync(~0u, o);
+      if (top == ordered(-INFINITY)) break;
+      const int owner = __ffs(__ballot_sync(~0u, o == top)) - 1;  // lanes in the order of their experts
+      const int e = __shfl_sync(~0u, e0 + at, owner);
+      if (lane == i) sel = e, mine = unordered(top);
+      if (lane == owner) taken |= 1u << at;
+    }
+  }
+  const L* row = static_cast<const L*>(a.logits) + t * a.ld;
   auto score_of = [&](float v) { return a.softmax ? raw_score(v) * inv : 1.f / (1.f + expf(-v)); };
+  float ml = sel >= 0 ? to_float(row[sel]) : -INFINITY;
   s_sel = sel >= 0 ? score_of(ml) : 0.f;
   if (a.bias) {
     const int found = __popc(__ballot_sync(~0u, sel >= 0));
-    const float off = error_at(ml, s_sel, sel >= 0 ? mine : 0.f);
-    // neighbours in the ranking, and the last chosen one against everything that was not
+    const float off = sel >= 0 ? key_error(a, ml, m, s_sel * (1.f + 0x1p-18f), mine) + 0x1p-120f : 0.f;
+    // neighbours in the ranking; equal logits with equal biases are no close call
     const float nv = __shfl_down_sync(~0u, mine, 1), no = __shfl_down_sync(~0u, off, 1), nl = __shfl_down_sync(~0u, ml, 1);
     const float mb = sel >= 0 ? a.bias[sel] : 0.f, nb = __shfl_down_sync(~0u, mb, 1);
-    if (lane + 1 < found && !(mine - off > nv + no) && !(ml == nl && mb == nb)) unsure = true;
-    if (found == a.k) {
-      const float lo = __shfl_sync(~0u, mine - off, a.k - 1), ll = __shfl_sync(~0u, ml, a.k - 1);
-      const float lb = __shfl_sync(~0u, mb, a.k - 1);
+    unsure = lane + 1 < found && !(mine - off > nv + no) && !(ml == nl && mb == nb);
+    // the least that any chosen one can be, against everything that was not chosen
+    const float lo = warp_min(sel >= 0 ? mine - off : INFINITY);
+    int reach = 0;
 #pragma unroll
-      for (int j = 0; j < NS; ++j)
-        if (!(taken >> j & 1) && key[j] > -INFINITY && !(lo > key[j] + err[j]) && !(l[j] == ll && me.bias[j] == lb))
-          unsure = true;
+    for (int j = 0; j < NS; ++j) reach += key[j] > -INFINITY && !(key[j] + err < lo);
+    if (found == a.k && __reduce_add_sync(~0u, reach) > found) {
+      const float ll = __shfl_sync(~0u, ml, a.k - 1), lb = __shfl_sync(~0u, mb, a.k - 1);
+      const float lk = __shfl_sync(~0u, mine, a.k - 1);
+      const int le = __shfl_sync(~0u, sel, a.k - 1);
+      float l[NS];
+      load_logits<L, NS>(a, t, e0, l);
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const bool chosen = key[j] > lk || (key[j] == lk && e0 + j <= le);
+        if (key[j] > -INFINITY && !chosen && !(key[j] + err < lo) && !(l[j] == ll && ex.bias[e0 + j] == lb)) unsure = true;
+      }
+    }
+    unsure = __any_sync(~0u, unsure);
+    if (unsure && !unsure_groups) {  // everything that may be among the best
+      to = exclusive(reach, count);
+      if (count <= kRouteMaxK) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+          if (key[j] > -INFINITY && !(key[j] + err < lo)) scratch.expert[to++] = e0 + j;
+        __syncwarp();
+        rank_candidates<L>(a, t, m, scratch.expert, count);
+        sel = lane < min(count, a.k) ? scratch.expert[lane] : -1;
+        __syncwarp();
+      }
     }
   }
-  unsure = __any_sync(~0u, unsure);
+  if (unsure_groups || (unsure && count > kRouteMaxK)) sel = select_exact<L, NS>(a, ex, t, m);
   if (unsure_groups || unsure) {
-    // everything that may be among the best: at or above the least that a chosen one can be
-    const float least = warp_min(sel >= 0 ? mine - (a.bias ? error_at(ml, s_sel, mine) : 0.f) : INFINITY);
-    int n = 0;
-#pragma unroll
-    for (int j = 0; j < NS; ++j) n += key[j] > -INFINITY && !(key[j] + err[j] < least);
-    int to = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(~0u, to, o);
-      if (lane >= o) to += v;
-    }
-    const int count = __shfl_sync(~0u, to, 31);
-    if (unsure_groups || count > 32) {
-      sel = select_exact<L, NS>(a, t, m);
-    } else {
-      to -= n;
-#pragma unroll
-      for (int j = 0; j < NS; ++j)
-        if (key[j] > -INFINITY && !(key[j] + err[j] < least)) list[to++] = me.e0 + j;
-      __syncwarp();
-      rank_candidates<L>(a, t, m, list, count);
-      sel = lane < min(count, a.k) ? list[lane] : -1;
-      __syncwarp();
-    }
-    ml = logit_of(sel);
+    ml = sel >= 0 ? to_float(row[sel]) : -INFINITY;
     s_sel = sel >= 0 ? score_of(ml) : 0.f;
   }
 }
@@ -443,20 +481,23 @@ __device__ __forceinline__ void scan_counts(const int* counts, int* offsets, int
 // One chunk of 32 tokens a block.  With a single chunk the whole dispatch is done here; else row_of
 // holds ranks inside the chunk and hist the chunk's counts.
 template <typename L, int NS>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_tokens_kernel(const __grid_constant__ RouteManyArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps, NS <= 8 ? 2 : 1)
+    route_tokens_kernel(const __grid_constant__ RouteManyArgs a) {
   __shared__ uint32_t mask[NS * 32];
   __shared__ int count[NS * 32], offset[NS * 32 + 1];
   __shared__ int16_t chosen[kRouteTokens][kRouteMaxK];
+  __shared__ RouteScratch scratch[kRouteWarps];
+  __shared__ __align__(16) Experts<NS> ex;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   for (int e = threadIdx.x; e < NS * 32; e += blockDim.x) mask[e] = 0;
-  __syncthreads();
   pdl_wait();
   const int t0 = blockIdx.x * kRouteTokens, n = min(kRouteTokens, a.T - t0);
-  const Lane<NS> me(a);
+  ex.fill(a);
+  __syncthreads();
   for (int i = warp; i < n; i += warps) {
     int sel;
     float s;
-    route_token<L, NS>(a, me, t0 + i, chosen[i], sel, s);
+    route_token<L, NS>(a, ex, t0 + i, scratch[warp], sel, s);
     const float sum = warp_sum(lane < a.k ? s : 0.f);
     if (lane < a.k) {
       const int64_t o = (int64_t)(t0 + i) * a.k + lane;
