@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "ops_common.cuh"
+#include "tcgen05_ptx.cuh"
 
 namespace colibri {
 namespace {
@@ -30,6 +31,7 @@ struct NormArgs {
   float* dgate;                    // backward: [gates][d]; groups inside one block's rows go straight here
   int64_t ldx, ldy, lddx1, lddp;   // row strides, elements
   int64_t rpg;                     // rows per gate row
+  int rows_per_gate;               // the same, at most T
   int T, d, after, before, param_bf16;
   int rows_per_block;              // backward
   float alpha, beta, eps;
@@ -72,6 +74,60 @@ __device__ __forceinline__ void store_cols(T* row, int c, int d, const float (&v
     }
   }
 }
+// What a thread holds of the rows ahead of the one it works on.  kRing: kDepth - 1 rows on their way by
+// asynchronous copies into 16-byte slots of shared memory that this thread alone writes and reads (no
+// barrier; registers hold one row only).  Else the next row's values in registers.
+constexpr int kDepth = 3;
+enum { kScalar, kVector, kRing };
+template <int MODE, typename T>
+struct Ahead {  // kScalar
+  T v[8];
+  static constexpr int kVecs = 0;
+  __device__ __forceinline__ void load(uint4*, const T* row, int c, int d) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = (c * 8 + j) * blockDim.x + threadIdx.x;
+      v[j] = col < d ? row[col] : T(0.f);
+    }
+  }
+  __device__ __forceinline__ void get(const uint4*, int, int, float (&o)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = to_float(v[j]);
+  }
+};
+template <typename T>
+struct Ahead<kVector, T> {
+  uint4 v[sizeof(T) / 2];
+  static constexpr int kVecs = 0;
+  __device__ __forceinline__ void load(uint4*, const T* row, int c, int d) {
+    const int col = (c * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      v[i] = col < d ? reinterpret_cast<const uint4*>(row + col)[i] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(const uint4*, int, int, float (&o)[8]) const {
+    load8(reinterpret_cast<const T*>(v), o);
+  }
+};
+template <typename T>
+struct Ahead<kRing, T> {
+  static constexpr int kVecs = sizeof(T) / 2;  // slots of eight values, a block width apart
+  __device__ __forceinline__ void load(uint4* slot, const T* row, int c, int d) {
+    const int col = (c * blockDim.x + threadIdx.x) * 8;
+    if (col >= d) return;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      ptx::cp_async_16(ptx::smem_u32(slot + i * blockDim.x), reinterpret_cast<const uint4*>(row + col) + i);
+  }
+  __device__ __forceinline__ void get(const uint4* slot, int c, int d, float (&o)[8]) const {
+    uint4 v[kVecs];
+    const bool in = (c * (int)blockDim.x + (int)threadIdx.x) * 8 < d;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = in ? slot[i * blockDim.x] : make_uint4(0, 0, 0, 0);
+    load8(reinterpret_cast<const T*>(v), o);
+  }
+};
+
 template <bool VEC>
 __device__ __forceinline__ bool col_in(int c, int j, int d) {
   return (VEC ? (c * (int)blockDim.x + (int)threadIdx.x) * 8 + j : (c * 8 + j) * (int)blockDim.x + (int)threadIdx.x) < d;
@@ -112,9 +168,9 @@ __device__ __forceinline__ float dot_of(const float (&v)[C][8], const float (&w)
 }
 
 // v <- (v [- mean]) and returns 1 / deviation.
-template <bool VEC, int C>
+template <bool VEC, int C, bool LAYER>
 __device__ __forceinline__ float norm_stats(float (&v)[C][8], int kind, int d, float eps, float* buf, int& turn) {
-  if (kind == COLIBRI_NORM_LAYER) {
+  if (LAYER && kind == COLIBRI_NORM_LAYER) {
     float s[1] = {sum_of(v)};
     block_sum(s, buf, turn);
     center<VEC>(v, s[0] / d, d);
@@ -124,60 +180,115 @@ __device__ __forceinline__ float norm_stats(float (&v)[C][8], int kind, int d, f
   return rsqrtf(s[0] / d + eps);
 }
 
-template <typename S, typename Y, bool VEC, int C, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_kernel(NormArgs a) {
+// The vectors of a call: in registers where a thread has one chunk of columns, else loaded for every row.
+template <bool VEC, int C, bool BIAS>
+struct Vectors {
+  static constexpr bool kKeep = C == 1;
+  float wa[C][8], wb[C][8], g[C][8], ba[BIAS ? C : 1][8], bb[BIAS ? C : 1][8];
+  int group = -1;
+  __device__ __forceinline__ void load(const NormArgs& a) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (a.after) load_param<VEC>(a.wa, a.param_bf16, 0, c, a.d, wa[c]);
+      if (a.before) load_param<VEC>(a.wb, a.param_bf16, 0, c, a.d, wb[c]);
+      if constexpr (BIAS) {
+        if (a.ba) load_param<VEC>(a.ba, a.param_bf16, 0, c, a.d, ba[c]);
+        if (a.bb) load_param<VEC>(a.bb, a.param_bf16, 0, c, a.d, bb[c]);
+      }
+    }
+  }
+  __device__ __forceinline__ void load_gate(const NormArgs& a, int now) {
+    if (kKeep && now == group) return;
+    group = now;
+#pragma unroll
+    for (int c = 0; c < C; ++c) load_param<VEC>(a.gate, a.param_bf16, now, c, a.d, g[c]);
+  }
+};
+
+// A block walks over rows; while it works on one, the loads of the next are in flight, so that the loads
+// do not wait for the row sums.  BIAS: either norm is a layer norm (with or without bias vectors).
+template <typename S, typename Y, int MODE, int C, bool BIAS, int MAXT, int BLOCKS>
+__global__ void __launch_bounds__(MAXT, BLOCKS) block_norm_kernel(NormArgs a) {
   __shared__ float buf[kSumBuf];
+  extern __shared__ uint4 slots[];
+  constexpr bool VEC = MODE != kScalar, RING = MODE == kRing;
   int turn = 0;
+  using AX = Ahead<MODE, S>;
+  using AY = Ahead<MODE, Y>;
+  Vectors<VEC, C, BIAS> v;
+  AX rx[C];
+  AY ry[C];
+  const int row_slots = (AX::kVecs + (a.y ? AY::kVecs : 0)) * C * blockDim.x;
   pdl_wait();
-  for (int row = blockIdx.x; row < a.T; row += gridDim.x) {
-    float x[C][8];
-    const S* px = static_cast<const S*>(a.x) + row * a.ldx;
+  auto fetch = [&](int row, int stage) {
+    if (row < a.T) {
+      uint4* slot = slots + stage * row_slots + threadIdx.x;
 #pragma unroll
-    for (int c = 0; c < C; ++c) load_cols<VEC>(px, c, a.d, x[c]);
-    if (a.y) {
-      float z[C][8], w[8];
-      const Y* py = static_cast<const Y*>(a.y) + row * a.ldy;
-#pragma unroll
-      for (int c = 0; c < C; ++c) load_cols<VEC>(py, c, a.d, z[c]);
-      if (a.after) {
-        const float r = norm_stats<VEC, C>(z, a.after, a.d, a.eps, buf, turn);
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          load_param<VEC>(a.wa, a.param_bf16, 0, c, a.d, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[c][j] *= r * w[j];
-          if (a.ba) {
-            load_param<VEC>(a.ba, a.param_bf16, 0, c, a.d, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[c][j] += w[j];
-          }
+      for (int c = 0; c < C; ++c) {
+        rx[c].load(slot, static_cast<const S*>(a.x) + row * a.ldx, c, a.d);
+        slot += AX::kVecs * blockDim.x;
+        if (a.y) {
+          ry[c].load(slot, static_cast<const Y*>(a.y) + row * a.ldy, c, a.d);
+          slot += AY::kVecs * blockDim.x;
         }
+      }
+    }
+    if (RING) ptx::cp_async_commit();
+  };
+  const int step = gridDim.x;
+  for (int i = 0; i < (RING ? kDepth - 1 : 1); ++i) fetch(blockIdx.x + i * step, i);
+  if (v.kKeep) v.load(a);
+  int stage = 0;
+  for (int row = blockIdx.x; row < a.T; row += step) {
+    float x[C][8], z[C][8];
+    if constexpr (RING) {
+      fetch(row + (kDepth - 1) * step, stage ? stage - 1 : kDepth - 1);
+      ptx::cp_async_wait<kDepth - 1>();
+    }
+    const uint4* slot = slots + stage * row_slots + threadIdx.x;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      rx[c].get(slot, c, a.d, x[c]);
+      slot += AX::kVecs * blockDim.x;
+      if (a.y) {
+        ry[c].get(slot, c, a.d, z[c]);
+        slot += AY::kVecs * blockDim.x;
+      }
+    }
+    if (++stage == kDepth) stage = 0;
+    if (!RING) fetch(row + step, 0);
+    if (a.gate) v.load_gate(a, row / a.rows_per_gate);
+    if (!v.kKeep) v.load(a);
+    if (a.y) {
+      if (a.after) {
+        const float r = norm_stats<VEC, C, BIAS>(z, a.after, a.d, a.eps, buf, turn);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            z[c][j] *= r * v.wa[c][j];
+            if (BIAS && a.ba) z[c][j] += v.ba[c][j];
+          }
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        if (a.gate) {
-          load_param<VEC>(a.gate, a.param_bf16, row / a.rpg, c, a.d, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[c][j] *= w[j];
-        }
         // the next norm reads x1 as it is stored, rounded to the stream's type
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[c][j] = to_float(from_float<S>(fmaf(a.beta, z[c][j], a.alpha * x[c][j])));
+        for (int j = 0; j < 8; ++j) {
+          if (a.gate) z[c][j] *= v.g[c][j];
+          x[c][j] = to_float(from_float<S>(fmaf(a.beta, z[c][j], a.alpha * x[c][j])));
+        }
         store_cols<VEC>(static_cast<S*>(a.x1) + (int64_t)row * a.d, c, a.d, x[c]);
       }
     }
     if (a.before) {
-      const float r = norm_stats<VEC, C>(x, a.before, a.d, a.eps, buf, turn);
+      const float r = norm_stats<VEC, C, BIAS>(x, a.before, a.d, a.eps, buf, turn);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float w[8];
-        load_param<VEC>(a.wb, a.param_bf16, 0, c, a.d, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[c][j] *= r * w[j];
-        if (a.bb) {
-          load_param<VEC>(a.bb, a.param_bf16, 0, c, a.d, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[c][j] += w[j];
+        for (int j = 0; j < 8; ++j) {
+          x[c][j] *= r * v.wb[c][j];
+          if (BIAS && a.bb) x[c][j] += v.bb[c][j];
         }
         store_cols<VEC>(static_cast<S*>(a.p) + (int64_t)row * a.d, c, a.d, x[c]);
       }
@@ -205,68 +316,112 @@ __device__ __forceinline__ void flush_gate(const NormArgs& a, int64_t g, int r0,
 // A block takes consecutive rows and keeps the column sums of its own columns in registers; the sums
 // of all blocks are added by norm_sums_kernel in block order (no atomics: the same bits every time).
 // BIAS: either norm is a layer norm (two more column sums).
-template <typename S, typename Y, bool VEC, int C, bool BIAS, int MAXT>
+template <typename S, typename Y, int MODE, int C, bool BIAS, int MAXT>
 __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormArgs a) {
   __shared__ float buf[kSumBuf];
+  extern __shared__ uint4 slots[];
+  constexpr bool VEC = MODE != kScalar, RING = MODE == kRing;
   int turn = 0;
   float swb[C][8] = {}, swa[C][8] = {}, sg[C][8] = {};
   float sbb[BIAS ? C : 1][8] = {}, sba[BIAS ? C : 1][8] = {};
   const int r0 = blockIdx.x * a.rows_per_block, r1 = min(r0 + a.rows_per_block, a.T);
   const float inv_d = 1.f / a.d;
+  using AS = Ahead<MODE, S>;
+  using AY = Ahead<MODE, Y>;
+  Vectors<VEC, C, BIAS> v;
+  AS rd[C], rq[C], rx[C];  // d_x1, d_p, x1
+  AY ry[C];
+  const int slot_d = 0, slot_q = slot_d + (a.dx1 ? AS::kVecs : 0), slot_x = slot_q + (a.before ? AS::kVecs : 0);
+  const int slot_y = slot_x + (a.before ? AS::kVecs : 0), slot_n = slot_y + (a.y ? AY::kVecs : 0);
   pdl_wait();
-  int64_t group = a.gate ? r0 / a.rpg : 0;
-  for (int row = r0; row < r1; ++row) {
-    float D[C][8], w[8];
-    if (a.gate && row / a.rpg != group) {
-      flush_gate<VEC, C>(a, group, r0, r1, sg);
-      group = row / a.rpg;
+  auto fetch = [&](int row, int stage) {
+    if (row < r1) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        uint4* slot = slots + (stage * C + c) * slot_n * blockDim.x + threadIdx.x;
+        if (a.dx1) rd[c].load(slot + slot_d * blockDim.x, static_cast<const S*>(a.dx1) + row * a.lddx1, c, a.d);
+        if (a.before) {
+          rq[c].load(slot + slot_q * blockDim.x, static_cast<const S*>(a.dp) + row * a.lddp, c, a.d);
+          rx[c].load(slot + slot_x * blockDim.x, static_cast<const S*>(a.x) + row * a.ldx, c, a.d);
+        }
+        if (a.y) ry[c].load(slot + slot_y * blockDim.x, static_cast<const Y*>(a.y) + row * a.ldy, c, a.d);
+      }
     }
+    if (RING) ptx::cp_async_commit();
+  };
+  for (int i = 0; i < (RING ? kDepth - 1 : 1); ++i) fetch(r0 + i, i);
+  if (v.kKeep) v.load(a);
+  int stage = 0;
+  int group = a.gate ? r0 / a.rows_per_gate : 0;
+  for (int row = r0; row < r1; ++row) {
+    if (a.gate) {
+      const int now = row / a.rows_per_gate;
+      if (now != group) {
+        flush_gate<VEC, C>(a, group, r0, r1, sg);
+        group = now;
+      }
+      v.load_gate(a, group);
+    }
+    if (!v.kKeep) v.load(a);
+    if constexpr (RING) {
+      fetch(row + kDepth - 1, stage ? stage - 1 : kDepth - 1);
+      ptx::cp_async_wait<kDepth - 1>();
+    }
+    float D[C][8], x[C][8], q[C][8], y[C][8];
+    const float zero[8] = {};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
+      const uint4* slot = slots + (stage * C + c) * slot_n * blockDim.x + threadIdx.x;
       if (a.dx1) {
-        load_cols<VEC>(static_cast<const S*>(a.dx1) + row * a.lddx1, c, a.d, D[c]);
+        rd[c].get(slot + slot_d * blockDim.x, c, a.d, D[c]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) D[c][j] = 0.f;
+        for (int j = 0; j < 8; ++j) D[c][j] = zero[j];
       }
+      if (a.before) {
+        rq[c].get(slot + slot_q * blockDim.x, c, a.d, q[c]);
+        rx[c].get(slot + slot_x * blockDim.x, c, a.d, x[c]);
+      }
+      if (a.y) ry[c].get(slot + slot_y * blockDim.x, c, a.d, y[c]);
     }
-    if (a.before) {
-      float x[C][8], q[C][8];
+    if (++stage == kDepth) stage = 0;
+    if (!RING) fetch(row + 1, 0);
+    // Row sums: about the mean first (layer), then both norms' squares with the terms of the next norm's
+    // gradient, which need no deviation yet: sum(d_n n) = r sum(d_n x).
+    const bool lb = BIAS && a.before == COLIBRI_NORM_LAYER, la = BIAS && a.after == COLIBRI_NORM_LAYER;
+    if (BIAS && (lb || la)) {
+      float s[2] = {lb ? sum_of(x) : 0.f, la ? sum_of(y) : 0.f};
+      block_sum(s, buf, turn);
+      if (lb) center<VEC>(x, s[0] * inv_d, a.d);
+      if (la) center<VEC>(y, s[1] * inv_d, a.d);
+    }
+    float ra = 1.f;
+    if (a.before || a.after) {
+      float t[4] = {0.f, 0.f, 0.f, a.after ? dot_of(y, y) : 0.f};
+      if (a.before) {
+        t[0] = dot_of(x, x);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        load_cols<VEC>(static_cast<const S*>(a.x) + row * a.ldx, c, a.d, x[c]);
-        load_cols<VEC>(static_cast<const S*>(a.dp) + row * a.lddp, c, a.d, q[c]);
-      }
-      if (BIAS && a.before == COLIBRI_NORM_LAYER) {
-        float s[1] = {sum_of(x)};
-        block_sum(s, buf, turn);
-        center<VEC>(x, s[0] * inv_d, a.d);
-      }
-      float t[3] = {dot_of(x, x), 0.f, 0.f};
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        load_param<VEC>(a.wb, a.param_bf16, 0, c, a.d, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float dn = q[c][j] * w[j];
-          t[1] = fmaf(dn, x[c][j], t[1]);
-          t[2] += dn;
-        }
+          for (int j = 0; j < 8; ++j) {
+            const float dn = q[c][j] * v.wb[c][j];
+            t[1] = fmaf(dn, x[c][j], t[1]);
+            t[2] += dn;
+          }
       }
       block_sum(t, buf, turn);
-      const float r = rsqrtf(t[0] * inv_d + a.eps);
-      // x becomes n = x r; sum(dn n) = r sum(dn x)
-      const float m1 = t[1] * inv_d * r, m0 = BIAS && a.before == COLIBRI_NORM_LAYER ? t[2] * inv_d : 0.f;
+      ra = rsqrtf(t[3] * inv_d + a.eps);
+      if (a.before) {
+        const float r = rsqrtf(t[0] * inv_d + a.eps), m1 = t[1] * inv_d * r, m0 = lb ? t[2] * inv_d : 0.f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        load_param<VEC>(a.wb, a.param_bf16, 0, c, a.d, w);
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float n = x[c][j] * r, dn = q[c][j] * w[j];
-          swb[c][j] = fmaf(q[c][j], n, swb[c][j]);
-          if constexpr (BIAS) sbb[c][j] += q[c][j];
-          D[c][j] = fmaf(r, dn - n * m1 - m0, D[c][j]);
-        }
+          for (int j = 0; j < 8; ++j) {
+            const float n = x[c][j] * r, dn = q[c][j] * v.wb[c][j];
+            swb[c][j] = fmaf(q[c][j], n, swb[c][j]);
+            if constexpr (BIAS) sbb[c][j] += q[c][j];
+            D[c][j] = fmaf(r, dn - n * m1 - m0, D[c][j]);
+          }
       }
     }
 #pragma unroll
@@ -277,56 +432,34 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormArgs a) {
       store_cols<VEC>(static_cast<S*>(a.dx) + (int64_t)row * a.d, c, a.d, o);
     }
     if (a.y) {
-      float y[C][8];
-#pragma unroll
-      for (int c = 0; c < C; ++c) load_cols<VEC>(static_cast<const Y*>(a.y) + row * a.ldy, c, a.d, y[c]);
-      float r = 1.f;
-      if (a.after) r = norm_stats<VEC, C>(y, a.after, a.d, a.eps, buf, turn);
       float t[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float wa[8];
-        if (a.after) {
-          load_param<VEC>(a.wa, a.param_bf16, 0, c, a.d, wa);
+      for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[c][j] *= r;  // now n
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) D[c][j] *= a.beta;
-        if (a.gate) {
-          float z[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = a.after ? y[c][j] * wa[j] : y[c][j];
-          if (BIAS && a.ba) {
-            load_param<VEC>(a.ba, a.param_bf16, 0, c, a.d, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] += w[j];
+        for (int j = 0; j < 8; ++j) {
+          D[c][j] *= a.beta;
+          if (a.after) y[c][j] *= ra;  // now n
+          if (a.gate) {
+            float z = a.after ? y[c][j] * v.wa[c][j] : y[c][j];
+            if (BIAS && a.ba) z += v.ba[c][j];
+            sg[c][j] = fmaf(D[c][j], z, sg[c][j]);
+            D[c][j] *= v.g[c][j];
           }
-          load_param<VEC>(a.gate, a.param_bf16, group, c, a.d, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            sg[c][j] = fmaf(D[c][j], z[j], sg[c][j]);
-            D[c][j] *= w[j];
-          }
-        }
-        if (a.after) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          if (a.after) {
             swa[c][j] = fmaf(D[c][j], y[c][j], swa[c][j]);
             if constexpr (BIAS) sba[c][j] += D[c][j];
-            D[c][j] *= wa[j];  // now d_n
+            D[c][j] *= v.wa[c][j];  // now d_n
             t[0] = fmaf(D[c][j], y[c][j], t[0]);
             t[1] += D[c][j];
           }
         }
-      }
       if (a.after) {
         block_sum(t, buf, turn);
-        const float m1 = t[0] * inv_d, m0 = BIAS && a.after == COLIBRI_NORM_LAYER ? t[1] * inv_d : 0.f;
+        const float m1 = t[0] * inv_d, m0 = la ? t[1] * inv_d : 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) D[c][j] = r * (D[c][j] - y[c][j] * m1 - m0);
+          for (int j = 0; j < 8; ++j) D[c][j] = ra * (D[c][j] - y[c][j] * m1 - m0);
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) store_cols<VEC>(static_cast<Y*>(a.dy) + (int64_t)row * a.d, c, a.d, D[c]);
@@ -410,35 +543,64 @@ __global__ void __launch_bounds__(kSumCols * kSumLanes) norm_sums_kernel(NormSum
 
 constexpr int kNormMaxD = 16384;
 
-int norm_threads(int d) { return std::min(1024, ((d + 7) / 8 + 31) / 32 * 32); }
+// Threads of a block with `chunks` runs of 8 columns each.
+int norm_threads(int d, int chunks) { return ((d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32; }
 
+// Launches a kernel with the shared memory of its rows ahead.
+template <typename K>
+cudaError_t launch_rows(K kernel, int slots, int chunks, int blocks, int threads, cudaStream_t s, const NormArgs& a) {
+  const size_t smem = (size_t)kDepth * slots * chunks * threads * sizeof(uint4);
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return pdl_launch(kernel, dim3(blocks), dim3(threads), smem, s, a);
+}
+
+// Forms by width: threads of a block, chunks of 8 columns a thread, blocks an SM.  The row sums' barriers
+// want several blocks an SM, the vectors registers; a layer norm's two more vectors, or values in
+// registers instead of the ring, cost the second block of 512.  The ring takes at most 196 KB.
+template <typename S, typename Y, bool VEC, bool BIAS>
+cudaError_t launch_forward_t(const NormArgs& a, int sms, cudaStream_t s) {
+  constexpr int R = VEC ? kRing : kScalar, V = VEC ? kVector : kScalar;
+  constexpr int kBlocks = VEC && !BIAS ? 2 : 1;
+  const int slots = Ahead<R, S>::kVecs + (a.y ? Ahead<R, Y>::kVecs : 0);
+  auto go = [&](auto kernel, int slots, int chunks, int per_sm) {
+    const int blocks = (int)std::min<int64_t>(a.T, (int64_t)sms * per_sm);
+    return launch_rows(kernel, slots, chunks, blocks, norm_threads(a.d, chunks), s, a);
+  };
+  if (a.d > 8 * 1024) return go(block_norm_kernel<S, Y, V, 2, BIAS, 1024, 1>, 0, 2, 1);
+  if (a.d > 4 * 1024) return go(block_norm_kernel<S, Y, R, 2, BIAS, 512, 1>, slots, 2, 1);
+  if (a.d > 2 * 1024) return go(block_norm_kernel<S, Y, R, 1, BIAS, 512, kBlocks>, slots, 1, kBlocks);
+  return go(block_norm_kernel<S, Y, R, 1, BIAS, 256, 2 * kBlocks>, slots, 1,
+            2 * kBlocks * std::max(1, 256 / norm_threads(a.d, 1)));
+}
 template <typename S, typename Y, bool VEC>
 cudaError_t launch_forward(const NormArgs& a, int sms, cudaStream_t s) {
-  const int threads = norm_threads(a.d);
-  const dim3 grid(std::min<int64_t>(a.T, (int64_t)sms * std::max(1, 2048 / threads)));
-  if (a.d > 8 * 1024)
-    return pdl_launch(block_norm_kernel<S, Y, VEC, 2, 1024>, grid, dim3(threads), 0, s, a);
-  if (threads > 512)
-    return pdl_launch(block_norm_kernel<S, Y, VEC, 1, 1024>, grid, dim3(threads), 0, s, a);
-  return pdl_launch(block_norm_kernel<S, Y, VEC, 1, 512>, grid, dim3(threads), 0, s, a);
+  if (a.after == COLIBRI_NORM_LAYER || a.before == COLIBRI_NORM_LAYER)
+    return launch_forward_t<S, Y, VEC, true>(a, sms, s);
+  return launch_forward_t<S, Y, VEC, false>(a, sms, s);
 }
 
 // Blocks of the backward pass: enough to fill the SMs at about 512 threads each, and at least 8 rows a
 // block where the batch allows, so that the partial column sums stay small beside the rows.
 int backward_blocks(int T, int d, int sms, int* rows_per_block) {
-  const int want = std::min(sms * std::max(1, 512 / norm_threads(d)), std::max(sms, T / 8));
+  const int want = std::min(sms * std::max(1, 512 / norm_threads(d, d > 8 * 1024 ? 2 : 1)), std::max(sms, T / 8));
   *rows_per_block = (T + want - 1) / want;
   return (T + *rows_per_block - 1) / *rows_per_block;
 }
 
 template <typename S, typename Y, bool VEC, bool BIAS>
 cudaError_t launch_backward_t(const NormArgs& a, int blocks, cudaStream_t s) {
-  const int threads = norm_threads(a.d);
-  if (a.d > 8 * 1024)
-    return pdl_launch(block_norm_backward_kernel<S, Y, VEC, 2, BIAS, 1024>, dim3(blocks), dim3(threads), 0, s, a);
-  if (threads > 512)
-    return pdl_launch(block_norm_backward_kernel<S, Y, VEC, 1, BIAS, 1024>, dim3(blocks), dim3(threads), 0, s, a);
-  return pdl_launch(block_norm_backward_kernel<S, Y, VEC, 1, BIAS, 512>, dim3(blocks), dim3(threads), 0, s, a);
+  constexpr int R = VEC ? kRing : kScalar, V = VEC ? kVector : kScalar, one = Ahead<R, S>::kVecs;
+  const int slots = (a.dx1 ? one : 0) + (a.before ? 2 * one : 0) + (a.y ? Ahead<R, Y>::kVecs : 0);
+  auto go = [&](auto kernel, int slots, int chunks) {
+    return launch_rows(kernel, slots, chunks, blocks, norm_threads(a.d, chunks), s, a);
+  };
+  if (a.d > 8 * 1024) return go(block_norm_backward_kernel<S, Y, V, 2, BIAS, 1024>, 0, 2);
+  if (a.d > 4 * 1024) return go(block_norm_backward_kernel<S, Y, V, 1, BIAS, 1024>, 0, 1);
+  if (a.d > 2 * 1024) return go(block_norm_backward_kernel<S, Y, R, 1, BIAS, 512>, slots, 1);
+  return go(block_norm_backward_kernel<S, Y, R, 1, BIAS, 256>, slots, 1);
 }
 
 template <typename S, typename Y, bool VEC>
@@ -522,6 +684,7 @@ extern "C" int colibri_moe_block_norm(const colibri_moe_norm_config_t* cfg, cons
   a.x = x, a.y = y, a.wa = w->after_weight, a.ba = w->after_bias, a.wb = w->before_weight, a.bb = w->before_bias;
   a.gate = w->gate, a.x1 = x1, a.p = p, a.ldx = ldx, a.ldy = ldy, a.rpg = cfg->rows_per_gate, a.T = T, a.d = d;
   a.after = cfg->after, a.before = cfg->before, a.param_bf16 = cfg->param_dtype == COLIBRI_DTYPE_BF16;
+  a.rows_per_gate = (int)std::min<int64_t>(std::max<int64_t>(cfg->rows_per_gate, 1), T);
   a.alpha = cfg->residual_scale, a.beta = cfg->block_scale, a.eps = cfg->eps;
   bool vec = d % 8 == 0 && ldx % 8 == 0 && (!y || ldy % 8 == 0);
   for (const void* q : {x, y, a.wa, a.ba, a.wb, a.bb, a.gate, (const void*)x1, (const void*)p}) vec = vec && ops_aligned16(q);
@@ -601,6 +764,7 @@ extern "C" int colibri_moe_block_norm_backward(const colibri_moe_norm_config_t* 
   a.gate = w->gate, a.dx1 = d_x1, a.dp = d_p, a.dx = d_x, a.dy = d_y, a.part = static_cast<float*>(workspace);
   a.dgate = grads->gate, a.ldx = ldx1, a.ldy = ldy, a.lddx1 = ld_dx1, a.lddp = ld_dp, a.rpg = cfg->rows_per_gate;
   a.T = T, a.d = d, a.after = cfg->after, a.before = cfg->before, a.rows_per_block = rows;
+  a.rows_per_gate = (int)std::min<int64_t>(std::max<int64_t>(cfg->rows_per_gate, 1), T);
   a.param_bf16 = cfg->param_dtype == COLIBRI_DTYPE_BF16;
   a.alpha = y ? cfg->residual_scale : 1.f, a.beta = cfg->block_scale, a.eps = cfg->eps;
   bool vec = d % 8 == 0 && (!d_x1 || ld_dx1 % 8 == 0) && (!next || (ldx1 % 8 == 0 && ld_dp % 8 == 0)) && (!y || ldy % 8 == 0);
