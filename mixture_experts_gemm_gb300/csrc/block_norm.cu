@@ -119,14 +119,19 @@ struct Ahead<kRing, T> {
     for (int i = 0; i < kVecs; ++i)
       ptx::cp_async_16(ptx::smem_u32(slot + i * blockDim.x), reinterpret_cast<const uint4*>(row + col) + i);
   }
-  __device__ __forceinline__ void get(const uint4* slot, int c, int d, float (&o)[8]) const {
+  __device__ __forceinline__ void get(const uint4* slot, int, int, float (&o)[8]) const {
     uint4 v[kVecs];
-    const bool in = (c * (int)blockDim.x + (int)threadIdx.x) * 8 < d;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = in ? slot[i * blockDim.x] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kVecs; ++i) v[i] = slot[i * blockDim.x];
     load8(reinterpret_cast<const T*>(v), o);
   }
 };
+// The slots of columns past d are never copied into: zeros, once, keep them out of the row sums.
+template <int MODE>
+__device__ __forceinline__ void clear_slots(uint4* slots, int n) {
+  if (MODE == kRing)
+    for (int i = 0; i < n; ++i) slots[i * blockDim.x + threadIdx.x] = make_uint4(0, 0, 0, 0);
+}
 
 template <bool VEC>
 __device__ __forceinline__ bool col_in(int c, int j, int d) {
@@ -138,6 +143,15 @@ __device__ __forceinline__ void load_param(const void* p, int bf16, int64_t row,
     load_cols<VEC>(static_cast<const __nv_bfloat16*>(p) + row * d, c, d, v);
   else
     load_cols<VEC>(static_cast<const float*>(p) + row * d, c, d, v);
+}
+
+// f(c, j) for every value of a thread.
+template <int C, typename F>
+__device__ __forceinline__ void each(F f) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f(c, j);
 }
 
 // Subtracts the row's mean (layer); the values past d stay zero.
@@ -169,15 +183,16 @@ __device__ __forceinline__ float dot_of(const float (&v)[C][8], const float (&w)
 
 // v <- (v [- mean]) and returns 1 / deviation.
 template <bool VEC, int C, bool LAYER>
-__device__ __forceinline__ float norm_stats(float (&v)[C][8], int kind, int d, float eps, float* buf, int& turn) {
+__device__ __forceinline__ float norm_stats(float (&v)[C][8], int kind, int d, float inv_d, float eps, float* buf,
+                                            int& turn) {
   if (LAYER && kind == COLIBRI_NORM_LAYER) {
     float s[1] = {sum_of(v)};
     block_sum(s, buf, turn);
-    center<VEC>(v, s[0] / d, d);
+    center<VEC>(v, s[0] * inv_d, d);
   }
   float s[1] = {dot_of(v, v)};
   block_sum(s, buf, turn);
-  return rsqrtf(s[0] / d + eps);
+  return rsqrtf(fmaf(s[0], inv_d, eps));
 }
 
 // The vectors of a call: in registers where a thread has one chunk of columns, else loaded for every row.
@@ -220,6 +235,7 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) block_norm_kernel(NormArgs a) {
   AY ry[C];
   const int row_slots = (AX::kVecs + (a.y ? AY::kVecs : 0)) * C * blockDim.x;
   pdl_wait();
+  clear_slots<MODE>(slots, kDepth * (AX::kVecs + (a.y ? AY::kVecs : 0)) * C);
   auto fetch = [&](int row, int stage) {
     if (row < a.T) {
       uint4* slot = slots + stage * row_slots + threadIdx.x;
@@ -236,6 +252,8 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) block_norm_kernel(NormArgs a) {
     if (RING) ptx::cp_async_commit();
   };
   const int step = gridDim.x;
+  const float inv_d = 1.f / a.d;
+  const bool one_gate = a.rows_per_gate >= a.T;
   for (int i = 0; i < (RING ? kDepth - 1 : 1); ++i) fetch(blockIdx.x + i * step, i);
   if (v.kKeep) v.load(a);
   int stage = 0;
@@ -257,39 +275,30 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) block_norm_kernel(NormArgs a) {
     }
     if (++stage == kDepth) stage = 0;
     if (!RING) fetch(row + step, 0);
-    if (a.gate) v.load_gate(a, row / a.rows_per_gate);
+    if (a.gate) v.load_gate(a, one_gate ? 0 : row / a.rows_per_gate);
     if (!v.kKeep) v.load(a);
     if (a.y) {
       if (a.after) {
-        const float r = norm_stats<VEC, C, BIAS>(z, a.after, a.d, a.eps, buf, turn);
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            z[c][j] *= r * v.wa[c][j];
-            if (BIAS && a.ba) z[c][j] += v.ba[c][j];
-          }
+        const float r = norm_stats<VEC, C, BIAS>(z, a.after, a.d, inv_d, a.eps, buf, turn);
+        each<C>([&](int c, int j) { z[c][j] *= r * v.wa[c][j]; });
+        if (BIAS && a.ba) each<C>([&](int c, int j) { z[c][j] += v.ba[BIAS ? c : 0][j]; });
       }
+      if (a.gate) each<C>([&](int c, int j) { z[c][j] *= v.g[c][j]; });
+      // the next norm reads x1 as it is stored, rounded to the stream's type
+      each<C>([&](int c, int j) {
+        x[c][j] = to_float(from_float<S>(fmaf(a.beta, z[c][j], a.alpha * x[c][j])));
+      });
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        // the next norm reads x1 as it is stored, rounded to the stream's type
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (a.gate) z[c][j] *= v.g[c][j];
-          x[c][j] = to_float(from_float<S>(fmaf(a.beta, z[c][j], a.alpha * x[c][j])));
-        }
         store_cols<VEC>(static_cast<S*>(a.x1) + (int64_t)row * a.d, c, a.d, x[c]);
       }
     }
     if (a.before) {
-      const float r = norm_stats<VEC, C, BIAS>(x, a.before, a.d, a.eps, buf, turn);
+      const float r = norm_stats<VEC, C, BIAS>(x, a.before, a.d, inv_d, a.eps, buf, turn);
+      each<C>([&](int c, int j) { x[c][j] *= r * v.wb[c][j]; });
+      if (BIAS && a.bb) each<C>([&](int c, int j) { x[c][j] += v.bb[BIAS ? c : 0][j]; });
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[c][j] *= r * v.wb[c][j];
-          if (BIAS && a.bb) x[c][j] += v.bb[c][j];
-        }
         store_cols<VEC>(static_cast<S*>(a.p) + (int64_t)row * a.d, c, a.d, x[c]);
       }
     }
@@ -334,6 +343,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormArgs a) {
   const int slot_d = 0, slot_q = slot_d + (a.dx1 ? AS::kVecs : 0), slot_x = slot_q + (a.before ? AS::kVecs : 0);
   const int slot_y = slot_x + (a.before ? AS::kVecs : 0), slot_n = slot_y + (a.y ? AY::kVecs : 0);
   pdl_wait();
+  clear_slots<MODE>(slots, kDepth * slot_n * C);
   auto fetch = [&](int row, int stage) {
     if (row < r1) {
 #pragma unroll
@@ -353,9 +363,10 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormArgs a) {
   if (v.kKeep) v.load(a);
   int stage = 0;
   int group = a.gate ? r0 / a.rows_per_gate : 0;
+  const bool one_gate = a.rows_per_gate >= a.T;
   for (int row = r0; row < r1; ++row) {
     if (a.gate) {
-      const int now = row / a.rows_per_gate;
+      const int now = one_gate ? 0 : row / a.rows_per_gate;
       if (now != group) {
         flush_gate<VEC, C>(a, group, r0, r1, sg);
         group = now;
@@ -406,7 +417,7 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormArgs a) {
           for (int j = 0; j < 8; ++j) {
             const float dn = q[c][j] * v.wb[c][j];
             t[1] = fmaf(dn, x[c][j], t[1]);
-            t[2] += dn;
+            if constexpr (BIAS) t[2] += dn;
           }
       }
       block_sum(t, buf, turn);
@@ -433,26 +444,28 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormArgs a) {
     }
     if (a.y) {
       float t[2] = {0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          D[c][j] *= a.beta;
-          if (a.after) y[c][j] *= ra;  // now n
-          if (a.gate) {
-            float z = a.after ? y[c][j] * v.wa[c][j] : y[c][j];
-            if (BIAS && a.ba) z += v.ba[c][j];
-            sg[c][j] = fmaf(D[c][j], z, sg[c][j]);
-            D[c][j] *= v.g[c][j];
-          }
-          if (a.after) {
-            swa[c][j] = fmaf(D[c][j], y[c][j], swa[c][j]);
-            if constexpr (BIAS) sba[c][j] += D[c][j];
-            D[c][j] *= v.wa[c][j];  // now d_n
-            t[0] = fmaf(D[c][j], y[c][j], t[0]);
-            t[1] += D[c][j];
-          }
+      each<C>([&](int c, int j) { D[c][j] *= a.beta; });
+      if (a.after) each<C>([&](int c, int j) { y[c][j] *= ra; });  // now n
+      if (a.gate) {
+        if (BIAS && a.ba) {
+          each<C>([&](int c, int j) {
+            sg[c][j] = fmaf(D[c][j], fmaf(y[c][j], v.wa[c][j], v.ba[BIAS ? c : 0][j]), sg[c][j]);
+          });
+        } else if (a.after) {
+          each<C>([&](int c, int j) { sg[c][j] = fmaf(D[c][j], y[c][j] * v.wa[c][j], sg[c][j]); });
+        } else {
+          each<C>([&](int c, int j) { sg[c][j] = fmaf(D[c][j], y[c][j], sg[c][j]); });
         }
+        each<C>([&](int c, int j) { D[c][j] *= v.g[c][j]; });
+      }
+      if (a.after)
+        each<C>([&](int c, int j) {
+          swa[c][j] = fmaf(D[c][j], y[c][j], swa[c][j]);
+          if constexpr (BIAS) sba[c][j] += D[c][j];
+          D[c][j] *= v.wa[c][j];  // now d_n
+          t[0] = fmaf(D[c][j], y[c][j], t[0]);
+          if constexpr (BIAS) t[1] += D[c][j];
+        });
       if (a.after) {
         block_sum(t, buf, turn);
         const float m1 = t[0] * inv_d, m0 = la ? t[1] * inv_d : 0.f;
