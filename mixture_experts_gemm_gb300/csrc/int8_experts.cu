@@ -46,72 +46,89 @@ __device__ __forceinline__ float quotient(float x, float scale, float inv, bool 
 
 constexpr int kQuantThreads = 256;
 
+// Eight values as loaded.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p), b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = bf16_lo(a.x), v[1] = bf16_hi(a.x), v[2] = bf16_lo(a.y), v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(a.z), v[5] = bf16_hi(a.z), v[6] = bf16_lo(a.w), v[7] = bf16_hi(a.w);
+  }
+};
+
 // One block a row, held in registers between the maximum and the quotients: C chunks of 8 columns a
-// thread (VEC: 16-byte loads), or read twice (C == 0).  HBM-bound: the row once in, its fp16 once out.
+// thread (16-byte loads), or read twice (C == 0).  HBM-bound: the row once in, its fp16 once out.
 template <typename T, typename Q, int C>
-__global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(QuantArgs a) {
-  __shared__ float s_max[2][8];
-  __shared__ int s_bad[2][8];
+__global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_kernel(QuantArgs a) {
+  __shared__ float s_max[kQuantThreads / 32];
   pdl_wait();
-  for (int i = blockIdx.x * kQuantThreads + threadIdx.x; i < a.n_ticket; i += gridDim.x * kQuantThreads) a.ticket[i] = 0;
+  for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x; i < a.n_ticket; i += (int64_t)gridDim.x * kQuantThreads)
+    a.ticket[i] = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int turn = 0;
-  for (int r = blockIdx.x; r < a.n; r += gridDim.x, turn ^= 1) {
-    int t = r;
-    if (a.rows) t = a.rows[r];
-    const bool real = t >= 0 && t < a.n_tokens;
-    const T* x = static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx;
-    Q* q = static_cast<Q*>(a.q) + (int64_t)r * a.K;
-    float v[C ? C : 1][8];
-    float top = 0.f;
-    bool bad = false;
-    if constexpr (C > 0) {
+  const int r = blockIdx.x;
+  int t = r;
+  if (a.rows) t = a.rows[r];
+  const bool real = t >= 0 && t < a.n_tokens;
+  const T* x = static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx;
+  Q* q = static_cast<Q*>(a.q) + (int64_t)r * a.K;
+  Raw8<T> raw[C ? C : 1] = {};
+  float top = 0.f;  // of |x|; a NaN or an infinity is kept as infinity
+  auto take = [&](float v) {
+    const float m = fabsf(v);
+    top = fmaxf(top, m < INFINITY ? m : INFINITY);
+  };
+  if constexpr (C > 0) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = (c * kQuantThreads + threadIdx.x) * 8;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[c][j] = 0.f;
-        if (real && col < a.K) load8(x + col, v[c]);
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          bad |= !(fabsf(v[c][j]) < INFINITY);
-          top = fmaxf(top, fabsf(v[c][j]));
-        }
-    } else if (real) {
-      for (int i = threadIdx.x; i < a.K; i += kQuantThreads) {
-        const float m = fabsf(to_float(x[i]));
-        bad |= !(m < INFINITY);
-        top = fmaxf(top, m);
-      }
+    for (int c = 0; c < C; ++c) {
+      const int col = (c * kQuantThreads + threadIdx.x) * 8;
+      if (real && col < a.K) raw[c].load(x + col);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    bad = __any_sync(~0u, bad);
-    if (lane == 0) s_max[turn][warp] = top, s_bad[turn][warp] = bad;
-    __syncthreads();  // one a row: the halves are used in turn
+    for (int c = 0; c < C; ++c) {
+      float v[8];
+      raw[c].get(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, s_max[turn][i]), bad |= s_bad[turn][i] != 0;
-    const float scale = bad ? NAN : __fdiv_rn(top, 127.f);
-    if (threadIdx.x == 0) a.scale[r] = scale;
-    const bool live = scale > 0.f, exact = scale < 1e-30f;  // 1 / scale may overflow there
-    const float inv = live ? __frcp_rn(scale) : 0.f;
-    if constexpr (C > 0) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = (c * kQuantThreads + threadIdx.x) * 8;
-        if (col >= a.K) break;
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = live ? quotient(v[c][j], scale, inv, exact) : 0.f;
-        store_q8(q + col, o);
-      }
-    } else {
-      for (int i = threadIdx.x; i < a.K; i += kQuantThreads)
-        q[i] = q_value<Q>(live ? quotient(to_float(x[i]), scale, inv, exact) : 0.f);
+      for (int j = 0; j < 8; ++j) take(v[j]);
     }
+  } else if (real) {
+    for (int i = threadIdx.x; i < a.K; i += kQuantThreads) take(to_float(x[i]));
+  }
+  top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));  // not negative: ordered as its bits
+  if (lane == 0) s_max[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQuantThreads / 32; ++i) top = fmaxf(top, s_max[i]);
+  const float scale = top < INFINITY ? __fdiv_rn(top, 127.f) : NAN;
+  if (threadIdx.x == 0) a.scale[r] = scale;
+  const bool live = scale > 0.f, exact = scale < 1e-30f;  // 1 / scale may overflow there
+  const float inv = live ? __frcp_rn(scale) : 0.f;
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int col = (c * kQuantThreads + threadIdx.x) * 8;
+      if (col >= a.K) break;
+      float v[8], o[8];
+      raw[c].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = live ? quotient(v[j], scale, inv, exact) : 0.f;
+      store_q8(q + col, o);
+    }
+  } else {
+    for (int i = threadIdx.x; i < a.K; i += kQuantThreads)
+      q[i] = q_value<Q>(live ? quotient(to_float(x[i]), scale, inv, exact) : 0.f);
   }
 }
 
@@ -127,8 +144,8 @@ int check_int8_config(const colibri_moe_int8_config_t* c) {
 }
 
 template <typename T, typename Q>
-cudaError_t quantize_t(const QuantArgs& q, int sms, cudaStream_t s) {
-  const dim3 grid(std::min(q.n, sms * 8)), block(kQuantThreads);
+cudaError_t quantize_t(const QuantArgs& q, cudaStream_t s) {
+  const dim3 grid(q.n), block(kQuantThreads);
   const bool vec = q.ldx % 8 == 0 && ops_aligned16(q.x) && ops_aligned16(q.q);  // K is a multiple of 16
   const int chunks = (q.K + 8 * kQuantThreads - 1) / (8 * kQuantThreads);
   if (!vec || chunks > 8) return pdl_launch(quantize_rows_kernel<T, Q, 0>, grid, block, 0, s, q);
@@ -139,27 +156,33 @@ cudaError_t quantize_t(const QuantArgs& q, int sms, cudaStream_t s) {
 }
 
 template <typename Q>
-cudaError_t quantize(int dtype, const QuantArgs& q, int sms, cudaStream_t s) {
-  return dtype == COLIBRI_DTYPE_F32 ? quantize_t<float, Q>(q, sms, s) : quantize_t<__nv_bfloat16, Q>(q, sms, s);
+cudaError_t quantize(int dtype, const QuantArgs& q, cudaStream_t s) {
+  return dtype == COLIBRI_DTYPE_F32 ? quantize_t<float, Q>(q, s) : quantize_t<__nv_bfloat16, Q>(q, s);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Few rows an expert on average: tiles of 64 rows, a deeper ring for the weights, and K may be split.
-bool wide_form(int R, int E) { return R > 32 * (int64_t)E; }
+// Token rows of a tile, by the rows that an expert gets on average (the exact numbers are on the device):
+// an expert's rows should fit one tile, so that its weights are converted once, and no tile should be
+// much wider than its rows, because a wider one leaves less room for weights in flight.
+int int8_tile_rows(int R, int E) {
+  const int64_t mean = R / std::min(E, R);
+  return mean <= 16 ? 32 : mean <= 48 ? 64 : mean <= 128 ? 128 : 256;
+}
 
 // The workspace of a product: the rows' scales and fp16 values, tickets and partial sums of split tiles.
 struct Int8Workspace {
   size_t scale, q, ticket, partial, bytes;
-  int items;
+  int items, tile_rows;
 };
 Int8Workspace int8_workspace(const colibri_moe_int8_config_t* c, int R, int sms) {
   Int8Workspace w = {};
-  w.items = wide_form(R, c->num_experts) ? 0 : kInt8SplitWaves * sms;
+  w.tile_rows = int8_tile_rows(R, c->num_experts);
+  w.items = sms * (kInt8PartialRows / w.tile_rows);
   w.q = round256((size_t)R * sizeof(float));
   w.ticket = w.q + round256((size_t)R * c->in_features * 2);
   w.partial = w.ticket + round256(w.items * sizeof(uint32_t));
-  w.bytes = w.partial + (size_t)w.items * kInt8NarrowRows * 128 * sizeof(float);
+  w.bytes = w.partial + (size_t)w.items * w.tile_rows * 128 * sizeof(float);
   return w;
 }
 
@@ -205,7 +228,7 @@ extern "C" int colibri_moe_int8_quantize(const colibri_moe_int8_config_t* cfg, c
   for (const void* p : {x, (const void*)q, (const void*)scale})
     if (!ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   const QuantArgs a = {x, ldx, n, nullptr, n, cfg->in_features, q, scale, nullptr, 0};
-  const cudaError_t e = quantize<int8_t>(cfg->dtype, a, sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = quantize<int8_t>(cfg->dtype, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 
@@ -244,15 +267,14 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
     if (p && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  const bool split = lay.items > 0;
   const QuantArgs qa = {x, ldx, n_tokens, rows, R, cfg->in_features, ws + lay.q, reinterpret_cast<float*>(ws + lay.scale),
-                        split ? reinterpret_cast<uint32_t*>(ws + lay.ticket) : nullptr, lay.items};
-  CUtensorMap maps[3];
-  if (!int8_tensor_maps(qa.q, R, w, w3, cfg->num_experts, cfg->out_features, cfg->in_features, maps)) return COLIBRI_ERR_CUDA;
-  if (quantize<__half>(cfg->dtype, qa, sms, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
-  const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, split ? reinterpret_cast<float*>(ws + lay.partial) : nullptr,
+                        reinterpret_cast<uint32_t*>(ws + lay.ticket), lay.items};
+  Int8Maps maps;
+  if (!int8_tensor_maps(qa.q, R, w, w3, cfg->num_experts, cfg->out_features, cfg->in_features, &maps)) return COLIBRI_ERR_CUDA;
+  if (quantize<__half>(cfg->dtype, qa, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
+  const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, reinterpret_cast<float*>(ws + lay.partial),
                       qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, 2000000000ull};
-  const cudaError_t e = launch_int8_mma(maps, !split, w3 != nullptr, cfg->out_dtype == COLIBRI_DTYPE_BF16, a, device, sms, s);
+  const cudaError_t e = launch_int8_mma(maps, lay.tile_rows, w3 != nullptr, cfg->out_dtype == COLIBRI_DTYPE_BF16, a, device, sms, s);
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 

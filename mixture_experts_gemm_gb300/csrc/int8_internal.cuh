@@ -10,17 +10,15 @@ namespace colibri {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // colibri_moe.cu; nullptr if the driver has none
 
-// The product kernel's forms: most token rows of a tile.
-constexpr int kInt8WideRows = 256, kInt8NarrowRows = 64;
 constexpr int kInt8MaxSplits = 8;     // parts of K a tile may be split into
-constexpr int kInt8SplitWaves = 4;    // items (tiles x parts) of a split product, at most this many per SM
+constexpr int kInt8PartialRows = 256;  // tile rows x items (tiles x parts) per SM that a split product may hold
 
 struct Int8Args {
   const float* scale;               // [R] of the quantised rows
   const int32_t* offsets;           // [E + 1]
   const float *w_scale, *w3_scale;  // [E, N]
   void* y;                          // [R, N]
-  float* partial;                   // narrow form: [items][kInt8NarrowRows][128], or nullptr: never split
+  float* partial;                   // [items][tile rows][128] sums of parts of K
   uint32_t* ticket;                 // [items], zero at launch: parts of a tile done
   int max_items;                    // capacity of the two
   int R, E, K, N;
@@ -39,9 +37,17 @@ struct QuantArgs {
   int n_ticket;
 };
 
+// Tensor maps: the quantised rows in boxes of 32, 64, 128 and 256 rows x 64 columns, the weights in boxes of
+// 128 rows (64 of each projection) x 64 bytes.
+constexpr int kTokMaps = 4;
+struct Int8Maps {
+  CUtensorMap q[kTokMaps], w, w3;
+};
+
 // rows: q [R, K] fp16 whole numbers; w, w3: [E * N, K] int8.
-bool int8_tensor_maps(const void* q, int R, const int8_t* w, const int8_t* w3, int E, int N, int K, CUtensorMap* maps);
-cudaError_t launch_int8_mma(const CUtensorMap* maps, bool wide, bool swiglu, bool bf16_out, const Int8Args& a, int device,
+bool int8_tensor_maps(const void* q, int R, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps);
+// tile_rows: 32, 64, 128 or 256 token rows a tile.
+cudaError_t launch_int8_mma(const Int8Maps& maps, int tile_rows, bool swiglu, bool bf16_out, const Int8Args& a, int device,
                             int sms, cudaStream_t s);
 
 }  // namespace colibri

@@ -15,15 +15,15 @@
 //
 // One persistent CTA per SM, 512 threads:
 //   warp 0       TMA producer of the raw weight ring (RS stages of 128 rows x 64 bytes);
-//   warp 6       TMA producer of the token rows of the operand ring (ST stages, 64 columns of K);
-//   warps 8..15  converters, two groups of four that take alternate stages: 16 bytes a thread become two
+//   warp 6       TMA producer of the token rows (SB stages, 64 columns of K);
+//   warps 8..15  converters to the fp16 weights (SA stages), two groups of four that take alternate stages: 16 bytes a thread become two
 //                16-byte stores of fp16 in the 128-byte swizzled layout (byte ^ 0x80 under an exponent of
 //                2^10 is 1024 + (v + 128); one subtraction leaves v);
 //   warp 1       one lane issues the MMAs, two accumulators in TMEM;
 //   warps 2..5   epilogue.
 // The converters' work is 2 instructions per weight (about 120 issue slots of the 512 cycles that the
 // MMAs of a 256-column stage take), so it hides behind the MMAs of wide tiles and behind HBM for narrow
-// ones.  Items are (tile, part of K) in a fixed order; a narrow product of few tiles is split along K, the
+// ones.  Items are (tile, part of K) in a fixed order; a product of few tiles is split along K, the
 // parts' sums kept in `partial` and added in order by whichever CTA finishes the tile (no floating-point
 // atomics: the same bits every time).
 //
@@ -44,21 +44,38 @@ constexpr int kConvWarp0 = 8, kConvGroups = 2, kConvGroupWarps = 4;
 constexpr int BM = 128, BK = 64;
 constexpr int kRawBytes = BM * BK;       // 8 KB
 constexpr int kABytes = BM * BK * 2;     // 16 KB
-constexpr int kTokBox = 32;              // token rows of one TMA box
+constexpr int kTokBox = 32;              // token rows of the smallest TMA box
 constexpr int kTokBoxBytes = kTokBox * BK * 2;
 constexpr int kMaxExperts = 512;
 
+// Rings, in blocks of 64 columns of K: raw weights (RS), converted weights (SA), token rows (SB).  One full
+// and one done barrier serve block `it` for both operands, at it % kSync.  A block goes around in about 2300
+// cycles (conversion 500, then barriers, MMAs and commit), whatever it holds: the narrower the tile, the
+// more blocks have to be on their way.
+constexpr int kSync = 8;
 template <int NT>
 struct Form {
-  static constexpr int ST = NT == kInt8WideRows ? 3 : 5;   // operand stages
-  static constexpr int RS = NT == kInt8WideRows ? 8 : 10;  // raw weight stages
+  static constexpr int SA = NT == 256 ? 3 : NT == 128 ? 5 : NT == 64 ? 6 : 7;
+  static constexpr int SB = NT == 256 ? 4 : NT == 128 ? 5 : NT == 64 ? 6 : 7;
+  static constexpr int RS = NT == 256 ? 5 : NT == 128 ? 6 : NT == 64 ? 8 : 9;
   static constexpr int kBBytes = NT * BK * 2;
-  static constexpr int kStage = kABytes + kBBytes;
-  static constexpr int kBars = 2 * ST + 2 * RS + 7;
+  static constexpr int kBars = 2 * kSync + 2 * RS + 7;
   static constexpr uint32_t kTmemCols = 2 * NT;
-  static constexpr int kSmem = 1024 + ST * kStage + RS * kRawBytes + kBars * 8 + 32 + 4 * (3 * kMaxExperts + 1);
+  static constexpr int kSmem =
+      1024 + SA * kABytes + SB * kBBytes + RS * kRawBytes + kBars * 8 + 32 + 4 * (3 * kMaxExperts + 1);
+  static_assert(SA < kSync && SB < kSync, "a barrier is not reused before both rings are");
+  // A raw slot alternates between the converter groups unless RS is a multiple of their number.  A group
+  // waits for its phase by parity, so the phase before (the other group's, block it - RS) must be over by
+  // then: the group's own last block, it - kConvGroups, needed the MMAs of block it - kConvGroups - SA.
+  static_assert(RS % kConvGroups == 0 || RS >= SA + kConvGroups, "raw phases by parity");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
-static_assert(Form<kInt8WideRows>::kSmem <= 227 * 1024 && Form<kInt8NarrowRows>::kSmem <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
 
 // Two bytes of signed integers (selected by `sel` out of w ^ 0x80808080) as two exact fp16.
 __device__ __forceinline__ uint32_t bytes_to_half2(uint32_t biased, uint32_t sel) {
@@ -86,15 +103,14 @@ struct Item {
 
 template <int NT, bool SWIGLU, typename O>
 __global__ void __launch_bounds__(kThreads, 1)
-    int8_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_w,
-                    const __grid_constant__ CUtensorMap tm_w3, const Int8Args a) {
+    int8_mma_kernel(const __grid_constant__ Int8Maps tm, const Int8Args a) {
   using F = Form<NT>;
-  constexpr int ST = F::ST, RS = F::RS;
+  constexpr int SA = F::SA, SB = F::SB, RS = F::RS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_a = smem;
-  uint8_t* s_b = s_a + ST * kABytes;
-  uint8_t* s_raw = s_b + ST * F::kBBytes;
+  uint8_t* s_b = s_a + SA * kABytes;
+  uint8_t* s_raw = s_b + SB * F::kBBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_raw + RS * kRawBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + F::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -103,17 +119,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* s_rows = s_row0 + kMaxExperts;                   // its rows
   int* s_tiles = s_rows + kMaxExperts;                  // token tiles before it [E + 1]
 
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * ST;
-  const uint32_t rfull0 = empty0 + 8 * ST, rempty0 = rfull0 + 8 * RS;
+  const uint32_t full0 = smem_u32(bars), done0 = full0 + 8 * kSync;
+  const uint32_t rfull0 = done0 + 8 * kSync, rempty0 = rfull0 + 8 * RS;
   const uint32_t tfull0 = rempty0 + 8 * RS, tempty0 = tfull0 + 16, drain = tempty0 + 16;
   const uint32_t joined = drain + 8, decided = joined + 8;  // a split tile's partial sums are out; who adds them
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_trigger();
   if (warp == 0 && lane == 0) {
-    for (int i = 0; i < ST; ++i) {
+    for (int i = 0; i < kSync; ++i) {
       mbar_init(full0 + 8 * i, 1 + kConvGroupWarps);  // token rows landed, weights converted
-      mbar_init(empty0 + 8 * i, 1);
+      mbar_init(done0 + 8 * i, 1);
     }
     for (int i = 0; i < RS; ++i) {
       mbar_init(rfull0 + 8 * i, 1);
@@ -128,9 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(decided, 1);
     *s_abort = 0;
     fence_mbar_init();
-    prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_w);
-    if constexpr (SWIGLU) prefetch_tmap(&tm_w3);
+    for (int i = 0; i < kTokMaps; ++i) prefetch_tmap(&tm.q[i]);
+    prefetch_tmap(&tm.w);
+    if constexpr (SWIGLU) prefetch_tmap(&tm.w3);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), F::kTmemCols);
@@ -189,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t tiles = (int64_t)s_tiles[a.E] * ch_tiles;
   // Parts of K: the number that leaves the SMs least idle in the last wave, a little against more parts.
   int parts = 1;
-  if (a.partial && tiles < 2 * (int64_t)gridDim.x) {
+  if (tiles < 2 * (int64_t)gridDim.x) {
     float least = 1e30f;
     for (int p = 1; p <= kInt8MaxSplits && p <= kblocks && tiles * p <= a.max_items; ++p) {
       const int waves = (int)((tiles * p + gridDim.x - 1) / gridDim.x);
@@ -224,134 +240,172 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it;
   };
 
+  // Waits until the MMAs of block it - behind are done: the slot that block `it` takes is free.  A done
+  // barrier cannot run two phases ahead of a waiter, because the blocks between need the waiter's work.
+  auto slot_free = [&](uint32_t it, uint32_t behind) {
+    const uint32_t j = it - behind;
+    return it < behind || mbar_wait(done0 + 8 * (j % kSync), j / kSync & 1, s_abort, a.timeout_ns);
+  };
+
+  // The producers' and the MMA warp run their loops with all lanes and let one elected lane issue: addresses
+  // and descriptors then stay in uniform registers (inside `if (lane == 0)` four MMAs and their loop took 600
+  // cycles, and a copy about 90).
   bool ok = true;
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ raw weights
-      uint32_t it = 0, issued = 0;
-      for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-        const Item t = item_at(i);
-        const int w_row = t.e * a.N + t.ch * kCh;
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const uint32_t r = it % RS;
-          if (!mbar_wait(rempty0 + 8 * r, (it / RS & 1) ^ 1, s_abort, a.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(rfull0 + 8 * r, kRawBytes);
-          const uint32_t dst = smem_u32(s_raw + r * kRawBytes);
-          tma_load_2d(dst, &tm_w, rfull0 + 8 * r, kb * BK, w_row);
-          if constexpr (SWIGLU) tma_load_2d(dst + kRawBytes / 2, &tm_w3, rfull0 + 8 * r, kb * BK, w_row);
-          issued = it + 1;
+    // -------------------------------------------------------------- raw weights
+    const bool elected = elect_one();
+    const uint32_t raw0 = smem_u32(s_raw);
+    uint32_t issued = 0, r = 0, ph = 0;
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item t = item_at(i);
+      const int w_row = t.e * a.N + t.ch * kCh;
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++issued) {
+        if (!__all_sync(~0u, mbar_wait(rempty0 + 8 * r, ph ^ 1, s_abort, a.timeout_ns))) {
+          ok = false;
+          break;
         }
+        const uint32_t full = rfull0 + 8 * r, dst = raw0 + r * kRawBytes;
+        const int x = kb * BK;
+        if (elected) {
+          mbar_arrive_expect_tx(full, kRawBytes);
+          tma_load_2d(dst, &tm.w, full, x, w_row);  // columns past K read as zeros
+          if constexpr (SWIGLU) tma_load_2d(dst + kRawBytes / 2, &tm.w3, full, x, w_row);
+        }
+        __syncwarp();
+        if (++r == RS) r = 0, ph ^= 1;
       }
-      if (!ok) *s_abort = 1;
-      // every copy of this thread has landed before the CTA can leave
-      volatile int never = 0;
-      for (uint32_t j = issued > RS ? issued - RS : 0; j < issued; ++j)
-        mbar_wait(rfull0 + 8 * (j % RS), j / RS & 1, &never, a.timeout_ns);
     }
+    if (!ok && lane == 0) *s_abort = 1;
+    // every copy has landed before the CTA can leave
+    volatile int never = 0;
+    for (uint32_t j = issued > RS ? issued - RS : 0; j < issued; ++j)
+      mbar_wait(rfull0 + 8 * (j % RS), j / RS & 1, &never, a.timeout_ns);
+    __syncwarp();
   } else if (warp == 6) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ token rows
-      uint32_t it = 0, issued = 0;
-      for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-        const Item t = item_at(i);
-        const int boxes = (t.n + kTokBox - 1) / kTokBox;
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const uint32_t s = it % ST;
-          if (!mbar_wait(empty0 + 8 * s, (it / ST & 1) ^ 1, s_abort, a.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(full0 + 8 * s, boxes * kTokBoxBytes);
-          const uint32_t dst = smem_u32(s_b + s * F::kBBytes);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(dst + b * kTokBoxBytes, &tm_q, full0 + 8 * s, kb * BK, t.row + b * kTokBox);
-          issued = it + 1;
+    // -------------------------------------------------------------- token rows
+    const bool elected = elect_one();
+    const uint32_t b0 = smem_u32(s_b);
+    uint32_t it = 0, sb = 0;
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item t = item_at(i);
+      const int boxes = (t.n + kTokBox - 1) / kTokBox;
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        if (!__all_sync(~0u, slot_free(it, SB))) {
+          ok = false;
+          break;
         }
-      }
-      if (!ok) {
-        *s_abort = 1;
-        // stopped early: no MMA reads the stages any more, but the copies must land.  A full barrier may
-        // lack its converters' arrivals, so give the copies the bound of one wait instead.
-        volatile int never = 0;
-        const uint32_t j = issued ? issued - 1 : 0;
-        if (issued) mbar_wait(full0 + 8 * (j % ST), j / ST & 1, &never, a.timeout_ns / 8);
+        const uint32_t full = full0 + 8 * (it % kSync);
+        uint32_t dst = b0 + sb * F::kBBytes;
+        const int x = kb * BK;
+        if (elected) {
+          mbar_arrive_expect_tx(full, boxes * kTokBoxBytes);
+          int row = t.row;
+#pragma unroll
+          for (int b = kTokMaps - 1; b >= 0; --b)  // at most one copy of each box height
+            if (boxes >> b & 1) {
+              tma_load_2d(dst, &tm.q[b], full, x, row);
+              dst += kTokBoxBytes << b, row += kTokBox << b;
+            }
+        }
+        __syncwarp();
+        if (++sb == SB) sb = 0;
       }
     }
+    if (!ok) {
+      if (lane == 0) *s_abort = 1;
+      // stopped early: no MMA reads the slots any more, but the copies must land.  A full barrier may
+      // lack its converters' arrivals, so give the copies a fixed time, far above a copy's, instead.
+      volatile int never = 0;
+      if (it) mbar_wait(full0 + 8 * ((it - 1) % kSync), (it - 1) / kSync & 1, &never, a.timeout_ns / 8);
+    }
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      uint32_t it = 0, acc_it = 0;
-      for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++acc_it) {
-        const Item t = item_at(i);
-        const uint32_t acc = acc_it & 1;
-        if (!mbar_wait(tempty0 + 8 * acc, (acc_it >> 1 & 1) ^ 1, s_abort, a.timeout_ns)) {
+    // -------------------------------------------------------------- MMA issuer
+    const bool elected = elect_one();
+    const uint64_t da0 = sw128_desc(smem_u32(s_a)), db0 = sw128_desc(smem_u32(s_b));
+    uint32_t it = 0, acc_it = 0, sa = 0, sb = 0;
+    for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++acc_it) {
+      const Item t = item_at(i);
+      const uint32_t acc = acc_it & 1;
+      if (!__all_sync(~0u, mbar_wait(tempty0 + 8 * acc, (acc_it >> 1 & 1) ^ 1, s_abort, a.timeout_ns))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = tmem_base + acc * NT, idesc = idesc_f16((t.n + kTokBox - 1) / kTokBox * kTokBox);
+      uint32_t more = 0;  // the first MMA of a tile overwrites the accumulator
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        if (!__all_sync(~0u, mbar_wait(full0 + 8 * (it % kSync), it / kSync & 1, s_abort, a.timeout_ns))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem_base + acc * NT, idesc = idesc_f16((t.n + kTokBox - 1) / kTokBox * kTokBox);
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const uint32_t s = it % ST;
-          if (!mbar_wait(full0 + 8 * s, it / ST & 1, s_abort, a.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t pa = smem_u32(s_a + s * kABytes), pb = smem_u32(s_b + s * F::kBBytes);
+        const uint64_t da = da0 + sa * (kABytes >> 4), db = db0 + sb * (F::kBBytes >> 4);
+        if (elected) {
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16(d, sw128_desc(pa + 32 * k), sw128_desc(pb + 32 * k), idesc, kb != t.kb0 || k != 0);
-          umma_commit(empty0 + 8 * s);
+          for (int k = 0; k < 4; ++k) umma_bf16(d, da + 2 * k, db + 2 * k, idesc, k ? 1 : more);
+          umma_commit(done0 + 8 * (it % kSync));
         }
-        if (!ok) break;
-        umma_commit(tfull0 + 8 * acc);
+        __syncwarp();
+        more = 1;
+        if (++sa == SA) sa = 0;
+        if (++sb == SB) sb = 0;
       }
-      if (!ok) *s_abort = 1;
+      if (!ok) break;
+      if (elected) umma_commit(tfull0 + 8 * acc);
+      __syncwarp();
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+    if (elected) {
       umma_commit(drain);  // completes when every MMA of this thread has
       volatile int never = 0;
       mbar_wait(drain, 0, &never, a.timeout_ns);
     }
+    __syncwarp();
   } else if (warp >= kConvWarp0) {
     // -------------------------------------------------------------- converters
-    const int group = (warp - kConvWarp0) / kConvGroupWarps;
+    const uint32_t group = (warp - kConvWarp0) / kConvGroupWarps;
     const int tid = threadIdx.x - 32 * (kConvWarp0 + group * kConvGroupWarps);  // 0..127
-    uint32_t it = 0;
+    uint32_t it0 = 0, r = group % RS, ph = group / RS & 1, sa = group % SA;  // this group's next block
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item t = item_at(i);
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        if (it % kConvGroups != (uint32_t)group) continue;
-        const uint32_t r = it % RS, s = it % ST;
-        bool got = mbar_wait(rfull0 + 8 * r, it / RS & 1, s_abort, a.timeout_ns);
-        got = got && mbar_wait(empty0 + 8 * s, (it / ST & 1) ^ 1, s_abort, a.timeout_ns);
+      const uint32_t n = t.kb1 - t.kb0;
+      for (uint32_t j = (group - it0) % kConvGroups; j < n; j += kConvGroups) {
+        const uint32_t it = it0 + j;
+        bool got = mbar_wait(rfull0 + 8 * r, ph, s_abort, a.timeout_ns);
+        uint4 v[4];
+        const uint4* src = reinterpret_cast<const uint4*>(s_raw + r * kRawBytes);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = src[tid + 128 * c];
+        got = got && slot_free(it, SA);
         if (!__all_sync(~0u, got)) {
           ok = false;
           break;
         }
-        const uint4* src = reinterpret_cast<const uint4*>(s_raw + r * kRawBytes);
-        uint8_t* dst = s_a + s * kABytes;
-        uint4 v[4];
+        __syncwarp();  // every lane has its bytes
+        if (lane == 0) mbar_arrive(rempty0 + 8 * r);
+        uint8_t* dst = s_a + sa * kABytes;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = src[tid + 128 * j];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // 16 bytes of raw row `row`: columns 16 c .. 16 c + 15, swizzled chunks 2 c and 2 c + 1
-          const int row = (tid >> 2) + 32 * j, c = tid & 3;
+        for (int c4 = 0; c4 < 4; ++c4) {
+          // 16 bytes of raw row `row`: columns 16 c .. 16 c + 15, swizzled chunks 2 c and 2 c + 1.  Eight
+          // neighbouring threads read 128 bytes in a row and write eight different 16-byte columns (two
+          // rows of opposite parity): no bank conflicts.
+          const int row = (tid >> 2) + 32 * c4, c = tid & 3;
           // gate rows 0..63 and up rows 64..127 alternate in runs of 16 lanes
           const int m = SWIGLU ? (row & 48) * 2 + (row & 15) + (row >> 6) * 16 : row;
           uint8_t* line = dst + m * 128;
-          *reinterpret_cast<uint4*>(line + (((2 * c) ^ (m & 7)) << 4)) = bytes_to_half8(v[j].x, v[j].y);
-          *reinterpret_cast<uint4*>(line + (((2 * c + 1) ^ (m & 7)) << 4)) = bytes_to_half8(v[j].z, v[j].w);
+          *reinterpret_cast<uint4*>(line + (((2 * c) ^ (m & 7)) << 4)) = bytes_to_half8(v[c4].x, v[c4].y);
+          *reinterpret_cast<uint4*>(line + (((2 * c + 1) ^ (m & 7)) << 4)) = bytes_to_half8(v[c4].z, v[c4].w);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(full0 + 8 * s);
-          mbar_arrive(rempty0 + 8 * r);
-        }
+        if (lane == 0) mbar_arrive(full0 + 8 * (it % kSync));
+        r += kConvGroups;
+        if (r >= RS) r -= RS, ph ^= 1;
+        sa += kConvGroups;
+        if (sa >= SA) sa -= SA;
       }
+      it0 += n;
     }
     if (!ok && lane == 0) *s_abort = 1;
   } else if (warp >= 2 && warp < 6) {
@@ -372,30 +426,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool in = n < a.N;
       float ws = 0.f;
       if (in) ws = (SWIGLU && lane >= 16 ? a.w3_scale : a.w_scale)[(int64_t)t.e * a.N + n];
-      // columns c0 .. c0 + 31 of the tile, summed over K, to y
+      // columns c0 .. c0 + 31 of the tile, summed over K, to y; eight at a time, none past the tile's rows
       auto finish = [&](const float (&v)[32], int c0) {
         const float sx = c0 + lane < t.n ? a.scale[t.row + c0 + lane] : 0.f;
-        if constexpr (SWIGLU) {
+        O* out = static_cast<O*>(a.y) + (int64_t)(t.row + c0 + (SWIGLU ? lane >> 4 : 0)) * a.N + n;
+        const int left = in ? t.n - c0 - (SWIGLU ? lane >> 4 : 0) : 0;  // rows from this lane's first one on
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            // lanes 0..15 take column c, the others c + 1: one exchange gives both their second value
-            const float s0 = __shfl_sync(~0u, sx, c), s1 = __shfl_sync(~0u, sx, c + 1);
-            const float v0 = v[c] * ws * s0, v1 = v[c + 1] * ws * s1;
-            const float other = __shfl_xor_sync(~0u, lane < 16 ? v1 : v0, 16);
-            const float g = lane < 16 ? v0 : other, u = lane < 16 ? other : v1;
-            const int col = c0 + c + (lane >> 4);
-            const float h = g / (1.f + expf(-g)) * u;
-            if (in && col < t.n) static_cast<O*>(a.y)[(int64_t)(t.row + col) * a.N + n] = from_float<O>(h);
-          }
-        } else {
+        for (int c8 = 0; c8 < 32; c8 += 8) {
+          if (c0 + c8 >= t.n) break;
+          float h[8];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float h = v[c] * ws * __shfl_sync(~0u, sx, c);
-            if (in && c0 + c < t.n) static_cast<O*>(a.y)[(int64_t)(t.row + c0 + c) * a.N + n] = from_float<O>(h);
+          for (int c = 0; c < 8; ++c) h[c] = v[c8 + c] * ws * __shfl_sync(~0u, sx, c8 + c);
+          if constexpr (SWIGLU) {
+            // lanes 0..15 take the even columns, the others the odd ones: one exchange gives both their
+            // second value
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+              const float other = __shfl_xor_sync(~0u, lane < 16 ? h[c + 1] : h[c], 16);
+              const float g = lane < 16 ? h[c] : other, u = lane < 16 ? other : h[c + 1];
+              if (c8 + c < left) out[(int64_t)(c8 + c) * a.N] = from_float<O>(silu_fast(g) * u);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if (c8 + c < left) out[(int64_t)(c8 + c) * a.N] = from_float<O>(h[c]);
           }
         }
       };
-      float* part = a.partial + i * (kInt8NarrowRows * 128) + q * 32 + lane;
+      float* part = a.partial + i * (NT * 128) + q * 32 + lane;
 #pragma unroll 1
       for (int c0 = 0; c0 < t.n; c0 += 32) {
         uint32_t raw[32];
@@ -403,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float v[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(raw[c]);
-        if (NT == kInt8WideRows || parts == 1) {
+        if (parts == 1) {
           finish(v, c0);
         } else {
 #pragma unroll
@@ -414,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty0 + 8 * acc);
-      if (NT != kInt8WideRows && parts > 1) {
+      if (parts > 1) {
         __threadfence();
         __syncwarp();
         if (lane == 0) mbar_arrive(joined);
@@ -434,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (*s_last) {
           __threadfence();
-          const float* all = a.partial + (int64_t)t.tile * parts * (kInt8NarrowRows * 128) + q * 32 + lane;
+          const float* all = a.partial + (int64_t)t.tile * parts * (NT * 128) + q * 32 + lane;
 #pragma unroll 1
           for (int c0 = 0; c0 < t.n; c0 += 32) {
             float v[32];
@@ -443,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int p = 0; p < parts; ++p)
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (c0 + c < t.n) v[c] += __ldcg(all + (int64_t)p * (kInt8NarrowRows * 128) + (c0 + c) * 128);
+                if (c0 + c < t.n) v[c] += __ldcg(all + (int64_t)p * (NT * 128) + (c0 + c) * 128);
             finish(v, c0);
           }
         }
@@ -466,7 +524,7 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64
 }
 
 template <int NT, bool SWIGLU, typename O>
-cudaError_t launch(const CUtensorMap* maps, const Int8Args& a, int device, int grid, cudaStream_t s) {
+cudaError_t launch(const Int8Maps& maps, const Int8Args& a, int device, int grid, cudaStream_t s) {
   static std::mutex mu;
   static bool ready[kOpsMaxDevices] = {};
   {
@@ -478,39 +536,36 @@ cudaError_t launch(const CUtensorMap* maps, const Int8Args& a, int device, int g
       ready[device] = true;
     }
   }
-  return pdl_launch(int8_mma_kernel<NT, SWIGLU, O>, dim3(grid), dim3(kThreads), Form<NT>::kSmem, s, maps[0], maps[1],
-                    maps[2], a);
+  return pdl_launch(int8_mma_kernel<NT, SWIGLU, O>, dim3(grid), dim3(kThreads), Form<NT>::kSmem, s, maps, a);
 }
 
 }  // namespace
 
-bool int8_tensor_maps(const void* q, int R, const int8_t* w, const int8_t* w3, int E, int N, int K, CUtensorMap* maps) {
-  const uint32_t box = w3 ? 64 : 128;
-  if (!make_map(&maps[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, K, R, 2, kTokBox, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-    return false;
-  if (!make_map(&maps[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, w, K, (uint64_t)E * N, 1, box, CU_TENSOR_MAP_SWIZZLE_NONE,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-    return false;
-  return make_map(&maps[2], CU_TENSOR_MAP_DATA_TYPE_UINT8, w3 ? w3 : w, K, (uint64_t)E * N, 1, box,
-                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+bool int8_tensor_maps(const void* q, int R, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps) {
+  for (int i = 0; i < kTokMaps; ++i)
+    if (!make_map(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, K, R, 2, kTokBox << i, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+      return false;
+  for (int i = 0; i < 2; ++i)
+    if (!make_map(i ? &maps->w3 : &maps->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, i && w3 ? w3 : w, K, (uint64_t)E * N, 1,
+                  w3 ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+      return false;
+  return true;
 }
 
-cudaError_t launch_int8_mma(const CUtensorMap* maps, bool wide, bool swiglu, bool bf16_out, const Int8Args& a, int device,
+cudaError_t launch_int8_mma(const Int8Maps& maps, int tile_rows, bool swiglu, bool bf16_out, const Int8Args& a, int device,
                             int sms, cudaStream_t s) {
-  using B = __nv_bfloat16;
-  if (wide) {
+  auto with = [&](auto nt) {
+    constexpr int NT = decltype(nt)::value;
+    using B = __nv_bfloat16;
     if (swiglu)
-      return bf16_out ? launch<kInt8WideRows, true, B>(maps, a, device, sms, s)
-                      : launch<kInt8WideRows, true, float>(maps, a, device, sms, s);
-    return bf16_out ? launch<kInt8WideRows, false, B>(maps, a, device, sms, s)
-                    : launch<kInt8WideRows, false, float>(maps, a, device, sms, s);
-  }
-  if (swiglu)
-    return bf16_out ? launch<kInt8NarrowRows, true, B>(maps, a, device, sms, s)
-                    : launch<kInt8NarrowRows, true, float>(maps, a, device, sms, s);
-  return bf16_out ? launch<kInt8NarrowRows, false, B>(maps, a, device, sms, s)
-                  : launch<kInt8NarrowRows, false, float>(maps, a, device, sms, s);
+      return bf16_out ? launch<NT, true, B>(maps, a, device, sms, s) : launch<NT, true, float>(maps, a, device, sms, s);
+    return bf16_out ? launch<NT, false, B>(maps, a, device, sms, s) : launch<NT, false, float>(maps, a, device, sms, s);
+  };
+  if (tile_rows == 256) return with(std::integral_constant<int, 256>{});
+  if (tile_rows == 128) return with(std::integral_constant<int, 128>{});
+  if (tile_rows == 64) return with(std::integral_constant<int, 64>{});
+  return with(std::integral_constant<int, 32>{});
 }
 
 }  // namespace colibri
