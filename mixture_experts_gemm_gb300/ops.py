@@ -17,11 +17,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
+import threading
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import (DTYPE_BF16, DTYPE_F32, ColibriError, Int8Config, NormConfig, NormVectors, RouteConfig, _check, lib)
+from . import DTYPE_BF16, DTYPE_F32, ColibriError, Int8Config, NormConfig, RouteConfig, _check, lib
 
 __all__ = ["block_norm", "block_norm_backward", "pre_norm", "route", "route_backward", "Routing", "int8_quantize",
            "int8_experts", "combine", "ColibriError"]
@@ -45,27 +47,31 @@ def _kind(table, key, name: str) -> int:
         raise ValueError(f"{name}: one of {', '.join(table)}, not {key!r}") from None
 
 
-def _matrix(t, name: str, rows: Optional[int] = None, cols: Optional[int] = None, dtype=None):
-    """(address, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{'n' if rows is None else rows}, "
-                         f"{'d' if cols is None else cols}]")
+def _matrix(t, name: str, T: int, d: int, dtype=None):
+    """(address, row stride) of a [T, d] CUDA tensor whose rows are contiguous."""
+    if t.shape != (T, d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, d)}")
     if not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is needed")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: {dtype} expected, not {t.dtype}")
-    n, d = t.shape
     s0, s1 = t.stride()
-    if d > 1 and s1 != 1:
+    if s1 != 1 and d > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), (s0 if n > 1 else max(d, 1))
+    return t.data_ptr(), (s0 if T > 1 else max(d, 1))
+
+
+def _shape(t, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: two dimensions expected, not {tuple(t.shape)}")
+    return t.shape
 
 
 def _vector(t, name: str, shape, dtype):
     """Address of a contiguous CUDA tensor of the given shape and type, or None for None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous CUDA tensor {tuple(shape)} of {dtype} expected, not "
                          f"{tuple(t.shape)} of {t.dtype}")
     return t.data_ptr()
@@ -104,6 +110,31 @@ class _on:
             self.guard.__exit__(*exc)
 
 
+def _run(f, t, stream, *args):
+    """f(stream handle, *args) on t's device and the given or current stream."""
+    if stream is None:
+        dev = t.get_device()
+        if dev == torch._C._cuda_getDevice():  # the usual case, without the context managers' microseconds
+            return f(torch._C._cuda_getCurrentRawStream(dev), *args)
+    with _on(t, stream) as s:
+        return f(s, *args)
+
+
+class _Scratch(threading.local):
+    """Arguments that the library reads during a call, a set for each thread: a size and two structs of five
+    pointers (colibri_moe_norm_params_t, colibri_moe_norm_grads_t)."""
+
+    def __init__(self):
+        self.size = ctypes.c_size_t()
+        self.p_size = ctypes.addressof(self.size)
+        self.vectors, self.grads = (ctypes.c_char * 40)(), (ctypes.c_char * 40)()
+        self.p_vectors, self.p_grads = ctypes.addressof(self.vectors), ctypes.addressof(self.grads)
+
+
+_scratch = _Scratch()
+_five = struct.Struct("5P")
+
+
 def _workspace(n: int, device):
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
@@ -115,31 +146,36 @@ def _at(t):
 # ------------------------------------------------------------------------------------------- norms
 @functools.lru_cache(maxsize=256)
 def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gate, residual_scale, block_scale, eps):
-    c = NormConfig(d, dtype, block_dtype, param_dtype, _kind(_NORMS, after, "after"), _kind(_NORMS, before, "before"),
-                   rows_per_gate, residual_scale, block_scale, eps)
+    c = NormConfig(d, _dtype(dtype, "x"), _dtype(block_dtype, "y"), _dtype(param_dtype, "the parameters"),
+                   _kind(_NORMS, after, "after"), _kind(_NORMS, before, "before"), rows_per_gate, float(residual_scale),
+                   float(block_scale), float(eps))
     return c, ctypes.addressof(c)
 
 
 def _norm_setup(T, d, dtype, block_dtype, after, after_weight, after_bias, before, before_weight, before_bias, gate,
                 rows_per_gate, residual_scale, block_scale, eps):
-    params = [p for p in (after_weight, after_bias, before_weight, before_bias, gate) if p is not None]
-    pt = params[0].dtype if params else torch.float32
-    rpg, n_gates = 0, 0
+    """(config's address, gate rows); the parameters' addresses go to this thread's scratch."""
+    pt = torch.float32
+    for p in (after_weight, before_weight, gate):
+        if p is not None:
+            pt = p.dtype
+            break
+    rpg = n_gates = 0
+    pg = None
     if gate is not None:
         if gate.dim() == 1:
             gate = gate.unsqueeze(0)
         rpg = max(T, 1) if rows_per_gate is None else int(rows_per_gate)
         if rpg <= 0:
             raise ValueError("rows_per_gate must be positive")
-        n_gates = -(-T // rpg)
-        if T == 0:
-            n_gates = gate.shape[0]
-    v = NormVectors(_vector(after_weight, "after_weight", (d,), pt), _vector(after_bias, "after_bias", (d,), pt),
-                    _vector(before_weight, "before_weight", (d,), pt), _vector(before_bias, "before_bias", (d,), pt),
-                    _vector(gate, "gate", (n_gates, d), pt))
-    c = _norm_config(d, _dtype(dtype, "x"), _dtype(block_dtype, "y"), _dtype(pt, "the parameters"), after, before, rpg,
-                     float(residual_scale), float(block_scale), float(eps))
-    return c, v, n_gates
+        n_gates = -(-T // rpg) if T else gate.shape[0]
+        pg = _vector(gate, "gate", (n_gates, d), pt)
+    one = (d,)
+    _five.pack_into(_scratch.vectors, 0, _vector(after_weight, "after_weight", one, pt) or 0,
+                    _vector(after_bias, "after_bias", one, pt) or 0,
+                    _vector(before_weight, "before_weight", one, pt) or 0,
+                    _vector(before_bias, "before_bias", one, pt) or 0, pg or 0)
+    return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, residual_scale, block_scale, eps)[1], n_gates
 
 
 def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, before="none", before_weight=None,
@@ -155,17 +191,20 @@ def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, b
     fp32 beside a bf16 stream); after and before are "none", "rms" or "layer"; gate is [d] (every token)
     or [ceil(T / rows_per_gate), d].  Returns (x1, p); p is None without a next norm, and without y
     x1 is None (a norm before a block alone)."""
-    T, d = x.shape if x.dim() == 2 else (None, None)
-    px, ldx = _matrix(x, "x")
+    T, d = _shape(x, "x")
+    dt = x.dtype
+    px, ldx = _matrix(x, "x", T, d)
     py, ldy = _matrix(y, "y", T, d) if y is not None else (None, 0)
-    (_, c), v, _ = _norm_setup(T, d, x.dtype, y.dtype if y is not None else x.dtype, after, after_weight, after_bias,
-                               before, before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
-    with _on(x, stream) as s:
-        x1 = torch.empty((T, d), dtype=x.dtype, device=x.device) if y is not None else None
-        p = torch.empty((T, d), dtype=x.dtype, device=x.device) if before != "none" else None
-        _check(lib().colibri_moe_block_norm(c, ctypes.addressof(v), px, ldx, py, ldy, T, _at(x1), _at(p), s),
+    c, _ = _norm_setup(T, d, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
+                       before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
+
+    def call(s):
+        x1 = torch.empty((T, d), dtype=dt, device=x.device) if y is not None else None
+        p = torch.empty((T, d), dtype=dt, device=x.device) if before != "none" else None
+        _check(lib().colibri_moe_block_norm(c, _scratch.p_vectors, px, ldx, py, ldy, T, _at(x1), _at(p), s),
                "colibri_moe_block_norm")
-    return x1, p
+        return x1, p
+    return _run(call, x, stream)
 
 
 def pre_norm(x, weight, bias=None, *, kind="rms", eps=1e-6, stream=None):
@@ -182,34 +221,37 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
     ref = d_x1 if d_x1 is not None else d_p
     if ref is None:
         raise ValueError("one of d_x1 and d_p is needed")
-    T, d = ref.shape if ref.dim() == 2 else (None, None)
+    T, d = _shape(ref, "d_x1" if d_x1 is not None else "d_p")
     dt = ref.dtype
     p1, ld1 = _matrix(d_x1, "d_x1", T, d, dt) if d_x1 is not None else (None, 0)
     pp, ldp = _matrix(d_p, "d_p", T, d, dt) if d_p is not None else (None, 0)
     px, ldx = _matrix(x1, "x1", T, d, dt) if x1 is not None else (None, 0)
     py, ldy = _matrix(y, "y", T, d) if y is not None else (None, 0)
-    (cfg, c), v, n_gates = _norm_setup(T, d, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
-                                       before, before_weight, before_bias, gate, rows_per_gate, residual_scale,
-                                       block_scale, eps)
-    with _on(ref, stream) as s:
-        new = lambda *shape: torch.empty(shape, dtype=torch.float32, device=ref.device)  # noqa: E731
-        out = dict(d_x=torch.empty((T, d), dtype=dt, device=ref.device))
+    c, n_gates = _norm_setup(T, d, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
+                             before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
+
+    def call(s):
+        dev = ref.device
+        out = dict(d_x=torch.empty((T, d), dtype=dt, device=dev))
         if y is not None:
-            out["d_y"] = torch.empty((T, d), dtype=y.dtype, device=ref.device)
+            out["d_y"] = torch.empty((T, d), dtype=y.dtype, device=dev)
         for name, param in (("d_wa", after_weight), ("d_ba", after_bias), ("d_wb", before_weight),
                             ("d_bb", before_bias)):
             if param is not None:
-                out[name] = new(d)
+                out[name] = torch.empty(d, dtype=torch.float32, device=dev)
         if gate is not None:
-            out["d_g"] = new(n_gates, d) if T else torch.zeros((n_gates, d), dtype=torch.float32, device=ref.device)
-        g = NormVectors(*[_at(out.get(n)) for n in ("d_wa", "d_ba", "d_wb", "d_bb", "d_g")])
-        n = ctypes.c_size_t()
-        _check(lib().colibri_moe_block_norm_backward_workspace(c, T, ctypes.addressof(n)), "colibri_moe_block_norm_backward")
-        ws = _workspace(n.value, ref.device)
-        _check(lib().colibri_moe_block_norm_backward(c, ctypes.addressof(v), p1, ld1, pp, ldp, px, ldx, py, ldy, T,
-                                                     _at(out["d_x"]), _at(out.get("d_y")), ctypes.addressof(g),
-                                                     _at(ws), n.value, s), "colibri_moe_block_norm_backward")
-    return out
+            out["d_g"] = (torch.empty if T else torch.zeros)((n_gates, d), dtype=torch.float32, device=dev)
+        _five.pack_into(_scratch.grads, 0, *[out[n].data_ptr() if n in out else 0
+                                             for n in ("d_wa", "d_ba", "d_wb", "d_bb", "d_g")])
+        L = lib()
+        _check(L.colibri_moe_block_norm_backward_workspace(c, T, _scratch.p_size), "colibri_moe_block_norm_backward")
+        n = _scratch.size.value
+        ws = _workspace(n, dev)
+        _check(L.colibri_moe_block_norm_backward(c, _scratch.p_vectors, p1, ld1, pp, ldp, px, ldx, py, ldy, T,
+                                                 _at(out["d_x"]), _at(out.get("d_y")), _scratch.p_grads, _at(ws), n, s),
+               "colibri_moe_block_norm_backward")
+        return out
+    return _run(call, ref, stream)
 
 
 # ----------------------------------------------------------------------------------------- routing
@@ -225,8 +267,8 @@ class Routing(NamedTuple):
 
 @functools.lru_cache(maxsize=256)
 def _route_config(E, k, score, groups, top_groups, group_top, renormalize, dtype, scale):
-    c = RouteConfig(E, k, _kind(_SCORES, score, "score"), groups, top_groups, group_top, int(bool(renormalize)), dtype,
-                    scale)
+    c = RouteConfig(E, k, _kind(_SCORES, score, "score"), groups, top_groups, group_top, int(bool(renormalize)),
+                    _dtype(dtype, "logits"), float(scale))
     return c, ctypes.addressof(c)
 
 
@@ -239,48 +281,52 @@ def route(logits, top_k: int, *, score="softmax", bias=None, groups=1, top_group
     being worth the sum of its group_top (1 or 2) largest biased scores.  Gates are the chosen scores
     without the bias, divided by their sum if renormalize, times scale.  Ties go to the lowest index; an
     expert with a logit or bias of -inf or NaN is never chosen."""
-    pl, ld = _matrix(logits, "logits")
-    T, E = logits.shape
+    T, E = _shape(logits, "logits")
+    pl, ld = _matrix(logits, "logits", T, E)
     pb = _vector(bias, "bias", (E,), torch.float32)
-    _, c = _route_config(E, int(top_k), score, int(groups), int(top_groups), int(group_top), renormalize,
-                         _dtype(logits.dtype, "logits"), float(scale))
-    with _on(logits, stream) as s:
-        n = ctypes.c_size_t()
-        _check(lib().colibri_moe_route_experts_workspace(c, T, ctypes.addressof(n)), "colibri_moe_route_experts")
-        dev, i32 = logits.device, torch.int32
-        k = int(top_k)
-        r = Routing(torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
-                    torch.empty(E, dtype=i32, device=dev), torch.empty(E + 1, dtype=i32, device=dev),
-                    torch.empty((T, k), dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev))
-        ws = _workspace(n.value, dev)
-        _check(lib().colibri_moe_route_experts(c, pl, ld, pb, T, r.idx.data_ptr(), r.gate.data_ptr(),
-                                               r.counts.data_ptr(), r.offsets.data_ptr(), r.row_of.data_ptr(),
-                                               r.token_of_row.data_ptr(), _at(ws), n.value, s),
-               "colibri_moe_route_experts")
-    return r
+    k = top_k
+    c = _route_config(E, k, score, groups, top_groups, group_top, renormalize, logits.dtype, scale)[1]
+
+    def call(s):
+        L, dev, n = lib(), logits.device, T * k
+        _check(L.colibri_moe_route_experts_workspace(c, T, _scratch.p_size), "colibri_moe_route_experts")
+        size = _scratch.size.value
+        # one allocation for the whole numbers and the workspace behind them
+        at = (3 * n + 2 * E + 1 + 63) // 64 * 64
+        ints = torch.empty(at + size // 4, dtype=torch.int32, device=dev)
+        p = ints.data_ptr()
+        gate = torch.empty((T, k), dtype=torch.float32, device=dev)
+        pair, row = (T, k), (k, 1)
+        r = Routing(ints.as_strided(pair, row, 0), gate, ints.as_strided((E,), (1,), 3 * n),
+                    ints.as_strided((E + 1,), (1,), 3 * n + E), ints.as_strided(pair, row, n),
+                    ints.as_strided((n,), (1,), 2 * n))
+        _check(L.colibri_moe_route_experts(c, pl, ld, pb, T, p, gate.data_ptr(), p + 12 * n, p + 12 * n + 4 * E, p + 4 * n,
+                                           p + 8 * n, p + 4 * at if size else None, size, s), "colibri_moe_route_experts")
+        return r
+    return _run(call, logits, stream)
 
 
 def route_backward(logits, idx, d_gate, *, score="softmax", renormalize=True, scale=1.0, stream=None):
     """d_logits [T, E] (the logits' type) from the gradient of the gates, the choice idx [T, k] held constant."""
-    pl, ld = _matrix(logits, "logits")
-    T, E = logits.shape
-    if idx.dim() != 2:
-        raise ValueError("idx: [T, k] expected")
-    k = idx.shape[1]
+    T, E = _shape(logits, "logits")
+    pl, ld = _matrix(logits, "logits", T, E)
+    k = _shape(idx, "idx")[1]
     pi = _vector(idx, "idx", (T, k), torch.int32)
     pg = _vector(d_gate, "d_gate", (T, k), torch.float32)
-    _, c = _route_config(E, k, score, 1, 1, 1, renormalize, _dtype(logits.dtype, "logits"), float(scale))
-    with _on(logits, stream) as s:
+    c = _route_config(E, k, score, 1, 1, 1, renormalize, logits.dtype, scale)[1]
+
+    def call(s):
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
         _check(lib().colibri_moe_route_experts_backward(c, pl, ld, pi, pg, T, out.data_ptr(), E, s),
                "colibri_moe_route_experts_backward")
-    return out
+        return out
+    return _run(call, logits, stream)
 
 
 # ----------------------------------------------------------------------------------- 8-bit experts
 @functools.lru_cache(maxsize=256)
 def _int8_config(K, N, E, dtype, out_dtype):
-    c = Int8Config(K, N, E, dtype, out_dtype)
+    c = Int8Config(K, N, E, _dtype(dtype, "x"), _dtype(out_dtype, "out_dtype"))
     return c, ctypes.addressof(c)
 
 
@@ -289,14 +335,17 @@ def int8_quantize(x, stream=None):
     activations, or the output channels of weights [E, N, K] once ahead of time."""
     K = x.shape[-1]
     flat = x.reshape(-1, K)
-    px, ldx = _matrix(flat, "x")
-    _, c = _int8_config(K, 1, 1, _dtype(x.dtype, "x"), DTYPE_F32)
-    with _on(x, stream) as s:
+    n = flat.shape[0]
+    px, ldx = _matrix(flat, "x", n, K)
+    c = _int8_config(K, 1, 1, x.dtype, torch.float32)[1]
+
+    def call(s):
         q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(lib().colibri_moe_int8_quantize(c, px, ldx, flat.shape[0], q.data_ptr(), scale.data_ptr(), s),
+        _check(lib().colibri_moe_int8_quantize(c, px, ldx, n, q.data_ptr(), scale.data_ptr(), s),
                "colibri_moe_int8_quantize")
-    return q, scale
+        return q, scale
+    return _run(call, x, stream)
 
 
 def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, out_dtype=None, stream=None):
@@ -307,47 +356,49 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
     (``Routing.offsets`` and ``.token_of_row``), or None: row r is x[r].  With w3 and w3_scale (same
     shapes) y = silu(v) * v3, the gated pair of projections in one pass.  Rows from offsets[E] on are
     not written.  out_dtype: fp32 or bf16, default x's."""
-    px, ldx = _matrix(x, "x")
-    if w.dim() != 3 or w.shape[2] != x.shape[1]:
-        raise ValueError(f"w: [E, N, {x.shape[1]}] expected, not {tuple(w.shape)}")
-    E, N, K = w.shape
-    n = x.shape[0]
-    i32 = torch.int32
-    pw = _vector(w, "w", (E, N, K), torch.int8)
-    ps = _vector(w_scale, "w_scale", (E, N), torch.float32)
+    n, K = _shape(x, "x")
+    px, ldx = _matrix(x, "x", n, K)
+    if w.dim() != 3:
+        raise ValueError(f"w: [E, N, {K}] expected, not {tuple(w.shape)}")
+    E, N, _ = w.shape
+    i32, weights, scales = torch.int32, (E, N, K), (E, N)
+    pw = _vector(w, "w", weights, torch.int8)
+    ps = _vector(w_scale, "w_scale", scales, torch.float32)
     if (w3 is None) != (w3_scale is None):
         raise ValueError("w3 and w3_scale go together")
-    pw3 = _vector(w3, "w3", (E, N, K), torch.int8)
-    ps3 = _vector(w3_scale, "w3_scale", (E, N), torch.float32)
+    pw3 = _vector(w3, "w3", weights, torch.int8)
+    ps3 = _vector(w3_scale, "w3_scale", scales, torch.float32)
     po = _vector(offsets, "offsets", (E + 1,), i32)
     R = n if rows is None else rows.numel()
     pr = _vector(rows, "rows", (R,), i32)
     out_dtype = x.dtype if out_dtype is None else out_dtype
-    _, c = _int8_config(K, N, E, _dtype(x.dtype, "x"), _dtype(out_dtype, "out_dtype"))
-    with _on(x, stream) as s:
-        size = ctypes.c_size_t()
-        _check(lib().colibri_moe_int8_experts_workspace(c, n, R, ctypes.addressof(size)), "colibri_moe_int8_experts")
-        ws = _workspace(size.value, x.device)
+    c = _int8_config(K, N, E, x.dtype, out_dtype)[1]
+
+    def call(s):
+        L = lib()
+        _check(L.colibri_moe_int8_experts_workspace(c, n, R, _scratch.p_size), "colibri_moe_int8_experts")
+        size = _scratch.size.value
+        ws = _workspace(size, x.device)
         y = torch.empty((R, N), dtype=out_dtype, device=x.device)
-        _check(lib().colibri_moe_int8_experts(c, px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws),
-                                              size.value, s), "colibri_moe_int8_experts")
-    return y
+        _check(L.colibri_moe_int8_experts(c, px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws), size, s),
+               "colibri_moe_int8_experts")
+        return y
+    return _run(call, x, stream)
 
 
 def combine(y, row_of, gate, *, out_dtype=None, stream=None):
     """out[t] = sum over a token's slots of gate * y[row_of], in slot order in fp32; rows of -1 are left out."""
-    py, _ = _matrix(y, "y")
-    if not y.is_contiguous():
-        raise ValueError("y: a contiguous tensor expected")
-    if row_of.dim() != 2:
-        raise ValueError("row_of: [T, k] expected")
-    T, k = row_of.shape
+    R, d = _shape(y, "y")
+    py = _vector(y, "y", (R, d), y.dtype)
+    T, k = _shape(row_of, "row_of")
     pr = _vector(row_of, "row_of", (T, k), torch.int32)
     pg = _vector(gate, "gate", (T, k), torch.float32)
     out_dtype = y.dtype if out_dtype is None else out_dtype
-    with _on(y, stream) as s:
-        out = torch.empty((T, y.shape[1]), dtype=out_dtype, device=y.device)
-        _check(lib().colibri_moe_combine_rows(py, _dtype(y.dtype, "y"), y.shape[0], pr, pg, T, k, y.shape[1],
-                                              out.data_ptr(), _dtype(out_dtype, "out_dtype"), s),
+    types = _dtype(y.dtype, "y"), _dtype(out_dtype, "out_dtype")
+
+    def call(s):
+        out = torch.empty((T, d), dtype=out_dtype, device=y.device)
+        _check(lib().colibri_moe_combine_rows(py, types[0], R, pr, pg, T, k, d, out.data_ptr(), types[1], s),
                "colibri_moe_combine_rows")
-    return out
+        return out
+    return _run(call, y, stream)
