@@ -318,6 +318,9 @@ COLIBRI_API int colibri_moe_ep_combine(colibri_moe_t* ctx, const float* y_back, 
  * Errors: COLIBRI_ERR_INVALID_ARG (NULL or host pointers, sizes or strides out of range, overlapping
  * inputs and outputs, a workspace too small), COLIBRI_ERR_UNSUPPORTED (sizes this build does not
  * run, as listed), COLIBRI_ERR_CUDA.  Nothing is enqueued when a call fails its checks.
+ * trusted_pointers (in each config; 0 or 1): with 1 the caller vouches that every pointer is device
+ * memory of the current device, and the call does not ask the driver, which costs about a microsecond
+ * of host time a pointer -- as much as the launches of a small call.
  * ====================================================================================== */
 
 /* ---- norms before and after a block, with its gate and the residual scale ----
@@ -338,6 +341,7 @@ typedef struct {
   int32_t after, before;  /* COLIBRI_NORM_*                                                        */
   int64_t rows_per_gate;  /* > 0 with a gate: row t uses gate row t / rows_per_gate                */
   float residual_scale, block_scale, eps;
+  int32_t trusted_pointers; /* see above                                                            */
 } colibri_moe_norm_config_t;
 
 /* [d_model] vectors of param_dtype, gate [ceil(T / rows_per_gate), d_model]; a weight is required
@@ -398,6 +402,7 @@ typedef struct {
   int32_t renormalize;  /* 0 or 1                                               */
   int32_t logits_dtype; /* COLIBRI_DTYPE_*                                      */
   float scale;
+  int32_t trusted_pointers; /* see above                                    */
 } colibri_moe_route_config_t;
 
 COLIBRI_API int colibri_moe_route_experts_workspace(const colibri_moe_route_config_t* cfg, int32_t T, size_t* bytes);
@@ -427,6 +432,7 @@ typedef struct {
   int32_t num_experts;   /* E, 1..512 (1: a plain linear layer)                                     */
   int32_t dtype;         /* COLIBRI_DTYPE_* of x                                                    */
   int32_t out_dtype;     /* COLIBRI_DTYPE_* of y                                                    */
+  int32_t trusted_pointers; /* see above                                                           */
 } colibri_moe_int8_config_t;
 
 /* q [n, K] int8 and scale [n] fp32 of x [n, K] (row stride ldx): activations, or weights once ahead of

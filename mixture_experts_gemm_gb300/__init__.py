@@ -62,7 +62,7 @@ class NormConfig(ctypes.Structure):
     _fields_ = [("d_model", ctypes.c_int32), ("dtype", ctypes.c_int32), ("block_dtype", ctypes.c_int32),
                 ("param_dtype", ctypes.c_int32), ("after", ctypes.c_int32), ("before", ctypes.c_int32),
                 ("rows_per_gate", ctypes.c_int64), ("residual_scale", ctypes.c_float),
-                ("block_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+                ("block_scale", ctypes.c_float), ("eps", ctypes.c_float), ("trusted_pointers", ctypes.c_int32)]
 
 
 class NormVectors(ctypes.Structure):
@@ -74,12 +74,13 @@ class NormVectors(ctypes.Structure):
 class RouteConfig(ctypes.Structure):
     _fields_ = [("num_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
                 ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
-                ("renormalize", ctypes.c_int32), ("logits_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+                ("renormalize", ctypes.c_int32), ("logits_dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("trusted_pointers", ctypes.c_int32)]
 
 
 class Int8Config(ctypes.Structure):
     _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("num_experts", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("trusted_pointers", ctypes.c_int32)]
 
 
 class Weights(ctypes.Structure):

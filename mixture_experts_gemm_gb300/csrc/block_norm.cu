@@ -637,7 +637,7 @@ bool norm_kind(int32_t k) { return k == COLIBRI_NORM_NONE || k == COLIBRI_NORM_R
 int check_norm_config(const colibri_moe_norm_config_t* c, const colibri_moe_norm_params_t* w, bool block, int32_t T) {
   if (!c || !w || T < 0) return COLIBRI_ERR_INVALID_ARG;
   if (c->d_model <= 0 || !ops_dtype(c->dtype) || !ops_dtype(c->block_dtype) || !ops_dtype(c->param_dtype) ||
-      !norm_kind(c->after) || !norm_kind(c->before) || !(c->eps >= 0.f))
+      !norm_kind(c->after) || !norm_kind(c->before) || !(c->eps >= 0.f) || (c->trusted_pointers & ~1))
     return COLIBRI_ERR_INVALID_ARG;
   if (c->d_model > kNormMaxD) return COLIBRI_ERR_UNSUPPORTED;
   // without a block output there is nothing to norm after, to gate or to add
@@ -692,7 +692,7 @@ extern "C" int colibri_moe_block_norm(const colibri_moe_norm_config_t* cfg, cons
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
   for (const void* q : {x, y, w->after_weight, w->after_bias, w->before_weight, w->before_bias, w->gate,
                         (const void*)x1, (const void*)p})
-    if (q && !ops_on_device(q, device)) return COLIBRI_ERR_INVALID_ARG;
+    if (q && !cfg->trusted_pointers && !ops_on_device(q, device)) return COLIBRI_ERR_INVALID_ARG;
   NormArgs a = {};
   a.x = x, a.y = y, a.wa = w->after_weight, a.ba = w->after_bias, a.wb = w->before_weight, a.bb = w->before_bias;
   a.gate = w->gate, a.x1 = x1, a.p = p, a.ldx = ldx, a.ldy = ldy, a.rpg = cfg->rows_per_gate, a.T = T, a.d = d;
@@ -758,7 +758,7 @@ extern "C" int colibri_moe_block_norm_backward(const colibri_moe_norm_config_t* 
                         w->before_bias, w->gate, (const void*)d_x, (const void*)d_y, (const void*)grads->after_weight,
                         (const void*)grads->after_bias, (const void*)grads->before_weight,
                         (const void*)grads->before_bias, (const void*)grads->gate, (const void*)workspace})
-    if (q && !ops_on_device(q, device)) return COLIBRI_ERR_INVALID_ARG;
+    if (q && !cfg->trusted_pointers && !ops_on_device(q, device)) return COLIBRI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0) {  // no rows: the column sums are zero (there is no gate row to sum into)
     for (float* g : {grads->after_weight, grads->after_bias, grads->before_weight, grads->before_bias})

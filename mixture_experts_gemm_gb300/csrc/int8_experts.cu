@@ -136,7 +136,7 @@ constexpr int kInt8MaxE = 512, kInt8MaxK = 65536, kInt8MaxN = 131072;
 
 int check_int8_config(const colibri_moe_int8_config_t* c) {
   if (!c || c->in_features <= 0 || c->out_features <= 0 || c->num_experts <= 0 || !ops_dtype(c->dtype) ||
-      !ops_dtype(c->out_dtype))
+      !ops_dtype(c->out_dtype) || (c->trusted_pointers & ~1))
     return COLIBRI_ERR_INVALID_ARG;
   if (c->in_features % 16 || c->in_features > kInt8MaxK || c->out_features > kInt8MaxN || c->num_experts > kInt8MaxE)
     return COLIBRI_ERR_UNSUPPORTED;
@@ -226,7 +226,7 @@ extern "C" int colibri_moe_int8_quantize(const colibri_moe_int8_config_t* cfg, c
   int device = 0, sms = 0;
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
   for (const void* p : {x, (const void*)q, (const void*)scale})
-    if (!ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
+    if (!cfg->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   const QuantArgs a = {x, ldx, n, nullptr, n, cfg->in_features, q, scale, nullptr, 0};
   const cudaError_t e = quantize<int8_t>(cfg->dtype, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
@@ -264,7 +264,7 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
   for (const void* p : {n_tokens ? x : nullptr, (const void*)rows, (const void*)offsets, (const void*)w,
                         (const void*)w_scale, (const void*)w3, (const void*)w3_scale, (const void*)y,
                         (const void*)workspace})
-    if (p && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
+    if (p && !cfg->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   const QuantArgs qa = {x, ldx, n_tokens, rows, R, cfg->in_features, ws + lay.q, reinterpret_cast<float*>(ws + lay.scale),

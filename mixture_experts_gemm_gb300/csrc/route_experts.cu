@@ -695,7 +695,7 @@ cudaError_t by_experts(int dtype, int E, F f) {
 int check_route_config(const colibri_moe_route_config_t* c, int32_t T, int64_t ld) {
   if (!c || T < 0) return COLIBRI_ERR_INVALID_ARG;
   if (c->num_experts < 1 || c->top_k < 1 || c->top_k > c->num_experts || !ops_dtype(c->logits_dtype) ||
-      (c->score != COLIBRI_SCORE_SOFTMAX && c->score != COLIBRI_SCORE_SIGMOID) || (c->renormalize & ~1))
+      (c->score != COLIBRI_SCORE_SOFTMAX && c->score != COLIBRI_SCORE_SIGMOID) || (c->renormalize & ~1) || (c->trusted_pointers & ~1))
     return COLIBRI_ERR_INVALID_ARG;
   if (c->groups < 1 || c->num_experts % c->groups || c->top_groups < 1 || c->top_groups > c->groups ||
       c->group_top < 1 || c->group_top > 2 || c->top_k > c->top_groups * (c->num_experts / c->groups))
@@ -738,7 +738,7 @@ extern "C" int colibri_moe_route_experts(const colibri_moe_route_config_t* cfg, 
   for (const void* p : {logits, (const void*)bias, (const void*)idx, (const void*)gate, (const void*)counts,
                         (const void*)offsets, (const void*)row_of, (const void*)token_of_row,
                         (const void*)(chunks > 1 ? workspace : nullptr)})
-    if (p && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
+    if (p && !cfg->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int E = cfg->num_experts;
   if (T == 0) {
@@ -784,7 +784,7 @@ extern "C" int colibri_moe_route_experts_backward(const colibri_moe_route_config
   int device = 0, sms = 0;
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
   for (const void* p : {logits, (const void*)idx, (const void*)d_gate, (const void*)d_logits})
-    if (!ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
+    if (!cfg->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   RouteBackArgs a = {logits, ld, ld_d, idx, d_gate, d_logits, T, cfg->num_experts, cfg->top_k,
                      cfg->score == COLIBRI_SCORE_SOFTMAX, cfg->renormalize, cfg->scale};
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -47,12 +47,19 @@ def _kind(table, key, name: str) -> int:
         raise ValueError(f"{name}: one of {', '.join(table)}, not {key!r}") from None
 
 
-def _matrix(t, name: str, T: int, d: int, dtype=None):
-    """(address, row stride) of a [T, d] CUDA tensor whose rows are contiguous."""
+def _device(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed")
+    return dev
+
+
+def _matrix(t, name: str, T: int, d: int, dev: int, dtype=None):
+    """(address, row stride) of a [T, d] tensor on CUDA device `dev` whose rows are contiguous."""
     if t.shape != (T, d):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, d)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor is needed")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, not on CUDA device {dev}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: {dtype} expected, not {t.dtype}")
     s0, s1 = t.stride()
@@ -67,13 +74,13 @@ def _shape(t, name: str):
     return t.shape
 
 
-def _vector(t, name: str, shape, dtype):
-    """Address of a contiguous CUDA tensor of the given shape and type, or None for None."""
+def _vector(t, name: str, shape, dtype, dev: int):
+    """Address of a contiguous tensor of the given shape and type on CUDA device `dev`, or None for None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous CUDA tensor {tuple(shape)} of {dtype} expected, not "
-                         f"{tuple(t.shape)} of {t.dtype}")
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor {tuple(shape)} of {dtype} on CUDA device {dev} expected, not "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -110,14 +117,12 @@ class _on:
             self.guard.__exit__(*exc)
 
 
-def _run(f, t, stream, *args):
-    """f(stream handle, *args) on t's device and the given or current stream."""
-    if stream is None:
-        dev = t.get_device()
-        if dev == torch._C._cuda_getDevice():  # the usual case, without the context managers' microseconds
-            return f(torch._C._cuda_getCurrentRawStream(dev), *args)
+def _run(f, t, dev: int, stream):
+    """f(stream handle) on t's device `dev` and the given or current stream."""
+    if stream is None and dev == torch._C._cuda_getDevice():  # the usual case, without the context managers
+        return f(torch._C._cuda_getCurrentRawStream(dev))
     with _on(t, stream) as s:
-        return f(s, *args)
+        return f(s)
 
 
 class _Scratch(threading.local):
@@ -148,11 +153,11 @@ def _at(t):
 def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gate, residual_scale, block_scale, eps):
     c = NormConfig(d, _dtype(dtype, "x"), _dtype(block_dtype, "y"), _dtype(param_dtype, "the parameters"),
                    _kind(_NORMS, after, "after"), _kind(_NORMS, before, "before"), rows_per_gate, float(residual_scale),
-                   float(block_scale), float(eps))
+                   float(block_scale), float(eps), 1)
     return c, ctypes.addressof(c)
 
 
-def _norm_setup(T, d, dtype, block_dtype, after, after_weight, after_bias, before, before_weight, before_bias, gate,
+def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, before, before_weight, before_bias, gate,
                 rows_per_gate, residual_scale, block_scale, eps):
     """(config's address, gate rows); the parameters' addresses go to this thread's scratch."""
     pt = torch.float32
@@ -169,12 +174,12 @@ def _norm_setup(T, d, dtype, block_dtype, after, after_weight, after_bias, befor
         if rpg <= 0:
             raise ValueError("rows_per_gate must be positive")
         n_gates = -(-T // rpg) if T else gate.shape[0]
-        pg = _vector(gate, "gate", (n_gates, d), pt)
+        pg = _vector(gate, "gate", (n_gates, d), pt, dev)
     one = (d,)
-    _five.pack_into(_scratch.vectors, 0, _vector(after_weight, "after_weight", one, pt) or 0,
-                    _vector(after_bias, "after_bias", one, pt) or 0,
-                    _vector(before_weight, "before_weight", one, pt) or 0,
-                    _vector(before_bias, "before_bias", one, pt) or 0, pg or 0)
+    _five.pack_into(_scratch.vectors, 0, _vector(after_weight, "after_weight", one, pt, dev) or 0,
+                    _vector(after_bias, "after_bias", one, pt, dev) or 0,
+                    _vector(before_weight, "before_weight", one, pt, dev) or 0,
+                    _vector(before_bias, "before_bias", one, pt, dev) or 0, pg or 0)
     return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, residual_scale, block_scale, eps)[1], n_gates
 
 
@@ -193,9 +198,10 @@ def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, b
     x1 is None (a norm before a block alone)."""
     T, d = _shape(x, "x")
     dt = x.dtype
-    px, ldx = _matrix(x, "x", T, d)
-    py, ldy = _matrix(y, "y", T, d) if y is not None else (None, 0)
-    c, _ = _norm_setup(T, d, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
+    dev = _device(x, "x")
+    px, ldx = _matrix(x, "x", T, d, dev)
+    py, ldy = _matrix(y, "y", T, d, dev) if y is not None else (None, 0)
+    c, _ = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
                        before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
 
     def call(s):
@@ -204,7 +210,7 @@ def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, b
         _check(lib().colibri_moe_block_norm(c, _scratch.p_vectors, px, ldx, py, ldy, T, _at(x1), _at(p), s),
                "colibri_moe_block_norm")
         return x1, p
-    return _run(call, x, stream)
+    return _run(call, x, dev, stream)
 
 
 def pre_norm(x, weight, bias=None, *, kind="rms", eps=1e-6, stream=None):
@@ -223,11 +229,12 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
         raise ValueError("one of d_x1 and d_p is needed")
     T, d = _shape(ref, "d_x1" if d_x1 is not None else "d_p")
     dt = ref.dtype
-    p1, ld1 = _matrix(d_x1, "d_x1", T, d, dt) if d_x1 is not None else (None, 0)
-    pp, ldp = _matrix(d_p, "d_p", T, d, dt) if d_p is not None else (None, 0)
-    px, ldx = _matrix(x1, "x1", T, d, dt) if x1 is not None else (None, 0)
-    py, ldy = _matrix(y, "y", T, d) if y is not None else (None, 0)
-    c, n_gates = _norm_setup(T, d, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
+    on = _device(ref, "d_x1")
+    p1, ld1 = _matrix(d_x1, "d_x1", T, d, on, dt) if d_x1 is not None else (None, 0)
+    pp, ldp = _matrix(d_p, "d_p", T, d, on, dt) if d_p is not None else (None, 0)
+    px, ldx = _matrix(x1, "x1", T, d, on, dt) if x1 is not None else (None, 0)
+    py, ldy = _matrix(y, "y", T, d, on) if y is not None else (None, 0)
+    c, n_gates = _norm_setup(T, d, on, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
                              before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
 
     def call(s):
@@ -251,7 +258,7 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
                                                  _at(out["d_x"]), _at(out.get("d_y")), _scratch.p_grads, _at(ws), n, s),
                "colibri_moe_block_norm_backward")
         return out
-    return _run(call, ref, stream)
+    return _run(call, ref, on, stream)
 
 
 # ----------------------------------------------------------------------------------------- routing
@@ -268,7 +275,7 @@ class Routing(NamedTuple):
 @functools.lru_cache(maxsize=256)
 def _route_config(E, k, score, groups, top_groups, group_top, renormalize, dtype, scale):
     c = RouteConfig(E, k, _kind(_SCORES, score, "score"), groups, top_groups, group_top, int(bool(renormalize)),
-                    _dtype(dtype, "logits"), float(scale))
+                    _dtype(dtype, "logits"), float(scale), 1)
     return c, ctypes.addressof(c)
 
 
@@ -282,37 +289,34 @@ def route(logits, top_k: int, *, score="softmax", bias=None, groups=1, top_group
     without the bias, divided by their sum if renormalize, times scale.  Ties go to the lowest index; an
     expert with a logit or bias of -inf or NaN is never chosen."""
     T, E = _shape(logits, "logits")
-    pl, ld = _matrix(logits, "logits", T, E)
-    pb = _vector(bias, "bias", (E,), torch.float32)
+    on = _device(logits, "logits")
+    pl, ld = _matrix(logits, "logits", T, E, on)
+    pb = _vector(bias, "bias", (E,), torch.float32, on)
     k = top_k
     c = _route_config(E, k, score, groups, top_groups, group_top, renormalize, logits.dtype, scale)[1]
 
     def call(s):
-        L, dev, n = lib(), logits.device, T * k
+        L, dev, i32 = lib(), logits.device, torch.int32
         _check(L.colibri_moe_route_experts_workspace(c, T, _scratch.p_size), "colibri_moe_route_experts")
         size = _scratch.size.value
-        # one allocation for the whole numbers and the workspace behind them
-        at = (3 * n + 2 * E + 1 + 63) // 64 * 64
-        ints = torch.empty(at + size // 4, dtype=torch.int32, device=dev)
-        p = ints.data_ptr()
-        gate = torch.empty((T, k), dtype=torch.float32, device=dev)
-        pair, row = (T, k), (k, 1)
-        r = Routing(ints.as_strided(pair, row, 0), gate, ints.as_strided((E,), (1,), 3 * n),
-                    ints.as_strided((E + 1,), (1,), 3 * n + E), ints.as_strided(pair, row, n),
-                    ints.as_strided((n,), (1,), 2 * n))
-        _check(L.colibri_moe_route_experts(c, pl, ld, pb, T, p, gate.data_ptr(), p + 12 * n, p + 12 * n + 4 * E, p + 4 * n,
-                                           p + 8 * n, p + 4 * at if size else None, size, s), "colibri_moe_route_experts")
+        r = Routing(torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
+                    torch.empty(E, dtype=i32, device=dev), torch.empty(E + 1, dtype=i32, device=dev),
+                    torch.empty((T, k), dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev))
+        ws = _workspace(size, dev)
+        _check(L.colibri_moe_route_experts(c, pl, ld, pb, T, *[t.data_ptr() for t in r], _at(ws), size, s),
+               "colibri_moe_route_experts")
         return r
-    return _run(call, logits, stream)
+    return _run(call, logits, on, stream)
 
 
 def route_backward(logits, idx, d_gate, *, score="softmax", renormalize=True, scale=1.0, stream=None):
     """d_logits [T, E] (the logits' type) from the gradient of the gates, the choice idx [T, k] held constant."""
     T, E = _shape(logits, "logits")
-    pl, ld = _matrix(logits, "logits", T, E)
+    on = _device(logits, "logits")
+    pl, ld = _matrix(logits, "logits", T, E, on)
     k = _shape(idx, "idx")[1]
-    pi = _vector(idx, "idx", (T, k), torch.int32)
-    pg = _vector(d_gate, "d_gate", (T, k), torch.float32)
+    pi = _vector(idx, "idx", (T, k), torch.int32, on)
+    pg = _vector(d_gate, "d_gate", (T, k), torch.float32, on)
     c = _route_config(E, k, score, 1, 1, 1, renormalize, logits.dtype, scale)[1]
 
     def call(s):
@@ -320,13 +324,13 @@ def route_backward(logits, idx, d_gate, *, score="softmax", renormalize=True, sc
         _check(lib().colibri_moe_route_experts_backward(c, pl, ld, pi, pg, T, out.data_ptr(), E, s),
                "colibri_moe_route_experts_backward")
         return out
-    return _run(call, logits, stream)
+    return _run(call, logits, on, stream)
 
 
 # ----------------------------------------------------------------------------------- 8-bit experts
 @functools.lru_cache(maxsize=256)
 def _int8_config(K, N, E, dtype, out_dtype):
-    c = Int8Config(K, N, E, _dtype(dtype, "x"), _dtype(out_dtype, "out_dtype"))
+    c = Int8Config(K, N, E, _dtype(dtype, "x"), _dtype(out_dtype, "out_dtype"), 1)
     return c, ctypes.addressof(c)
 
 
@@ -336,7 +340,8 @@ def int8_quantize(x, stream=None):
     K = x.shape[-1]
     flat = x.reshape(-1, K)
     n = flat.shape[0]
-    px, ldx = _matrix(flat, "x", n, K)
+    on = _device(x, "x")
+    px, ldx = _matrix(flat, "x", n, K, on)
     c = _int8_config(K, 1, 1, x.dtype, torch.float32)[1]
 
     def call(s):
@@ -345,7 +350,7 @@ def int8_quantize(x, stream=None):
         _check(lib().colibri_moe_int8_quantize(c, px, ldx, n, q.data_ptr(), scale.data_ptr(), s),
                "colibri_moe_int8_quantize")
         return q, scale
-    return _run(call, x, stream)
+    return _run(call, x, on, stream)
 
 
 def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, out_dtype=None, stream=None):
@@ -357,20 +362,21 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
     shapes) y = silu(v) * v3, the gated pair of projections in one pass.  Rows from offsets[E] on are
     not written.  out_dtype: fp32 or bf16, default x's."""
     n, K = _shape(x, "x")
-    px, ldx = _matrix(x, "x", n, K)
+    on = _device(x, "x")
+    px, ldx = _matrix(x, "x", n, K, on)
     if w.dim() != 3:
         raise ValueError(f"w: [E, N, {K}] expected, not {tuple(w.shape)}")
     E, N, _ = w.shape
     i32, weights, scales = torch.int32, (E, N, K), (E, N)
-    pw = _vector(w, "w", weights, torch.int8)
-    ps = _vector(w_scale, "w_scale", scales, torch.float32)
+    pw = _vector(w, "w", weights, torch.int8, on)
+    ps = _vector(w_scale, "w_scale", scales, torch.float32, on)
     if (w3 is None) != (w3_scale is None):
         raise ValueError("w3 and w3_scale go together")
-    pw3 = _vector(w3, "w3", weights, torch.int8)
-    ps3 = _vector(w3_scale, "w3_scale", scales, torch.float32)
-    po = _vector(offsets, "offsets", (E + 1,), i32)
+    pw3 = _vector(w3, "w3", weights, torch.int8, on)
+    ps3 = _vector(w3_scale, "w3_scale", scales, torch.float32, on)
+    po = _vector(offsets, "offsets", (E + 1,), i32, on)
     R = n if rows is None else rows.numel()
-    pr = _vector(rows, "rows", (R,), i32)
+    pr = _vector(rows, "rows", (R,), i32, on)
     out_dtype = x.dtype if out_dtype is None else out_dtype
     c = _int8_config(K, N, E, x.dtype, out_dtype)[1]
 
@@ -383,16 +389,17 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
         _check(L.colibri_moe_int8_experts(c, px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws), size, s),
                "colibri_moe_int8_experts")
         return y
-    return _run(call, x, stream)
+    return _run(call, x, on, stream)
 
 
 def combine(y, row_of, gate, *, out_dtype=None, stream=None):
     """out[t] = sum over a token's slots of gate * y[row_of], in slot order in fp32; rows of -1 are left out."""
     R, d = _shape(y, "y")
-    py = _vector(y, "y", (R, d), y.dtype)
+    on = _device(y, "y")
+    py = _vector(y, "y", (R, d), y.dtype, on)
     T, k = _shape(row_of, "row_of")
-    pr = _vector(row_of, "row_of", (T, k), torch.int32)
-    pg = _vector(gate, "gate", (T, k), torch.float32)
+    pr = _vector(row_of, "row_of", (T, k), torch.int32, on)
+    pg = _vector(gate, "gate", (T, k), torch.float32, on)
     out_dtype = y.dtype if out_dtype is None else out_dtype
     types = _dtype(y.dtype, "y"), _dtype(out_dtype, "out_dtype")
 
@@ -401,4 +408,4 @@ def combine(y, row_of, gate, *, out_dtype=None, stream=None):
         _check(lib().colibri_moe_combine_rows(py, types[0], R, pr, pg, T, k, d, out.data_ptr(), types[1], s),
                "colibri_moe_combine_rows")
         return out
-    return _run(call, y, stream)
+    return _run(call, y, on, stream)
