@@ -77,6 +77,20 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Waits for the phase of `bar` with parity `parity`, at most timeout_ns or until *abort.  The clock is read
+// once in 64 tries: reading it takes longer than most of these waits last.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t tries = 1;; ++tries) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (tries % 64 == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort || now - t0 > timeout_ns) return false;
+    }
+  }
+}
+
 // Two bytes of signed integers (selected by `sel` out of w ^ 0x80808080) as two exact fp16.
 __device__ __forceinline__ uint32_t bytes_to_half2(uint32_t biased, uint32_t sel) {
   const uint32_t u = __byte_perm(biased, 0x64646464u, sel);
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // barrier cannot run two phases ahead of a waiter, because the blocks between need the waiter's work.
   auto slot_free = [&](uint32_t it, uint32_t behind) {
     const uint32_t j = it - behind;
-    return it < behind || mbar_wait(done0 + 8 * (j % kSync), j / kSync & 1, s_abort, a.timeout_ns);
+    return it < behind || wait_for(done0 + 8 * (j % kSync), j / kSync & 1, s_abort, a.timeout_ns);
   };
 
   // The producers' and the MMA warp run their loops with all lanes and let one elected lane issue: addresses
@@ -260,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item t = item_at(i);
       const int w_row = t.e * a.N + t.ch * kCh;
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++issued) {
-        if (!__all_sync(~0u, mbar_wait(rempty0 + 8 * r, ph ^ 1, s_abort, a.timeout_ns))) {
+        if (!__all_sync(~0u, wait_for(rempty0 + 8 * r, ph ^ 1, s_abort, a.timeout_ns))) {
           ok = false;
           break;
         }
@@ -279,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every copy has landed before the CTA can leave
     volatile int never = 0;
     for (uint32_t j = issued > RS ? issued - RS : 0; j < issued; ++j)
-      mbar_wait(rfull0 + 8 * (j % RS), j / RS & 1, &never, a.timeout_ns);
+      wait_for(rfull0 + 8 * (j % RS), j / RS & 1, &never, a.timeout_ns);
     __syncwarp();
   } else if (warp == 6) {
     // -------------------------------------------------------------- token rows
@@ -316,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // stopped early: no MMA reads the slots any more, but the copies must land.  A full barrier may
       // lack its converters' arrivals, so give the copies a fixed time, far above a copy's, instead.
       volatile int never = 0;
-      if (it) mbar_wait(full0 + 8 * ((it - 1) % kSync), (it - 1) / kSync & 1, &never, a.timeout_ns / 8);
+      if (it) wait_for(full0 + 8 * ((it - 1) % kSync), (it - 1) / kSync & 1, &never, a.timeout_ns / 8);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -327,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++acc_it) {
       const Item t = item_at(i);
       const uint32_t acc = acc_it & 1;
-      if (!__all_sync(~0u, mbar_wait(tempty0 + 8 * acc, (acc_it >> 1 & 1) ^ 1, s_abort, a.timeout_ns))) {
+      if (!__all_sync(~0u, wait_for(tempty0 + 8 * acc, (acc_it >> 1 & 1) ^ 1, s_abort, a.timeout_ns))) {
         ok = false;
         break;
       }
@@ -335,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tmem_base + acc * NT, idesc = idesc_f16((t.n + kTokBox - 1) / kTokBox * kTokBox);
       uint32_t more = 0;  // the first MMA of a tile overwrites the accumulator
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        if (!__all_sync(~0u, mbar_wait(full0 + 8 * (it % kSync), it / kSync & 1, s_abort, a.timeout_ns))) {
+        if (!__all_sync(~0u, wait_for(full0 + 8 * (it % kSync), it / kSync & 1, s_abort, a.timeout_ns))) {
           ok = false;
           break;
         }
@@ -359,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elected) {
       umma_commit(drain);  // completes when every MMA of this thread has
       volatile int never = 0;
-      mbar_wait(drain, 0, &never, a.timeout_ns);
+      wait_for(drain, 0, &never, a.timeout_ns);
     }
     __syncwarp();
   } else if (warp >= kConvWarp0) {
@@ -372,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t n = t.kb1 - t.kb0;
       for (uint32_t j = (group - it0) % kConvGroups; j < n; j += kConvGroups) {
         const uint32_t it = it0 + j;
-        bool got = mbar_wait(rfull0 + 8 * r, ph, s_abort, a.timeout_ns);
+        bool got = wait_for(rfull0 + 8 * r, ph, s_abort, a.timeout_ns);
         uint4 v[4];
         const uint4* src = reinterpret_cast<const uint4*>(s_raw + r * kRawBytes);
 #pragma unroll
@@ -415,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x, ++acc_it) {
       const Item t = item_at(i);
       const uint32_t acc = acc_it & 1;
-      if (!__all_sync(~0u, mbar_wait(tfull0 + 8 * acc, acc_it >> 1 & 1, s_abort, a.timeout_ns))) {
+      if (!__all_sync(~0u, wait_for(tfull0 + 8 * acc, acc_it >> 1 & 1, s_abort, a.timeout_ns))) {
         if (lane == 0) *s_abort = 1;
         break;
       }
@@ -478,14 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(joined);
         bool got = true;
         if (warp == 2 && lane == 0) {
-          got = mbar_wait(joined, acc_it & 1, s_abort, a.timeout_ns);
+          got = wait_for(joined, acc_it & 1, s_abort, a.timeout_ns);
           if (got) {
             __threadfence();
             *s_last = atomicAdd(&a.ticket[t.tile], 1u) == (uint32_t)(parts - 1);
             mbar_arrive(decided);
           }
         }
-        got = got && mbar_wait(decided, acc_it & 1, s_abort, a.timeout_ns);
+        got = got && wait_for(decided, acc_it & 1, s_abort, a.timeout_ns);
         if (!__all_sync(~0u, got)) {
           if (lane == 0) *s_abort = 1;
           break;
