@@ -75,6 +75,7 @@ template <typename T, typename Q, int C>
 __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_kernel(QuantArgs a) {
   __shared__ float s_max[kQuantThreads / 32];
   pdl_wait();
+  pdl_trigger();  // after the wait: what starts early may read what was there before this kernel
   for (int64_t i = (int64_t)blockIdx.x * kQuantThreads + threadIdx.x; i < a.n_ticket; i += (int64_t)gridDim.x * kQuantThreads)
     a.ticket[i] = 0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

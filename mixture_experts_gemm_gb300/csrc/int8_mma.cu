@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), F::kTmemCols);
     tmem_relinquish();
   }
-  pdl_wait();  // the quantised rows, and the offsets of the routing before
+  // The quantiser lets this kernel start once everything before it is done: offsets and weights may be read
+  // at once; the warps that read its rows and scales (6, 2..5) wait for it.
   if (warp == 7) {
     // Segments inside 0..R, none reaching back into an earlier one; tiles of each expert.
     const int per = (a.E + 31) / 32;
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 6) {
     // -------------------------------------------------------------- token rows
+    pdl_wait();
     const bool elected = elect_one();
     const uint32_t b0 = smem_u32(s_b);
     uint32_t it = 0, sb = 0;
@@ -424,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) *s_abort = 1;
   } else if (warp >= 2 && warp < 6) {
     // -------------------------------------------------------------- epilogue
+    pdl_wait();
     const int q = warp & 3;  // the TMEM lanes this warp may read
     uint32_t acc_it = 0;
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x, ++acc_it) {
