@@ -125,11 +125,13 @@ __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_k
       raw[c].get(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = live ? quotient(v[j], scale, inv, exact) : 0.f;
-      store_q8(q + col, o);
+      for (int i = 0; i < a.copies; ++i) store_q8(q + (int64_t)i * a.n * a.K + col, o);
     }
   } else {
-    for (int i = threadIdx.x; i < a.K; i += kQuantThreads)
-      q[i] = q_value<Q>(live ? quotient(to_float(x[i]), scale, inv, exact) : 0.f);
+    for (int i = threadIdx.x; i < a.K; i += kQuantThreads) {
+      const Q v = q_value<Q>(live ? quotient(to_float(x[i]), scale, inv, exact) : 0.f);
+      for (int j = 0; j < a.copies; ++j) q[(int64_t)j * a.n * a.K + i] = v;
+    }
   }
 }
 
@@ -171,17 +173,21 @@ int int8_tile_rows(int R, int E) {
   return mean <= 16 ? 32 : mean <= 48 ? 64 : mean <= 128 ? 128 : 256;
 }
 
+// Of few rows, all SMs read the same few kilobytes at the same time; copies spread them over L2.
+constexpr int kInt8CopiedRows = 64, kInt8Copies = 8;
+
 // The workspace of a product: the rows' scales and fp16 values, tickets and partial sums of split tiles.
 struct Int8Workspace {
   size_t scale, q, ticket, partial, bytes;
-  int items, tile_rows;
+  int items, tile_rows, copies;
 };
 Int8Workspace int8_workspace(const colibri_moe_int8_config_t* c, int R, int sms) {
   Int8Workspace w = {};
   w.tile_rows = int8_tile_rows(R, c->num_experts);
   w.items = sms * (kInt8PartialRows / w.tile_rows);
+  w.copies = R <= kInt8CopiedRows ? kInt8Copies : 1;
   w.q = round256((size_t)R * sizeof(float));
-  w.ticket = w.q + round256((size_t)R * c->in_features * 2);
+  w.ticket = w.q + round256((size_t)w.copies * R * c->in_features * 2);
   w.partial = w.ticket + round256(w.items * sizeof(uint32_t));
   w.bytes = w.partial + (size_t)w.items * w.tile_rows * 128 * sizeof(float);
   return w;
@@ -228,7 +234,7 @@ extern "C" int colibri_moe_int8_quantize(const colibri_moe_int8_config_t* cfg, c
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
   for (const void* p : {x, (const void*)q, (const void*)scale})
     if (!cfg->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
-  const QuantArgs a = {x, ldx, n, nullptr, n, cfg->in_features, q, scale, nullptr, 0};
+  const QuantArgs a = {x, ldx, n, nullptr, n, cfg->in_features, q, 1, scale, nullptr, 0};
   const cudaError_t e = quantize<int8_t>(cfg->dtype, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
@@ -268,13 +274,14 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
     if (p && !cfg->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
-  const QuantArgs qa = {x, ldx, n_tokens, rows, R, cfg->in_features, ws + lay.q, reinterpret_cast<float*>(ws + lay.scale),
+  const QuantArgs qa = {x, ldx, n_tokens, rows, R, cfg->in_features, ws + lay.q, lay.copies,
+                        reinterpret_cast<float*>(ws + lay.scale),
                         reinterpret_cast<uint32_t*>(ws + lay.ticket), lay.items};
   Int8Maps maps;
-  if (!int8_tensor_maps(qa.q, R, w, w3, cfg->num_experts, cfg->out_features, cfg->in_features, &maps)) return COLIBRI_ERR_CUDA;
+  if (!int8_tensor_maps(qa.q, (int64_t)lay.copies * R, w, w3, cfg->num_experts, cfg->out_features, cfg->in_features, &maps)) return COLIBRI_ERR_CUDA;
   if (quantize<__half>(cfg->dtype, qa, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
   const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, reinterpret_cast<float*>(ws + lay.partial),
-                      qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, 2000000000ull};
+                      qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, lay.copies, 2000000000ull};
   const cudaError_t e = launch_int8_mma(maps, lay.tile_rows, w3 != nullptr, cfg->out_dtype == COLIBRI_DTYPE_BF16, a, device, sms, s);
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }

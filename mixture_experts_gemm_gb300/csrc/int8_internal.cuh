@@ -22,6 +22,7 @@ struct Int8Args {
   uint32_t* ticket;                 // [items], zero at launch: parts of a tile done
   int max_items;                    // capacity of the two
   int R, E, K, N;
+  int copies;                       // of the quantised rows, R apart
   uint64_t timeout_ns;
 };
 
@@ -31,7 +32,8 @@ struct QuantArgs {
   int n_tokens;
   const int32_t* rows;  // token of each row, or nullptr: the row itself
   int n, K;             // rows to write
-  void* q;              // [n, K] int8 or fp16
+  void* q;              // [copies][n, K] int8 or fp16
+  int copies;
   float* scale;         // [n]
   uint32_t* ticket;     // cleared for the product kernel, or nullptr
   int n_ticket;
@@ -44,8 +46,8 @@ struct Int8Maps {
   CUtensorMap q[kTokMaps], w, w3;
 };
 
-// rows: q [R, K] fp16 whole numbers; w, w3: [E * N, K] int8.
-bool int8_tensor_maps(const void* q, int R, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps);
+// q [rows, K] fp16 whole numbers; w, w3: [E * N, K] int8.
+bool int8_tensor_maps(const void* q, int64_t rows, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps);
 // tile_rows: 32, 64, 128 or 256 token rows a tile.
 cudaError_t launch_int8_mma(const Int8Maps& maps, int tile_rows, bool swiglu, bool bf16_out, const Int8Args& a, int device,
                             int sms, cudaStream_t s);

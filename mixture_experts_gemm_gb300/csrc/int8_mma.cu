@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     const bool elected = elect_one();
     const uint32_t b0 = smem_u32(s_b);
+    const int copy = blockIdx.x % a.copies * a.R;
     uint32_t it = 0, sb = 0;
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item t = item_at(i);
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int x = kb * BK;
         if (elected) {
           mbar_arrive_expect_tx(full, boxes * kTokBoxBytes);
-          int row = t.row;
+          int row = t.row + copy;
 #pragma unroll
           for (int b = kTokMaps - 1; b >= 0; --b)  // at most one copy of each box height
             if (boxes >> b & 1) {
@@ -558,9 +559,9 @@ cudaError_t launch(const Int8Maps& maps, const Int8Args& a, int device, int grid
 
 }  // namespace
 
-bool int8_tensor_maps(const void* q, int R, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps) {
+bool int8_tensor_maps(const void* q, int64_t rows, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps) {
   for (int i = 0; i < kTokMaps; ++i)
-    if (!make_map(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, K, R, 2, kTokBox << i, CU_TENSOR_MAP_SWIZZLE_128B,
+    if (!make_map(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, K, (uint64_t)rows, 2, kTokBox << i, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
       return false;
   for (int i = 0; i < 2; ++i)
