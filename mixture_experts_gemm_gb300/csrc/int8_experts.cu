@@ -278,7 +278,9 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
                         reinterpret_cast<float*>(ws + lay.scale),
                         reinterpret_cast<uint32_t*>(ws + lay.ticket), lay.items};
   Int8Maps maps;
-  if (!int8_tensor_maps(qa.q, (int64_t)lay.copies * R, w, w3, cfg->num_experts, cfg->out_features, cfg->in_features, &maps)) return COLIBRI_ERR_CUDA;
+  if (!int8_tensor_maps(lay.tile_rows, qa.q, (int64_t)lay.copies * R, w, w3, cfg->num_experts, cfg->out_features,
+                        cfg->in_features, &maps))
+    return COLIBRI_ERR_CUDA;
   if (quantize<__half>(cfg->dtype, qa, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
   const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, reinterpret_cast<float*>(ws + lay.partial),
                       qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, lay.copies, 2000000000ull};

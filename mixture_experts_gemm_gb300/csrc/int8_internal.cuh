@@ -40,14 +40,15 @@ struct QuantArgs {
 };
 
 // Tensor maps: the quantised rows in boxes of 32, 64, 128 and 256 rows x 64 columns, the weights in boxes of
-// 128 rows (64 of each projection) x 64 bytes.
+// 128 rows (64 of each projection) x a stage's bytes (64 or 128).
 constexpr int kTokMaps = 4;
 struct Int8Maps {
   CUtensorMap q[kTokMaps], w, w3;
 };
 
 // q [rows, K] fp16 whole numbers; w, w3: [E * N, K] int8.
-bool int8_tensor_maps(const void* q, int64_t rows, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps);
+bool int8_tensor_maps(int tile_rows, const void* q, int64_t rows, const int8_t* w, const int8_t* w3, int E, int N, int K,
+                      Int8Maps* maps);
 // tile_rows: 32, 64, 128 or 256 token rows a tile.
 cudaError_t launch_int8_mma(const Int8Maps& maps, int tile_rows, bool swiglu, bool bf16_out, const Int8Args& a, int device,
                             int sms, cudaStream_t s);

@@ -48,25 +48,25 @@ constexpr int kTokBox = 32;              // token rows of the smallest TMA box
 constexpr int kTokBoxBytes = kTokBox * BK * 2;
 constexpr int kMaxExperts = 512;
 
-// Rings, in blocks of 64 columns of K: raw weights (RS), converted weights (SA), token rows (SB).  One full
-// and one done barrier serve block `it` for both operands, at it % kSync.  A block goes around in about 2300
-// cycles (conversion 500, then barriers, MMAs and commit), whatever it holds: the narrower the tile, the
-// more blocks have to be on their way.
+// Rings, in stages of KS blocks of 64 columns of K: raw weights (RS), converted weights (SA), token rows
+// (SB).  One full and one done barrier serve stage `it` for both operands, at it % kSync.  The MMA warp's
+// loop takes about 500 cycles a stage of one block, 700 of two.
 constexpr int kSync = 8;
 template <int NT>
 struct Form {
-  static constexpr int SA = NT == 256 ? 3 : NT == 128 ? 5 : NT == 64 ? 6 : 7;
-  static constexpr int SB = NT == 256 ? 4 : NT == 128 ? 5 : NT == 64 ? 6 : 7;
-  static constexpr int RS = NT == 256 ? 5 : NT == 128 ? 6 : NT == 64 ? 8 : 9;
-  static constexpr int kBBytes = NT * BK * 2;
+  static constexpr int KS = NT == 32 ? 2 : 1;
+  static constexpr int SA = NT == 256 ? 3 : NT == 128 ? 5 : NT == 64 ? 6 : 3;
+  static constexpr int SB = NT == 256 ? 4 : NT == 128 ? 5 : NT == 64 ? 6 : 4;
+  static constexpr int RS = NT == 256 ? 5 : NT == 128 ? 6 : NT == 64 ? 8 : 5;
+  static constexpr int kRaw = KS * kRawBytes, kA = KS * kABytes;
+  static constexpr int kB1 = NT * BK * 2, kB = KS * kB1;
   static constexpr int kBars = 2 * kSync + 2 * RS + 7;
   static constexpr uint32_t kTmemCols = 2 * NT;
-  static constexpr int kSmem =
-      1024 + SA * kABytes + SB * kBBytes + RS * kRawBytes + kBars * 8 + 32 + 4 * (3 * kMaxExperts + 1);
+  static constexpr int kSmem = 1024 + SA * kA + SB * kB + RS * kRaw + kBars * 8 + 32 + 4 * (3 * kMaxExperts + 1);
   static_assert(SA < kSync && SB < kSync, "a barrier is not reused before both rings are");
   // A raw slot alternates between the converter groups unless RS is a multiple of their number.  A group
-  // waits for its phase by parity, so the phase before (the other group's, block it - RS) must be over by
-  // then: the group's own last block, it - kConvGroups, needed the MMAs of block it - kConvGroups - SA.
+  // waits for its phase by parity, so the phase before (the other group's, stage it - RS) must be over by
+  // then: the group's own last stage, it - kConvGroups, needed the MMAs of stage it - kConvGroups - SA.
   static_assert(RS % kConvGroups == 0 || RS >= SA + kConvGroups, "raw phases by parity");
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -112,20 +112,20 @@ struct Item {
   int e, row, n;       // expert, first row, rows of the tile
   int ch;              // weight tile
   int part, tile;      // part of K, tile number
-  int kb0, kb1;        // K blocks
+  int kb0, kb1;        // stages of K
 };
 
 template <int NT, bool SWIGLU, typename O>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_mma_kernel(const __grid_constant__ Int8Maps tm, const Int8Args a) {
   using F = Form<NT>;
-  constexpr int SA = F::SA, SB = F::SB, RS = F::RS;
+  constexpr int SA = F::SA, SB = F::SB, RS = F::RS, KS = F::KS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_a = smem;
-  uint8_t* s_b = s_a + SA * kABytes;
-  uint8_t* s_raw = s_b + SB * F::kBBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_raw + RS * kRawBytes);
+  uint8_t* s_b = s_a + SA * F::kA;
+  uint8_t* s_raw = s_b + SB * F::kB;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_raw + RS * F::kRaw);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + F::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* s_last = reinterpret_cast<volatile int*>(tmem_slot + 2);
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   constexpr int kCh = SWIGLU ? 64 : 128;  // output channels of a tile
   const int ch_tiles = (a.N + kCh - 1) / kCh;
-  const int kblocks = (a.K + BK - 1) / BK;
+  const int kblocks = (a.K + BK * KS - 1) / (BK * KS);
   const int64_t tiles = (int64_t)s_tiles[a.E] * ch_tiles;
   // Parts of K: the number that leaves the SMs least idle in the last wave, a little against more parts.
   int parts = 1;
@@ -279,12 +279,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t full = rfull0 + 8 * r, dst = raw0 + r * kRawBytes;
-        const int x = kb * BK;
+        const uint32_t full = rfull0 + 8 * r, dst = raw0 + r * F::kRaw;
+        const int x = kb * (BK * KS);
         if (elected) {
-          mbar_arrive_expect_tx(full, kRawBytes);
+          mbar_arrive_expect_tx(full, F::kRaw);
           tma_load_2d(dst, &tm.w, full, x, w_row);  // columns past K read as zeros
-          if constexpr (SWIGLU) tma_load_2d(dst + kRawBytes / 2, &tm.w3, full, x, w_row);
+          if constexpr (SWIGLU) tma_load_2d(dst + F::kRaw / 2, &tm.w3, full, x, w_row);
         }
         __syncwarp();
         if (++r == RS) r = 0, ph ^= 1;
@@ -312,15 +312,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t full = full0 + 8 * (it % kSync);
-        uint32_t dst = b0 + sb * F::kBBytes;
-        const int x = kb * BK;
+        uint32_t dst = b0 + sb * F::kB;
+        const int x = kb * (BK * KS);
         if (elected) {
-          mbar_arrive_expect_tx(full, boxes * kTokBoxBytes);
+          mbar_arrive_expect_tx(full, KS * boxes * kTokBoxBytes);
           int row = t.row + copy;
 #pragma unroll
           for (int b = kTokMaps - 1; b >= 0; --b)  // at most one copy of each box height
             if (boxes >> b & 1) {
-              tma_load_2d(dst, &tm.q[b], full, x, row);
+#pragma unroll
+              for (int k = 0; k < KS; ++k) tma_load_2d(dst + k * F::kB1, &tm.q[b], full, x + k * BK, row);
               dst += kTokBoxBytes << b, row += kTokBox << b;
             }
         }
@@ -357,10 +358,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint64_t da = da0 + sa * (kABytes >> 4), db = db0 + sb * (F::kBBytes >> 4);
+        const uint64_t da = da0 + sa * (F::kA >> 4), db = db0 + sb * (F::kB >> 4);
         if (elected) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_bf16(d, da + 2 * k, db + 2 * k, idesc, k ? 1 : more);
+          for (int k = 0; k < 4 * KS; ++k)
+            umma_bf16(d, da + (k >> 2) * (kABytes >> 4) + 2 * (k & 3), db + (k >> 2) * (F::kB1 >> 4) + 2 * (k & 3), idesc,
+                      k ? 1 : more);
           umma_commit(done0 + 8 * (it % kSync));
         }
         __syncwarp();
@@ -382,7 +385,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kConvWarp0) {
     // -------------------------------------------------------------- converters
     const uint32_t group = (warp - kConvWarp0) / kConvGroupWarps;
-    const int tid = threadIdx.x - 32 * (kConvWarp0 + group * kConvGroupWarps);  // 0..127
+    // A warp takes 32 rows, eight at a time: a lane one row's 16 bytes (16 columns of one block of 64), two
+    // neighbouring swizzled chunks of fp16.  Which row makes both sides free of bank conflicts among eight
+    // neighbouring lanes (two rows, 4 c's): they write to rows of opposite parity (even against odd chunks);
+    // they read 64-byte raw rows in a row, or 128-byte raw rows, swizzled by the copy, whose numbers differ
+    // in bit 2.  Everything but the stage is known before the loop.
+    const int w4 = (warp - kConvWarp0) % kConvGroupWarps, c = lane & 3, pair = lane >> 3;
+    const int r8 = KS == 1 ? lane >> 2 : (lane & 4 ? 4 + ((pair + 1) & 3) : pair);
+    const uint32_t src0 = KS == 1 ? (w4 * 32 + r8) * 64 + c * 16 : (w4 * 32 + r8) * 128 + ((c ^ r8) << 4);
+    // gate rows 0..63 and up rows 64..127 alternate in runs of 16 lanes
+    const int m0 = SWIGLU ? (w4 & 1) * 64 + (w4 >> 1) * 16 : w4 * 32;
+    const uint32_t dst0 = (m0 + r8) * 128 + (((2 * c) ^ r8) << 4);
     uint32_t it0 = 0, r = group % RS, ph = group / RS & 1, sa = group % SA;  // this group's next block
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item t = item_at(i);
@@ -390,10 +403,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t j = (group - it0) % kConvGroups; j < n; j += kConvGroups) {
         const uint32_t it = it0 + j;
         bool got = wait_for(rfull0 + 8 * r, ph, s_abort, a.timeout_ns);
-        uint4 v[4];
-        const uint4* src = reinterpret_cast<const uint4*>(s_raw + r * kRawBytes);
+        uint4 v[4 * KS];
+        const uint8_t* src = s_raw + r * F::kRaw;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = src[tid + 128 * c];
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int o = 0; o < 4; ++o)  // chunk 4 + c of a swizzled row is 64 bytes away from chunk c
+            v[4 * k + o] = *reinterpret_cast<const uint4*>(src + (src0 ^ (k * 64)) + o * 8 * (KS * 64));
         got = got && slot_free(it, SA);
         if (!__all_sync(~0u, got)) {
           ok = false;
@@ -401,19 +417,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();  // every lane has its bytes
         if (lane == 0) mbar_arrive(rempty0 + 8 * r);
-        uint8_t* dst = s_a + sa * kABytes;
+        uint8_t* dst = s_a + sa * F::kA;
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-          // 16 bytes of raw row `row`: columns 16 c .. 16 c + 15, swizzled chunks 2 c and 2 c + 1.  Eight
-          // neighbouring threads read 128 bytes in a row and write eight different 16-byte columns (two
-          // rows of opposite parity): no bank conflicts.
-          const int row = (tid >> 2) + 32 * c4, c = tid & 3;
-          // gate rows 0..63 and up rows 64..127 alternate in runs of 16 lanes
-          const int m = SWIGLU ? (row & 48) * 2 + (row & 15) + (row >> 6) * 16 : row;
-          uint8_t* line = dst + m * 128;
-          *reinterpret_cast<uint4*>(line + (((2 * c) ^ (m & 7)) << 4)) = bytes_to_half8(v[c4].x, v[c4].y);
-          *reinterpret_cast<uint4*>(line + (((2 * c + 1) ^ (m & 7)) << 4)) = bytes_to_half8(v[c4].z, v[c4].w);
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int o = 0; o < 4; ++o) {
+            const int row = SWIGLU ? (o >> 1) * 32 + (o & 1) * 8 : o * 8;
+            const uint4 q = v[4 * k + o];
+            *reinterpret_cast<uint4*>(dst + k * kABytes + row * 128 + dst0) = bytes_to_half8(q.x, q.y);
+            *reinterpret_cast<uint4*>(dst + k * kABytes + row * 128 + (dst0 ^ 16)) = bytes_to_half8(q.z, q.w);
+          }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full0 + 8 * (it % kSync));
@@ -532,11 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows, int elem,
-              uint32_t box_rows, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
+              uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promo) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner * elem};
-  const cuuint32_t box[2] = {BK, box_rows}, estr[2] = {1, 1};
+  const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
   return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promo,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -559,14 +572,17 @@ cudaError_t launch(const Int8Maps& maps, const Int8Args& a, int device, int grid
 
 }  // namespace
 
-bool int8_tensor_maps(const void* q, int64_t rows, const int8_t* w, const int8_t* w3, int E, int N, int K, Int8Maps* maps) {
+bool int8_tensor_maps(int tile_rows, const void* q, int64_t rows, const int8_t* w, const int8_t* w3, int E, int N, int K,
+                      Int8Maps* maps) {
   for (int i = 0; i < kTokMaps; ++i)
-    if (!make_map(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, K, (uint64_t)rows, 2, kTokBox << i, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+    if (!make_map(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, K, (uint64_t)rows, 2, BK, kTokBox << i,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
       return false;
+  const int blocks = tile_rows == 256 ? Form<256>::KS : tile_rows == 128 ? Form<128>::KS : tile_rows == 64 ? Form<64>::KS : Form<32>::KS;
   for (int i = 0; i < 2; ++i)
     if (!make_map(i ? &maps->w3 : &maps->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, i && w3 ? w3 : w, K, (uint64_t)E * N, 1,
-                  w3 ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+                  BK * blocks, w3 ? 64 : 128, blocks == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
       return false;
   return true;
 }
