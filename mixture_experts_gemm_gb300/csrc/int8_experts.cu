@@ -36,12 +36,26 @@ __device__ __forceinline__ int8_t q_value<int8_t>(float v) {
   return (int8_t)(int)v;
 }
 
+__device__ __forceinline__ float quotient(float x, float scale) {
+  return fminf(fmaxf(rintf(__fdiv_rn(x, scale)), -127.f), 127.f);
+}
 // round(x / scale) as the IEEE quotient gives it.  The product with 1 / scale is within 127 * 2^-22 of the
 // quotient; only where that could cross a half is the division done (about one value in five thousand).
-__device__ __forceinline__ float quotient(float x, float scale, float inv, bool exact) {
-  const float p = x * inv, t = rintf(p);
-  if (exact || fabsf(fabsf(p - t) - 0.5f) < 1e-4f) return fminf(fmaxf(rintf(__fdiv_rn(x, scale)), -127.f), 127.f);
-  return t;
+// Adding and taking away 1.5 * 2^23 rounds to an integer, ties to even.
+__device__ __forceinline__ void quotients(float (&v)[8], float scale, float inv, bool exact) {
+  float t[8], worst = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float p = v[j] * inv;
+    t[j] = __fadd_rn(__fadd_rn(p, 12582912.f), -12582912.f);
+    worst = fmaxf(worst, fabsf(p - t[j]));
+  }
+  if (exact || worst > 0.4999f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = quotient(v[j], scale);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = t[j];
 }
 
 constexpr int kQuantThreads = 256;
@@ -71,7 +85,7 @@ struct Raw8<__nv_bfloat16> {
 
 // One block a row, held in registers between the maximum and the quotients: C chunks of 8 columns a
 // thread (16-byte loads), or read twice (C == 0).  HBM-bound: the row once in, its fp16 once out.
-template <typename T, typename Q, int C>
+template <typename T, typename Q, int C, bool COPIES>
 __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_kernel(QuantArgs a) {
   __shared__ float s_max[kQuantThreads / 32];
   pdl_wait();
@@ -86,10 +100,10 @@ __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_k
   const T* x = static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx;
   Q* q = static_cast<Q*>(a.q) + (int64_t)r * a.K;
   Raw8<T> raw[C ? C : 1] = {};
-  float top = 0.f;  // of |x|; a NaN or an infinity is kept as infinity
+  float top = 0.f, zero = 0.f;  // of |x|; 0, or NaN once a NaN or an infinity was there
   auto take = [&](float v) {
-    const float m = fabsf(v);
-    top = fmaxf(top, m < INFINITY ? m : INFINITY);
+    top = fmaxf(top, fabsf(v));
+    zero = fmaf(v, 0.f, zero);
   };
   if constexpr (C > 0) {
 #pragma unroll
@@ -107,6 +121,7 @@ __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_k
   } else if (real) {
     for (int i = threadIdx.x; i < a.K; i += kQuantThreads) take(to_float(x[i]));
   }
+  if (!(zero == 0.f)) top = INFINITY;
   top = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top)));  // not negative: ordered as its bits
   if (lane == 0) s_max[warp] = top;
   __syncthreads();
@@ -121,15 +136,18 @@ __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_k
     for (int c = 0; c < C; ++c) {
       const int col = (c * kQuantThreads + threadIdx.x) * 8;
       if (col >= a.K) break;
-      float v[8], o[8];
-      raw[c].get(v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = live ? quotient(v[j], scale, inv, exact) : 0.f;
-      for (int i = 0; i < a.copies; ++i) store_q8(q + (int64_t)i * a.n * a.K + col, o);
+      float v[8] = {};
+      if (live) {
+        raw[c].get(v);
+        quotients(v, scale, inv, exact);
+      }
+      store_q8(q + col, v);
+      if (COPIES)
+        for (int i = 1; i < a.copies; ++i) store_q8(q + (int64_t)i * a.n * a.K + col, v);
     }
   } else {
     for (int i = threadIdx.x; i < a.K; i += kQuantThreads) {
-      const Q v = q_value<Q>(live ? quotient(to_float(x[i]), scale, inv, exact) : 0.f);
+      const Q v = q_value<Q>(live ? quotient(to_float(x[i]), scale) : 0.f);
       for (int j = 0; j < a.copies; ++j) q[(int64_t)j * a.n * a.K + i] = v;
     }
   }
@@ -146,21 +164,21 @@ int check_int8_config(const colibri_moe_int8_config_t* c) {
   return COLIBRI_OK;
 }
 
-template <typename T, typename Q>
+template <typename T, typename Q, bool COPIES>
 cudaError_t quantize_t(const QuantArgs& q, cudaStream_t s) {
   const dim3 grid(q.n), block(kQuantThreads);
   const bool vec = q.ldx % 8 == 0 && ops_aligned16(q.x) && ops_aligned16(q.q);  // K is a multiple of 16
   const int chunks = (q.K + 8 * kQuantThreads - 1) / (8 * kQuantThreads);
-  if (!vec || chunks > 8) return pdl_launch(quantize_rows_kernel<T, Q, 0>, grid, block, 0, s, q);
-  if (chunks == 1) return pdl_launch(quantize_rows_kernel<T, Q, 1>, grid, block, 0, s, q);
-  if (chunks == 2) return pdl_launch(quantize_rows_kernel<T, Q, 2>, grid, block, 0, s, q);
-  if (chunks <= 4) return pdl_launch(quantize_rows_kernel<T, Q, 4>, grid, block, 0, s, q);
-  return pdl_launch(quantize_rows_kernel<T, Q, 8>, grid, block, 0, s, q);
+  if (!vec || chunks > 8) return pdl_launch(quantize_rows_kernel<T, Q, 0, COPIES>, grid, block, 0, s, q);
+  if (chunks == 1) return pdl_launch(quantize_rows_kernel<T, Q, 1, COPIES>, grid, block, 0, s, q);
+  if (chunks == 2) return pdl_launch(quantize_rows_kernel<T, Q, 2, COPIES>, grid, block, 0, s, q);
+  if (chunks <= 4) return pdl_launch(quantize_rows_kernel<T, Q, 4, COPIES>, grid, block, 0, s, q);
+  return pdl_launch(quantize_rows_kernel<T, Q, 8, COPIES>, grid, block, 0, s, q);
 }
 
-template <typename Q>
+template <typename Q, bool COPIES>
 cudaError_t quantize(int dtype, const QuantArgs& q, cudaStream_t s) {
-  return dtype == COLIBRI_DTYPE_F32 ? quantize_t<float, Q>(q, s) : quantize_t<__nv_bfloat16, Q>(q, s);
+  return dtype == COLIBRI_DTYPE_F32 ? quantize_t<float, Q, COPIES>(q, s) : quantize_t<__nv_bfloat16, Q, COPIES>(q, s);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -235,7 +253,7 @@ extern "C" int colibri_moe_int8_quantize(const colibri_moe_int8_config_t* cfg, c
   for (const void* p : {x, (const void*)q, (const void*)scale})
     if (!cfg->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
   const QuantArgs a = {x, ldx, n, nullptr, n, cfg->in_features, q, 1, scale, nullptr, 0};
-  const cudaError_t e = quantize<int8_t>(cfg->dtype, a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = quantize<int8_t, false>(cfg->dtype, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 
@@ -281,7 +299,9 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
   if (!int8_tensor_maps(lay.tile_rows, qa.q, (int64_t)lay.copies * R, w, w3, cfg->num_experts, cfg->out_features,
                         cfg->in_features, &maps))
     return COLIBRI_ERR_CUDA;
-  if (quantize<__half>(cfg->dtype, qa, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
+  const cudaError_t quantized =
+      qa.copies > 1 ? quantize<__half, true>(cfg->dtype, qa, s) : quantize<__half, false>(cfg->dtype, qa, s);
+  if (quantized != cudaSuccess) return COLIBRI_ERR_CUDA;
   const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, reinterpret_cast<float*>(ws + lay.partial),
                       qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, lay.copies, 2000000000ull};
   const cudaError_t e = launch_int8_mma(maps, lay.tile_rows, w3 != nullptr, cfg->out_dtype == COLIBRI_DTYPE_BF16, a, device, sms, s);
