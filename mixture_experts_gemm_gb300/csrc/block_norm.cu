@@ -14,6 +14,12 @@
 // HBM-bound: each of x, y read once, x1, p written once; a row stays in registers between the loads
 // and the stores, so both norms cost no second pass.  All statistics and sums are fp32, the variance is
 // taken about the mean in a second sum over the registers (no E[v^2] - mean^2 cancellation).
+//
+// Measured on one GB300 (bf16 stream, RMS norms, 8192 x 4096): forward with an fp32 block output 67 us
+// (336 MB, 5.0 TB/s, 0.74 of the measured copy rate), backward 115 us (403 MB, 3.5 TB/s, 0.51).  What
+// bounds them is instruction issue and the row sums' barriers (the forward pass executes about 320
+// instructions a warp and row, for 8 columns a lane), not the copies: without the rows ahead the forward
+// pass took 92 us.  Odd widths take single-column accesses: 3001 x 1409 fp32, layer norms, 29 us, floor 10.
 #include <algorithm>
 
 #include "ops_common.cuh"
