@@ -315,8 +315,9 @@ COLIBRI_API int colibri_moe_ep_combine(colibri_moe_t* ctx, const float* y_back, 
  * workspace is scratch of the size the call's _workspace function gives, 256-byte aligned; its
  * contents need no initialisation, and calls that may overlap on the GPU need one each.  Sums, norm
  * statistics and scores are fp32 or wider; a value is rounded to bf16 once, when it is stored.
+ * Inputs and outputs must not overlap, except where a call says so.
  * Errors: COLIBRI_ERR_INVALID_ARG (NULL or host pointers, sizes or strides out of range, overlapping
- * inputs and outputs, a workspace too small), COLIBRI_ERR_UNSUPPORTED (sizes this build does not
+ * rows of the norms' inputs and outputs, a workspace too small), COLIBRI_ERR_UNSUPPORTED (sizes this build does not
  * run, as listed), COLIBRI_ERR_CUDA.  Nothing is enqueued when a call fails its checks.
  * trusted_pointers (in each config; 0 or 1): with 1 the caller vouches that every pointer is device
  * memory of the current device, and the call does not ask the driver, which costs about a microsecond
@@ -446,7 +447,8 @@ COLIBRI_API int colibri_moe_int8_experts_workspace(const colibri_moe_int8_config
 
 /* x [n_tokens, K] (row stride ldx), w [E, N, K] int8 (16-byte aligned), w_scale [E, N] fp32, w3 and
  * w3_scale likewise or both NULL; offsets [E + 1] int32, as routing writes them (offsets[e] .. offsets[e +
- * 1] are expert e's rows; values outside 0..R are clamped); rows [R] int32 gives the token of each row
+ * 1] are expert e's rows; values outside 0..R are clamped, and rows that an earlier segment holds stay
+ * with it); rows [R] int32 gives the token of each row
  * (outside 0..n_tokens-1: a row of zeros), or NULL: row r is token r (R <= n_tokens).  y [R, N]: rows from
  * offsets[E] on are not written.  R == 0 is a no-op. */
 COLIBRI_API int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, const void* x, int64_t ldx,

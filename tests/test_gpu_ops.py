@@ -496,6 +496,18 @@ def test_int8_forms(ops):
     assert ops.int8_experts(x.cuda()[:0, :64].contiguous(), w.cuda(), ws.cuda(), torch.zeros(4, dtype=torch.int32, device="cuda")).shape == (0, 40)
 
 
+@pytest.mark.parametrize("K,n,first", [(64, 3, 1), (96, 70, 3), (16400, 2, 0), (2064, 130, 5)])
+def test_int8_rows_off_16_bytes(ops, K, n, first):
+    """Rows that start off 16 bytes, or are wider than the quantiser's registers: read value by value."""
+    g = gen(K)
+    x = randn(g, n, K + first, dtype=BF16)
+    w, ws = int8_weights(g, 2, 24, K)
+    off = torch.tensor([0, n // 2, n]).int()
+    rows = torch.randperm(n, generator=g).int()
+    y = ops.int8_experts(x.cuda()[:, first:], w.cuda(), ws.cuda(), off.cuda(), rows=rows.cuda(), out_dtype=F32)
+    check_int8(y, x[:, first:], rows, off, [w], [ws], F32)
+
+
 def int8_weights(g, E, N, K):
     return (32 * randn(g, E, N, K)).round().clamp(-127, 127).to(torch.int8), (0.5 + torch.rand(E, N, generator=g)) / 64
 
