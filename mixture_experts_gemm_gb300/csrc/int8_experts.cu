@@ -279,7 +279,8 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
   if (rc) return rc;
   if (n_tokens < 0 || R < 0 || (!rows && R > n_tokens)) return COLIBRI_ERR_INVALID_ARG;
   if (R == 0) return COLIBRI_OK;
-  if ((n_tokens > 0 && (!x || ldx < cfg->in_features)) || !offsets || !w || !w_scale || !y || (w3 != nullptr) != (w3_scale != nullptr))
+  if ((n_tokens > 0 && (!x || ldx < cfg->in_features)) || !offsets || !w || !w_scale || !y ||
+      (w3 != nullptr) != (w3_scale != nullptr))
     return COLIBRI_ERR_INVALID_ARG;
   if (!ops_aligned16(w) || !ops_aligned16(w3)) return COLIBRI_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return COLIBRI_ERR_INVALID_ARG;
@@ -306,7 +307,8 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
   if (quantized != cudaSuccess) return COLIBRI_ERR_CUDA;
   const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, reinterpret_cast<float*>(ws + lay.partial),
                       qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, lay.copies, 2000000000ull};
-  const cudaError_t e = launch_int8_mma(maps, lay.tile_rows, w3 != nullptr, cfg->out_dtype == COLIBRI_DTYPE_BF16, a, device, sms, s);
+  const bool bf16_out = cfg->out_dtype == COLIBRI_DTYPE_BF16;
+  const cudaError_t e = launch_int8_mma(maps, lay.tile_rows, w3 != nullptr, bf16_out, a, device, sms, s);
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 

@@ -23,8 +23,8 @@
 //   warp 1       issues the MMAs, two accumulators in TMEM;
 //   warps 2..5   epilogue.
 // The converters' work is about 1.5 instructions per weight, so it hides behind the MMAs of wide tiles (512
-// cycles a block of 64 columns of K) and behind HBM for narrow ones.  Items are (tile, part of K) in a fixed order; a product of few tiles is split along K, the
-// parts' sums kept in `partial` and added in order by whichever CTA finishes the tile (no floating-point
+// cycles a block of 64 columns of K) and behind HBM for narrow ones.  Items are (tile, part of K) in a
+// fixed order; a product of few tiles is split along K, the parts' sums kept in `partial` and added in order by whichever CTA finishes the tile (no floating-point
 // atomics: the same bits every time).
 //
 // Measured on one GB300 (whole calls, quantiser included): one token, two experts of 4096 x 14336 x 2, 48 us
@@ -587,7 +587,10 @@ bool int8_tensor_maps(int tile_rows, const void* q, int64_t rows, const int8_t* 
     if (!make_map(&maps->q[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, q, K, (uint64_t)rows, 2, BK, kTokBox << i,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
       return false;
-  const int blocks = tile_rows == 256 ? Form<256>::KS : tile_rows == 128 ? Form<128>::KS : tile_rows == 64 ? Form<64>::KS : Form<32>::KS;
+  const int blocks = tile_rows == 256   ? Form<256>::KS
+                     : tile_rows == 128 ? Form<128>::KS
+                     : tile_rows == 64  ? Form<64>::KS
+                                        : Form<32>::KS;
   for (int i = 0; i < 2; ++i)
     if (!make_map(i ? &maps->w3 : &maps->w, CU_TENSOR_MAP_DATA_TYPE_UINT8, i && w3 ? w3 : w, K, (uint64_t)E * N, 1,
                   BK * blocks, w3 ? 64 : 128, blocks == 2 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,

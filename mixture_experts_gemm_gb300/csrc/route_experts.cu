@@ -702,7 +702,8 @@ cudaError_t by_experts(int dtype, int E, F f) {
 int check_route_config(const colibri_moe_route_config_t* c, int32_t T, int64_t ld) {
   if (!c || T < 0) return COLIBRI_ERR_INVALID_ARG;
   if (c->num_experts < 1 || c->top_k < 1 || c->top_k > c->num_experts || !ops_dtype(c->logits_dtype) ||
-      (c->score != COLIBRI_SCORE_SOFTMAX && c->score != COLIBRI_SCORE_SIGMOID) || (c->renormalize & ~1) || (c->trusted_pointers & ~1))
+      (c->score != COLIBRI_SCORE_SOFTMAX && c->score != COLIBRI_SCORE_SIGMOID) || (c->renormalize & ~1) ||
+      (c->trusted_pointers & ~1))
     return COLIBRI_ERR_INVALID_ARG;
   if (c->groups < 1 || c->num_experts % c->groups || c->top_groups < 1 || c->top_groups > c->groups ||
       c->group_top < 1 || c->group_top > 2 || c->top_k > c->top_groups * (c->num_experts / c->groups))

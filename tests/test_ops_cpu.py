@@ -138,6 +138,13 @@ def test_int8_no_rows_and_quantize(moe):
     assert L.colibri_moe_combine_rows(None, 0, 0, None, None, 0, 2, 8, None, 0, None) == 0
 
 
+def test_trusted_pointers_is_a_flag(moe):
+    assert norm_call(moe, cfg=dict(trusted_pointers=2)) == -1
+    assert route_call(moe, trusted_pointers=-1)[0] == -1
+    assert int8_call(moe, trusted_pointers=2) == -1
+    assert norm_call(moe, cfg=dict(trusted_pointers=1), x=None) == -1  # it does not stand for a NULL
+
+
 def test_valid_calls_without_a_gpu_report_cuda_errors(moe):
     torch = pytest.importorskip("torch")
     if torch.cuda.is_available():
