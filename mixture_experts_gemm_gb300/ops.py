@@ -338,16 +338,15 @@ def int8_quantize(x, stream=None):
     """(q int8, scale fp32) of the rows of x [..., K]: scale = max |x| / 127, q = round(x / scale).  Rows of
     activations, or the output channels of weights [E, N, K] once ahead of time."""
     K = x.shape[-1]
-    flat = x.reshape(-1, K)
-    n = flat.shape[0]
     on = _device(x, "x")
-    px, ldx = _matrix(flat, "x", n, K, on)
     c = _int8_config(K, 1, 1, x.dtype, torch.float32)[1]
 
     def call(s):
+        flat = x.reshape(-1, K)  # a copy where x cannot be viewed so: made, read and freed on this call's stream
+        px, ldx = _matrix(flat, "x", flat.shape[0], K, on)
         q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(lib().colibri_moe_int8_quantize(c, px, ldx, n, q.data_ptr(), scale.data_ptr(), s),
+        _check(lib().colibri_moe_int8_quantize(c, px, ldx, flat.shape[0], q.data_ptr(), scale.data_ptr(), s),
                "colibri_moe_int8_quantize")
         return q, scale
     return _run(call, x, on, stream)
