@@ -149,6 +149,8 @@ def _at(t):
 
 
 # ------------------------------------------------------------------------------------------- norms
+# The library reads a config through its address.  Every call holds the (struct, address) pair in a local until the
+# library has returned: the caches may drop a struct while another thread fills them.
 @functools.lru_cache(maxsize=256)
 def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gate, residual_scale, block_scale, eps):
     c = NormConfig(d, _dtype(dtype, "x"), _dtype(block_dtype, "y"), _dtype(param_dtype, "the parameters"),
@@ -159,7 +161,7 @@ def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gat
 
 def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, before, before_weight, before_bias, gate,
                 rows_per_gate, residual_scale, block_scale, eps):
-    """(config's address, gate rows); the parameters' addresses go to this thread's scratch."""
+    """(config, gate rows); the parameters' addresses go to this thread's scratch."""
     pt = torch.float32
     for p in (after_weight, before_weight, gate):
         if p is not None:
@@ -180,7 +182,7 @@ def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, 
                     _vector(after_bias, "after_bias", one, pt, dev) or 0,
                     _vector(before_weight, "before_weight", one, pt, dev) or 0,
                     _vector(before_bias, "before_bias", one, pt, dev) or 0, pg or 0)
-    return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, residual_scale, block_scale, eps)[1], n_gates
+    return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, residual_scale, block_scale, eps), n_gates
 
 
 def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, before="none", before_weight=None,
@@ -201,13 +203,13 @@ def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, b
     dev = _device(x, "x")
     px, ldx = _matrix(x, "x", T, d, dev)
     py, ldy = _matrix(y, "y", T, d, dev) if y is not None else (None, 0)
-    c, _ = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
-                       before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
+    config, _ = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
+                            before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
 
     def call(s):
         x1 = torch.empty((T, d), dtype=dt, device=x.device) if y is not None else None
         p = torch.empty((T, d), dtype=dt, device=x.device) if before != "none" else None
-        _check(lib().colibri_moe_block_norm(c, _scratch.p_vectors, px, ldx, py, ldy, T, _at(x1), _at(p), s),
+        _check(lib().colibri_moe_block_norm(config[1], _scratch.p_vectors, px, ldx, py, ldy, T, _at(x1), _at(p), s),
                "colibri_moe_block_norm")
         return x1, p
     return _run(call, x, dev, stream)
@@ -234,8 +236,9 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
     pp, ldp = _matrix(d_p, "d_p", T, d, on, dt) if d_p is not None else (None, 0)
     px, ldx = _matrix(x1, "x1", T, d, on, dt) if x1 is not None else (None, 0)
     py, ldy = _matrix(y, "y", T, d, on) if y is not None else (None, 0)
-    c, n_gates = _norm_setup(T, d, on, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
-                             before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
+    config, n_gates = _norm_setup(T, d, on, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
+                                  before, before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale,
+                                  eps)
 
     def call(s):
         dev = ref.device
@@ -251,10 +254,11 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
         _five.pack_into(_scratch.grads, 0, *[out[n].data_ptr() if n in out else 0
                                              for n in ("d_wa", "d_ba", "d_wb", "d_bb", "d_g")])
         L = lib()
-        _check(L.colibri_moe_block_norm_backward_workspace(c, T, _scratch.p_size), "colibri_moe_block_norm_backward")
+        _check(L.colibri_moe_block_norm_backward_workspace(config[1], T, _scratch.p_size),
+               "colibri_moe_block_norm_backward")
         n = _scratch.size.value
         ws = _workspace(n, dev)
-        _check(L.colibri_moe_block_norm_backward(c, _scratch.p_vectors, p1, ld1, pp, ldp, px, ldx, py, ldy, T,
+        _check(L.colibri_moe_block_norm_backward(config[1], _scratch.p_vectors, p1, ld1, pp, ldp, px, ldx, py, ldy, T,
                                                  _at(out["d_x"]), _at(out.get("d_y")), _scratch.p_grads, _at(ws), n, s),
                "colibri_moe_block_norm_backward")
         return out
@@ -293,17 +297,17 @@ def route(logits, top_k: int, *, score="softmax", bias=None, groups=1, top_group
     pl, ld = _matrix(logits, "logits", T, E, on)
     pb = _vector(bias, "bias", (E,), torch.float32, on)
     k = top_k
-    c = _route_config(E, k, score, groups, top_groups, group_top, renormalize, logits.dtype, scale)[1]
+    config = _route_config(E, k, score, groups, top_groups, group_top, renormalize, logits.dtype, scale)
 
     def call(s):
         L, dev, i32 = lib(), logits.device, torch.int32
-        _check(L.colibri_moe_route_experts_workspace(c, T, _scratch.p_size), "colibri_moe_route_experts")
+        _check(L.colibri_moe_route_experts_workspace(config[1], T, _scratch.p_size), "colibri_moe_route_experts")
         size = _scratch.size.value
         r = Routing(torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
                     torch.empty(E, dtype=i32, device=dev), torch.empty(E + 1, dtype=i32, device=dev),
                     torch.empty((T, k), dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev))
         ws = _workspace(size, dev)
-        _check(L.colibri_moe_route_experts(c, pl, ld, pb, T, *[t.data_ptr() for t in r], _at(ws), size, s),
+        _check(L.colibri_moe_route_experts(config[1], pl, ld, pb, T, *[t.data_ptr() for t in r], _at(ws), size, s),
                "colibri_moe_route_experts")
         return r
     return _run(call, logits, on, stream)
@@ -317,11 +321,11 @@ def route_backward(logits, idx, d_gate, *, score="softmax", renormalize=True, sc
     k = _shape(idx, "idx")[1]
     pi = _vector(idx, "idx", (T, k), torch.int32, on)
     pg = _vector(d_gate, "d_gate", (T, k), torch.float32, on)
-    c = _route_config(E, k, score, 1, 1, 1, renormalize, logits.dtype, scale)[1]
+    config = _route_config(E, k, score, 1, 1, 1, renormalize, logits.dtype, scale)
 
     def call(s):
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-        _check(lib().colibri_moe_route_experts_backward(c, pl, ld, pi, pg, T, out.data_ptr(), E, s),
+        _check(lib().colibri_moe_route_experts_backward(config[1], pl, ld, pi, pg, T, out.data_ptr(), E, s),
                "colibri_moe_route_experts_backward")
         return out
     return _run(call, logits, on, stream)
@@ -339,14 +343,14 @@ def int8_quantize(x, stream=None):
     activations, or the output channels of weights [E, N, K] once ahead of time."""
     K = x.shape[-1]
     on = _device(x, "x")
-    c = _int8_config(K, 1, 1, x.dtype, torch.float32)[1]
+    config = _int8_config(K, 1, 1, x.dtype, torch.float32)
 
     def call(s):
         flat = x.reshape(-1, K)  # a copy where x cannot be viewed so: made, read and freed on this call's stream
         px, ldx = _matrix(flat, "x", flat.shape[0], K, on)
         q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
         scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(lib().colibri_moe_int8_quantize(c, px, ldx, flat.shape[0], q.data_ptr(), scale.data_ptr(), s),
+        _check(lib().colibri_moe_int8_quantize(config[1], px, ldx, flat.shape[0], q.data_ptr(), scale.data_ptr(), s),
                "colibri_moe_int8_quantize")
         return q, scale
     return _run(call, x, on, stream)
@@ -377,16 +381,16 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
     R = n if rows is None else rows.numel()
     pr = _vector(rows, "rows", (R,), i32, on)
     out_dtype = x.dtype if out_dtype is None else out_dtype
-    c = _int8_config(K, N, E, x.dtype, out_dtype)[1]
+    config = _int8_config(K, N, E, x.dtype, out_dtype)
 
     def call(s):
         L = lib()
-        _check(L.colibri_moe_int8_experts_workspace(c, n, R, _scratch.p_size), "colibri_moe_int8_experts")
+        _check(L.colibri_moe_int8_experts_workspace(config[1], n, R, _scratch.p_size), "colibri_moe_int8_experts")
         size = _scratch.size.value
         ws = _workspace(size, x.device)
         y = torch.empty((R, N), dtype=out_dtype, device=x.device)
-        _check(L.colibri_moe_int8_experts(c, px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws), size, s),
-               "colibri_moe_int8_experts")
+        _check(L.colibri_moe_int8_experts(config[1], px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws), size,
+                                          s), "colibri_moe_int8_experts")
         return y
     return _run(call, x, on, stream)
 

@@ -1,5 +1,8 @@
 """The host side of ops.py without a GPU: CPU tensors that say they are on CUDA device 0, and a library that
 looks at the arguments it is given instead of launching anything."""
+import gc
+import weakref
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -67,3 +70,60 @@ def test_quantize_copies_on_its_stream(host):
         assert px % 4 == 0 and ldx >= x.shape[-1] and n == scale.numel()
     with pytest.raises(ValueError, match="contiguous"):
         ops.int8_quantize(w[0].t().as_subclass(Watched))
+
+
+def calls(ops):
+    """One call of each kind, over small tensors."""
+    x, y, w = cuda(torch.ones(4, 32)), cuda(torch.ones(4, 32)), cuda(torch.ones(32))
+    idx, i32 = cuda(torch.zeros(4, 2, dtype=torch.int32)), torch.int32
+    w8, ws = cuda(torch.ones(2, 8, 32, dtype=torch.int8)), cuda(torch.ones(2, 8))
+    norms = dict(after="rms", after_weight=w, before="rms", before_weight=w)
+    return dict(
+        block_norm=lambda: ops.block_norm(x, y, **norms),
+        block_norm_backward=lambda: ops.block_norm_backward(x, x, x, y, **norms),
+        route=lambda: ops.route(x, 2),
+        route_experts_backward=lambda: ops.route_backward(x, idx, cuda(torch.ones(4, 2))),
+        int8_quantize=lambda: ops.int8_quantize(x),
+        int8_experts=lambda: ops.int8_experts(x, w8, ws, cuda(torch.zeros(3, dtype=i32))))
+
+
+@pytest.mark.parametrize("name", ["block_norm", "block_norm_backward", "route", "route_experts_backward",
+                                  "int8_quantize", "int8_experts"])
+def test_configs_outlive_their_call(host, monkeypatch, name):
+    """Other threads may bring any number of other configs while a call is in the allocator: what the call gives
+    the library stays in memory until the library returns."""
+    ops, library, _ = host
+    alive = {}
+
+    def watched(kind):
+        class Config(kind):
+            def __init__(self, *args):
+                super().__init__(*args)
+                alive.setdefault(ops.ctypes.addressof(self), weakref.ref(self))  # the first one there: the call's
+        return Config
+
+    for kind in ("NormConfig", "RouteConfig", "Int8Config"):
+        monkeypatch.setattr(ops, kind, watched(getattr(ops, kind)))
+    caches = [ops._norm_config, ops._route_config, ops._int8_config]
+    for c in caches:
+        c.cache_clear()
+    real, looked = torch.empty, []
+
+    def empty(*args, **kw):
+        for i in range(300):
+            ops._norm_config(i + 100, torch.float32, torch.float32, torch.float32, "rms", "rms", 0, 1.0, 1.0, 1e-6)
+            ops._route_config(i + 100, 2, "softmax", 1, 1, 1, True, torch.float32, 1.0)
+            ops._int8_config(i + 100, 8, 1, torch.float32, torch.float32)
+        gc.collect()
+        return real(*args, **kw)
+
+    def see(c, *args):
+        looked.append(alive[c]() is not None)
+
+    whole = {"route": "route_experts"}.get(name, name)
+    library.see["colibri_moe_" + whole] = library.see[f"colibri_moe_{whole}_workspace"] = see
+    monkeypatch.setattr(torch, "empty", empty)
+    calls(ops)[name]()
+    for c in caches:
+        c.cache_clear()
+    assert looked and all(looked)
