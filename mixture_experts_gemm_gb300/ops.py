@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import struct
 import threading
 from typing import NamedTuple, Optional
@@ -150,12 +151,13 @@ def _at(t):
 
 # ------------------------------------------------------------------------------------------- norms
 # The library reads a config through its address.  Every call holds the (struct, address) pair in a local until the
-# library has returned: the caches may drop a struct while another thread fills them.
+# library has returned: the caches may drop a struct while another thread fills them.  Scalars are plain numbers by
+# then: a tensor would be found again by its identity, whatever it holds now.
 @functools.lru_cache(maxsize=256)
 def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gate, residual_scale, block_scale, eps):
     c = NormConfig(d, _dtype(dtype, "x"), _dtype(block_dtype, "y"), _dtype(param_dtype, "the parameters"),
-                   _kind(_NORMS, after, "after"), _kind(_NORMS, before, "before"), rows_per_gate, float(residual_scale),
-                   float(block_scale), float(eps), 1)
+                   _kind(_NORMS, after, "after"), _kind(_NORMS, before, "before"), rows_per_gate, residual_scale,
+                   block_scale, eps, 1)
     return c, ctypes.addressof(c)
 
 
@@ -182,7 +184,8 @@ def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, 
                     _vector(after_bias, "after_bias", one, pt, dev) or 0,
                     _vector(before_weight, "before_weight", one, pt, dev) or 0,
                     _vector(before_bias, "before_bias", one, pt, dev) or 0, pg or 0)
-    return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, residual_scale, block_scale, eps), n_gates
+    return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, float(residual_scale), float(block_scale),
+                        float(eps)), n_gates
 
 
 def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, before="none", before_weight=None,
@@ -278,8 +281,8 @@ class Routing(NamedTuple):
 
 @functools.lru_cache(maxsize=256)
 def _route_config(E, k, score, groups, top_groups, group_top, renormalize, dtype, scale):
-    c = RouteConfig(E, k, _kind(_SCORES, score, "score"), groups, top_groups, group_top, int(bool(renormalize)),
-                    _dtype(dtype, "logits"), float(scale), 1)
+    c = RouteConfig(E, k, _kind(_SCORES, score, "score"), groups, top_groups, group_top, int(renormalize),
+                    _dtype(dtype, "logits"), scale, 1)
     return c, ctypes.addressof(c)
 
 
@@ -296,8 +299,9 @@ def route(logits, top_k: int, *, score="softmax", bias=None, groups=1, top_group
     on = _device(logits, "logits")
     pl, ld = _matrix(logits, "logits", T, E, on)
     pb = _vector(bias, "bias", (E,), torch.float32, on)
-    k = top_k
-    config = _route_config(E, k, score, groups, top_groups, group_top, renormalize, logits.dtype, scale)
+    k, index = operator.index(top_k), operator.index
+    config = _route_config(E, k, score, index(groups), index(top_groups), index(group_top), bool(renormalize),
+                           logits.dtype, float(scale))
 
     def call(s):
         L, dev, i32 = lib(), logits.device, torch.int32
@@ -321,7 +325,7 @@ def route_backward(logits, idx, d_gate, *, score="softmax", renormalize=True, sc
     k = _shape(idx, "idx")[1]
     pi = _vector(idx, "idx", (T, k), torch.int32, on)
     pg = _vector(d_gate, "d_gate", (T, k), torch.float32, on)
-    config = _route_config(E, k, score, 1, 1, 1, renormalize, logits.dtype, scale)
+    config = _route_config(E, k, score, 1, 1, 1, bool(renormalize), logits.dtype, float(scale))
 
     def call(s):
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)

@@ -127,3 +127,25 @@ def test_configs_outlive_their_call(host, monkeypatch, name):
     for c in caches:
         c.cache_clear()
     assert looked and all(looked)
+
+
+def test_scalars_are_read_at_every_call(host):
+    """A scalar held in a tensor (a schedule's, a counter's) and changed in place between two calls."""
+    ops, library, _ = host
+    seen = []
+    library.see["colibri_moe_block_norm"] = lambda c, *a: seen.append(
+        [getattr(ops.NormConfig.from_address(c), n) for n in ("residual_scale", "block_scale", "eps", "rows_per_gate")])
+    library.see["colibri_moe_route_experts"] = lambda c, *a: seen.append(
+        [getattr(ops.RouteConfig.from_address(c), n) for n in ("top_k", "groups", "top_groups", "group_top", "scale")])
+    x, y, w, logits = cuda(torch.ones(4, 32)), cuda(torch.ones(4, 32)), cuda(torch.ones(2, 32)), cuda(torch.ones(4, 16))
+    scalars, counts = [torch.tensor(0.5) for _ in range(4)], [torch.tensor(v) for v in (2, 4, 2, 1)]
+    for step in (1, 2):
+        for v in scalars:
+            v.fill_(0.5 * step)
+        ops.block_norm(x, y, gate=w, rows_per_gate=2, residual_scale=scalars[0], block_scale=scalars[1], eps=scalars[2])
+        assert seen.pop() == [0.5 * step] * 3 + [2]
+        counts[0].fill_(2 * step), counts[3].fill_(step)
+        r = ops.route(logits, counts[0], groups=counts[1], top_groups=counts[2], group_top=counts[3], scale=scalars[3])
+        assert seen.pop() == [2 * step, 4, 2, step, 0.5 * step] and r.idx.shape == (4, 2 * step)
+    with pytest.raises(TypeError):
+        ops.route(logits, 2.0)
