@@ -19,7 +19,6 @@ import ctypes
 import functools
 import operator
 import struct
-import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -126,19 +125,8 @@ def _run(f, t, dev: int, stream):
         return f(s)
 
 
-class _Scratch(threading.local):
-    """Arguments that the library reads during a call, a set for each thread: a size and two structs of five
-    pointers (colibri_moe_norm_params_t, colibri_moe_norm_grads_t)."""
-
-    def __init__(self):
-        self.size = ctypes.c_size_t()
-        self.p_size = ctypes.addressof(self.size)
-        self.vectors, self.grads = (ctypes.c_char * 40)(), (ctypes.c_char * 40)()
-        self.p_vectors, self.p_grads = ctypes.addressof(self.vectors), ctypes.addressof(self.grads)
-
-
-_scratch = _Scratch()
-_five = struct.Struct("5P")
+# Five pointers: colibri_moe_norm_params_t and colibri_moe_norm_grads_t.  Every call packs and holds its own.
+_five = struct.Struct("5P").pack
 
 
 def _workspace(n: int, device):
@@ -163,7 +151,7 @@ def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gat
 
 def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, before, before_weight, before_bias, gate,
                 rows_per_gate, residual_scale, block_scale, eps):
-    """(config, gate rows); the parameters' addresses go to this thread's scratch."""
+    """(config, gate rows, the parameters' addresses)."""
     pt = torch.float32
     for p in (after_weight, before_weight, gate):
         if p is not None:
@@ -180,12 +168,12 @@ def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, 
         n_gates = -(-T // rpg) if T else gate.shape[0]
         pg = _vector(gate, "gate", (n_gates, d), pt, dev)
     one = (d,)
-    _five.pack_into(_scratch.vectors, 0, _vector(after_weight, "after_weight", one, pt, dev) or 0,
+    vectors = _five(_vector(after_weight, "after_weight", one, pt, dev) or 0,
                     _vector(after_bias, "after_bias", one, pt, dev) or 0,
                     _vector(before_weight, "before_weight", one, pt, dev) or 0,
                     _vector(before_bias, "before_bias", one, pt, dev) or 0, pg or 0)
     return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, float(residual_scale), float(block_scale),
-                        float(eps)), n_gates
+                        float(eps)), n_gates, vectors
 
 
 def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, before="none", before_weight=None,
@@ -206,13 +194,14 @@ def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, b
     dev = _device(x, "x")
     px, ldx = _matrix(x, "x", T, d, dev)
     py, ldy = _matrix(y, "y", T, d, dev) if y is not None else (None, 0)
-    config, _ = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias, before,
-                            before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale, eps)
+    config, _, vectors = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
+                                     before, before_weight, before_bias, gate, rows_per_gate, residual_scale,
+                                     block_scale, eps)
 
     def call(s):
         x1 = torch.empty((T, d), dtype=dt, device=x.device) if y is not None else None
         p = torch.empty((T, d), dtype=dt, device=x.device) if before != "none" else None
-        _check(lib().colibri_moe_block_norm(config[1], _scratch.p_vectors, px, ldx, py, ldy, T, _at(x1), _at(p), s),
+        _check(lib().colibri_moe_block_norm(config[1], vectors, px, ldx, py, ldy, T, _at(x1), _at(p), s),
                "colibri_moe_block_norm")
         return x1, p
     return _run(call, x, dev, stream)
@@ -239,9 +228,9 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
     pp, ldp = _matrix(d_p, "d_p", T, d, on, dt) if d_p is not None else (None, 0)
     px, ldx = _matrix(x1, "x1", T, d, on, dt) if x1 is not None else (None, 0)
     py, ldy = _matrix(y, "y", T, d, on) if y is not None else (None, 0)
-    config, n_gates = _norm_setup(T, d, on, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
-                                  before, before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale,
-                                  eps)
+    config, n_gates, vectors = _norm_setup(T, d, on, dt, y.dtype if y is not None else dt, after, after_weight,
+                                           after_bias, before, before_weight, before_bias, gate, rows_per_gate,
+                                           residual_scale, block_scale, eps)
 
     def call(s):
         dev = ref.device
@@ -254,15 +243,15 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
                 out[name] = torch.empty(d, dtype=torch.float32, device=dev)
         if gate is not None:
             out["d_g"] = (torch.empty if T else torch.zeros)((n_gates, d), dtype=torch.float32, device=dev)
-        _five.pack_into(_scratch.grads, 0, *[out[n].data_ptr() if n in out else 0
-                                             for n in ("d_wa", "d_ba", "d_wb", "d_bb", "d_g")])
+        grads = _five(*[out[n].data_ptr() if n in out else 0 for n in ("d_wa", "d_ba", "d_wb", "d_bb", "d_g")])
         L = lib()
-        _check(L.colibri_moe_block_norm_backward_workspace(config[1], T, _scratch.p_size),
+        size = ctypes.c_size_t()
+        _check(L.colibri_moe_block_norm_backward_workspace(config[1], T, ctypes.byref(size)),
                "colibri_moe_block_norm_backward")
-        n = _scratch.size.value
+        n = size.value
         ws = _workspace(n, dev)
-        _check(L.colibri_moe_block_norm_backward(config[1], _scratch.p_vectors, p1, ld1, pp, ldp, px, ldx, py, ldy, T,
-                                                 _at(out["d_x"]), _at(out.get("d_y")), _scratch.p_grads, _at(ws), n, s),
+        _check(L.colibri_moe_block_norm_backward(config[1], vectors, p1, ld1, pp, ldp, px, ldx, py, ldy, T,
+                                                 _at(out["d_x"]), _at(out.get("d_y")), grads, _at(ws), n, s),
                "colibri_moe_block_norm_backward")
         return out
     return _run(call, ref, on, stream)
@@ -305,8 +294,9 @@ def route(logits, top_k: int, *, score="softmax", bias=None, groups=1, top_group
 
     def call(s):
         L, dev, i32 = lib(), logits.device, torch.int32
-        _check(L.colibri_moe_route_experts_workspace(config[1], T, _scratch.p_size), "colibri_moe_route_experts")
-        size = _scratch.size.value
+        need = ctypes.c_size_t()
+        _check(L.colibri_moe_route_experts_workspace(config[1], T, ctypes.byref(need)), "colibri_moe_route_experts")
+        size = need.value
         r = Routing(torch.empty((T, k), dtype=i32, device=dev), torch.empty((T, k), dtype=torch.float32, device=dev),
                     torch.empty(E, dtype=i32, device=dev), torch.empty(E + 1, dtype=i32, device=dev),
                     torch.empty((T, k), dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev))
@@ -389,8 +379,9 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
 
     def call(s):
         L = lib()
-        _check(L.colibri_moe_int8_experts_workspace(config[1], n, R, _scratch.p_size), "colibri_moe_int8_experts")
-        size = _scratch.size.value
+        need = ctypes.c_size_t()
+        _check(L.colibri_moe_int8_experts_workspace(config[1], n, R, ctypes.byref(need)), "colibri_moe_int8_experts")
+        size = need.value
         ws = _workspace(size, x.device)
         y = torch.empty((R, N), dtype=out_dtype, device=x.device)
         _check(L.colibri_moe_int8_experts(config[1], px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws), size,

@@ -149,3 +149,41 @@ def test_scalars_are_read_at_every_call(host):
         assert seen.pop() == [2 * step, 4, 2, step, 0.5 * step] and r.idx.shape == (4, 2 * step)
     with pytest.raises(TypeError):
         ops.route(logits, 2.0)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_calls_inside_a_call(host, monkeypatch, backward):
+    """A call that runs while another one of the same thread is in the allocator (a finaliser, a mode's hook) leaves
+    the outer call's vectors alone."""
+    ops, library, _ = host
+    x, y = cuda(torch.ones(4, 32)), cuda(torch.ones(4, 32))
+    vectors = [cuda(torch.ones(32)) for _ in range(4)]
+    seen, nested = [], []
+
+    def look(address):
+        return list(ops.ctypes.cast(address, ops.ctypes.POINTER(ops.ctypes.c_void_p))[:5])
+
+    def one(a, b):
+        norms = dict(after="rms", after_weight=a, before="rms", before_weight=b)
+        return ops.block_norm_backward(x, x, x, y, **norms) if backward else ops.block_norm(x, y, **norms)
+
+    def see(*args):
+        seen.append([look(args[1])] + ([look(args[13])] if backward else []))
+
+    library.see["colibri_moe_block_norm_backward" if backward else "colibri_moe_block_norm"] = see
+    real = torch.empty
+
+    def empty(*args, **kw):
+        t = real(*args, **kw)
+        if not nested:
+            nested.append(None)
+            nested[0] = one(*vectors[2:])
+        return t
+
+    monkeypatch.setattr(torch, "empty", empty)
+    out = one(*vectors[:2])
+    inner, outer = seen
+    for s, v, o in ((inner, vectors[2:], nested[0]), (outer, vectors[:2], out)):
+        assert s[0] == [v[0].data_ptr(), None, v[1].data_ptr(), None, None]
+        if backward:
+            assert s[1] == [o["d_wa"].data_ptr(), None, o["d_wb"].data_ptr(), None, None]
