@@ -151,13 +151,13 @@ def _norm_config(d, dtype, block_dtype, param_dtype, after, before, rows_per_gat
 
 def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, before, before_weight, before_bias, gate,
                 rows_per_gate, residual_scale, block_scale, eps):
-    """(config, gate rows, the parameters' addresses)."""
+    """(config, the parameters' addresses)."""
     pt = torch.float32
     for p in (after_weight, before_weight, gate):
         if p is not None:
             pt = p.dtype
             break
-    rpg = n_gates = 0
+    rpg = 0
     pg = None
     if gate is not None:
         if gate.dim() == 1:
@@ -173,7 +173,7 @@ def _norm_setup(T, d, dev, dtype, block_dtype, after, after_weight, after_bias, 
                     _vector(before_weight, "before_weight", one, pt, dev) or 0,
                     _vector(before_bias, "before_bias", one, pt, dev) or 0, pg or 0)
     return _norm_config(d, dtype, block_dtype, pt, after, before, rpg, float(residual_scale), float(block_scale),
-                        float(eps)), n_gates, vectors
+                        float(eps)), vectors
 
 
 def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, before="none", before_weight=None,
@@ -194,9 +194,9 @@ def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, b
     dev = _device(x, "x")
     px, ldx = _matrix(x, "x", T, d, dev)
     py, ldy = _matrix(y, "y", T, d, dev) if y is not None else (None, 0)
-    config, _, vectors = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
-                                     before, before_weight, before_bias, gate, rows_per_gate, residual_scale,
-                                     block_scale, eps)
+    config, vectors = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
+                                  before, before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale,
+                                  eps)
 
     def call(s):
         x1 = torch.empty((T, d), dtype=dt, device=x.device) if y is not None else None
@@ -216,8 +216,9 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
                         before_weight=None, before_bias=None, gate=None, rows_per_gate=None, residual_scale=1.0,
                         block_scale=1.0, eps=1e-6, stream=None):
     """Gradients of block_norm from those of its results, as a dict: d_x, d_y, and in fp32 d_wa, d_ba
-    (after), d_wb, d_bb (before), d_g, whichever the call has.  x1 and y are the forward call's (x1: x
-    itself without y); d_x1 may be None where there is a next norm, d_p is None where there is none."""
+    (after), d_wb, d_bb (before), d_g (in the gate's shape), whichever the call has.  x1 and y are the
+    forward call's (x1: x itself without y); d_x1 may be None where there is a next norm, d_p is None
+    where there is none."""
     ref = d_x1 if d_x1 is not None else d_p
     if ref is None:
         raise ValueError("one of d_x1 and d_p is needed")
@@ -228,9 +229,9 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
     pp, ldp = _matrix(d_p, "d_p", T, d, on, dt) if d_p is not None else (None, 0)
     px, ldx = _matrix(x1, "x1", T, d, on, dt) if x1 is not None else (None, 0)
     py, ldy = _matrix(y, "y", T, d, on) if y is not None else (None, 0)
-    config, n_gates, vectors = _norm_setup(T, d, on, dt, y.dtype if y is not None else dt, after, after_weight,
-                                           after_bias, before, before_weight, before_bias, gate, rows_per_gate,
-                                           residual_scale, block_scale, eps)
+    config, vectors = _norm_setup(T, d, on, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
+                                  before, before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale,
+                                  eps)
 
     def call(s):
         dev = ref.device
@@ -242,7 +243,7 @@ def block_norm_backward(d_x1, d_p, x1, y=None, *, after="none", after_weight=Non
             if param is not None:
                 out[name] = torch.empty(d, dtype=torch.float32, device=dev)
         if gate is not None:
-            out["d_g"] = (torch.empty if T else torch.zeros)((n_gates, d), dtype=torch.float32, device=dev)
+            out["d_g"] = (torch.empty if T else torch.zeros)(gate.shape, dtype=torch.float32, device=dev)
         grads = _five(*[out[n].data_ptr() if n in out else 0 for n in ("d_wa", "d_ba", "d_wb", "d_bb", "d_g")])
         L = lib()
         size = ctypes.c_size_t()

@@ -187,3 +187,12 @@ def test_calls_inside_a_call(host, monkeypatch, backward):
         assert s[0] == [v[0].data_ptr(), None, v[1].data_ptr(), None, None]
         if backward:
             assert s[1] == [o["d_wa"].data_ptr(), None, o["d_wb"].data_ptr(), None, None]
+
+
+@pytest.mark.parametrize("T", [0, 4])
+def test_gate_gradient_has_the_gate_s_shape(host, T):
+    ops, library, _ = host
+    x, d = cuda(torch.ones(T, 32)), 32
+    for shape, per_gate in (((d,), None), ((1, d), None), ((2, d), 2)):
+        out = ops.block_norm_backward(x, None, x, x, gate=cuda(torch.ones(shape)), rows_per_gate=per_gate)
+        assert out["d_g"].shape == shape
