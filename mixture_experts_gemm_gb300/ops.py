@@ -6,7 +6,9 @@ order (``route``), experts in 8-bit integers (``int8_experts``) and their combin
 the backward passes of the norms and of the routing.  Every call runs on CUDA tensors, asynchronously
 on ``stream`` (default: the current stream), allocates its outputs and workspace from torch, and can be
 captured into a CUDA graph.  Errors raise ``ColibriError`` (checks of the library) or ``ValueError``
-(shapes and types that cannot be passed on).
+(shapes and types that cannot be passed on).  Results are not attached to autograd: the backward passes
+are calls of their own, and a call on tensors that ask for a gradient warns.  With a ``stream`` of its own
+a call orders nothing: its inputs must be ready there and stay alive until that stream has read them.
 
     x1, p = block_norm(x, y, after="rms", after_weight=w_a, before="rms", before_weight=w_b)
     r = route(logits, 8, score="sigmoid", bias=b, groups=8, top_groups=4, group_top=2, scale=2.5)
@@ -19,6 +21,7 @@ import ctypes
 import functools
 import operator
 import struct
+import warnings
 from typing import NamedTuple, Optional
 
 import torch
@@ -125,6 +128,15 @@ def _run(f, t, dev: int, stream):
         return f(s)
 
 
+def _unattached(name: str, gradient: str, *tensors):
+    """Says that a call's results leave autograd's graph, where one of its tensors asks for a gradient."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"{name}: the result is not attached to autograd and carries no gradient; {gradient}. Under "
+                          "torch.no_grad(), or with detached tensors, this is not said", stacklevel=3)
+            return
+
+
 # Five pointers: colibri_moe_norm_params_t and colibri_moe_norm_grads_t.  Every call packs and holds its own.
 _five = struct.Struct("5P").pack
 
@@ -197,6 +209,8 @@ def block_norm(x, y=None, *, after="none", after_weight=None, after_bias=None, b
     config, vectors = _norm_setup(T, d, dev, dt, y.dtype if y is not None else dt, after, after_weight, after_bias,
                                   before, before_weight, before_bias, gate, rows_per_gate, residual_scale, block_scale,
                                   eps)
+    _unattached("block_norm", "block_norm_backward computes it", x, y, after_weight, after_bias, before_weight,
+                before_bias, gate)
 
     def call(s):
         x1 = torch.empty((T, d), dtype=dt, device=x.device) if y is not None else None
@@ -292,6 +306,7 @@ def route(logits, top_k: int, *, score="softmax", bias=None, groups=1, top_group
     k, index = operator.index(top_k), operator.index
     config = _route_config(E, k, score, index(groups), index(top_groups), index(group_top), bool(renormalize),
                            logits.dtype, float(scale))
+    _unattached("route", "route_backward computes that of the gates", logits)
 
     def call(s):
         L, dev, i32 = lib(), logits.device, torch.int32
@@ -339,6 +354,7 @@ def int8_quantize(x, stream=None):
     K = x.shape[-1]
     on = _device(x, "x")
     config = _int8_config(K, 1, 1, x.dtype, torch.float32)
+    _unattached("int8_quantize", "there is no backward pass", x)
 
     def call(s):
         flat = x.reshape(-1, K)  # a copy where x cannot be viewed so: made, read and freed on this call's stream
@@ -377,6 +393,7 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
     pr = _vector(rows, "rows", (R,), i32, on)
     out_dtype = x.dtype if out_dtype is None else out_dtype
     config = _int8_config(K, N, E, x.dtype, out_dtype)
+    _unattached("int8_experts", "there is no backward pass", x, w_scale, w3_scale)
 
     def call(s):
         L = lib()
@@ -401,6 +418,7 @@ def combine(y, row_of, gate, *, out_dtype=None, stream=None):
     pg = _vector(gate, "gate", (T, k), torch.float32, on)
     out_dtype = y.dtype if out_dtype is None else out_dtype
     types = _dtype(y.dtype, "y"), _dtype(out_dtype, "out_dtype")
+    _unattached("combine", "there is no backward pass", y, gate)
 
     def call(s):
         out = torch.empty((T, d), dtype=out_dtype, device=y.device)

@@ -196,3 +196,39 @@ def test_gate_gradient_has_the_gate_s_shape(host, T):
     for shape, per_gate in (((d,), None), ((1, d), None), ((2, d), 2)):
         out = ops.block_norm_backward(x, None, x, x, gate=cuda(torch.ones(shape)), rows_per_gate=per_gate)
         assert out["d_g"].shape == shape
+
+
+@pytest.mark.parametrize("name", ["block_norm", "route", "int8_quantize", "int8_experts", "combine"])
+def test_a_lost_gradient_is_said(host, name):
+    """Results are not attached to autograd: a call on tensors that ask for a gradient says so, unless gradients are
+    off; it still runs."""
+    import warnings
+    ops, _, _ = host
+    x, y = cuda(torch.ones(4, 32)), cuda(torch.ones(4, 32))
+    w8 = cuda(torch.ones(2, 8, 32, dtype=torch.int8))
+
+    def call(x, y):
+        if name == "block_norm":
+            return ops.block_norm(x, y)
+        if name == "route":
+            return ops.route(x, 2)
+        if name == "int8_quantize":
+            return ops.int8_quantize(x)
+        if name == "int8_experts":
+            return ops.int8_experts(x, w8, cuda(torch.ones(2, 8)), cuda(torch.zeros(3, dtype=torch.int32)))
+        return ops.combine(x, cuda(torch.zeros(2, 2, dtype=torch.int32)), cuda(torch.ones(2, 2)))
+
+    leaf = cuda(torch.ones(4, 32)).requires_grad_(True)
+    with pytest.warns(UserWarning, match="autograd"):
+        call(leaf, y)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        call(x, y)
+        with torch.no_grad():
+            call(leaf, y)
+        call(leaf.detach(), y)
+    if name == "block_norm":
+        with pytest.warns(UserWarning, match="autograd"):
+            call(x, leaf)
+        with pytest.warns(UserWarning, match="autograd"):
+            ops.pre_norm(x, cuda(torch.ones(32)).requires_grad_(True))
