@@ -384,7 +384,8 @@ COLIBRI_API int colibri_moe_block_norm_backward(const colibri_moe_norm_config_t*
  *   groups: the experts in `groups` equal runs; a group's score is the sum of its group_top largest s_e +
  *           bias_e (group_top 1 without a bias: its largest logit); the top_groups best groups are kept
  *   idx    = the top_k experts of the kept groups by (key descending, index ascending), groups likewise
- *   gate   = scale * s_idx, divided by the sum of the chosen s if renormalize (0 / 0 gives 0)
+ *   gate   = scale * s_idx, divided by the sum of the chosen s if renormalize (0 / 0 gives 0; scores far below
+ *            fp32's range keep their ratios, below e^-700 they are 0)
  * The ranking is that of the keys evaluated in 64 bits.  An expert whose logit or bias is -inf or NaN
  * is masked: it is never chosen (a NaN logit counts as -inf).  A token with fewer than top_k experts
  * left gets idx -1, gate 0, row_of -1 in its last slots.

@@ -303,15 +303,17 @@ struct RouteScratch {
   int16_t expert[kRouteMaxK];
 };
 
-// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score.
+// Routes token t with one warp: lane i (i < k) returns its expert (-1: none) and its score; m, the softmax's
+// largest logit (0 for sigmoids).
 template <typename L, int NS>
 __device__ __forceinline__ void route_token(const RouteManyArgs& a, const Experts<NS>& ex, int t,
-                                            RouteScratch& scratch, int& sel, float& s_sel) {
+                                            RouteScratch& scratch, int& sel, float& s_sel, float& m) {
   const int lane = threadIdx.x & 31;
   const int e0 = lane * NS;
   float key[NS];
   load_logits<L, NS>(a, t, e0, key);
-  float m = 0.f, inv = 0.f;
+  float inv = 0.f;
+  m = 0.f;
   auto raw_score = [&](float v) { return v == -INFINITY ? 0.f : (v == m ? 1.f : expf(v - m)); };
   if (a.softmax) {
     m = -INFINITY;
@@ -459,6 +461,22 @@ __device__ __forceinline__ void route_token(const RouteManyArgs& a, const Expert
   }
 }
 
+// Gates that divide by the chosen scores' sum hang on the scores' ratios alone, which stay what they are where
+// fp32 loses the scores themselves (a sigmoid below a logit of about -88, a softmax of experts that far below
+// the row's largest).  A token with a chosen score below kTinyScore takes its scores less a factor that is
+// common to all of them: softmax, e^largest of the chosen over the row's sum; sigmoid, where s = e^l / (1 + e^l),
+// e^largest if that is below one (else the largest score is a half or more, and what is lost is below 2^-125).
+// Scores that 64 bits lose too, below e^-700, are zero: a logit of the type's lowest value is as good as masked.
+// base: the softmax's largest logit, 0 for sigmoids.
+constexpr float kTinyScore = 0x1p-100f;
+__device__ __forceinline__ float relative_score(bool live, float l, float base, bool softmax) {
+  if (l - base < -700.f) live = false;
+  const float top = warp_max(live ? l : -INFINITY);
+  if (!live) return 0.f;
+  if (softmax) return l == top ? 1.f : expf(l - top);
+  return top < 0.f ? expf(l - top) / (1.f + expf(l)) : 1.f / (1.f + expf(-l));
+}
+
 // offsets[e] = rows before expert e, from counts in shared memory, by one warp; returns nothing past it.
 __device__ __forceinline__ void scan_counts(const int* counts, int* offsets, int E) {
   const int lane = threadIdx.x & 31;
@@ -503,8 +521,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NS <= 8 ? 2 : 1)
   __syncthreads();
   for (int i = warp; i < n; i += warps) {
     int sel;
-    float s;
-    route_token<L, NS>(a, ex, t0 + i, scratch[warp], sel, s);
+    float s, base;
+    route_token<L, NS>(a, ex, t0 + i, scratch[warp], sel, s, base);
+    if (a.renorm && __any_sync(~0u, sel >= 0 && s < kTinyScore)) {
+      const L* row = static_cast<const L*>(a.logits) + (t0 + i) * a.ld;
+      s = relative_score(sel >= 0, sel >= 0 ? to_float(row[sel]) : 0.f, base, a.softmax);
+    }
     const float sum = warp_sum(lane < a.k ? s : 0.f);
     if (lane < a.k) {
       const int64_t o = (int64_t)(t0 + i) * a.k + lane;
@@ -667,7 +689,9 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackArgs a) {
     }
     if (!a.softmax) {
       if (a.renorm) {
-        const float s = e >= 0 ? v[0] : 0.f, sum = warp_sum(s), q = sum > 0.f ? s / sum : 0.f;
+        float s = e >= 0 ? v[0] : 0.f;
+        if (__any_sync(~0u, e >= 0 && s < kTinyScore)) s = relative_score(e >= 0, l, 0.f, false);
+        const float sum = warp_sum(s), q = sum > 0.f ? s / sum : 0.f;
         const float mean = warp_sum(q * g);
         if (e >= 0) mine[e] = a.scale * q * (g - mean) * common;
       } else if (e >= 0) {

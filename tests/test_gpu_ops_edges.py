@@ -1,5 +1,8 @@
 """The block operators on the GPU where ranges, host threads and streams meet their limits."""
+import numpy as np
 import pytest
+
+import ops_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +33,48 @@ def test_quantize_of_a_copy_on_another_stream(ops):
         got = ops.int8_quantize(x, stream=side)
         side.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# Logits whose scores leave fp32's range one by one or all together.
+FAR = {
+    "apart": lambda g, T, E: -60 - 80 * torch.rand(T, E, generator=g),          # scores of 1e-26 to 1e-61
+    "close": lambda g, T, E: -90 - 0.5 * torch.rand(T, E, generator=g),
+    "lowest": lambda g, T, E: -200 - 3 * torch.rand(T, E, generator=g),
+    "one near": lambda g, T, E: torch.where(torch.arange(E) % 5 == 0, -20.0, -100 - torch.rand(T, E, generator=g)),
+    "one above": lambda g, T, E: torch.where(torch.arange(E) % 5 == 0, 1.0, -88 - torch.rand(T, E, generator=g)),
+}
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("far", list(FAR))
+def test_renormalised_gates_of_scores_below_fp32(ops, score, far):
+    """The chosen scores' ratios, whatever their size.  A gate is expf(l - largest) over a sum of such terms:
+    the difference of at most 100 is rounded by 100 * 2^-24, expf is good to 2 ulp, five additions, two
+    quotients and a product to 2^-24 each: less than 1e-5 in all; what is below 1e-37 may be lost."""
+    T, E, k = 40, 20, 4
+    l = FAR[far](gen(21), T, E)
+    bias = 0.01 * torch.randperm(E, generator=gen(22)).float()
+    if score == "softmax":
+        l[:, 3] = 0.0       # the row's largest logit, which the bias keeps out
+        bias[3] = -5.0
+    r = ops.route(l.cuda(), k, score=score, bias=bias.cuda(), renormalize=True, scale=2.5)
+    want = ref.route(l.numpy(), k, score, bias.numpy(), 1, 1, 1, True, 2.5)
+    assert np.array_equal(r.idx.cpu().numpy(), want["idx"])
+    got = r.gate.double().cpu().numpy()
+    off = np.abs(got - want["gate"]) - (1e-5 * np.abs(want["gate"]) + 1e-37)
+    assert (off <= 0).all(), (got.flat[off.argmax()], want["gate"].flat[off.argmax()])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("far", list(FAR))
+def test_gradient_of_renormalised_gates_of_scores_below_fp32(ops, score, far):
+    """scale q_i (g_i - sum q g) (1 - s_i) with q as above: 1e-5 for each of q and the sum."""
+    T, E, k = 40, 20, 4
+    l = FAR[far](gen(23), T, E)
+    idx = torch.rand(T, E, generator=gen(24)).topk(k).indices
+    dg = torch.randn(T, k, generator=gen(25))
+    got = ops.route_backward(l.cuda(), idx.int().cuda(), dg.cuda(), score=score, renormalize=True, scale=2.5)
+    l64 = l.double().requires_grad_(True)
+    (ref.gates(l64, idx, score, True, 2.5) * dg.double()).sum().backward()
+    off = (got.double().cpu() - l64.grad).abs() - 2e-5 * 2.5 * dg.double().abs().amax(1, keepdim=True)
+    assert float(off.max()) <= 0
