@@ -21,6 +21,8 @@
 // instructions a warp and row, for 8 columns a lane), not the copies: without the rows ahead the forward
 // pass took 92 us.  Odd widths take single-column accesses: 3001 x 1409 fp32, layer norms, 29 us, floor 10.
 #include <algorithm>
+#include <mutex>
+#include <type_traits>
 
 #include "ops_common.cuh"
 #include "tcgen05_ptx.cuh"
@@ -565,40 +567,54 @@ constexpr int kNormMaxD = 16384;
 // Threads of a block with `chunks` runs of 8 columns each.
 int norm_threads(int d, int chunks) { return ((d + 8 * chunks - 1) / (8 * chunks) + 31) / 32 * 32; }
 
-// Launches a kernel with the shared memory of its rows ahead.
-template <typename K>
-cudaError_t launch_rows(K kernel, int slots, int chunks, int blocks, int threads, cudaStream_t s, const NormArgs& a) {
+// What the widest form's rows ahead take: 512 threads of 2 chunks, x and y in fp32.
+constexpr int kRingBytes = kDepth * 4 * 2 * 512 * (int)sizeof(uint4);
+
+// Launches a kernel with the shared memory of its rows ahead.  The limit that a kernel has on a device is raised
+// once, to what any call needs, and never lowered: it belongs to the kernel, not to the call, and other
+// threads launch the same kernel at other widths.
+template <void (*kernel)(NormArgs)>
+cudaError_t launch_rows(int slots, int chunks, int blocks, int threads, int device, cudaStream_t s, const NormArgs& a) {
   const size_t smem = (size_t)kDepth * slots * chunks * threads * sizeof(uint4);
+  if (smem > kRingBytes) return cudaErrorInvalidConfiguration;
   if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    static bool ready[kOpsMaxDevices] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[device]) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+      if (e != cudaSuccess) return e;
+      ready[device] = true;
+    }
   }
   return pdl_launch(kernel, dim3(blocks), dim3(threads), smem, s, a);
 }
+template <void (*kernel)(NormArgs)>
+using Kernel = std::integral_constant<void (*)(NormArgs), kernel>;
 
 // Forms by width: threads of a block, chunks of 8 columns a thread, blocks an SM.  The row sums' barriers
 // want several blocks an SM, the vectors registers; a layer norm's two more vectors, or values in
 // registers instead of the ring, cost the second block of 512.  The ring takes at most 196 KB.
 template <typename S, typename Y, bool VEC, bool BIAS>
-cudaError_t launch_forward_t(const NormArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_forward_t(const NormArgs& a, int device, int sms, cudaStream_t s) {
   constexpr int R = VEC ? kRing : kScalar, V = VEC ? kVector : kScalar;
   constexpr int kBlocks = VEC && !BIAS ? 2 : 1;
   const int slots = Ahead<R, S>::kVecs + (a.y ? Ahead<R, Y>::kVecs : 0);
   auto go = [&](auto kernel, int slots, int chunks, int per_sm) {
     const int blocks = (int)std::min<int64_t>(a.T, (int64_t)sms * per_sm);
-    return launch_rows(kernel, slots, chunks, blocks, norm_threads(a.d, chunks), s, a);
+    return launch_rows<kernel>(slots, chunks, blocks, norm_threads(a.d, chunks), device, s, a);
   };
-  if (a.d > 8 * 1024) return go(block_norm_kernel<S, Y, V, 2, BIAS, 1024, 1>, 0, 2, 1);
-  if (a.d > 4 * 1024) return go(block_norm_kernel<S, Y, R, 2, BIAS, 512, 1>, slots, 2, 1);
-  if (a.d > 2 * 1024) return go(block_norm_kernel<S, Y, R, 1, BIAS, 512, kBlocks>, slots, 1, kBlocks);
-  return go(block_norm_kernel<S, Y, R, 1, BIAS, 256, 2 * kBlocks>, slots, 1,
+  if (a.d > 8 * 1024) return go(Kernel<block_norm_kernel<S, Y, V, 2, BIAS, 1024, 1>>{}, 0, 2, 1);
+  if (a.d > 4 * 1024) return go(Kernel<block_norm_kernel<S, Y, R, 2, BIAS, 512, 1>>{}, slots, 2, 1);
+  if (a.d > 2 * 1024) return go(Kernel<block_norm_kernel<S, Y, R, 1, BIAS, 512, kBlocks>>{}, slots, 1, kBlocks);
+  return go(Kernel<block_norm_kernel<S, Y, R, 1, BIAS, 256, 2 * kBlocks>>{}, slots, 1,
             2 * kBlocks * std::max(1, 256 / norm_threads(a.d, 1)));
 }
 template <typename S, typename Y, bool VEC>
-cudaError_t launch_forward(const NormArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_forward(const NormArgs& a, int device, int sms, cudaStream_t s) {
   if (a.after == COLIBRI_NORM_LAYER || a.before == COLIBRI_NORM_LAYER)
-    return launch_forward_t<S, Y, VEC, true>(a, sms, s);
-  return launch_forward_t<S, Y, VEC, false>(a, sms, s);
+    return launch_forward_t<S, Y, VEC, true>(a, device, sms, s);
+  return launch_forward_t<S, Y, VEC, false>(a, device, sms, s);
 }
 
 // Blocks of the backward pass: enough to fill the SMs at about 512 threads each, and at least 8 rows a
@@ -610,23 +626,23 @@ int backward_blocks(int T, int d, int sms, int* rows_per_block) {
 }
 
 template <typename S, typename Y, bool VEC, bool BIAS>
-cudaError_t launch_backward_t(const NormArgs& a, int blocks, cudaStream_t s) {
+cudaError_t launch_backward_t(const NormArgs& a, int blocks, int device, cudaStream_t s) {
   constexpr int R = VEC ? kRing : kScalar, V = VEC ? kVector : kScalar, one = Ahead<R, S>::kVecs;
   const int slots = (a.dx1 ? one : 0) + (a.before ? 2 * one : 0) + (a.y ? Ahead<R, Y>::kVecs : 0);
   auto go = [&](auto kernel, int slots, int chunks) {
-    return launch_rows(kernel, slots, chunks, blocks, norm_threads(a.d, chunks), s, a);
+    return launch_rows<kernel>(slots, chunks, blocks, norm_threads(a.d, chunks), device, s, a);
   };
-  if (a.d > 8 * 1024) return go(block_norm_backward_kernel<S, Y, V, 2, BIAS, 1024>, 0, 2);
-  if (a.d > 4 * 1024) return go(block_norm_backward_kernel<S, Y, V, 1, BIAS, 1024>, 0, 1);
-  if (a.d > 2 * 1024) return go(block_norm_backward_kernel<S, Y, R, 1, BIAS, 512>, slots, 1);
-  return go(block_norm_backward_kernel<S, Y, R, 1, BIAS, 256>, slots, 1);
+  if (a.d > 8 * 1024) return go(Kernel<block_norm_backward_kernel<S, Y, V, 2, BIAS, 1024>>{}, 0, 2);
+  if (a.d > 4 * 1024) return go(Kernel<block_norm_backward_kernel<S, Y, V, 1, BIAS, 1024>>{}, 0, 1);
+  if (a.d > 2 * 1024) return go(Kernel<block_norm_backward_kernel<S, Y, R, 1, BIAS, 512>>{}, slots, 1);
+  return go(Kernel<block_norm_backward_kernel<S, Y, R, 1, BIAS, 256>>{}, slots, 1);
 }
 
 template <typename S, typename Y, bool VEC>
-cudaError_t launch_backward(const NormArgs& a, int blocks, cudaStream_t s) {
+cudaError_t launch_backward(const NormArgs& a, int blocks, int device, cudaStream_t s) {
   if (a.after == COLIBRI_NORM_LAYER || a.before == COLIBRI_NORM_LAYER)
-    return launch_backward_t<S, Y, VEC, true>(a, blocks, s);
-  return launch_backward_t<S, Y, VEC, false>(a, blocks, s);
+    return launch_backward_t<S, Y, VEC, true>(a, blocks, device, s);
+  return launch_backward_t<S, Y, VEC, false>(a, blocks, device, s);
 }
 
 template <typename F>
@@ -711,7 +727,7 @@ extern "C" int colibri_moe_block_norm(const colibri_moe_norm_config_t* cfg, cons
   const cudaError_t e = by_type(cfg->dtype, cfg->block_dtype, vec, [&](auto st, auto yt, bool v) {
     using S = decltype(st);
     using Y = decltype(yt);
-    return v ? launch_forward<S, Y, true>(a, sms, s) : launch_forward<S, Y, false>(a, sms, s);
+    return v ? launch_forward<S, Y, true>(a, device, sms, s) : launch_forward<S, Y, false>(a, device, sms, s);
   });
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
@@ -793,7 +809,7 @@ extern "C" int colibri_moe_block_norm_backward(const colibri_moe_norm_config_t* 
   cudaError_t e = by_type(cfg->dtype, cfg->block_dtype, vec, [&](auto st, auto yt, bool v) {
     using S = decltype(st);
     using Y = decltype(yt);
-    return v ? launch_backward<S, Y, true>(a, blocks, s) : launch_backward<S, Y, false>(a, blocks, s);
+    return v ? launch_backward<S, Y, true>(a, blocks, device, s) : launch_backward<S, Y, false>(a, blocks, device, s);
   });
   if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
   NormSumsArgs q = {a.part,

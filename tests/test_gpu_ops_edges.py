@@ -1,4 +1,6 @@
 """The block operators on the GPU where ranges, host threads and streams meet their limits."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -78,3 +80,47 @@ def test_gradient_of_renormalised_gates_of_scores_below_fp32(ops, score, far):
     (ref.gates(l64, idx, score, True, 2.5) * dg.double()).sum().backward()
     off = (got.double().cpu() - l64.grad).abs() - 2e-5 * 2.5 * dg.double().abs().amax(1, keepdim=True)
     assert float(off.max()) <= 0
+
+
+def test_threads_at_different_widths(ops):
+    """Host threads, a stream each, that launch the same kernels with different amounts of shared memory: every
+    call is accepted and gives what it gives alone.  The C calls, as fast as they go."""
+    import ctypes
+    import mixture_experts_gemm_gb300 as moe
+    shapes = [(4096, True), (4096, False), (2104, True), (2104, False)]
+    f, w = moe.lib().colibri_moe_block_norm, torch.ones(4096, device="cuda")
+    data = {d: [torch.randn(2, d, generator=gen(d + i)).cuda() for i in (0, 1)] for d, _ in shapes}
+
+    def caller(d, block, stream):
+        x, y = data[d]
+        x1, p = torch.empty_like(x), torch.empty_like(x)
+        c = moe.NormConfig(d, 0, 0, 0, int(block), 1, 0, 1.0, 1.0, 1e-6, 1)
+        v = moe.NormVectors(w.data_ptr() if block else None, None, w.data_ptr(), None, None)
+        args = (ctypes.addressof(c), ctypes.addressof(v), x.data_ptr(), d, y.data_ptr() if block else None, d, 2,
+                x1.data_ptr() if block else None, p.data_ptr(), stream.cuda_stream)
+        return (lambda: f(*args)), p, (c, v, x1)
+
+    alone = {}
+    for s in shapes:
+        call, p, _ = caller(*s, torch.cuda.current_stream())
+        assert call() == 0
+        alone[s] = p
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(mine):
+        stream = torch.cuda.Stream()
+        many = [caller(*s, stream) for s in mine]
+        codes = [call() for _ in range(4000) for call, _, _ in many]
+        stream.synchronize()
+        if any(codes):
+            failed.append(f"{sum(map(bool, codes))} of {len(codes)} calls: {min(codes)}")
+        failed.extend(s for s, (_, p, _) in zip(mine, many) if not torch.equal(p, alone[s]))
+
+    torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=(m,)) for m in (shapes[:1], shapes[1:2], shapes[2:3], shapes[3:])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
