@@ -315,7 +315,8 @@ COLIBRI_API int colibri_moe_ep_combine(colibri_moe_t* ctx, const float* y_back, 
  * workspace is scratch of the size the call's _workspace function gives, 256-byte aligned; its
  * contents need no initialisation, and calls that may overlap on the GPU need one each.  Sums, norm
  * statistics and scores are fp32 or wider; a value is rounded to bf16 once, when it is stored.
- * Inputs and outputs must not overlap, except where a call says so.
+ * Inputs and outputs must not overlap, except where a call says so.  A call takes up to 2^31 - 2^24 - 1
+ * rows (T, R); more are COLIBRI_ERR_UNSUPPORTED.
  * Errors: COLIBRI_ERR_INVALID_ARG (NULL or host pointers, sizes or strides out of range, overlapping
  * rows of the norms' inputs and outputs, a workspace too small), COLIBRI_ERR_UNSUPPORTED (sizes this build does not
  * run, as listed), COLIBRI_ERR_CUDA.  Nothing is enqueued when a call fails its checks.

@@ -661,7 +661,7 @@ int check_norm_config(const colibri_moe_norm_config_t* c, const colibri_moe_norm
   if (c->d_model <= 0 || !ops_dtype(c->dtype) || !ops_dtype(c->block_dtype) || !ops_dtype(c->param_dtype) ||
       !norm_kind(c->after) || !norm_kind(c->before) || !(c->eps >= 0.f) || (c->trusted_pointers & ~1))
     return COLIBRI_ERR_INVALID_ARG;
-  if (c->d_model > kNormMaxD) return COLIBRI_ERR_UNSUPPORTED;
+  if (c->d_model > kNormMaxD || T > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
   // without a block output there is nothing to norm after, to gate or to add
   if (!block && (c->after != COLIBRI_NORM_NONE || w->gate || c->before == COLIBRI_NORM_NONE))
     return COLIBRI_ERR_INVALID_ARG;
@@ -735,7 +735,7 @@ extern "C" int colibri_moe_block_norm(const colibri_moe_norm_config_t* cfg, cons
 extern "C" int colibri_moe_block_norm_backward_workspace(const colibri_moe_norm_config_t* cfg, int32_t T,
                                                          size_t* bytes) {
   if (!cfg || !bytes || T < 0 || cfg->d_model <= 0) return COLIBRI_ERR_INVALID_ARG;
-  if (cfg->d_model > kNormMaxD) return COLIBRI_ERR_UNSUPPORTED;
+  if (cfg->d_model > kNormMaxD || T > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
   int device = 0, sms = 0, rows = 0;
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
   *bytes = T ? (size_t)backward_blocks(T, cfg->d_model, sms, &rows) * kSlots * cfg->d_model * sizeof(float) : 0;

@@ -264,6 +264,7 @@ extern "C" int colibri_moe_int8_experts_workspace(const colibri_moe_int8_config_
   const int rc = check_int8_config(cfg);
   if (rc) return rc;
   if (!bytes || n_tokens < 0 || R < 0) return COLIBRI_ERR_INVALID_ARG;
+  if (R > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
   int device = 0, sms = 0;
   if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
   *bytes = R ? int8_workspace(cfg, R, sms).bytes : 0;
@@ -278,6 +279,7 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
   const int rc = check_int8_config(cfg);
   if (rc) return rc;
   if (n_tokens < 0 || R < 0 || (!rows && R > n_tokens)) return COLIBRI_ERR_INVALID_ARG;
+  if (R > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
   if (R == 0) return COLIBRI_OK;
   if ((n_tokens > 0 && (!x || ldx < cfg->in_features)) || !offsets || !w || !w_scale || !y ||
       (w3 != nullptr) != (w3_scale != nullptr))
@@ -316,7 +318,7 @@ extern "C" int colibri_moe_combine_rows(const void* y, int32_t y_dtype, int32_t 
                                         const float* gate, int32_t T, int32_t k, int32_t d, void* out,
                                         int32_t out_dtype, void* stream) {
   if (T < 0 || R < 0 || k < 1 || d < 1 || !ops_dtype(y_dtype) || !ops_dtype(out_dtype)) return COLIBRI_ERR_INVALID_ARG;
-  if (k > 32 || d > 65535 * 256) return COLIBRI_ERR_UNSUPPORTED;
+  if (k > 32 || d > 65535 * 256 || T > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
   if (T == 0) return COLIBRI_OK;
   if ((R > 0 && !y) || !row_of || !gate || !out) return COLIBRI_ERR_INVALID_ARG;
   int device = 0, sms = 0;

@@ -76,6 +76,9 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* buf, int& turn) 
 
 // ---- host side of the entry points
 constexpr int kOpsMaxDevices = 64;
+// Row numbers are 32-bit.  Loops over rows, and rows fetched ahead, pass the last one by a few grid widths or one
+// block's rows (at most 2^31 / 128): with this limit none of them wraps.
+constexpr int32_t kOpsMaxRows = INT32_MAX - (1 << 24);
 
 inline bool ops_on_device(const void* p, int device) {
   cudaPointerAttributes at;

@@ -735,6 +735,7 @@ int check_route_config(const colibri_moe_route_config_t* c, int32_t T, int64_t l
   if (c->num_experts > kRouteMaxE || c->top_k > kRouteMaxK || c->groups > kRouteMaxGroups) return COLIBRI_ERR_UNSUPPORTED;
   if (ld < c->num_experts) return COLIBRI_ERR_INVALID_ARG;
   if ((int64_t)T * c->top_k > INT32_MAX) return COLIBRI_ERR_INVALID_ARG;
+  if (T > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
   return COLIBRI_OK;
 }
 

@@ -124,3 +124,25 @@ def test_threads_at_different_widths(ops):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+def test_as_many_rows_as_a_call_takes(ops):
+    """Rows of one value, 2^31 - 2^24 - 1 of them: the first and the last come out as alone."""
+    T = 2**31 - 2**24 - 1
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    ends = [slice(0, 500), slice(T - 500, T)]
+    w = torch.full((1,), 0.75, dtype=BF16, device="cuda")
+    x = torch.empty(T, 1, dtype=BF16, device="cuda").uniform_(0.5, 2.0)
+    norm = dict(before="rms", before_weight=w, eps=1.0)
+    p = ops.pre_norm(x, w, eps=1.0)
+    d = ops.block_norm_backward(None, p, x, **norm)["d_x"]
+    for at in ends:
+        assert torch.equal(p[at], ops.pre_norm(x[at], w, eps=1.0))
+        assert torch.equal(d[at], ops.block_norm_backward(None, p[at], x[at], **norm)["d_x"])
+    del p, d
+    row = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")[:, None]
+    out = ops.combine(x, row, torch.ones(T, 1, device="cuda"))
+    assert torch.equal(out, x.flip(0))
+    del x, row, out
+    torch.cuda.empty_cache()
