@@ -117,6 +117,19 @@ __device__ __forceinline__ uint32_t idesc_f16(int n) {
   return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(BM >> 4) << 24);
 }
 
+// silu(v) u as it is stored.  The fast exp and quotient are off by about 2 + 1.2 |v| ulp of fp32 and give 0 below v
+// near -87: far below a rounding to bf16, but not for an fp32 result.  That takes expf of what cannot overflow
+// and the approximate reciprocal, good to an ulp, of a sum between 1 and 2 (512 tokens: 82 us, 80 with the fast
+// forms, 92 with a true quotient and its range checks).
+template <typename O>
+__device__ __forceinline__ O gated(float v, float u) {
+  if constexpr (sizeof(O) == 2) return from_float<O>(silu_fast(v) * u);
+  const float t = expf(-fabsf(v));
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + t));
+  return from_float<O>(v * (v < 0.f ? t * s : s) * u);
+}
+
 struct Item {
   int e, row, n;       // expert, first row, rows of the tile
   int ch;              // weight tile
@@ -484,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 8; c += 2) {
               const float other = __shfl_xor_sync(~0u, lane < 16 ? h[c + 1] : h[c], 16);
               const float g = lane < 16 ? h[c] : other, u = lane < 16 ? other : h[c + 1];
-              if (c8 + c < left) out[(int64_t)(c8 + c) * a.N] = from_float<O>(silu_fast(g) * u);
+              if (c8 + c < left) out[(int64_t)(c8 + c) * a.N] = gated<O>(g, u);
             }
           } else {
 #pragma unroll

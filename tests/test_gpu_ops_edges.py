@@ -146,3 +146,24 @@ def test_as_many_rows_as_a_call_takes(ops):
     assert torch.equal(out, x.flip(0))
     del x, row, out
     torch.cuda.empty_cache()
+
+
+def test_gated_products_in_fp32(ops):
+    """silu(v) * u in fp32, with v and u exact (powers of two as scales): expf to 2 ulp, one addition, one
+    quotient and one product to half an ulp each, 7 * 2^-24 in all."""
+    K, N = 16, 254
+    whole = torch.cat([torch.arange(-127, 0), torch.arange(1, 128)])
+    w = torch.zeros(1, N, K, dtype=torch.int8)
+    w[0, :, 0] = whole.to(torch.int8)
+    w3 = torch.zeros_like(w)
+    w3[0, :, 0] = whole.flip(0).to(torch.int8)
+    x = torch.zeros(6, K)
+    x[:, 0] = 127.0 * 2.0 ** torch.arange(-4, 2)
+    ws, off = torch.full((1, N), 2.0**-7), torch.tensor([0, 6]).int()
+    y = ops.int8_experts(x.cuda(), w.cuda(), ws.cuda(), off.cuda(), w3=w3.cuda(), w3_scale=ws.cuda(), out_dtype=F32)
+    scale = x[:, :1].double()  # a row's scale times its one quantised value, 127
+    v, u = scale * whole.double() / 128, scale * whole.flip(0).double() / 128
+    want = v / (1 + torch.exp(-v)) * u
+    off = (y.double().cpu() - want).abs() - (8 * 2.0**-24 * want.abs() + 1e-37 * u.abs())
+    i = int(off.argmax())
+    assert float(off.max()) <= 0, (float(v.flatten()[i]), float(y.flatten()[i]), float(want.flatten()[i]))
