@@ -436,6 +436,7 @@ typedef struct {
   int32_t dtype;         /* COLIBRI_DTYPE_* of x                                                    */
   int32_t out_dtype;     /* COLIBRI_DTYPE_* of y                                                    */
   int32_t trusted_pointers; /* see above                                                           */
+  int32_t wait_limit_us; /* most a wait inside the product may last: 1..10000000, 0 for two seconds */
 } colibri_moe_int8_config_t;
 
 /* q [n, K] int8 and scale [n] fp32 of x [n, K] (row stride ldx): activations, or weights once ahead of
@@ -452,8 +453,8 @@ COLIBRI_API int colibri_moe_int8_experts_workspace(const colibri_moe_int8_config
  * 1] are expert e's rows; values outside 0..R are clamped, and rows that an earlier segment holds stay
  * with it); rows [R] int32 gives the token of each row
  * (outside 0..n_tokens-1: a row of zeros), or NULL: row r is token r (R <= n_tokens).  y [R, N]: rows from
- * offsets[E] on are not written.  R == 0 is a no-op.  Every wait inside the product is bounded by two
- * seconds; should one give up, the kernel stops and y is undefined (there is no context to report it). */
+ * offsets[E] on are not written.  R == 0 is a no-op.  Every wait inside the product is bounded by
+ * wait_limit_us; should one give up, the kernel stops and y is undefined (there is no context to report it). */
 COLIBRI_API int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, const void* x, int64_t ldx,
                                          int32_t n_tokens, const int32_t* rows, int32_t R, const int32_t* offsets,
                                          const int8_t* w, const float* w_scale, const int8_t* w3,

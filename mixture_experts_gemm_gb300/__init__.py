@@ -80,7 +80,8 @@ class RouteConfig(ctypes.Structure):
 
 class Int8Config(ctypes.Structure):
     _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("num_experts", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("trusted_pointers", ctypes.c_int32)]
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("trusted_pointers", ctypes.c_int32),
+                ("wait_limit_us", ctypes.c_int32)]
 
 
 class Weights(ctypes.Structure):

@@ -155,10 +155,12 @@ __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_k
 }
 
 constexpr int kInt8MaxE = 512, kInt8MaxK = 65536, kInt8MaxN = 131072;
+constexpr int kInt8WaitUs = 2000000, kInt8MaxWaitUs = 10000000;
 
 int check_int8_config(const colibri_moe_int8_config_t* c) {
   if (!c || c->in_features <= 0 || c->out_features <= 0 || c->num_experts <= 0 || !ops_dtype(c->dtype) ||
-      !ops_dtype(c->out_dtype) || (c->trusted_pointers & ~1))
+      !ops_dtype(c->out_dtype) || (c->trusted_pointers & ~1) || c->wait_limit_us < 0 ||
+      c->wait_limit_us > kInt8MaxWaitUs)
     return COLIBRI_ERR_INVALID_ARG;
   if (c->in_features % 16 || c->in_features > kInt8MaxK || c->out_features > kInt8MaxN || c->num_experts > kInt8MaxE)
     return COLIBRI_ERR_UNSUPPORTED;
@@ -308,7 +310,8 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
       qa.copies > 1 ? quantize<__half, true>(cfg->dtype, qa, s) : quantize<__half, false>(cfg->dtype, qa, s);
   if (quantized != cudaSuccess) return COLIBRI_ERR_CUDA;
   const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, reinterpret_cast<float*>(ws + lay.partial),
-                      qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, lay.copies, 2000000000ull};
+                      qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, lay.copies,
+                      (cfg->wait_limit_us ? cfg->wait_limit_us : kInt8WaitUs) * 1000ull};
   const bool bf16_out = cfg->out_dtype == COLIBRI_DTYPE_BF16;
   const cudaError_t e = launch_int8_mma(maps, lay.tile_rows, w3 != nullptr, bf16_out, a, device, sms, s);
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;

@@ -34,8 +34,8 @@
 // bound by the tensor cores, the narrowest by HBM and about 10 us of launches, first copies and epilogue,
 // those between by the MMA warp's loop and the epilogue (without it 512 tokens take 70 us).
 //
-// Every wait is bounded by timeout_ns: when one gives up, all roles stop, copies in flight are waited for
-// (bounded) and TMEM is freed.
+// Every wait is bounded by timeout_ns: when one gives up, all roles stop, copies and MMAs in flight are waited
+// for (at most kDrainNs each, whatever the limit) and TMEM is freed.
 #include <mutex>
 
 #include "int8_internal.cuh"
@@ -54,6 +54,7 @@ constexpr int kABytes = BM * BK * 2;     // 16 KB
 constexpr int kTokBox = 32;              // token rows of the smallest TMA box
 constexpr int kTokBoxBytes = kTokBox * BK * 2;
 constexpr int kMaxExperts = 512;
+constexpr uint64_t kDrainNs = 50000000;  // far above the time of a copy or of a stage's MMAs
 
 // Rings, in stages of KS blocks of 64 columns of K: raw weights (RS), converted weights (SA), token rows
 // (SB).  One full and one done barrier serve stage `it` for both operands, at it % kSync.  The MMA warp's
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every copy has landed before the CTA can leave
     volatile int never = 0;
     for (uint32_t j = issued > RS ? issued - RS : 0; j < issued; ++j)
-      wait_for(rfull0 + 8 * (j % RS), j / RS & 1, &never, a.timeout_ns);
+      wait_for(rfull0 + 8 * (j % RS), j / RS & 1, &never, kDrainNs);
     __syncwarp();
   } else if (warp == 6) {
     // -------------------------------------------------------------- token rows
@@ -351,13 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++sb == SB) sb = 0;
       }
     }
-    if (!ok) {
-      if (lane == 0) *s_abort = 1;
-      // stopped early: no MMA reads the slots any more, but the copies must land.  A full barrier may
-      // lack its converters' arrivals, so give the copies a fixed time, far above a copy's, instead.
-      volatile int never = 0;
-      if (it) wait_for(full0 + 8 * ((it - 1) % kSync), (it - 1) / kSync & 1, &never, a.timeout_ns / 8);
-    }
+    if (!ok && lane == 0) *s_abort = 1;
+    // Whichever role stopped early: the copies of the last SB stages (those before had their MMAs) land before the
+    // CTA can leave.  A stage may then lack its converters' arrivals, and its barrier never completes: the
+    // wait for it ends by kDrainNs.
+    volatile int never = 0;
+    for (uint32_t j = it > SB ? it - SB : 0; j < it; ++j)
+      wait_for(full0 + 8 * (j % kSync), j / kSync & 1, &never, kDrainNs);
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elected) {
       umma_commit(drain);  // completes when every MMA of this thread has
       volatile int never = 0;
-      wait_for(drain, 0, &never, a.timeout_ns);
+      wait_for(drain, 0, &never, kDrainNs);
     }
     __syncwarp();
   } else if (warp >= kConvWarp0) {

@@ -167,3 +167,41 @@ def test_gated_products_in_fp32(ops):
     off = (y.double().cpu() - want).abs() - (8 * 2.0**-24 * want.abs() + 1e-37 * u.abs())
     i = int(off.argmax())
     assert float(off.max()) <= 0, (float(v.flatten()[i]), float(y.flatten()[i]), float(want.flatten()[i]))
+
+# Rows of every expert, one case for each width of the product's tiles, with and without the second projection.
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("counts", [[1, 0, 1], [40, 30, 36], [128, 1, 97], [300, 257, 255]], ids=str)
+def test_a_wait_that_runs_out(ops, counts, gated):
+    """A product told to wait for a microsecond at most gives up while its first weights are on their way: it stops,
+    and the next call, in the same workspace, gives what a call without the limit gives."""
+    import ctypes
+    import mixture_experts_gemm_gb300 as moe
+    K, N, E, R = 4096, 520, len(counts), sum(counts)
+    x = torch.randn(R, K, generator=gen(R)).cuda().to(BF16)
+    w = [torch.randint(-127, 128, (E, N, K), generator=gen(R + i)).to(torch.int8).cuda() for i in (1, 2)]
+    ws = torch.full((E, N), 1e-3, device="cuda")
+    off = torch.tensor([0] + counts, device="cuda").cumsum(0).int()
+    kw = dict(w3=w[1], w3_scale=ws) if gated else {}
+    want = ops.int8_experts(x, w[0], ws, off, **kw)
+    L, at = moe.lib(), ctypes.byref
+
+    def config(us):
+        return moe.Int8Config(K, N, E, moe.DTYPE_BF16, moe.DTYPE_BF16, 0, us)
+
+    size = ctypes.c_size_t()
+    assert L.colibri_moe_int8_experts_workspace(at(config(0)), R, R, at(size)) == 0
+    space = torch.empty(size.value, dtype=torch.uint8, device="cuda")
+    w3, s3 = (w[1].data_ptr(), ws.data_ptr()) if gated else (None, None)
+
+    def call(us):
+        y = torch.empty(R, N, dtype=BF16, device="cuda")
+        s = torch.cuda.current_stream().cuda_stream
+        assert L.colibri_moe_int8_experts(at(config(us)), x.data_ptr(), K, R, None, R, off.data_ptr(), w[0].data_ptr(),
+                                          ws.data_ptr(), w3, s3, y.data_ptr(), space.data_ptr(), size.value, s) == 0
+        torch.cuda.synchronize()
+        return y
+
+    for _ in range(2):
+        call(1)
+        assert torch.equal(call(0), want)
+    assert torch.equal(call(10_000_000), want)

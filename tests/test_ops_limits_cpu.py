@@ -50,3 +50,9 @@ def test_rows_near_2_31_are_refused(moe, name):
     torch = pytest.importorskip("torch")
     if not torch.cuda.is_available():  # accepted up to the limit: the next thing that is missing is a device
         assert call(MOST) in (0, -4)
+
+
+def test_wait_limits(moe):
+    for us, code in ((-1, -1), (10_000_001, -1), (10_000_000, 0), (1, 0), (0, 0)):
+        c = moe.Int8Config(16, 1, 4, 1, 1, 0, us)
+        assert moe.lib().colibri_moe_int8_quantize(ctypes.byref(c), None, 16, 0, None, None, None) == code
