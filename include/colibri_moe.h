@@ -436,7 +436,8 @@ typedef struct {
   int32_t dtype;         /* COLIBRI_DTYPE_* of x                                                    */
   int32_t out_dtype;     /* COLIBRI_DTYPE_* of y                                                    */
   int32_t trusted_pointers; /* see above                                                           */
-  int32_t wait_limit_us; /* most a wait inside the product may last: 1..10000000, 0 for two seconds */
+  int32_t wait_limit_us; /* most a wait inside the product may last: 1..10000000, 0 for two seconds;
+                            kept to within about 20 us below a millisecond, else within one */
 } colibri_moe_int8_config_t;
 
 /* q [n, K] int8 and scale [n] fp32 of x [n, K] (row stride ldx): activations, or weights once ahead of
@@ -454,12 +455,18 @@ COLIBRI_API int colibri_moe_int8_experts_workspace(const colibri_moe_int8_config
  * with it); rows [R] int32 gives the token of each row
  * (outside 0..n_tokens-1: a row of zeros), or NULL: row r is token r (R <= n_tokens).  y [R, N]: rows from
  * offsets[E] on are not written.  R == 0 is a no-op.  Every wait inside the product is bounded by
- * wait_limit_us; should one give up, the kernel stops and y is undefined (there is no context to report it). */
+ * wait_limit_us; should one give up, the kernel stops, y is undefined and the device's status word says so. */
 COLIBRI_API int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, const void* x, int64_t ldx,
                                          int32_t n_tokens, const int32_t* rows, int32_t R, const int32_t* offsets,
                                          const int8_t* w, const float* w_scale, const int8_t* w3,
                                          const float* w3_scale, void* y, void* workspace, size_t workspace_bytes,
                                          void* stream);
+
+/* Reads and clears the current device's status word of colibri_moe_int8_experts (one for all streams, graphs and
+ * threads): *status = COLIBRI_INT8_WAIT_EXPIRED if a wait of any product since the last read gave up, so that
+ * its y is undefined, else 0.  Synchronous: it waits for the device first.  Not during a stream capture. */
+#define COLIBRI_INT8_WAIT_EXPIRED 1
+COLIBRI_API int colibri_moe_int8_status(int32_t* status);
 
 /* out[t] = sum over s < k of gate[t, s] * y[row_of[t, s]] in slot order in fp32, slots with a row outside
  * 0..R-1 left out (their gates multiply nothing): the combine for any number of experts, k 1..32, d >= 1.

@@ -42,7 +42,7 @@ EXPORTED = ("colibri_moe_create", "colibri_moe_load_weights", "colibri_moe_forwa
             "colibri_moe_block_norm", "colibri_moe_block_norm_backward_workspace", "colibri_moe_block_norm_backward",
             "colibri_moe_route_experts_workspace", "colibri_moe_route_experts", "colibri_moe_route_experts_backward",
             "colibri_moe_int8_quantize", "colibri_moe_int8_experts_workspace", "colibri_moe_int8_experts",
-            "colibri_moe_combine_rows", "colibri_moe_destroy", "colibri_moe_strerror")
+            "colibri_moe_int8_status", "colibri_moe_combine_rows", "colibri_moe_destroy", "colibri_moe_strerror")
 
 
 class ColibriError(RuntimeError):
@@ -136,6 +136,7 @@ def lib() -> ctypes.CDLL:
             "colibri_moe_int8_experts_workspace": ([vp, i32, i32, vp], ctypes.c_int),
             "colibri_moe_int8_experts": ([vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
                                          ctypes.c_int),
+            "colibri_moe_int8_status": ([vp], ctypes.c_int),
             "colibri_moe_combine_rows": ([vp, i32, i32, vp, vp, i32, i32, i32, vp, i32, vp], ctypes.c_int),
             "colibri_moe_destroy": ([vp], None),
             "colibri_moe_strerror": ([ctypes.c_int], ctypes.c_char_p),

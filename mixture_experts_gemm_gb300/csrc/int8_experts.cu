@@ -156,6 +156,8 @@ __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_k
 
 constexpr int kInt8MaxE = 512, kInt8MaxK = 65536, kInt8MaxN = 131072;
 constexpr int kInt8WaitUs = 2000000, kInt8MaxWaitUs = 10000000;
+// The clock is read once in 64 tries of about 8 us, at every one under a millisecond's limit.
+Int8Limit int8_limit(int us) { return {us * 1000ull, us < 1000 ? 0u : 63u}; }
 
 int check_int8_config(const colibri_moe_int8_config_t* c) {
   if (!c || c->in_features <= 0 || c->out_features <= 0 || c->num_experts <= 0 || !ops_dtype(c->dtype) ||
@@ -311,10 +313,22 @@ extern "C" int colibri_moe_int8_experts(const colibri_moe_int8_config_t* cfg, co
   if (quantized != cudaSuccess) return COLIBRI_ERR_CUDA;
   const Int8Args a = {qa.scale, offsets, w_scale, w3_scale, y, reinterpret_cast<float*>(ws + lay.partial),
                       qa.ticket, lay.items, R, cfg->num_experts, cfg->in_features, cfg->out_features, lay.copies,
-                      (cfg->wait_limit_us ? cfg->wait_limit_us : kInt8WaitUs) * 1000ull};
+                      int8_limit(cfg->wait_limit_us ? cfg->wait_limit_us : kInt8WaitUs)};
   const bool bf16_out = cfg->out_dtype == COLIBRI_DTYPE_BF16;
   const cudaError_t e = launch_int8_mma(maps, lay.tile_rows, w3 != nullptr, bf16_out, a, device, sms, s);
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+extern "C" int colibri_moe_int8_status(int32_t* status) {
+  if (!status) return COLIBRI_ERR_INVALID_ARG;
+  int device = 0, sms = 0, v = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  if (int8_take_status(&v) != cudaSuccess) {
+    cudaGetLastError();
+    return COLIBRI_ERR_CUDA;
+  }
+  *status = v;
+  return COLIBRI_OK;
 }
 
 extern "C" int colibri_moe_combine_rows(const void* y, int32_t y_dtype, int32_t R, const int32_t* row_of,

@@ -13,6 +13,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();  // colibri_moe.cu; nullptr if th
 constexpr int kInt8MaxSplits = 8;     // parts of K a tile may be split into
 constexpr int kInt8PartialRows = 256;  // tile rows x items (tiles x parts) per SM that a split product may hold
 
+// How long a wait may last, and how often it reads the clock: at the tries whose number has none of these bits.
+struct Int8Limit {
+  uint64_t ns;
+  uint32_t clock_mask;
+};
+
 struct Int8Args {
   const float* scale;               // [R] of the quantised rows
   const int32_t* offsets;           // [E + 1]
@@ -23,7 +29,7 @@ struct Int8Args {
   int max_items;                    // capacity of the two
   int R, E, K, N;
   int copies;                       // of the quantised rows, R apart
-  uint64_t timeout_ns;
+  Int8Limit limit;
 };
 
 struct QuantArgs {
@@ -52,5 +58,7 @@ bool int8_tensor_maps(int tile_rows, const void* q, int64_t rows, const int8_t* 
 // tile_rows: 32, 64, 128 or 256 token rows a tile.
 cudaError_t launch_int8_mma(const Int8Maps& maps, int tile_rows, bool swiglu, bool bf16_out, const Int8Args& a, int device,
                             int sms, cudaStream_t s);
+// Waits for the current device, then reads and clears its status word.
+cudaError_t int8_take_status(int* status);
 
 }  // namespace colibri

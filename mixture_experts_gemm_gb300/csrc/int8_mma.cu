@@ -34,8 +34,8 @@
 // bound by the tensor cores, the narrowest by HBM and about 10 us of launches, first copies and epilogue,
 // those between by the MMA warp's loop and the epilogue (without it 512 tokens take 70 us).
 //
-// Every wait is bounded by timeout_ns: when one gives up, all roles stop, copies and MMAs in flight are waited
-// for (at most kDrainNs each, whatever the limit) and TMEM is freed.
+// Every wait is bounded by the call's limit: when one gives up, all roles stop, copies and MMAs in flight are waited
+// for (at most kDrain each, whatever the limit), TMEM is freed and the device's status word gets a bit.
 #include <mutex>
 
 #include "int8_internal.cuh"
@@ -54,7 +54,12 @@ constexpr int kABytes = BM * BK * 2;     // 16 KB
 constexpr int kTokBox = 32;              // token rows of the smallest TMA box
 constexpr int kTokBoxBytes = kTokBox * BK * 2;
 constexpr int kMaxExperts = 512;
-constexpr uint64_t kDrainNs = 50000000;  // far above the time of a copy or of a stage's MMAs
+constexpr Int8Limit kDrain = {50000000, 63};  // 50 ms, far above the time of a copy or of a stage's MMAs
+
+// What the waits of all products on this device have come to since it was last taken: 1 once one gave up.
+__device__ int g_status;
+__device__ int g_taken;
+__global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0); }
 
 // Rings, in stages of KS blocks of 64 columns of K: raw weights (RS), converted weights (SA), token rows
 // (SB).  One full and one done barrier serve stage `it` for both operands, at it % kSync.  The MMA warp's
@@ -87,16 +92,16 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Waits for the phase of `bar` with parity `parity`, at most timeout_ns or until *abort.  The clock is read
-// once in 64 tries: reading it takes longer than most of these waits last.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns) {
+// Waits for the phase of `bar` with parity `parity`, at most limit.ns or until *abort.  A try that fails lasts
+// about 8 us.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, Int8Limit limit) {
   uint64_t t0 = 0;
   for (uint32_t tries = 1;; ++tries) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (tries % 64 == 0) {
+    if ((tries & limit.clock_mask) == 0) {
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
-      if (*abort || now - t0 > timeout_ns) return false;
+      if (*abort || now - t0 > limit.ns) return false;
     }
   }
 }
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // barrier cannot run two phases ahead of a waiter, because the blocks between need the waiter's work.
   auto slot_free = [&](uint32_t it, uint32_t behind) {
     const uint32_t j = it - behind;
-    return it < behind || wait_for(done0 + 8 * (j % kSync), j / kSync & 1, s_abort, a.timeout_ns);
+    return it < behind || wait_for(done0 + 8 * (j % kSync), j / kSync & 1, s_abort, a.limit);
   };
 
   // The producers' and the MMA warp run their loops with all lanes and let one elected lane issue: addresses
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Item t = item_at(i);
       const int w_row = t.e * a.N + t.ch * kCh;
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++issued) {
-        if (!__all_sync(~0u, wait_for(rempty0 + 8 * r, ph ^ 1, s_abort, a.timeout_ns))) {
+        if (!__all_sync(~0u, wait_for(rempty0 + 8 * r, ph ^ 1, s_abort, a.limit))) {
           ok = false;
           break;
         }
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every copy has landed before the CTA can leave
     volatile int never = 0;
     for (uint32_t j = issued > RS ? issued - RS : 0; j < issued; ++j)
-      wait_for(rfull0 + 8 * (j % RS), j / RS & 1, &never, kDrainNs);
+      wait_for(rfull0 + 8 * (j % RS), j / RS & 1, &never, kDrain);
     __syncwarp();
   } else if (warp == 6) {
     // -------------------------------------------------------------- token rows
@@ -355,10 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) *s_abort = 1;
     // Whichever role stopped early: the copies of the last SB stages (those before had their MMAs) land before the
     // CTA can leave.  A stage may then lack its converters' arrivals, and its barrier never completes: the
-    // wait for it ends by kDrainNs.
+    // wait for it ends by kDrain.
     volatile int never = 0;
     for (uint32_t j = it > SB ? it - SB : 0; j < it; ++j)
-      wait_for(full0 + 8 * (j % kSync), j / kSync & 1, &never, kDrainNs);
+      wait_for(full0 + 8 * (j % kSync), j / kSync & 1, &never, kDrain);
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++acc_it) {
       const Item t = item_at(i);
       const uint32_t acc = acc_it & 1;
-      if (!__all_sync(~0u, wait_for(tempty0 + 8 * acc, (acc_it >> 1 & 1) ^ 1, s_abort, a.timeout_ns))) {
+      if (!__all_sync(~0u, wait_for(tempty0 + 8 * acc, (acc_it >> 1 & 1) ^ 1, s_abort, a.limit))) {
         ok = false;
         break;
       }
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tmem_base + acc * NT, idesc = idesc_f16((t.n + kTokBox - 1) / kTokBox * kTokBox);
       uint32_t more = 0;  // the first MMA of a tile overwrites the accumulator
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        if (!__all_sync(~0u, wait_for(full0 + 8 * (it % kSync), it / kSync & 1, s_abort, a.timeout_ns))) {
+        if (!__all_sync(~0u, wait_for(full0 + 8 * (it % kSync), it / kSync & 1, s_abort, a.limit))) {
           ok = false;
           break;
         }
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elected) {
       umma_commit(drain);  // completes when every MMA of this thread has
       volatile int never = 0;
-      wait_for(drain, 0, &never, kDrainNs);
+      wait_for(drain, 0, &never, kDrain);
     }
     __syncwarp();
   } else if (warp >= kConvWarp0) {
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t n = t.kb1 - t.kb0;
       for (uint32_t j = (group - it0) % kConvGroups; j < n; j += kConvGroups) {
         const uint32_t it = it0 + j;
-        bool got = wait_for(rfull0 + 8 * r, ph, s_abort, a.timeout_ns);
+        bool got = wait_for(rfull0 + 8 * r, ph, s_abort, a.limit);
         uint4 v[4 * KS];
         const uint8_t* src = s_raw + r * F::kRaw;
 #pragma unroll
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x, ++acc_it) {
       const Item t = item_at(i);
       const uint32_t acc = acc_it & 1;
-      if (!__all_sync(~0u, wait_for(tfull0 + 8 * acc, acc_it >> 1 & 1, s_abort, a.timeout_ns))) {
+      if (!__all_sync(~0u, wait_for(tfull0 + 8 * acc, acc_it >> 1 & 1, s_abort, a.limit))) {
         if (lane == 0) *s_abort = 1;
         break;
       }
@@ -532,14 +537,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(joined);
         bool got = true;
         if (warp == 2 && lane == 0) {
-          got = wait_for(joined, acc_it & 1, s_abort, a.timeout_ns);
+          got = wait_for(joined, acc_it & 1, s_abort, a.limit);
           if (got) {
             __threadfence();
             *s_last = atomicAdd(&a.ticket[t.tile], 1u) == (uint32_t)(parts - 1);
             mbar_arrive(decided);
           }
         }
-        got = got && wait_for(decided, acc_it & 1, s_abort, a.timeout_ns);
+        got = got && wait_for(decided, acc_it & 1, s_abort, a.limit);
         if (!__all_sync(~0u, got)) {
           if (lane == 0) *s_abort = 1;
           break;
@@ -565,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem_base, F::kTmemCols);
+  if (threadIdx.x == 0 && *s_abort) atomicOr(&g_status, COLIBRI_INT8_WAIT_EXPIRED);
 }
 
 bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows, int elem,
@@ -611,6 +617,16 @@ bool int8_tensor_maps(int tile_rows, const void* q, int64_t rows, const int8_t* 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
       return false;
   return true;
+}
+
+cudaError_t int8_take_status(int* status) {
+  static std::mutex mu;  // g_taken holds one caller's answer at a time
+  std::lock_guard<std::mutex> lock(mu);
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return e;
+  take_status_kernel<<<1, 1>>>();
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : cudaMemcpyFromSymbol(status, g_taken, sizeof(int));
 }
 
 cudaError_t launch_int8_mma(const Int8Maps& maps, int tile_rows, bool swiglu, bool bf16_out, const Int8Args& a, int device,

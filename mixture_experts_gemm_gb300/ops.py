@@ -29,7 +29,7 @@ import torch
 from . import DTYPE_BF16, DTYPE_F32, ColibriError, Int8Config, NormConfig, RouteConfig, _check, lib
 
 __all__ = ["block_norm", "block_norm_backward", "pre_norm", "route", "route_backward", "Routing", "int8_quantize",
-           "int8_experts", "combine", "ColibriError"]
+           "int8_experts", "int8_status", "combine", "ColibriError"]
 
 _DTYPE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -374,7 +374,8 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
     fp32; offsets [E + 1] int32 bounds every expert's rows and rows [R] int32 gives their tokens
     (``Routing.offsets`` and ``.token_of_row``), or None: row r is x[r].  With w3 and w3_scale (same
     shapes) y = silu(v) * v3, the gated pair of projections in one pass.  Rows from offsets[E] on are
-    not written.  out_dtype: fp32 or bf16, default x's."""
+    not written.  out_dtype: fp32 or bf16, default x's.  Should a wait inside the product run out (two
+    seconds), y is undefined and ``int8_status`` says so."""
     n, K = _shape(x, "x")
     on = _device(x, "x")
     px, ldx = _matrix(x, "x", n, K, on)
@@ -406,6 +407,15 @@ def int8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, o
                                           s), "colibri_moe_int8_experts")
         return y
     return _run(call, x, on, stream)
+
+
+def int8_status(device=None) -> int:
+    """Waits for the device, then reads and clears its status word: 0, or 1 if a wait of any ``int8_experts`` call there
+    gave up since the last read (its result is then undefined)."""
+    status = ctypes.c_int32()
+    with torch.cuda.device(device):
+        _check(lib().colibri_moe_int8_status(ctypes.byref(status)), "colibri_moe_int8_status")
+    return status.value
 
 
 def combine(y, row_of, gate, *, out_dtype=None, stream=None):

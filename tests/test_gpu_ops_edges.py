@@ -172,8 +172,8 @@ def test_gated_products_in_fp32(ops):
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("counts", [[1, 0, 1], [40, 30, 36], [128, 1, 97], [300, 257, 255]], ids=str)
 def test_a_wait_that_runs_out(ops, counts, gated):
-    """A product told to wait for a microsecond at most gives up while its first weights are on their way: it stops,
-    and the next call, in the same workspace, gives what a call without the limit gives."""
+    """A product told to wait for a microsecond at most (to within about 20) finishes, or stops and says so; the next
+    call, in the same workspace, gives what a call without the limit gives."""
     import ctypes
     import mixture_experts_gemm_gb300 as moe
     K, N, E, R = 4096, 520, len(counts), sum(counts)
@@ -202,6 +202,44 @@ def test_a_wait_that_runs_out(ops, counts, gated):
         return y
 
     for _ in range(2):
-        call(1)
-        assert torch.equal(call(0), want)
+        y = call(1)
+        assert ops.int8_status() == 1 or torch.equal(y, want)
+        assert torch.equal(call(0), want) and ops.int8_status() == 0
     assert torch.equal(call(10_000_000), want)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("R", [10, 40, 100, 600])  # one for each width of the product's tiles
+def test_a_wait_that_runs_out_is_reported(ops, R, gated):
+    """The status word: clear after calls that finish, set once by one that gave up, from any stream or graph.  A part
+    of K is 128 steps of 64 here, at least 20 us of products that the epilogue waits for, two tries and more."""
+    K, N = 65536, 256
+    x = torch.randn(R, K, generator=gen(3)).cuda()
+    w = torch.randint(-127, 128, (1, N, K), generator=gen(4), dtype=torch.int8).cuda()
+    ws, off = torch.ones(1, N, device="cuda"), torch.tensor([0, R], device="cuda").int()
+    assert ops.int8_status() in (0, 1)
+    kw = dict(w3=w, w3_scale=ws) if gated else {}
+    want = ops.int8_experts(x, w, ws, off, **kw)
+    assert ops.int8_status() == 0
+
+    def short(stream=None):
+        """The call with a limit of a microsecond."""
+        real = ops._int8_config
+        config = ops.Int8Config(K, N, 1, 0, 0, 1, 1)
+        ops._int8_config = lambda *a: (config, ops.ctypes.addressof(config))
+        try:
+            return ops.int8_experts(x, w, ws, off, stream=stream, **kw)
+        finally:
+            ops._int8_config = real
+
+    for stream in (None, torch.cuda.Stream()):
+        short(stream)
+        y = ops.int8_experts(x, w, ws, off, stream=stream, **kw)
+        assert ops.int8_status() == 1 and ops.int8_status(0) == 0
+        assert torch.equal(y, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        short()
+    assert ops.int8_status() == 0
+    graph.replay()
+    assert ops.int8_status("cuda:0") == 1 and ops.int8_status() == 0

@@ -56,3 +56,10 @@ def test_wait_limits(moe):
     for us, code in ((-1, -1), (10_000_001, -1), (10_000_000, 0), (1, 0), (0, 0)):
         c = moe.Int8Config(16, 1, 4, 1, 1, 0, us)
         assert moe.lib().colibri_moe_int8_quantize(ctypes.byref(c), None, 16, 0, None, None, None) == code
+
+
+def test_status_without_a_device(moe):
+    assert moe.lib().colibri_moe_int8_status(None) == -1
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        assert moe.lib().colibri_moe_int8_status(ctypes.byref(ctypes.c_int32())) == -4
