@@ -39,25 +39,27 @@ class Block:
         self.w2 = rn(experts, d, f) / f ** 0.5
         self.q1, self.q3, self.q2 = (ops.int8_quantize(w) for w in (self.w1, self.w3, self.w2))
 
+    def choose(self, x):
+        """The experts' input p and its routing."""
+        p = ops.pre_norm(x, self.norm_in)
+        return p, ops.route(p.float() @ self.w_router.t(), self.top_k, bias=self.bias, **self.routing)
+
     def forward(self, x):
         """x [T, d] bf16 -> (x1, the next block's input), both bf16."""
-        p = ops.pre_norm(x, self.norm_in)
-        r = ops.route(p.float() @ self.w_router.t(), self.top_k, bias=self.bias, **self.routing)
+        p, r = self.choose(x)
         h = ops.int8_experts(p, *self.q1, r.offsets, rows=r.token_of_row, w3=self.q3[0], w3_scale=self.q3[1])
         y = ops.combine(ops.int8_experts(h, *self.q2, r.offsets), r.row_of, r.gate, out_dtype=torch.float32)
         return ops.block_norm(x, y, after="rms", after_weight=self.norm_out, before="rms", before_weight=self.norm_next,
                               block_scale=0.5)
 
-    def reference(self, x):
-        """The same block in fp32 from the unquantised weights, expert by expert."""
+    def reference(self, x, idx=None):
+        """The same block in fp32 from the unquantised weights, expert by expert; with idx [T, k], by those experts
+        (a token whose choice is a close call may have others here)."""
         rms = lambda v, w: v * torch.rsqrt((v * v).mean(-1, keepdim=True) + 1e-6) * w  # noqa: E731
         x = x.float()
         p = rms(x, self.norm_in).bfloat16().float()
         s = torch.sigmoid(p @ self.w_router.t())
-        key = (s + self.bias).view(x.shape[0], self.routing["groups"], -1)
-        worth = key.topk(2, -1).values.sum(-1)
-        keep = torch.zeros_like(worth).scatter_(1, worth.topk(self.routing["top_groups"], 1).indices, 1.0).bool()
-        idx = key.masked_fill(~keep[:, :, None], -1e9).flatten(1).topk(self.top_k, 1).indices
+        idx = self.best(s) if idx is None else idx.long()
         gate = s.gather(1, idx)
         gate = gate / gate.sum(1, keepdim=True)
         y = torch.zeros_like(x)
@@ -69,6 +71,13 @@ class Block:
         x1 = x + 0.5 * rms(y, self.norm_out)
         return x1, rms(x1, self.norm_next)
 
+    def best(self, s):
+        """The experts that scores s [T, E] choose, in plain form."""
+        key = (s + self.bias).view(s.shape[0], self.routing["groups"], -1)
+        worth = key.topk(2, -1).values.sum(-1)
+        keep = torch.zeros_like(worth).scatter_(1, worth.topk(self.routing["top_groups"], 1).indices, 1.0).bool()
+        return key.masked_fill(~keep[:, :, None], -1e9).flatten(1).topk(self.top_k, 1).indices
+
     def gradients(self, x1, y, logits, idx, d_x1, d_p1, d_gate):
         """Gradients of the norms' inputs and vectors, and of the router's logits."""
         norms = ops.block_norm_backward(d_x1, d_p1, x1, y, after="rms", after_weight=self.norm_out, before="rms",
@@ -79,7 +88,7 @@ class Block:
 
 def error_of(block, x):
     """Largest |x1 - reference| over the reference's root mean square, and of the next input."""
-    out, want = block.forward(x), block.reference(x)
+    out, want = block.forward(x), block.reference(x, block.choose(x)[1].idx)
     return [float((a.float() - b).abs().max() / b.square().mean().sqrt()) for a, b in zip(out, want)]
 
 
