@@ -418,7 +418,8 @@ COLIBRI_API int colibri_moe_route_experts(const colibri_moe_route_config_t* cfg,
                                           size_t workspace_bytes, void* stream);
 
 /* d_logits [T, E] (row stride ld_d, the logits' type) from the gradient of gate: the choice idx [T, k] is
- * constant, slots with an index outside 0..E-1 contribute nothing, masked experts get 0.  The bias takes no
+ * constant and, as routing writes it, of distinct experts a token; slots with an index outside 0..E-1 contribute
+ * nothing, masked experts get 0.  The bias takes no
  * gradient: it does not enter the gates.  groups, top_groups and group_top are not used. */
 COLIBRI_API int colibri_moe_route_experts_backward(const colibri_moe_route_config_t* cfg, const void* logits,
                                                    int64_t ld, const int32_t* idx, const float* d_gate, int32_t T,

@@ -16,10 +16,11 @@
 // taken about the mean in a second sum over the registers (no E[v^2] - mean^2 cancellation).
 //
 // Measured on one GB300 (bf16 stream, RMS norms, 8192 x 4096): forward with an fp32 block output 67 us
-// (336 MB, 5.0 TB/s, 0.74 of the measured copy rate), backward 115 us (403 MB, 3.5 TB/s, 0.51).  What
-// bounds them is instruction issue and the row sums' barriers (the forward pass executes about 320
-// instructions a warp and row, for 8 columns a lane), not the copies: without the rows ahead the forward
-// pass took 92 us.  Odd widths take single-column accesses: 3001 x 1409 fp32, layer norms, 29 us, floor 10.
+// (336 MB, 5.0 TB/s, 0.74 of the measured copy rate), backward 115 us (403 MB, 3.5 TB/s, 0.51).  Neither DRAM
+// (0.54 and 0.41 busy) nor instruction issue (0.52 and 0.65 of the slots; the forward pass executes about 320
+// instructions a warp and row, for 8 columns a lane) is full: between them stand the row sums' barriers, which
+// 30 and 16 resident warps an SM do not hide.  Without the rows ahead the forward pass took 92 us, with more
+// instructions 78.  Odd widths take single-column accesses: 3001 x 1409 fp32, layer norms, 29 us, floor 10.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>

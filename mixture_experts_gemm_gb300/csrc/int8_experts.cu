@@ -85,7 +85,7 @@ struct Raw8<__nv_bfloat16> {
 
 // One block a row, held in registers between the maximum and the quotients: C chunks of 8 columns a
 // thread (16-byte loads), or read twice (C == 0).  The row once in, its fp16 once out: 16384 rows of 14336 from
-// 8192 tokens in about 0.25 ms (705 MB of floor, 0.10 ms; bound by instruction issue).
+// 8192 tokens in 0.17 ms by itself (705 MB of floor, 0.10 ms; issue slots 0.64, DRAM 0.68 busy).
 template <typename T, typename Q, int C, bool COPIES>
 __global__ void __launch_bounds__(kQuantThreads, C <= 2 ? 6 : 4) quantize_rows_kernel(QuantArgs a) {
   __shared__ float s_max[kQuantThreads / 32];
@@ -188,16 +188,25 @@ cudaError_t quantize(int dtype, const QuantArgs& q, cudaStream_t s) {
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Token rows of a tile, by the rows that an expert gets on average (the exact numbers are on the device):
-// an expert's rows should fit one tile, so that its weights are converted once, and no tile should be
-// much wider than its rows, because a wider one leaves less room for weights in flight.
+// Token rows of a tile, by the rows that an expert gets on average (the exact numbers are on the device): narrow
+// tiles leave more room for weights in flight, and rows that do not fit one tile have the expert's weights
+// converted again.  us on a GB300 with random routing, for eight experts of 2048 x 5632 x 2 / 64 of 2048 x 1409,
+// top-6, unevenly loaded / eight of 4096 x 4096, by the mean:
+//   mean  16: 32 rows  46 /  57 / 64,  64 rows  55 /  65 / 45
+//   mean  24: 32 rows  47 /  63 / 60,  64 rows  56 /  66 / 47
+//   mean  40: 64 rows  58 /  76 / 47, 128 rows  59 /  70 / 48
+//   mean  56: 64 rows  62 /  88 / 58, 128 rows  61 /  74 / 49
+//   mean  80: 128 rows 64 /  86 / 51, 256 rows  64 /  83 / 51
+//   mean 112: 128 rows 68 / 100 / 63, 256 rows  67 /  92 / 54
+//   mean 160: 128 rows 109 / 117 / 82, 256 rows 82 / 113 / 60
+// The steps at 16 and 48 lie between the shapes' own; the one at 128 lies above all of theirs (about 80).
 int int8_tile_rows(int R, int E) {
   const int64_t mean = R / std::min(E, R);
   return mean <= 16 ? 32 : mean <= 48 ? 64 : mean <= 128 ? 128 : 256;
 }
 
-// Of few rows, all SMs read the same few kilobytes at the same time; copies spread them over L2 (one token:
-// 60 -> 56 us; more rows only pay for the writes: 512 tokens 82 -> 84 us with four copies).
+// Of few rows, all SMs read the same few kilobytes at the same time; copies spread them over L2.  One copy / eight,
+// us: 8 rows 40 / 37, 30 rows 48 / 45, 64 rows 44 / 44, 96 rows 45 / 45, 128 rows 45 / 46 (the writes).
 constexpr int kInt8CopiedRows = 64, kInt8Copies = 8;
 
 // The workspace of a product: the rows' scales and fp16 values, tickets and partial sums of split tiles.

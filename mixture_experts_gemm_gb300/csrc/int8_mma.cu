@@ -24,15 +24,20 @@
 //   warps 2..5   epilogue.
 // The converters' work is about 1.5 instructions per weight, so it hides behind the MMAs of wide tiles (512
 // cycles a block of 64 columns of K) and behind HBM for narrow ones.  Items are (tile, part of K) in a
-// fixed order; a product of few tiles is split along K, the parts' sums kept in `partial` and added in order by whichever CTA finishes the tile (no floating-point
-// atomics: the same bits every time).
+// fixed order; a product of few tiles is split along K, the parts' sums kept in `partial` and added in order by
+// whichever CTA finishes the tile (no floating-point atomics: the same bits every time).
 //
-// Measured on one GB300 (whole calls, quantiser included): one token, two experts of 4096 x 14336 x 2, 48 us
-// (235 MB of weights, 4.9 TB/s, 0.72 of the measured copy rate); 512 tokens, eight experts of 2048 x 5632 x 2,
-// 78 us; 1021 tokens, top-6 of 64 experts of 2048 x 1409, 85 us; 8192 tokens, eight experts of 14336 x 4096,
-// 1.33 to 1.45 ms, of which this kernel 1.10 ms (1.75 PFLOP/s, 0.91 of cuBLAS bf16).  The widest tiles are
-// bound by the tensor cores, the narrowest by HBM and about 10 us of launches, first copies and epilogue,
-// those between by the MMA warp's loop and the epilogue (without it 512 tokens take 70 us).
+// Bytes become fp16 by the exponent: the byte is placed under that of 2^10, and one subtraction leaves the integer (a
+// known method: Kim et al., "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale
+// Production", 2022).
+//
+// Measured on one GB300 (whole calls, quantiser included): one token, two experts of 4096 x 14336 x 2, 47 us
+// (235 MB of weights, 5.0 TB/s, 0.73 of the measured copy rate); 512 tokens, eight experts of 2048 x 5632 x 2,
+// 79 to 84 us; 1021 tokens, top-6 of 64 experts of 2048 x 1409, 85 to 88 us; 8192 tokens, eight experts of
+// 14336 x 4096, 1.29 ms in a burst, 1.48 ms kept up (power), of which this kernel 1.10 ms (1.74 PFLOP/s, 0.91 of
+// cuBLAS bf16; tensor pipe active 0.76).  The widest tiles are bound by the tensor cores, the narrowest by HBM and
+// about 10 us of launches, first copies and epilogue, those between (tensor pipe 0.24 to 0.29, DRAM 0.33 to
+// 0.39, issue 0.43) by the MMA warp's loop and the epilogue (without it 512 tokens take about 10 us less).
 //
 // Every wait is bounded by the call's limit: when one gives up, all roles stop, copies and MMAs in flight are waited
 // for (at most kDrain each, whatever the limit), TMEM is freed and the device's status word gets a bit.

@@ -9,7 +9,7 @@
 // experts left gets index -1, gate 0 and row -1 in its last slots.
 //
 // The choice is that of the keys in 64 bits: scores are fp32, with a bound on their error beside them;
-// where a choice is not decided by more than the bounds (about one token in a thousand on normal
+// where a choice is not decided by more than the bounds (about one token in two thousand on normal
 // logits), the warp ranks that token again with 64-bit keys.  So which experts serve a token does not
 // hang on the rounding of one exp.  Two slots that hold the same logit and bias are equal, not close:
 // the lower index is right without a second look.
@@ -20,9 +20,9 @@
 // tokens come from one 32-bit token mask per expert.
 //
 // Measured on one GB300: one token of 256 experts in 8 groups 6 us on the device (the latency of one
-// kernel); 8192 tokens 35 us a call (three kernels: about 25, 4 and 5 us, and about 13 us once for the few
-// close calls of such a batch), against 1.4 us of bytes: bound by instruction issue (about 1200 a token)
-// and by the 64-bit unit.  Gradient, 8192 x 64: 6 us on the device.
+// kernel); 8192 tokens 34 to 38 us a call (three kernels: about 25, 4 and 5 us, of the first about 13 us once for
+// the few close calls of such a batch), against 1.4 us of bytes: bound by instruction issue (about 1200 a token,
+// 0.56 of the slots) and by the 64-bit unit.  Gradient, 8192 x 64: 6 us on the device.
 #include <algorithm>
 
 #include "ops_common.cuh"
