@@ -649,6 +649,12 @@ __global__ void __launch_bounds__(256) route_backward_kernel(RouteBackArgs a) {
       float m = -INFINITY;
       if (a.renorm) {
         m = warp_max(e >= 0 ? l : -INFINITY);
+        if (m < -350.f) {  // the row's largest may be 700 above (a row with logits above 350 is not looked for)
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int i = lane; i < a.E; i += 32) top = fmaxf(top, to_float(row[i]));
+          if (l - warp_max(top) < -700.f) e = -1, g = 0.f;  // a score of zero, as the forward pass has it
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < NS; ++j) {

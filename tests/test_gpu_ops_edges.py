@@ -1,4 +1,5 @@
 """The block operators on the GPU where ranges, host threads and streams meet their limits."""
+import math
 import threading
 
 import numpy as np
@@ -80,6 +81,31 @@ def test_gradient_of_renormalised_gates_of_scores_below_fp32(ops, score, far):
     (ref.gates(l64, idx, score, True, 2.5) * dg.double()).sum().backward()
     off = (got.double().cpu() - l64.grad).abs() - 2e-5 * 2.5 * dg.double().abs().amax(1, keepdim=True)
     assert float(off.max()) <= 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gates_of_logits_masked_by_the_lowest_value(ops, score, dtype):
+    """Experts masked by the type's lowest logit, chosen because a bias keeps the others out: their scores are zero, so
+    their gates and gradients are, as 0 / 0 of the definition.  A row of nothing but the lowest value masks
+    nobody under a softmax."""
+    T, E, k = 6, 8, 3
+    l = torch.full((T, E), torch.finfo(dtype).min, dtype=dtype)
+    l[:4, 0], l[1, 1] = 2.0, -1.0
+    bias = torch.zeros(E)
+    bias[:2] = -math.inf
+    r = ops.route(l.cuda(), k, score=score, bias=bias.cuda())
+    dg = torch.randn(T, k, generator=gen(31))
+    d = ops.route_backward(l.cuda(), r.idx, dg.cuda(), score=score)
+    assert r.idx.tolist() == [[2, 3, 4]] * T
+    assert (r.gate[:4] == 0).all() and (d[:4] == 0).all()
+    if score == "sigmoid":
+        assert (r.gate == 0).all() and (d == 0).all()
+    else:
+        assert ((r.gate[4:] - 1 / 3).abs() < 1e-6).all()
+        want = torch.zeros(2, E, dtype=torch.float64)
+        want[:, 2:5] = (dg[4:].double() - dg[4:].double().mean(1, keepdim=True)) / 3
+        assert ((d[4:].double().cpu() - want).abs() <= 1e-6 + ref.half_step(dtype) * want.abs()).all()
 
 
 def test_threads_at_different_widths(ops):
