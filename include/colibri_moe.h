@@ -476,6 +476,47 @@ COLIBRI_API int colibri_moe_combine_rows(const void* y, int32_t y_dtype, int32_t
                                          const float* gate, int32_t T, int32_t k, int32_t d, void* out,
                                          int32_t out_dtype, void* stream);
 
+/* ---- tokens to their experts' rows and back ----
+ * The dispatch order of any choice of experts idx [T, k] (a replayed choice, another router's, one with slots dropped):
+ * rows grouped by expert, ascending tokens inside each (a token's slots in order), no padding, as routing writes it:
+ * counts [E], offsets [E + 1], row_of [T, k] and token_of_row [T * k] (-1 at rows from offsets[E] on).  A slot with
+ * an index outside 0..E-1 has no row (row_of -1).  k 1..32, E 1..512.  T == 0 zeroes counts and offsets.
+ * trusted_pointers, here and in the calls below: see above. */
+COLIBRI_API int colibri_moe_dispatch_order(const int32_t* idx, int32_t T, int32_t k, int32_t E, int32_t* counts,
+                                           int32_t* offsets, int32_t* row_of, int32_t* token_of_row,
+                                           int32_t trusted_pointers, void* stream);
+
+/* rows [R, d] = x[token_of_row] (x [T, d] of row stride ldx), zeros where the token is outside 0..T-1.  d 1..65536. */
+COLIBRI_API int colibri_moe_dispatch_rows(const void* x, int32_t dtype, int64_t ldx, int32_t T,
+                                          const int32_t* token_of_row, int32_t R, int32_t d, void* rows,
+                                          int32_t trusted_pointers, void* stream);
+
+/* The gradient of dispatch_rows: d_x[t] = sum over s < k of d_rows[row_of[t, s]], in slot order in fp32, slots with a
+ * row outside 0..R-1 left out.  d_rows [R, d] contiguous in dtype, d_x [T, d] in out_dtype. */
+COLIBRI_API int colibri_moe_dispatch_backward(const void* d_rows, int32_t dtype, int32_t R, const int32_t* row_of,
+                                              int32_t T, int32_t k, int32_t d, void* d_x, int32_t out_dtype,
+                                              int32_t trusted_pointers, void* stream);
+
+/* The gradients of colibri_moe_combine_rows, from that of its result, d_out [T, d] (row stride ld_out, in dtype):
+ *   d_y[row_of[t, s]] = gate[t, s] * d_out[t],   d_gate[t, s] = <d_out[t], y[row_of[t, s]]>   (fp32 sums)
+ * y and d_y [R, d] contiguous in y_dtype, d_gate [T, k] fp32 (0 for slots without a row).  row_of and token_of_row are
+ * one dispatch order: token_of_row[row_of[t, s]] == t.  Rows whose token is outside 0..T-1 get zeros; a row that
+ * several slots of its token name gets the sum of their gates. */
+COLIBRI_API int colibri_moe_combine_backward(const void* d_out, int32_t dtype, int64_t ld_out, const void* y,
+                                             int32_t y_dtype, int32_t R, const int32_t* row_of, const float* gate,
+                                             const int32_t* token_of_row, int32_t T, int32_t k, int32_t d, void* d_y,
+                                             float* d_gate, int32_t trusted_pointers, void* stream);
+
+/* ---- the gated activation between an expert's projections, and its gradients ----
+ *   h = silu(u) * v,   d_u = d_h * v * p * (1 + u * (1 - p)),   d_v = d_h * u * p,   p = 1 / (1 + exp(-u)), silu(u) = u p
+ * u and v [R, f] of row strides ldu and ldv (the halves of one product, say) in dtype; h [R, f] contiguous in out_dtype;
+ * d_h of row stride ld_h in h_dtype, d_u and d_v contiguous in dtype.  f 1..65536. */
+COLIBRI_API int colibri_moe_gated(const void* u, int64_t ldu, const void* v, int64_t ldv, int32_t dtype, int32_t R,
+                                  int32_t f, void* h, int32_t out_dtype, int32_t trusted_pointers, void* stream);
+COLIBRI_API int colibri_moe_gated_backward(const void* d_h, int32_t h_dtype, int64_t ld_h, const void* u, int64_t ldu,
+                                           const void* v, int64_t ldv, int32_t dtype, int32_t R, int32_t f, void* d_u,
+                                           void* d_v, int32_t trusted_pointers, void* stream);
+
 /* Frees everything the context owns (the articles' colibri_free, the release call every program
  * must make once it is done: zskr.cn 4.3, m.nxbn.cn 4.3).  NULL-safe. */
 COLIBRI_API void colibri_moe_destroy(colibri_moe_t* ctx);

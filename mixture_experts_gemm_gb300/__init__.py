@@ -42,7 +42,9 @@ EXPORTED = ("colibri_moe_create", "colibri_moe_load_weights", "colibri_moe_forwa
             "colibri_moe_block_norm", "colibri_moe_block_norm_backward_workspace", "colibri_moe_block_norm_backward",
             "colibri_moe_route_experts_workspace", "colibri_moe_route_experts", "colibri_moe_route_experts_backward",
             "colibri_moe_int8_quantize", "colibri_moe_int8_experts_workspace", "colibri_moe_int8_experts",
-            "colibri_moe_int8_status", "colibri_moe_combine_rows", "colibri_moe_destroy", "colibri_moe_strerror")
+            "colibri_moe_int8_status", "colibri_moe_combine_rows", "colibri_moe_dispatch_order",
+            "colibri_moe_dispatch_rows", "colibri_moe_dispatch_backward", "colibri_moe_combine_backward",
+            "colibri_moe_gated", "colibri_moe_gated_backward", "colibri_moe_destroy", "colibri_moe_strerror")
 
 
 class ColibriError(RuntimeError):
@@ -138,6 +140,13 @@ def lib() -> ctypes.CDLL:
                                          ctypes.c_int),
             "colibri_moe_int8_status": ([vp], ctypes.c_int),
             "colibri_moe_combine_rows": ([vp, i32, i32, vp, vp, i32, i32, i32, vp, i32, vp], ctypes.c_int),
+            "colibri_moe_dispatch_order": ([vp, i32, i32, i32, vp, vp, vp, vp, i32, vp], ctypes.c_int),
+            "colibri_moe_dispatch_rows": ([vp, i32, i64, i32, vp, i32, i32, vp, i32, vp], ctypes.c_int),
+            "colibri_moe_dispatch_backward": ([vp, i32, i32, vp, i32, i32, i32, vp, i32, i32, vp], ctypes.c_int),
+            "colibri_moe_combine_backward": ([vp, i32, i64, vp, i32, i32, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp],
+                                             ctypes.c_int),
+            "colibri_moe_gated": ([vp, i64, vp, i64, i32, i32, i32, vp, i32, i32, vp], ctypes.c_int),
+            "colibri_moe_gated_backward": ([vp, i32, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, vp], ctypes.c_int),
             "colibri_moe_destroy": ([vp], None),
             "colibri_moe_strerror": ([ctypes.c_int], ctypes.c_char_p),
         }

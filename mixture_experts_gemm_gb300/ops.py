@@ -2,8 +2,9 @@
 
 The counterparts of the context-free calls of ``include/colibri_moe.h``: norms before and after a
 block with its gate and residual scale (``block_norm``), routing to many experts with the dispatch
-order (``route``), experts in 8-bit integers (``int8_experts``) and their combine (``combine``), with
-the backward passes of the norms and of the routing.  Every call runs on CUDA tensors, asynchronously
+order (``route``), experts in 8-bit integers (``int8_experts``) and their combine (``combine``), tokens to
+their experts' rows and back for any choice of experts (``dispatch_order``, ``dispatch``), the gated activation
+(``gated``), with the backward passes of all but the 8-bit integers.  Every call runs on CUDA tensors, asynchronously
 on ``stream`` (default: the current stream), allocates its outputs and workspace from torch, and can be
 captured into a CUDA graph.  Errors raise ``ColibriError`` (checks of the library) or ``ValueError``
 (shapes and types that cannot be passed on).  Results are not attached to autograd: the backward passes
@@ -29,7 +30,8 @@ import torch
 from . import DTYPE_BF16, DTYPE_F32, ColibriError, Int8Config, NormConfig, RouteConfig, _check, lib
 
 __all__ = ["block_norm", "block_norm_backward", "pre_norm", "route", "route_backward", "Routing", "int8_quantize",
-           "int8_experts", "int8_status", "combine", "ColibriError"]
+           "int8_experts", "int8_status", "combine", "combine_backward", "dispatch_order", "Order", "dispatch",
+           "dispatch_backward", "gated", "gated_backward", "ColibriError"]
 
 _DTYPE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -436,3 +438,128 @@ def combine(y, row_of, gate, *, out_dtype=None, stream=None):
                "colibri_moe_combine_rows")
         return out
     return _run(call, y, on, stream)
+
+
+# ------------------------------------------------------------------------- tokens to rows and back
+class Order(NamedTuple):
+    """The dispatch order of a choice of experts (rows grouped by expert, tokens ascending), as Routing has it."""
+    counts: torch.Tensor        # [E] int32
+    offsets: torch.Tensor       # [E + 1] int32
+    row_of: torch.Tensor        # [T, k] int32, -1 where idx names no expert
+    token_of_row: torch.Tensor  # [T * k] int32, -1 from offsets[E] on
+
+
+def dispatch_order(idx, num_experts: int, *, stream=None) -> Order:
+    """The dispatch order of any choice idx [T, k] (int32) of experts: a replayed one, another router's, one with slots
+    dropped (an index outside 0..num_experts-1 gets no row).  A token may name an expert more than once."""
+    T, k = _shape(idx, "idx")
+    on = _device(idx, "idx")
+    pi = _vector(idx, "idx", (T, k), torch.int32, on)
+    E = operator.index(num_experts)
+    if E < 1:
+        raise ValueError("num_experts must be positive")
+
+    def call(s):
+        dev, i32 = idx.device, torch.int32
+        o = Order(torch.empty(E, dtype=i32, device=dev), torch.empty(E + 1, dtype=i32, device=dev),
+                  torch.empty((T, k), dtype=i32, device=dev), torch.empty(T * k, dtype=i32, device=dev))
+        _check(lib().colibri_moe_dispatch_order(pi, T, k, E, *[t.data_ptr() for t in o], 1, s),
+               "colibri_moe_dispatch_order")
+        return o
+    return _run(call, idx, on, stream)
+
+
+def dispatch(x, token_of_row, *, stream=None):
+    """rows [R, d]: x[token_of_row], zeros where the token is -1 (x's rows may be strided)."""
+    T, d = _shape(x, "x")
+    on = _device(x, "x")
+    px, ldx = _matrix(x, "x", T, d, on)
+    dt = _dtype(x.dtype, "x")
+    R = token_of_row.numel()
+    pt = _vector(token_of_row, "token_of_row", (R,), torch.int32, on)
+    _unattached("dispatch", "dispatch_backward computes it", x)
+
+    def call(s):
+        rows = torch.empty((R, d), dtype=x.dtype, device=x.device)
+        _check(lib().colibri_moe_dispatch_rows(px, dt, ldx, T, pt, R, d, rows.data_ptr(), 1, s),
+               "colibri_moe_dispatch_rows")
+        return rows
+    return _run(call, x, on, stream)
+
+
+def dispatch_backward(d_rows, row_of, *, out_dtype=None, stream=None):
+    """d_x [T, d]: the sum of d_rows[row_of] over a token's slots, in slot order in fp32; rows of -1 are left out."""
+    R, d = _shape(d_rows, "d_rows")
+    on = _device(d_rows, "d_rows")
+    pr = _vector(d_rows, "d_rows", (R, d), d_rows.dtype, on)
+    T, k = _shape(row_of, "row_of")
+    po = _vector(row_of, "row_of", (T, k), torch.int32, on)
+    out_dtype = d_rows.dtype if out_dtype is None else out_dtype
+    types = _dtype(d_rows.dtype, "d_rows"), _dtype(out_dtype, "out_dtype")
+
+    def call(s):
+        d_x = torch.empty((T, d), dtype=out_dtype, device=d_rows.device)
+        _check(lib().colibri_moe_dispatch_backward(pr, types[0], R, po, T, k, d, d_x.data_ptr(), types[1], 1, s),
+               "colibri_moe_dispatch_backward")
+        return d_x
+    return _run(call, d_rows, on, stream)
+
+
+def combine_backward(d_out, y, row_of, gate, token_of_row, *, stream=None):
+    """(d_y [R, d] in y's type, d_gate [T, k] fp32): the gradients of ``combine`` from that of its result, d_out [T, d].
+
+    row_of and token_of_row are one dispatch order (``Routing`` or ``Order``).  Rows without a token get zeros, slots
+    without a row a gate's gradient of 0."""
+    T, d = _shape(d_out, "d_out")
+    on = _device(d_out, "d_out")
+    pd, ldd = _matrix(d_out, "d_out", T, d, on)
+    R = _shape(y, "y")[0]
+    py = _vector(y, "y", (R, d), y.dtype, on)
+    k = _shape(row_of, "row_of")[1]
+    po = _vector(row_of, "row_of", (T, k), torch.int32, on)
+    pg = _vector(gate, "gate", (T, k), torch.float32, on)
+    pt = _vector(token_of_row, "token_of_row", (R,), torch.int32, on)
+    types = _dtype(d_out.dtype, "d_out"), _dtype(y.dtype, "y")
+
+    def call(s):
+        d_y = torch.empty((R, d), dtype=y.dtype, device=y.device)
+        d_gate = torch.empty((T, k), dtype=torch.float32, device=y.device)
+        _check(lib().colibri_moe_combine_backward(pd, types[0], ldd, py, types[1], R, po, pg, pt, T, k, d, d_y.data_ptr(),
+                                                  d_gate.data_ptr(), 1, s), "colibri_moe_combine_backward")
+        return d_y, d_gate
+    return _run(call, d_out, on, stream)
+
+
+# ------------------------------------------------------------------------------ gated activation
+def gated(u, v, *, out_dtype=None, stream=None):
+    """silu(u) * v of two [R, f] tensors of one type, whose rows may be strided (the halves of one product, say)."""
+    R, f = _shape(u, "u")
+    on = _device(u, "u")
+    pu, ldu = _matrix(u, "u", R, f, on)
+    pv, ldv = _matrix(v, "v", R, f, on, u.dtype)
+    out_dtype = u.dtype if out_dtype is None else out_dtype
+    types = _dtype(u.dtype, "u"), _dtype(out_dtype, "out_dtype")
+    _unattached("gated", "gated_backward computes it", u, v)
+
+    def call(s):
+        h = torch.empty((R, f), dtype=out_dtype, device=u.device)
+        _check(lib().colibri_moe_gated(pu, ldu, pv, ldv, types[0], R, f, h.data_ptr(), types[1], 1, s), "colibri_moe_gated")
+        return h
+    return _run(call, u, on, stream)
+
+
+def gated_backward(d_h, u, v, *, stream=None):
+    """(d_u, d_v), in the type of u and v, from the gradient of ``gated``'s result (of its own type)."""
+    R, f = _shape(u, "u")
+    on = _device(u, "u")
+    ph, ldh = _matrix(d_h, "d_h", R, f, on)
+    pu, ldu = _matrix(u, "u", R, f, on)
+    pv, ldv = _matrix(v, "v", R, f, on, u.dtype)
+    types = _dtype(d_h.dtype, "d_h"), _dtype(u.dtype, "u")
+
+    def call(s):
+        d_u, d_v = (torch.empty((R, f), dtype=u.dtype, device=u.device) for _ in range(2))
+        _check(lib().colibri_moe_gated_backward(ph, types[0], ldh, pu, ldu, pv, ldv, types[1], R, f, d_u.data_ptr(),
+                                                d_v.data_ptr(), 1, s), "colibri_moe_gated_backward")
+        return d_u, d_v
+    return _run(call, u, on, stream)
