@@ -517,6 +517,61 @@ COLIBRI_API int colibri_moe_gated_backward(const void* d_h, int32_t h_dtype, int
                                            const void* v, int64_t ldv, int32_t dtype, int32_t R, int32_t f, void* d_u,
                                            void* d_v, int32_t trusted_pointers, void* stream);
 
+/* ---- experts in 8-bit floating point (e4m3): a scale for every block of 128 ----
+ * A block's scale is max |x| / 448 and its values q = e4m3(x / scale) (IEEE fp32 quotients, ties to even, at most 448 in
+ * size).  A block of zeros gives zeros; one that holds an infinity or a NaN has the scale NaN, and every result that it
+ * enters is NaN.  Blocks: 128 neighbouring columns of a row (activations, sx), or 128 x 128 of a weight matrix
+ * (w_scale [E, ceil(N / 128), ceil(K / 128)] fp32); the last block of a row or column may be shorter.
+ *   v[r, n] = sum_b sx[r, b] * w_scale[e, n / 128, b] * sum_{k in b} q[r, k] * w[e, n, k],   r in segment e
+ *   y[r, n] = v[r, n],  or with w3:  silu(v[r, n]) * v3[r, n]
+ * and the gradients of v, with the gradient of y in the same format:
+ *   d_x[r, k] = sum_b sd[r, b] * w_scale[e, b, k / 128] * sum_{n in b} qd[r, n] * w[e, n, k]        (blocks along n)
+ *   d_w[e, n, k] = sum_b td[b, n] * tx[b, k] * sum_{r in b} qd'[r, n] * q'[r, k]
+ * with, for d_w, a scale for every column and 128 rows of the expert's segment (counted from its first one). */
+typedef struct {
+  int32_t in_features;   /* K, 16..65536, a multiple of 16                                          */
+  int32_t out_features;  /* N, 1..131072 (channels of y; with w3, of each projection)               */
+  int32_t num_experts;   /* E, 1..512 (1: a plain linear layer)                                      */
+  int32_t dtype;         /* COLIBRI_DTYPE_* of x, d_y and d_x                                        */
+  int32_t out_dtype;     /* COLIBRI_DTYPE_* of y, or of d_w                                          */
+  int32_t trusted_pointers; /* see above                                                            */
+  int32_t wait_limit_us; /* as for the 8-bit integers                                               */
+} colibri_moe_fp8_config_t;
+
+/* q [n, K] e4m3 bytes and scales of x [n, K] (row stride ldx).  square 0: a scale for every 128 columns of a row, scale
+ * [n, ceil(K / 128)].  square 1: weights, the n rows in num_experts equal matrices (n a multiple of it): a scale for every
+ * block of 128 x 128, scale [num_experts, ceil(n / num_experts / 128), ceil(K / 128)].  Uses cfg's in_features,
+ * num_experts and dtype. */
+COLIBRI_API int colibri_moe_fp8_quantize(const colibri_moe_fp8_config_t* cfg, const void* x, int64_t ldx, int32_t n,
+                                         int32_t square, uint8_t* q, float* scale, void* stream);
+
+COLIBRI_API int colibri_moe_fp8_experts_workspace(const colibri_moe_fp8_config_t* cfg, int32_t n_tokens, int32_t R,
+                                                  size_t* bytes);
+
+/* As colibri_moe_int8_experts: x [n_tokens, K] (row stride ldx) is quantised within the call; w and w3 [E, N, K] e4m3
+ * bytes (16-byte aligned), offsets [E + 1], rows [R] or NULL.  y [R, N]: rows from offsets[E] on are not written. */
+COLIBRI_API int colibri_moe_fp8_experts(const colibri_moe_fp8_config_t* cfg, const void* x, int64_t ldx,
+                                        int32_t n_tokens, const int32_t* rows, int32_t R, const int32_t* offsets,
+                                        const uint8_t* w, const float* w_scale, const uint8_t* w3,
+                                        const float* w3_scale, void* y, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+COLIBRI_API int colibri_moe_fp8_experts_backward_workspace(const colibri_moe_fp8_config_t* cfg, int32_t n_tokens,
+                                                           int32_t R, size_t* bytes);
+
+/* The gradients of colibri_moe_fp8_experts without w3, from d_y [R, N] (row stride ld_dy): d_rows [R, K] in dtype, one
+ * row for each of y's (colibri_moe_dispatch_backward adds up a token's; rows from offsets[E] on are not written), or
+ * NULL with w and w_scale; d_w [E, N, K] in out_dtype (zeros for an expert without rows), or NULL with x and rows. */
+COLIBRI_API int colibri_moe_fp8_experts_backward(const colibri_moe_fp8_config_t* cfg, const void* d_y, int64_t ld_dy,
+                                                 const void* x, int64_t ldx, int32_t n_tokens, const int32_t* rows,
+                                                 int32_t R, const int32_t* offsets, const uint8_t* w,
+                                                 const float* w_scale, void* d_rows, void* d_w, void* workspace,
+                                                 size_t workspace_bytes, void* stream);
+
+/* As colibri_moe_int8_status, for the products of the two calls above. */
+#define COLIBRI_FP8_WAIT_EXPIRED 1
+COLIBRI_API int colibri_moe_fp8_status(int32_t* status);
+
 /* Frees everything the context owns (the articles' colibri_free, the release call every program
  * must make once it is done: zskr.cn 4.3, m.nxbn.cn 4.3).  NULL-safe. */
 COLIBRI_API void colibri_moe_destroy(colibri_moe_t* ctx);

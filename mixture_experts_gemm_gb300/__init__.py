@@ -44,7 +44,9 @@ EXPORTED = ("colibri_moe_create", "colibri_moe_load_weights", "colibri_moe_forwa
             "colibri_moe_int8_quantize", "colibri_moe_int8_experts_workspace", "colibri_moe_int8_experts",
             "colibri_moe_int8_status", "colibri_moe_combine_rows", "colibri_moe_dispatch_order",
             "colibri_moe_dispatch_rows", "colibri_moe_dispatch_backward", "colibri_moe_combine_backward",
-            "colibri_moe_gated", "colibri_moe_gated_backward", "colibri_moe_destroy", "colibri_moe_strerror")
+            "colibri_moe_gated", "colibri_moe_gated_backward", "colibri_moe_fp8_quantize",
+            "colibri_moe_fp8_experts_workspace", "colibri_moe_fp8_experts", "colibri_moe_fp8_experts_backward_workspace",
+            "colibri_moe_fp8_experts_backward", "colibri_moe_fp8_status", "colibri_moe_destroy", "colibri_moe_strerror")
 
 
 class ColibriError(RuntimeError):
@@ -81,6 +83,12 @@ class RouteConfig(ctypes.Structure):
 
 
 class Int8Config(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("num_experts", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("trusted_pointers", ctypes.c_int32),
+                ("wait_limit_us", ctypes.c_int32)]
+
+
+class Fp8Config(ctypes.Structure):
     _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("num_experts", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("trusted_pointers", ctypes.c_int32),
                 ("wait_limit_us", ctypes.c_int32)]
@@ -147,6 +155,14 @@ def lib() -> ctypes.CDLL:
                                              ctypes.c_int),
             "colibri_moe_gated": ([vp, i64, vp, i64, i32, i32, i32, vp, i32, i32, vp], ctypes.c_int),
             "colibri_moe_gated_backward": ([vp, i32, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, vp], ctypes.c_int),
+            "colibri_moe_fp8_quantize": ([vp, vp, i64, i32, i32, vp, vp, vp], ctypes.c_int),
+            "colibri_moe_fp8_experts_workspace": ([vp, i32, i32, vp], ctypes.c_int),
+            "colibri_moe_fp8_experts": ([vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp],
+                                        ctypes.c_int),
+            "colibri_moe_fp8_experts_backward_workspace": ([vp, i32, i32, vp], ctypes.c_int),
+            "colibri_moe_fp8_experts_backward": ([vp, vp, i64, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp, vp,
+                                                  ctypes.c_size_t, vp], ctypes.c_int),
+            "colibri_moe_fp8_status": ([vp], ctypes.c_int),
             "colibri_moe_destroy": ([vp], None),
             "colibri_moe_strerror": ([ctypes.c_int], ctypes.c_char_p),
         }

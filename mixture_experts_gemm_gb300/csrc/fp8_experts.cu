@@ -1,0 +1,604 @@
+// Experts in 8-bit floating point: the quantisers and the entry points (the products are in fp8_mma.cuh).
+//
+//   scale = max |x| / 448 over a block of 128,  q = e4m3(x / scale)   (IEEE fp32 quotients, ties to even)
+//
+// Blocks lie along a row (activations and gradients, for products that sum over a row's columns), down 128 rows of
+// an expert (for the weights' gradient, which sums over rows), or cover 128 x 128 (weights).
+#include <algorithm>
+#include <mutex>
+
+#include <cuda_fp8.h>
+
+#include "fp8_internal.cuh"
+
+namespace colibri {
+namespace {
+
+__device__ int g_status;  // what the waits of all products on this device have come to since it was last taken
+__device__ int g_taken;
+__global__ void take_status_kernel() { g_taken = atomicExch(&g_status, 0); }
+
+constexpr float kTop = 448.f;
+
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// A block's scale as every lane that shares `top` (the largest |x|, infinite after a NaN or an infinity) has it.
+struct Scale {
+  float scale, inv;
+  bool live, exact;
+  __device__ __forceinline__ explicit Scale(float top) {
+    scale = top < INFINITY ? __fdiv_rn(top, kTop) : NAN;
+    live = scale > 0.f;
+    exact = scale < 1e-30f;  // 1 / scale may overflow there
+    inv = live ? __frcp_rn(scale) : 0.f;
+  }
+};
+
+// e4m3(x / scale) of the IEEE quotient, eight at a time.  The product with 1 / scale is within 3 ulp of the quotient; it
+// rounds to the same e4m3 unless it is that near to the middle of two (20 bits below the three that are kept).
+// Only there, and below e4m3's normal range where the middles lie elsewhere, is the division done.
+__device__ __forceinline__ uint2 quantised8(const float (&x)[8], const Scale& s) {
+  if (!s.live) return make_uint2(0, 0);
+  float p[8];
+  bool doubt = s.exact;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    p[j] = x[j] * s.inv;
+    const uint32_t u = __float_as_uint(p[j]);
+    doubt |= ((u + 8 - 0x80000u) & 0xfffffu) <= 16u || (fabsf(p[j]) < 0.0156255f && p[j] != 0.f);
+  }
+  if (doubt) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = __fdiv_rn(x[j], s.scale);
+  }
+  return make_uint2(e4m3_pair(p[0], p[1]) | e4m3_pair(p[2], p[3]) << 16,
+                    e4m3_pair(p[4], p[5]) | e4m3_pair(p[6], p[7]) << 16);
+}
+
+// Largest |v|, infinite once a NaN or an infinity is among them.
+__device__ __forceinline__ float top_of(float top, float v) {
+  const float m = fabsf(v);
+  return m < INFINITY ? fmaxf(top, m) : INFINITY;
+}
+
+// Columns col .. col + 7 of a row of `cols`; zeros past its end.
+template <typename T, bool VEC>
+__device__ __forceinline__ void read8(const T* row, int col, int cols, float (&v)[8]) {
+  if constexpr (VEC) {
+    if (col < cols) {
+      load8(row + col, v);
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = !VEC && col + j < cols ? to_float(row[col + j]) : 0.f;
+}
+
+// ------------------------------------------------------------------------------------- along rows
+struct RowQuant {
+  const void* x;
+  int64_t ldx;
+  int n_tokens;
+  const int32_t* rows;  // token of each row, or nullptr: the row itself
+  int n, cols;          // rows to write; columns of x
+  uint8_t* q;           // [n][ldq], zeros from cols on
+  int ldq;
+  float* scale;         // of row r, block b at b * block_step + r * row_step
+  int64_t row_step, block_step;
+  uint32_t* ticket;     // cleared for the product, or nullptr
+  int n_ticket;
+};
+
+constexpr int kRowThreads = 256, kRowsAt = 32, kColsAt = 256;  // rows and columns of a thread block
+
+// Half a warp a block of 128, a warp four rows' 256 columns; all four are on their way before the first is used.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(RowQuant a) {
+  __shared__ float s_scale[kRowsAt][2];
+  pdl_wait();
+  pdl_trigger();  // after the wait: what starts early may read what was there before this kernel
+  if (blockIdx.y == 0)
+    for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < a.n_ticket; i += (int64_t)gridDim.x * kRowThreads)
+      a.ticket[i] = 0;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = blockIdx.x * kRowsAt, col = blockIdx.y * kColsAt + lane * 8;
+  float v[4][8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = r0 + j * 8 + warp;
+    int t = -1;
+    if (r < a.n) t = a.rows ? a.rows[r] : r;
+    const bool real = t >= 0 && t < a.n_tokens;
+    read8<T, VEC>(static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx, col, real ? a.cols : 0, v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = r0 + j * 8 + warp;
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = top_of(top, v[j][i]);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const Scale s(top);
+    if ((lane & 15) == 0) s_scale[j * 8 + warp][lane >> 4] = s.scale;
+    if (r < a.n && col < a.ldq) *reinterpret_cast<uint2*>(a.q + (int64_t)r * a.ldq + col) = quantised8(v[j], s);
+  }
+  __syncthreads();
+  if (threadIdx.x < 2 * kRowsAt) {
+    const int b = threadIdx.x / kRowsAt, r = threadIdx.x % kRowsAt, blk = blockIdx.y * 2 + b;
+    if (r0 + r < a.n && blk * kFp8Block < a.cols)
+      a.scale[blk * a.block_step + (r0 + r) * a.row_step] = s_scale[r][b];
+  }
+}
+
+// ------------------------------------------------------------------------------ tiles of 128 x 128
+enum TileScale { kColumns, kSquare };
+
+struct TileQuant {
+  const void* x;
+  int64_t ldx;
+  int n_tokens;
+  const int32_t* rows;     // token of each row, or nullptr: the row itself
+  const int32_t* offsets;  // kColumns: [E + 1], the experts' rows; a tile's rows are 128 of one expert
+  int E, R;
+  int matrix_rows;         // kSquare: rows of each matrix; a tile's rows are 128 of one matrix
+  int cols;
+  uint8_t* q;              // kColumns: [tiles * 128][ldq], zeros past an expert's rows; kSquare: [rows][ldq]
+  int ldq;
+  float* scale;            // kColumns: [tiles][lds]; kSquare: [tiles][ceil(cols / 128)]
+  int64_t lds;
+  uint8_t* row_q;          // or nullptr: the same rows with scales along them, [R][ldq] and
+  float* row_scale;        // [ceil(cols / 128)][R]
+  uint32_t* ticket;
+  int n_ticket;
+};
+
+constexpr int kTileThreads = 256;
+
+// A block of threads takes tiles of the same 128 rows: a thread eight columns of eight rows, 16 apart.
+template <typename T, bool VEC, int KIND>
+__global__ void __launch_bounds__(kTileThreads) quantise_tiles_kernel(TileQuant a) {
+  __shared__ int s_row0[kFp8MaxExperts], s_rows[kFp8MaxExperts], s_tiles[kFp8MaxExperts + 1];
+  __shared__ float s_top[8][kFp8Block];
+  __shared__ float s_row_scale[kFp8Block];
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.y == 0)
+    for (int64_t i = (int64_t)blockIdx.x * kTileThreads + threadIdx.x; i < a.n_ticket; i += (int64_t)gridDim.x * kTileThreads)
+      a.ticket[i] = 0;
+  int64_t first;  // row of x (or of `rows`)
+  int n;
+  if constexpr (KIND == kColumns) {
+    if (warp == 0)
+      fp8_segments(a.offsets, a.E, a.R, lane, s_row0, s_rows, s_tiles, [](int m) { return (m + kFp8Block - 1) / kFp8Block; });
+    __syncthreads();
+    if ((int)blockIdx.x >= s_tiles[a.E]) return;
+    int lo = 0, hi = a.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (s_tiles[mid] <= (int)blockIdx.x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int at = ((int)blockIdx.x - s_tiles[lo]) * kFp8Block;
+    first = s_row0[lo] + at;
+    n = min(s_rows[lo] - at, kFp8Block);
+  } else {
+    const int per = (a.matrix_rows + kFp8Block - 1) / kFp8Block, m = blockIdx.x / per, at = (blockIdx.x - m * per) * kFp8Block;
+    first = (int64_t)m * a.matrix_rows + at;
+    n = min(a.matrix_rows - at, kFp8Block);
+  }
+  const int ty = threadIdx.x >> 4;
+  const int64_t out0 = KIND == kColumns ? (int64_t)blockIdx.x * kFp8Block : first;
+  const T* src[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int i = ty + 16 * j;
+    int64_t t = -1;
+    if (i < n) t = a.rows ? a.rows[first + i] : first + i;
+    src[j] = t >= 0 && t < a.n_tokens ? static_cast<const T*>(a.x) + t * a.ldx : nullptr;
+  }
+  for (int ct = blockIdx.y; ct * kFp8Block < a.ldq; ct += gridDim.y) {
+    const int c = (threadIdx.x & 15) * 8, col = ct * kFp8Block + c;
+    float v[8][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      read8<T, VEC>(src[j] ? src[j] : static_cast<const T*>(a.x), col, src[j] ? a.cols : 0, v[j]);
+    float top[8] = {};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = top_of(top[i], v[j][i]);
+    if constexpr (KIND == kSquare) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top[0] = fmaxf(top[0], top[i]);
+      top[0] = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top[0])));  // not negative: ordered as its bits
+      if (lane == 0) s_top[warp][0] = top[0];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 16));
+        if (lane < 16) s_top[warp][c + i] = top[i];
+      }
+    }
+    if (KIND == kColumns && a.row_q) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = top_of(m, v[j][i]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        const Scale s(m);
+        const int i = ty + 16 * j;
+        if ((lane & 15) == 0) s_row_scale[i] = s.scale;
+        if (i < n && col < a.ldq) *reinterpret_cast<uint2*>(a.row_q + (first + i) * a.ldq + col) = quantised8(v[j], s);
+      }
+    }
+    __syncthreads();
+    if constexpr (KIND == kSquare) {
+      float m = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) m = fmaxf(m, s_top[w][0]);
+      const Scale s(m);
+      if (threadIdx.x == 0) a.scale[(int64_t)blockIdx.x * a.lds + ct] = s.scale;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (ty + 16 * j < n && col < a.ldq)
+          *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = quantised8(v[j], s);
+    } else {
+      if (threadIdx.x < kFp8Block) {
+        float m = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, s_top[w][threadIdx.x]);
+        s_top[0][threadIdx.x] = m;  // this thread alone reads and writes the column
+        a.scale[(int64_t)blockIdx.x * a.lds + ct * kFp8Block + threadIdx.x] = Scale(m).scale;
+        if (a.row_q && (int)threadIdx.x < n) a.row_scale[(int64_t)ct * a.R + first + threadIdx.x] = s_row_scale[threadIdx.x];
+      }
+      __syncthreads();
+      // column by column: eight rows' quotients by one scale
+      uint32_t out[8][2] = {};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Scale s(s_top[0][c + i]);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = v[j][i];
+        const uint2 q = quantised8(x, s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j][i >> 2] |= ((j < 4 ? q.x : q.y) >> (8 * (j & 3)) & 0xff) << (8 * (i & 3));
+      }
+      if (col < a.ldq) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = make_uint2(out[j][0], out[j][1]);
+      }
+    }
+    __syncthreads();  // the next tile's maxima
+  }
+}
+
+// --------------------------------------------------------------------------------------- host side
+constexpr int kMaxK = 65536, kMaxN = 131072;
+constexpr int kWaitUs = 2000000, kMaxWaitUs = 10000000;
+
+int check_config(const colibri_moe_fp8_config_t* c) {
+  if (!c || c->in_features <= 0 || c->out_features <= 0 || c->num_experts <= 0 || !ops_dtype(c->dtype) ||
+      !ops_dtype(c->out_dtype) || (c->trusted_pointers & ~1) || c->wait_limit_us < 0 || c->wait_limit_us > kMaxWaitUs)
+    return COLIBRI_ERR_INVALID_ARG;
+  if (c->in_features % 16 || c->in_features > kMaxK || c->out_features > kMaxN || c->num_experts > kFp8MaxExperts)
+    return COLIBRI_ERR_UNSUPPORTED;
+  return COLIBRI_OK;
+}
+// The clock is read once in 64 tries of about 8 us, at every one under a millisecond's limit.
+Fp8Limit limit_of(const colibri_moe_fp8_config_t* c) {
+  const int us = c->wait_limit_us ? c->wait_limit_us : kWaitUs;
+  return {us * 1000ull, us < 1000 ? 0u : 63u};
+}
+
+int up(int n, int to) { return (n + to - 1) / to * to; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+int blocks_of(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// The status word's address on the current device, looked up once.
+int* status_word(int device) {
+  static std::mutex mu;
+  static int* at[kOpsMaxDevices] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (!at[device] && cudaGetSymbolAddress(reinterpret_cast<void**>(&at[device]), g_status) != cudaSuccess) {
+    cudaGetLastError();
+    at[device] = nullptr;
+  }
+  return at[device];
+}
+
+template <typename F>
+cudaError_t with_type(int32_t t, F f) {
+  return t == COLIBRI_DTYPE_F32 ? f(float()) : f(__nv_bfloat16());
+}
+bool vectors(const void* x, int64_t ldx, int cols) { return ops_aligned16(x) && ldx % 8 == 0 && cols % 8 == 0; }
+
+cudaError_t quantise_rows(int dtype, const RowQuant& a, cudaStream_t s) {
+  const dim3 grid((unsigned)(((int64_t)a.n + kRowsAt - 1) / kRowsAt), (a.ldq + kColsAt - 1) / kColsAt), block(kRowThreads);
+  return with_type(dtype, [&](auto t) {
+    return vectors(a.x, a.ldx, a.cols) ? pdl_launch(quantise_rows_kernel<decltype(t), true>, grid, block, 0, s, a)
+                                       : pdl_launch(quantise_rows_kernel<decltype(t), false>, grid, block, 0, s, a);
+  });
+}
+template <int KIND>
+cudaError_t quantise_tiles(int dtype, const TileQuant& a, unsigned tiles, int sms, cudaStream_t s) {
+  // column tiles of the same rows to one block of threads, as many blocks as fill the card
+  const int across = (a.ldq + kFp8Block - 1) / kFp8Block;
+  const unsigned share = (unsigned)std::min<int64_t>(across, std::max<int64_t>(1, ((int64_t)sms * 12 + tiles - 1) / tiles));
+  const dim3 grid(tiles, share), block(kTileThreads);
+  return with_type(dtype, [&](auto t) {
+    return vectors(a.x, a.ldx, a.cols) ? pdl_launch(quantise_tiles_kernel<decltype(t), true, KIND>, grid, block, 0, s, a)
+                                       : pdl_launch(quantise_tiles_kernel<decltype(t), false, KIND>, grid, block, 0, s, a);
+  });
+}
+
+// ---- tensor maps: bytes in boxes of 128 columns under the 128-byte swizzle
+bool map_of(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool map_rows(CUtensorMap* m, const void* q, int64_t rows, int ldq, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)ldq, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ldq};
+  return map_of(m, q, 2, dims, strides, box_rows);
+}
+bool map_weights(CUtensorMap* m, const void* w, const colibri_moe_fp8_config_t* c, int box_rows) {
+  const cuuint64_t K = c->in_features, N = c->out_features;
+  const cuuint64_t dims[3] = {K, N, (cuuint64_t)c->num_experts}, strides[2] = {K, N * K};
+  return map_of(m, w, 3, dims, strides, box_rows);
+}
+
+// Tiles of 256 x 256 on CTA pairs where experts have more rows than a tile of 128.
+bool pair_rows(int R, int E) { return R / std::min(E, R) > 128; }
+
+struct Workspace {
+  size_t q, scale, ticket, partial;          // rows' values and scales
+  size_t dq, dscale, xq, xscale;             // by columns, for the weights' gradient
+  size_t bytes;
+  int items, blocks;                         // of split tiles; blocks of 128 rows of one expert, at most
+};
+Workspace workspace_of(const colibri_moe_fp8_config_t* c, int R, int sms, bool backward) {
+  Workspace w = {};
+  const int cols = backward ? up(c->out_features, 16) : c->in_features;
+  w.items = 2 * sms;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t was = at;
+    at += round256(bytes);
+    return was;
+  };
+  w.q = take((size_t)R * cols);
+  w.scale = take((size_t)R * blocks_of(cols) * sizeof(float));
+  w.ticket = take(2 * w.items * sizeof(uint32_t));
+  w.partial = take((size_t)w.items * 128 * 128 * sizeof(float));
+  if (backward) {
+    w.blocks = (int)((R + 127 * (int64_t)std::min(c->num_experts, R)) / 128);
+    w.dq = take((size_t)w.blocks * 128 * cols);
+    w.dscale = take((size_t)w.blocks * up(c->out_features, 256) * sizeof(float));
+    w.xq = take((size_t)w.blocks * 128 * c->in_features);
+    w.xscale = take((size_t)w.blocks * up(c->in_features, 256) * sizeof(float));
+  }
+  w.bytes = at;
+  return w;
+}
+
+int check_pointers(const colibri_moe_fp8_config_t* c, std::initializer_list<const void*> ps, int device) {
+  for (const void* p : ps)
+    if (p && !c->trusted_pointers && !ops_on_device(p, device)) return COLIBRI_ERR_INVALID_ARG;
+  return COLIBRI_OK;
+}
+int workspace_bytes_of(const colibri_moe_fp8_config_t* c, int32_t n_tokens, int32_t R, size_t* bytes, bool backward) {
+  const int rc = check_config(c);
+  if (rc) return rc;
+  if (!bytes || n_tokens < 0 || R < 0) return COLIBRI_ERR_INVALID_ARG;
+  if (R > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  *bytes = R ? workspace_of(c, R, sms, backward).bytes : 0;
+  return COLIBRI_OK;
+}
+
+}  // namespace
+}  // namespace colibri
+
+using namespace colibri;
+
+extern "C" int colibri_moe_fp8_quantize(const colibri_moe_fp8_config_t* cfg, const void* x, int64_t ldx, int32_t n,
+                                        int32_t square, uint8_t* q, float* scale, void* stream) {
+  const int rc = check_config(cfg);
+  if (rc) return rc;
+  if (n < 0 || (square & ~1) || (square && n % cfg->num_experts)) return COLIBRI_ERR_INVALID_ARG;
+  if (n > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
+  if (n == 0) return COLIBRI_OK;
+  if (!x || !q || !scale || ldx < cfg->in_features || !ops_aligned16(q)) return COLIBRI_ERR_INVALID_ARG;
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  if (const int bad = check_pointers(cfg, {x, q, scale}, device)) return bad;
+  const int K = cfg->in_features;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (square) {
+    TileQuant a = {};
+    a.x = x, a.ldx = ldx, a.n_tokens = n, a.matrix_rows = n / cfg->num_experts, a.cols = a.ldq = K, a.q = q;
+    a.scale = scale, a.lds = blocks_of(K);
+    e = quantise_tiles<kSquare>(cfg->dtype, a, (unsigned)cfg->num_experts * blocks_of(a.matrix_rows), sms, s);
+  } else {
+    e = quantise_rows(cfg->dtype, {x, ldx, n, nullptr, n, K, q, K, scale, blocks_of(K), 1, nullptr, 0}, s);
+  }
+  return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+extern "C" int colibri_moe_fp8_experts_workspace(const colibri_moe_fp8_config_t* cfg, int32_t n_tokens, int32_t R,
+                                                 size_t* bytes) {
+  return workspace_bytes_of(cfg, n_tokens, R, bytes, false);
+}
+
+extern "C" int colibri_moe_fp8_experts(const colibri_moe_fp8_config_t* cfg, const void* x, int64_t ldx,
+                                       int32_t n_tokens, const int32_t* rows, int32_t R, const int32_t* offsets,
+                                       const uint8_t* w, const float* w_scale, const uint8_t* w3,
+                                       const float* w3_scale, void* y, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  const int rc = check_config(cfg);
+  if (rc) return rc;
+  if (n_tokens < 0 || R < 0 || (!rows && R > n_tokens)) return COLIBRI_ERR_INVALID_ARG;
+  if (R > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
+  if (R == 0) return COLIBRI_OK;
+  const int K = cfg->in_features, N = cfg->out_features, E = cfg->num_experts;
+  if ((n_tokens > 0 && (!x || ldx < K)) || !offsets || !w || !w_scale || !y || (w3 != nullptr) != (w3_scale != nullptr))
+    return COLIBRI_ERR_INVALID_ARG;
+  if (!ops_aligned16(w) || !ops_aligned16(w3)) return COLIBRI_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return COLIBRI_ERR_INVALID_ARG;
+  if (workspace_bytes < workspace_of(cfg, R, 0, false).bytes) return COLIBRI_ERR_INVALID_ARG;  // what any device needs
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  const Workspace lay = workspace_of(cfg, R, sms, false);
+  if (workspace_bytes < lay.bytes) return COLIBRI_ERR_INVALID_ARG;
+  if (const int bad = check_pointers(cfg, {n_tokens ? x : nullptr, rows, offsets, w, w_scale, w3, w3_scale, y, workspace},
+                                     device))
+    return bad;
+  int* word = status_word(device);
+  if (!word) return COLIBRI_ERR_CUDA;
+  const bool pair = pair_rows(R, E), gated = w3 != nullptr;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  Fp8Maps maps;
+  bool ok = true;
+  for (int i = 0; i < kFp8TokMaps; ++i) ok = ok && map_rows(&maps.a[i], ws + lay.q, R, K, 32 << i);
+  const int box = gated ? (pair ? 64 : 32) : 128;
+  ok = ok && map_weights(&maps.b, w, cfg, box) && map_weights(&maps.b3, gated ? w3 : w, cfg, box);
+  if (!ok) return COLIBRI_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* scale = reinterpret_cast<float*>(ws + lay.scale);
+  uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + lay.ticket);
+  if (quantise_rows(cfg->dtype, {x, ldx, n_tokens, rows, R, K, ws + lay.q, K, scale, 1, R, ticket, lay.items}, s) !=
+      cudaSuccess)
+    return COLIBRI_ERR_CUDA;
+  const Fp8Args a = {offsets, scale, R, w_scale, w3_scale, nullptr, 0, y, reinterpret_cast<float*>(ws + lay.partial),
+                     ticket, lay.items, R, E, N, K, limit_of(cfg), word};
+  const cudaError_t e =
+      launch_fp8_forward(maps, a, pair, gated, cfg->out_dtype == COLIBRI_DTYPE_BF16, device, sms, s);
+  return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+extern "C" int colibri_moe_fp8_experts_backward_workspace(const colibri_moe_fp8_config_t* cfg, int32_t n_tokens,
+                                                          int32_t R, size_t* bytes) {
+  return workspace_bytes_of(cfg, n_tokens, R, bytes, true);
+}
+
+extern "C" int colibri_moe_fp8_experts_backward(const colibri_moe_fp8_config_t* cfg, const void* d_y, int64_t ld_dy,
+                                                const void* x, int64_t ldx, int32_t n_tokens, const int32_t* rows,
+                                                int32_t R, const int32_t* offsets, const uint8_t* w,
+                                                const float* w_scale, void* d_rows, void* d_w, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  const int rc = check_config(cfg);
+  if (rc) return rc;
+  if (n_tokens < 0 || R < 0 || (d_w && !rows && R > n_tokens)) return COLIBRI_ERR_INVALID_ARG;
+  if (R > kOpsMaxRows) return COLIBRI_ERR_UNSUPPORTED;
+  const int K = cfg->in_features, N = cfg->out_features, E = cfg->num_experts;
+  if (!d_rows && !d_w) return COLIBRI_ERR_INVALID_ARG;
+  if ((d_rows != nullptr) != (w != nullptr) || (w != nullptr) != (w_scale != nullptr) || !ops_aligned16(w))
+    return COLIBRI_ERR_INVALID_ARG;
+  if (R > 0 && (!d_y || ld_dy < N || !offsets)) return COLIBRI_ERR_INVALID_ARG;
+  if (d_w && R > 0 && n_tokens > 0 && (!x || ldx < K)) return COLIBRI_ERR_INVALID_ARG;
+  if (R > 0) {
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return COLIBRI_ERR_INVALID_ARG;
+    if (workspace_bytes < workspace_of(cfg, R, 0, true).bytes) return COLIBRI_ERR_INVALID_ARG;
+  }
+  int device = 0, sms = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (const int bad = check_pointers(cfg, {d_w}, device)) return bad;
+  if (R == 0) {
+    if (!d_w) return COLIBRI_OK;
+    const size_t bytes = (size_t)E * N * K * ops_elem(cfg->out_dtype);
+    return cudaMemsetAsync(d_w, 0, bytes, s) == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+  }
+  const Workspace lay = workspace_of(cfg, R, sms, true);
+  if (workspace_bytes < lay.bytes) return COLIBRI_ERR_INVALID_ARG;
+  if (const int bad = check_pointers(cfg, {d_y, d_w && n_tokens ? x : nullptr, d_w ? rows : nullptr, offsets, w, w_scale,
+                                           d_rows, workspace},
+                                     device))
+    return bad;
+  int* word = status_word(device);
+  if (!word) return COLIBRI_ERR_CUDA;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const int ldn = up(N, 16);
+  float* scale = reinterpret_cast<float*>(ws + lay.scale);
+  float* partial = reinterpret_cast<float*>(ws + lay.partial);
+  uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + lay.ticket);  // the products' tickets, one after the other
+  float *dscale = reinterpret_cast<float*>(ws + lay.dscale), *xscale = reinterpret_cast<float*>(ws + lay.xscale);
+  Fp8Maps maps, wmaps;
+  if (d_rows) {
+    bool ok = true;
+    for (int i = 0; i < kFp8TokMaps; ++i) ok = ok && map_rows(&maps.a[i], ws + lay.q, R, ldn, 32 << i);
+    if (!ok || !map_weights(&maps.b, w, cfg, 128)) return COLIBRI_ERR_CUDA;
+    maps.b3 = maps.b;
+  }
+  if (d_w) {
+    bool ok = map_rows(&wmaps.a[0], ws + lay.dq, (int64_t)lay.blocks * 128, ldn, 128);
+    ok = ok && map_rows(&wmaps.b, ws + lay.xq, (int64_t)lay.blocks * 128, K, 128);
+    if (!ok) return COLIBRI_ERR_CUDA;
+    wmaps.a[1] = wmaps.a[2] = wmaps.a[0];
+    wmaps.b3 = wmaps.b;
+  }
+  cudaError_t e = cudaSuccess;
+  if (d_w) {
+    TileQuant t = {};
+    t.x = d_y, t.ldx = ld_dy, t.n_tokens = R, t.offsets = offsets, t.E = E, t.R = R, t.cols = N, t.ldq = ldn;
+    t.q = ws + lay.dq, t.scale = dscale, t.lds = up(N, 256);
+    t.row_q = d_rows ? ws + lay.q : nullptr, t.row_scale = scale;
+    t.ticket = ticket, t.n_ticket = 2 * lay.items;
+    e = quantise_tiles<kColumns>(cfg->dtype, t, lay.blocks, sms, s);
+    if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
+    t.x = x, t.ldx = ldx, t.n_tokens = n_tokens, t.rows = rows, t.cols = t.ldq = K;
+    t.q = ws + lay.xq, t.scale = xscale, t.lds = up(K, 256), t.row_q = nullptr, t.n_ticket = 0;
+    e = quantise_tiles<kColumns>(cfg->dtype, t, lay.blocks, sms, s);
+  } else {
+    e = quantise_rows(cfg->dtype, {d_y, ld_dy, R, nullptr, R, N, ws + lay.q, ldn, scale, 1, R, ticket, 2 * lay.items}, s);
+  }
+  if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
+  if (d_rows) {
+    const Fp8Args a = {offsets, scale, R, w_scale, nullptr, nullptr, 0, d_rows, partial, ticket, lay.items, R, E, N, K,
+                       limit_of(cfg), word};
+    e = launch_fp8_rows(maps, a, pair_rows(R, E), cfg->dtype == COLIBRI_DTYPE_BF16, device, sms, s);
+    if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
+  }
+  if (d_w) {
+    const Fp8Args a = {offsets, dscale, up(N, 256), nullptr, nullptr, xscale, up(K, 256), d_w, partial,
+                       ticket + lay.items, lay.items, R, E, N, K, limit_of(cfg), word};
+    const bool pair = (int64_t)E * ((N + 255) / 256) * ((K + 255) / 256) >= sms / 2;
+    e = launch_fp8_weights(wmaps, a, pair, cfg->out_dtype == COLIBRI_DTYPE_BF16, device, sms, s);
+  }
+  return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
+}
+
+extern "C" int colibri_moe_fp8_status(int32_t* status) {
+  if (!status) return COLIBRI_ERR_INVALID_ARG;
+  int device = 0, sms = 0, v = 0;
+  if (!ops_device(&device, &sms)) return COLIBRI_ERR_CUDA;
+  static std::mutex mu;  // g_taken holds one caller's answer at a time
+  std::lock_guard<std::mutex> lock(mu);
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) {
+    take_status_kernel<<<1, 1>>>();
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_taken, sizeof(int));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return COLIBRI_ERR_CUDA;
+  }
+  *status = v;
+  return COLIBRI_OK;
+}

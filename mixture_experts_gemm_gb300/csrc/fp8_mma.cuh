@@ -1,0 +1,627 @@
+// Products of rows and weights in e4m3 with a scale for every block of 128, on the tensor cores (tcgen05).
+//
+//   D[m, n] = sum over blocks b of 128 of  sa[b, m] * sb[b, n] * sum_{k in b} A[m, k] B[n, k]
+//
+// The tensor cores sum one block of 128 in fp32 (products of two e4m3 are exact there); since its scales differ
+// from the next block's, every block's sum leaves TMEM, is multiplied by its scales and added to fp32
+// accumulators in registers.  That costs a fused multiply-add and a TMEM read for every 128 multiply-adds of the
+// tensor cores, on other units and by other warps, so it runs beside them: TMEM holds several blocks' sums.
+//
+// One persistent CTA per SM on tiles of 128 x 128, or CTA pairs (cta_group::2) on tiles of 256 x 256 whose halves
+// of B each CTA loads once for both.  384 threads:
+//   warp 0      TMA producer of B, warp 2 of A (a ring of S stages, 128 rows x 128 bytes of each)
+//   warp 1      issues the MMAs, four to a block, into the next of NB sums in TMEM
+//   warps 4-11  take the sums: a thread a row (TMEM lane) of half of the columns; then the epilogue
+// Operands whose contraction runs down the rows of memory (the weights in the rows' gradient, both operands in the
+// weights' gradient) are MN-major: the same 128 x 128 boxes under another descriptor, so nothing is transposed in
+// memory and the weights are kept once.
+// Items are (tile, part of the contraction) in a fixed order; a product of few tiles is split, the parts' sums kept
+// in `partial` and added in order by whichever CTA finishes the tile: the same bits every time.
+// Every wait is bounded by the call's limit: when one gives up, all roles stop, copies and MMAs in flight are
+// waited for (at most kDrain each), TMEM is freed and the device's status word gets a bit.
+#pragma once
+
+#include <mutex>
+
+#include "fp8_internal.cuh"
+#include "tcgen05_ptx.cuh"
+
+namespace colibri {
+namespace fp8 {
+
+using namespace ptx;
+
+constexpr int kThreads = 384;
+constexpr int kTakers = 8, kTaker0 = 4;       // warps that take the sums
+constexpr int kTileBytes = 128 * 128;         // an operand's 128 rows (or columns) of a block
+constexpr int kBoxBytes = 32 * 128;           // the smallest box of rows
+constexpr int kStageCols = 16, kStageLd = 20; // epilogue staging: 32 rows of 16 floats a warp
+constexpr Fp8Limit kDrain = {50000000, 63};   // 50 ms, far above the time of a copy or of a stage's MMAs
+
+template <bool PAIR>
+struct Form {
+  static constexpr int NT = PAIR ? 256 : 128;  // tile columns
+  static constexpr int MT = PAIR ? 256 : 128;  // tile rows, 128 a CTA
+  static constexpr int C = NT / 2;             // columns of a taker thread
+  static constexpr int NB = 512 / NT;          // sums in TMEM
+  static constexpr int S = 6;
+  static constexpr int kBars = 2 * S + 2 * NB + 3;
+  static constexpr int kSmem = 1024 + S * 2 * kTileBytes + kTakers * 32 * kStageLd * 4 + kBars * 8 + 32 +
+                               4 * (3 * kFp8MaxExperts + 1);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
+// Waits for the phase of `bar` with parity `parity`, at most limit.ns or until *abort.  CLUSTER: arrivals come from
+// the pair's other CTA, too.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, Fp8Limit limit) {
+  uint64_t t0 = 0;
+  for (uint32_t tries = 1;; ++tries) {
+    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if ((tries & limit.clock_mask) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort || now - t0 > limit.ns) return false;
+    }
+  }
+}
+
+// Box of a matrix [rows, columns] (y, x) or of an expert's (z, y, x); PAIR: completing on the leader's barrier.
+template <bool PAIR>
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+  if constexpr (PAIR)
+    tma_load_2d_pair(dst, m, bar, x, y);
+  else
+    tma_load_2d(dst, m, bar, x, y);
+}
+template <bool PAIR>
+__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// MN-major operand of 128 rows of the contraction x 128 columns, as a box with the 128-byte swizzle leaves it: atoms of
+// 8 rows x 128 bytes, the next eight rows 1024 bytes on (a second 128 columns would be kTileBytes on).
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kTileBytes >> 4) << 16;  // next columns
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;        // next 8 rows
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+// e4m3 x e4m3 -> fp32, m x n.
+constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(more)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(more)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    umma_commit_pair(bar, 0x3);
+  else
+    umma_commit(bar);
+}
+
+// Two fp32 in one register pair.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t two(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void one_each(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t x, uint64_t f) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(f));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t f) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(f));
+  return r;
+}
+
+// silu(v) u as it is stored: fast exp and quotient for bf16; for fp32 expf of what cannot overflow and the
+// approximate reciprocal, good to an ulp, of a sum between 1 and 2.
+template <typename O>
+__device__ __forceinline__ float gated_value(float v, float u) {
+  if constexpr (sizeof(O) == 2) return silu_fast(v) * u;
+  const float t = expf(-fabsf(v));
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + t));
+  return v * (v < 0.f ? t * s : s) * u;
+}
+
+struct Item {
+  int64_t i;           // item number
+  int tile, part;
+  int e, row, n;       // expert; first row of this CTA's 128 and how many of them there are
+  int col;             // first column of the tile (of y)
+  int kb0, kb1;        // blocks of the contraction
+  int first;           // kFp8Weights: the expert's first block of rows
+};
+
+template <int MODE, bool PAIR, bool GATED, typename O>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_mma_kernel(const __grid_constant__ Fp8Maps tm, const __grid_constant__ Fp8Args a) {
+  using F = Form<PAIR>;
+  constexpr int S = F::S, NB = F::NB, NT = F::NT, MT = F::MT, C = F::C;
+  constexpr bool kWeights = MODE == kFp8Weights, kFromWeights = !kWeights;  // whether B is the weights
+  static_assert(!GATED || MODE == kFp8Forward);
+  constexpr int kCh = GATED ? NT / 2 : NT;  // columns of y in a tile
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_a = smem;
+  uint8_t* s_b = s_a + S * kTileBytes;
+  float* s_stage = reinterpret_cast<float*>(s_b + S * kTileBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_stage + kTakers * 32 * kStageLd);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + F::kBars);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* s_last = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int* s_row0 = reinterpret_cast<int*>(tmem_slot + 8);  // first row of each expert
+  int* s_rows = s_row0 + kFp8MaxExperts;                // its rows
+  int* s_tiles = s_rows + kFp8MaxExperts;               // row tiles (kFp8Weights: blocks of rows) before it [E + 1]
+
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S;
+  const uint32_t tfull0 = empty0 + 8 * S, tempty0 = tfull0 + 8 * NB;
+  const uint32_t drain = tempty0 + 8 * NB, joined = drain + 8, decided = joined + 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
+  const bool leader = rank == 0;
+
+  pdl_trigger();
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full0 + 8 * i, 2);  // A and B landed (PAIR: the leader's, both CTAs')
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(tfull0 + 8 * i, 1);
+      mbar_init(tempty0 + 8 * i, PAIR ? 2 * kTakers : kTakers);
+    }
+    mbar_init(drain, 1);
+    mbar_init(joined, kTakers);
+    mbar_init(decided, 1);
+    *s_abort = 0;
+    fence_mbar_init();
+    for (int i = 0; i < kFp8TokMaps; ++i) prefetch_tmap(&tm.a[i]);
+    prefetch_tmap(&tm.b);
+    if constexpr (GATED) prefetch_tmap(&tm.b3);
+  }
+  __syncwarp();
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
+  }
+  // The quantiser lets this kernel start once everything before it is done: offsets and weights may be read at once;
+  // the warps that read its rows and scales wait for it.
+  if (warp == 3)
+    fp8_segments(a.offsets, a.E, a.R, lane, s_row0, s_rows, s_tiles,
+                 [](int n) { return kWeights ? (n + kFp8Block - 1) / kFp8Block : (n + MT - 1) / MT; });
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int out_cols = MODE == kFp8Forward ? a.N : a.K;  // of y
+  const int col_tiles = (out_cols + kCh - 1) / kCh;
+  const int m_tiles = (a.N + MT - 1) / MT;               // kFp8Weights
+  const int kblocks = ((MODE == kFp8Forward ? a.K : a.N) + kFp8Block - 1) / kFp8Block;  // not kFp8Weights
+  const int64_t tiles = kWeights ? (int64_t)a.E * m_tiles * col_tiles : (int64_t)s_tiles[a.E] * col_tiles;
+  const int units = PAIR ? gridDim.x >> 1 : gridDim.x, unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  // Parts of the contraction: the number that leaves the SMs least idle in the last wave, a little against more parts.
+  int parts = 1;
+  if (!PAIR && tiles < 2 * (int64_t)units) {
+    const int most = kWeights ? max(1, (a.R + kFp8Block - 1) / kFp8Block) : kblocks;
+    float least = 1e30f;
+    for (int p = 1; p <= kFp8MaxSplits && p <= most && tiles * p <= a.max_items; ++p) {
+      const int waves = (int)((tiles * p + units - 1) / units);
+      const float cost = (float)waves / p + (p > 1 ? 0.04f : 0.f) + 0.01f * p;
+      if (cost < least) least = cost, parts = p;
+    }
+  }
+  const int64_t items = tiles * parts;
+
+  // item -> its tile: row tiles of an expert fastest, so that CTAs at work share the other operand in L2
+  auto item_at = [&](int64_t i) {
+    Item it;
+    it.i = i;
+    it.tile = (int)(i / parts);
+    it.part = (int)(i - (int64_t)it.tile * parts);
+    int blocks = kblocks;
+    if constexpr (kWeights) {
+      const int each = m_tiles * col_tiles;
+      it.e = it.tile / each;
+      const int local = it.tile - it.e * each;
+      it.col = local / m_tiles * kCh;
+      it.row = local % m_tiles * MT + rank * 128;  // of d_w's N rows
+      it.n = min(max(a.N - it.row, 0), 128);
+      it.first = s_tiles[it.e];
+      blocks = s_tiles[it.e + 1] - it.first;
+    } else {
+      int lo = 0, hi = a.E;  // the last expert whose tiles begin at or before it (those without rows begin with it)
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if ((int64_t)s_tiles[mid] * col_tiles <= it.tile)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      it.e = lo;
+      const int tt = s_tiles[lo + 1] - s_tiles[lo], local = it.tile - s_tiles[lo] * col_tiles;
+      it.col = local / tt * kCh;
+      const int t = local % tt, n = s_rows[lo];
+      const int each = PAIR ? MT : ((n + tt - 1) / tt + 31) / 32 * 32;  // even tiles, whole boxes
+      const int at = t * each + rank * 128;
+      it.row = s_row0[lo] + at;
+      it.n = max(min(PAIR ? 128 : each, n - at), 0);
+      it.first = 0;
+    }
+    it.kb0 = (int)((int64_t)blocks * it.part / parts);
+    it.kb1 = (int)((int64_t)blocks * (it.part + 1) / parts);
+    return it;
+  };
+
+  bool ok = true;
+  if (warp == 0 || warp == 2) {
+    // -------------------------------------------------------------- producers: B (warp 0) and A (warp 2)
+    const bool b_side = warp == 0;
+    if (!b_side || kWeights) pdl_wait();
+    const bool elected = elect_one();
+    const uint32_t base = smem_u32(b_side ? s_b : s_a);
+    uint32_t it = 0, st = 0, ph = 0;
+    for (int64_t i = unit; ok && i < items; i += units) {
+      const Item t = item_at(i);
+      const int boxes = PAIR || kWeights ? 4 : (t.n + 31) / 32;
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        if (!__all_sync(~0u, wait_for(empty0 + 8 * st, ph ^ 1, s_abort, a.limit))) {
+          ok = false;
+          break;
+        }
+        uint32_t full = full0 + 8 * st, dst = base + st * kTileBytes;
+        const int k = kb * kFp8Block;
+        if (elected) {
+          const uint32_t bytes = (PAIR ? 2 : 1) * (b_side ? kTileBytes : boxes * kBoxBytes);
+          if (!PAIR || leader) mbar_arrive_expect_tx(full, bytes);
+          if constexpr (PAIR) full = mapa_shared(full, 0);
+          if (b_side) {
+            if constexpr (kWeights) {
+              load2<PAIR>(dst, &tm.b, full, t.col + rank * 128, (t.first + kb) * kFp8Block);
+            } else if constexpr (MODE == kFp8Rows) {
+              load3<PAIR>(dst, &tm.b, full, t.col + rank * 128, k, t.e);
+            } else if constexpr (GATED) {
+              // every taker thread's columns: C / 2 channels of w, then the same of w3
+              constexpr int kRuns = PAIR ? 1 : 2, kBytes = C / 2 * 128;
+#pragma unroll
+              for (int r = 0; r < kRuns; ++r) {
+                const int ch = t.col + (PAIR ? rank : r) * (C / 2);
+                load3<PAIR>(dst + 2 * r * kBytes, &tm.b, full, k, ch, t.e);
+                load3<PAIR>(dst + (2 * r + 1) * kBytes, &tm.b3, full, k, ch, t.e);
+              }
+            } else {
+              load3<PAIR>(dst, &tm.b, full, k, t.col + rank * 128, t.e);
+            }
+          } else if constexpr (kWeights) {
+            load2<PAIR>(dst, &tm.a[2], full, t.row, (t.first + kb) * kFp8Block);
+          } else {
+            int row = t.row;
+#pragma unroll
+            for (int b = kFp8TokMaps - 1; b >= 0; --b)  // at most one copy of each box height
+              if (boxes >> b & 1) {
+                load2<PAIR>(dst, &tm.a[b], full, k, row);
+                dst += kBoxBytes << b, row += 32 << b;
+              }
+          }
+        }
+        __syncwarp();
+        if (++st == S) st = 0, ph ^= 1;
+      }
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+    // Every copy has landed before the CTA can leave (PAIR: on the leader's barriers; the CTAs leave together).  After a
+    // wait that gave up a stage may lack its other operand: the wait for it ends by kDrain.
+    volatile int never = 0;
+    if (leader)
+      for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_for(full0 + 8 * (j % S), j / S & 1, &never, kDrain);
+    __syncwarp();
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMA issuer
+    if (leader) {
+      constexpr uint32_t id = idesc(MT, NT, kWeights, MODE != kFp8Forward);
+      constexpr int kStepA = kWeights ? 4096 >> 4 : 2, kStepB = MODE != kFp8Forward ? 4096 >> 4 : 2;  // 32 of the block
+      const bool elected = elect_one();
+      const uint64_t da0 = kWeights ? mn_desc(smem_u32(s_a)) : sw128_desc(smem_u32(s_a));
+      const uint64_t db0 = MODE != kFp8Forward ? mn_desc(smem_u32(s_b)) : sw128_desc(smem_u32(s_b));
+      uint32_t st = 0, ph = 0, buf = 0, bph = 0;
+      for (int64_t i = unit; ok && i < items; i += units) {
+        const Item t = item_at(i);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          bool got = wait_for<PAIR>(tempty0 + 8 * buf, bph ^ 1, s_abort, a.limit);
+          got = got && wait_for(full0 + 8 * st, ph, s_abort, a.limit);
+          if (!__all_sync(~0u, got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = da0 + st * (kTileBytes >> 4), db = db0 + st * (kTileBytes >> 4);
+          if (elected) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma<PAIR>(tmem_base + buf * NT, da + k * kStepA, db + k * kStepB, id, k != 0);
+            commit<PAIR>(empty0 + 8 * st);
+            commit<PAIR>(tfull0 + 8 * buf);
+          }
+          __syncwarp();
+          if (++st == S) st = 0, ph ^= 1;
+          if (++buf == NB) buf = 0, bph ^= 1;
+        }
+      }
+      if (!ok && lane == 0) *s_abort = 1;
+      if (elected) {
+        if constexpr (PAIR)
+          umma_commit_pair(drain, 0x1);
+        else
+          umma_commit(drain);  // completes when every MMA of this thread has
+        volatile int never = 0;
+        wait_for(drain, 0, &never, kDrain);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kTaker0) {
+    // -------------------------------------------------------------- takers
+    pdl_wait();
+    const int q = warp & 3, half = (warp - kTaker0) >> 2;  // TMEM lanes 32 q .. of columns half * C ..
+    const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+    const int kb_w = (a.K + kFp8Block - 1) / kFp8Block, nb_w = (a.N + kFp8Block - 1) / kFp8Block;  // the weights' blocks
+    float* stage = s_stage + (warp - kTaker0) * (32 * kStageLd);
+    uint32_t buf = 0, bph = 0, joins = 0;
+    for (int64_t i = unit; ok && i < items; i += units) {
+      const Item t = item_at(i);
+      const bool mine = q * 32 < t.n;  // whether any of this warp's rows exist
+      uint64_t acc[C / 2];
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) acc[c] = 0;
+      // scales: of the row, a stride apart from block to block; of the weights' block
+      const int m = min(q * 32 + lane, max(t.n - 1, 0));
+      const float* sa = a.a_scale + (kWeights ? (int64_t)t.first * a.lda : 0) + t.row + m;
+      const float *sw = nullptr, *sw3 = nullptr, *sx = nullptr;
+      int64_t w_step = 0;
+      if constexpr (kFromWeights) {
+        const int blk = (t.col + (GATED ? 0 : half * C)) / kFp8Block;  // a tile past the last column has no block
+        const int64_t at = MODE == kFp8Forward ? ((int64_t)t.e * nb_w + min(blk, nb_w - 1)) * kb_w
+                                               : (int64_t)t.e * nb_w * kb_w + min(blk, kb_w - 1);
+        sw = a.w_scale + at;
+        if constexpr (GATED) sw3 = a.w3_scale + at;
+        w_step = MODE == kFp8Forward ? 1 : kb_w;
+      } else {
+        sx = a.x_scale + (int64_t)t.first * a.ldx + t.col + half * C;
+      }
+      float fa = 0.f, fw = 0.f, fw3 = 0.f;  // the next block's
+      auto fetch = [&](int kb) {
+        fa = sa[kb * a.lda];
+        if constexpr (kFromWeights) fw = __ldg(sw + kb * w_step);
+        if constexpr (GATED) fw3 = __ldg(sw3 + kb * w_step);
+      };
+      if (mine && t.kb0 < t.kb1) fetch(t.kb0);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        const float f0 = kFromWeights ? fa * fw : fa, f1 = GATED ? fa * fw3 : 0.f;
+        if (mine && kb + 1 < t.kb1) fetch(kb + 1);
+        if (!__all_sync(~0u, wait_for(tfull0 + 8 * buf, bph, s_abort, a.limit))) {
+          ok = false;
+          break;
+        }
+        if (mine) {
+          tc_fence_after();
+          const uint32_t from = tmem_base + lanes + buf * NT + half * C;
+#pragma unroll
+          for (int c0 = 0; c0 < C; c0 += 16) {
+            uint32_t r[16];
+            tmem_ld16_sync(from + c0, r);
+            const float f = GATED && c0 >= C / 2 ? f1 : f0;
+            const uint64_t ff = two(f, f);
+            if constexpr (kWeights) {
+              const float4* x4 = reinterpret_cast<const float4*>(sx + (int64_t)kb * a.ldx + c0);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float4 x = __ldg(x4 + c);
+                fma2(acc[c0 / 2 + 2 * c], mul2(two(r[4 * c], r[4 * c + 1]), two(x.x, x.y)), ff);
+                fma2(acc[c0 / 2 + 2 * c + 1], mul2(two(r[4 * c + 2], r[4 * c + 3]), two(x.z, x.w)), ff);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) fma2(acc[c0 / 2 + c], two(r[2 * c], r[2 * c + 1]), ff);
+            }
+          }
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (!PAIR || leader)
+            mbar_arrive(tempty0 + 8 * buf);
+          else
+            mbar_arrive_peer(mapa_shared(tempty0 + 8 * buf, 0));
+        }
+        if (++buf == NB) buf = 0, bph ^= 1;
+      }
+      if (!ok) {
+        if (lane == 0) *s_abort = 1;
+        break;
+      }
+      float v[C];
+#pragma unroll
+      for (int c = 0; c < C / 2; ++c) one_each(acc[c], v[2 * c], v[2 * c + 1]);
+      if (parts > 1) {
+        const int64_t at = (int64_t)(half * C) * 128 + q * 32 + lane;
+        if (mine) {
+          float* part = a.partial + t.i * (NT * 128) + at;
+#pragma unroll
+          for (int c = 0; c < C; ++c) part[c * 128] = v[c];
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(joined);
+        bool got = true;
+        if (warp == kTaker0 && lane == 0) {
+          got = wait_for(joined, joins & 1, s_abort, a.limit);
+          if (got) {
+            __threadfence();
+            *s_last = atomicAdd(&a.ticket[t.tile], 1u) == (uint32_t)(parts - 1);
+            mbar_arrive(decided);
+          }
+        }
+        __syncwarp();
+        got = got && wait_for(decided, joins & 1, s_abort, a.limit);
+        ++joins;
+        if (!__all_sync(~0u, got)) {
+          if (lane == 0) *s_abort = 1;
+          ok = false;
+          break;
+        }
+        if (!*s_last) continue;
+        __threadfence();
+        if (mine) {
+          const float* all = a.partial + (int64_t)t.tile * parts * (NT * 128) + at;
+#pragma unroll
+          for (int c = 0; c < C; ++c) v[c] = 0.f;
+          for (int p = 0; p < parts; ++p)
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] += __ldcg(all + (int64_t)p * (NT * 128) + c * 128);
+        }
+      }
+      if (!mine) continue;
+      // 16 columns at a time through shared memory, so that stores cover whole sectors of a row
+      constexpr int kOut = GATED ? C / 2 : C, kVec = 16 / sizeof(O), kLanes = kStageCols / kVec;
+      const int rows = min(t.n - q * 32, 32);
+      const int64_t row0 = (kWeights ? (int64_t)t.e * a.N : 0) + t.row + q * 32;
+      O* y = static_cast<O*>(a.y) + row0 * out_cols;
+      const bool wide = out_cols % kVec == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+#pragma unroll
+      for (int c0 = 0; c0 < kOut; c0 += kStageCols) {
+        const int col = t.col + half * kOut + c0;
+        __syncwarp();  // the last columns have been read
+#pragma unroll
+        for (int c = 0; c < kStageCols; c += 4) {
+          float h[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (GATED)
+              h[j] = gated_value<O>(v[c0 + c + j], v[kOut + c0 + c + j]);
+            else
+              h[j] = v[c0 + c + j];
+          }
+          *reinterpret_cast<float4*>(stage + lane * kStageLd + c) = make_float4(h[0], h[1], h[2], h[3]);
+        }
+        __syncwarp();
+        if (wide) {
+          const int c = lane % kLanes * kVec;
+#pragma unroll
+          for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
+            const float* from = stage + r * kStageLd + c;
+            if (r < rows && col + c < out_cols) {
+              O* to = y + (int64_t)r * out_cols + col + c;
+              if constexpr (sizeof(O) == 2) {
+                const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
+                *reinterpret_cast<uint4*>(to) =
+                    make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
+              } else {
+                *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(from);
+              }
+            }
+          }
+        } else {
+          const int c = lane % kStageCols;
+          if (col + c < out_cols)
+            for (int r = lane / kStageCols; r < rows; r += 2)
+              y[(int64_t)r * out_cols + col + c] = from_float<O>(stage[r * kStageLd + c]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // no CTA leaves while its peer may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, 512);
+    else
+      tmem_dealloc(tmem_base, 512);
+  }
+  if (threadIdx.x == 0 && *s_abort) atomicOr(a.status, COLIBRI_FP8_WAIT_EXPIRED);
+}
+
+template <int MODE, bool PAIR, bool GATED, typename O>
+cudaError_t launch(const Fp8Maps& maps, const Fp8Args& a, int device, int sms, cudaStream_t s) {
+  static std::mutex mu;
+  static bool ready[kOpsMaxDevices] = {};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[device]) {
+      const cudaError_t e = cudaFuncSetAttribute(fp8_mma_kernel<MODE, PAIR, GATED, O>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Form<PAIR>::kSmem);
+      if (e != cudaSuccess) return e;
+      ready[device] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(PAIR ? sms & ~1 : sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Form<PAIR>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_mma_kernel<MODE, PAIR, GATED, O>, maps, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace fp8
+}  // namespace colibri

@@ -4,7 +4,8 @@ The counterparts of the context-free calls of ``include/colibri_moe.h``: norms b
 block with its gate and residual scale (``block_norm``), routing to many experts with the dispatch
 order (``route``), experts in 8-bit integers (``int8_experts``) and their combine (``combine``), tokens to
 their experts' rows and back for any choice of experts (``dispatch_order``, ``dispatch``), the gated activation
-(``gated``), with the backward passes of all but the 8-bit integers.  Every call runs on CUDA tensors, asynchronously
+(``gated``), experts in 8-bit floating point (``fp8_experts``), with the backward passes of all but the 8-bit
+integers.  Every call runs on CUDA tensors, asynchronously
 on ``stream`` (default: the current stream), allocates its outputs and workspace from torch, and can be
 captured into a CUDA graph.  Errors raise ``ColibriError`` (checks of the library) or ``ValueError``
 (shapes and types that cannot be passed on).  Results are not attached to autograd: the backward passes
@@ -27,11 +28,12 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import DTYPE_BF16, DTYPE_F32, ColibriError, Int8Config, NormConfig, RouteConfig, _check, lib
+from . import DTYPE_BF16, DTYPE_F32, ColibriError, Fp8Config, Int8Config, NormConfig, RouteConfig, _check, lib
 
 __all__ = ["block_norm", "block_norm_backward", "pre_norm", "route", "route_backward", "Routing", "int8_quantize",
            "int8_experts", "int8_status", "combine", "combine_backward", "dispatch_order", "Order", "dispatch",
-           "dispatch_backward", "gated", "gated_backward", "ColibriError"]
+           "dispatch_backward", "gated", "gated_backward", "fp8_quantize", "fp8_experts", "fp8_experts_backward",
+           "fp8_status", "ColibriError"]
 
 _DTYPE = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 _NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -563,3 +565,145 @@ def gated_backward(d_h, u, v, *, stream=None):
                                                 d_v.data_ptr(), 1, s), "colibri_moe_gated_backward")
         return d_u, d_v
     return _run(call, u, on, stream)
+
+
+# ------------------------------------------------------------------------ 8-bit floating-point experts
+_FP8, _BLOCK = torch.float8_e4m3fn, 128
+
+
+@functools.lru_cache(maxsize=256)
+def _fp8_config(K, N, E, dtype, out_dtype):
+    c = Fp8Config(K, N, E, _dtype(dtype, "x"), _dtype(out_dtype, "out_dtype"), 1)
+    return c, ctypes.addressof(c)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // _BLOCK)
+
+
+def _fp8_weights(w, w_scale, on: int):
+    """(E, N, K, address of w [E, N, K], address of its scales)."""
+    if w.dim() != 3:
+        raise ValueError(f"w: [E, N, K] expected, not {tuple(w.shape)}")
+    E, N, K = w.shape
+    pw = _vector(w, "w", (E, N, K), _FP8, on)
+    if w_scale is None:
+        raise ValueError("w and w_scale go together")
+    return E, N, K, pw, _vector(w_scale, "w_scale", (E, _blocks(N), _blocks(K)), torch.float32, on)
+
+
+def fp8_quantize(x, *, square=False, stream=None):
+    """(q float8_e4m3fn in x's shape, scale fp32) of x [..., n, K]: scale = max |x| / 448 over a block, q = x / scale
+    rounded to e4m3.  Blocks of 128 columns of a row, scale [..., n, ceil(K / 128)]; or with square (weights, once
+    ahead of time) of 128 x 128, scale [..., ceil(n / 128), ceil(K / 128)]."""
+    if x.dim() < (2 if square else 1):
+        raise ValueError(f"x: a matrix or more expected, not {tuple(x.shape)}")
+    K = x.shape[-1]
+    on = _device(x, "x")
+    n = x.shape[-2] if square else 1
+    config = _fp8_config(K, 1, max(x.numel() // (n * K), 1) if square and n * K else 1, x.dtype, torch.float32)
+    _unattached("fp8_quantize", "there is no backward pass", x)
+
+    def call(s):
+        flat = x.reshape(-1, K)  # a copy where x cannot be viewed so: made, read and freed on this call's stream
+        px, ldx = _matrix(flat, "x", flat.shape[0], K, on)
+        q = torch.empty(x.shape, dtype=_FP8, device=x.device)
+        shape = (*x.shape[:-2], _blocks(n), _blocks(K)) if square else (*x.shape[:-1], _blocks(K))
+        scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+        _check(lib().colibri_moe_fp8_quantize(config[1], px, ldx, flat.shape[0], int(square), q.data_ptr(),
+                                              scale.data_ptr(), s), "colibri_moe_fp8_quantize")
+        return q, scale
+    return _run(call, x, on, stream)
+
+
+def fp8_experts(x, w, w_scale, offsets, *, rows=None, w3=None, w3_scale=None, out_dtype=None, stream=None):
+    """y [R, N]: the rows of every expert times its weights in e4m3, a scale for every block of 128.
+
+    x [n, K] (fp32 or bf16) is quantised within the call, in blocks of 128 columns of a row; w [E, N, K] e4m3 with
+    w_scale [E, ceil(N / 128), ceil(K / 128)] fp32 (``fp8_quantize(..., square=True)``, or a checkpoint's); offsets
+    and rows as for ``int8_experts``.  With w3 and w3_scale (same shapes) y = silu(v) * v3, the gated pair of
+    projections in one pass.  Rows from offsets[E] on are not written.  out_dtype: fp32 or bf16, default x's.
+    Should a wait inside the product run out (two seconds), y is undefined and ``fp8_status`` says so."""
+    n, K = _shape(x, "x")
+    on = _device(x, "x")
+    px, ldx = _matrix(x, "x", n, K, on)
+    E, N, wk, pw, ps = _fp8_weights(w, w_scale, on)
+    if wk != K:
+        raise ValueError(f"w: [E, N, {K}] expected, not {tuple(w.shape)}")
+    if (w3 is None) != (w3_scale is None):
+        raise ValueError("w3 and w3_scale go together")
+    pw3 = _vector(w3, "w3", (E, N, K), _FP8, on)
+    ps3 = _vector(w3_scale, "w3_scale", w_scale.shape, torch.float32, on)
+    po = _vector(offsets, "offsets", (E + 1,), torch.int32, on)
+    R = n if rows is None else rows.numel()
+    pr = _vector(rows, "rows", (R,), torch.int32, on)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    config = _fp8_config(K, N, E, x.dtype, out_dtype)
+    _unattached("fp8_experts", "fp8_experts_backward computes it", x, w_scale, w3_scale)
+
+    def call(s):
+        L = lib()
+        need = ctypes.c_size_t()
+        _check(L.colibri_moe_fp8_experts_workspace(config[1], n, R, ctypes.byref(need)), "colibri_moe_fp8_experts")
+        size = need.value
+        ws = _workspace(size, x.device)
+        y = torch.empty((R, N), dtype=out_dtype, device=x.device)
+        _check(L.colibri_moe_fp8_experts(config[1], px, ldx, n, pr, R, po, pw, ps, pw3, ps3, y.data_ptr(), _at(ws), size,
+                                         s), "colibri_moe_fp8_experts")
+        return y
+    return _run(call, x, on, stream)
+
+
+def fp8_experts_backward(d_y, x, w, w_scale, offsets, *, rows=None, weight_dtype=torch.float32, stream=None):
+    """(d_rows [R, K], d_w [E, N, K]): the gradients of ``fp8_experts`` without w3, from that of y, d_y [R, N].
+
+    d_rows, in d_y's type, has a row for each of y's (``dispatch_backward`` adds up a token's; rows from offsets[E]
+    on are not written): d_y quantised in blocks of 128 columns times the weights.  d_w, of weight_dtype (fp32 or
+    bf16), is that of the weights' values, w * w_scale: d_y and x [n, K] quantised in blocks of 128 rows of an
+    expert, summed over its rows (zeros for an expert without any).  With x None there is no d_w, with w and
+    w_scale None no d_rows (None in their place; x's type is d_y's)."""
+    R, N = _shape(d_y, "d_y")
+    on = _device(d_y, "d_y")
+    pd, ldd = _matrix(d_y, "d_y", R, N, on)
+    E = offsets.numel() - 1
+    if E < 1:
+        raise ValueError("offsets: [E + 1] expected")
+    po = _vector(offsets, "offsets", (E + 1,), torch.int32, on)
+    if w is None and x is None:
+        raise ValueError("one of x and w is needed")
+    n, K, pw, ps, px, ldx, pr = R, None, None, None, None, 0, None
+    if w is not None:
+        we, wn, K, pw, ps = _fp8_weights(w, w_scale, on)
+        if (we, wn) != (E, N):
+            raise ValueError(f"w: [{E}, {N}, K] expected, not {tuple(w.shape)}")
+    elif w_scale is not None:
+        raise ValueError("w and w_scale go together")
+    if x is not None:
+        n, K = _shape(x, "x")[0], K or x.shape[1]
+        px, ldx = _matrix(x, "x", n, K, on, d_y.dtype)
+        pr = _vector(rows, "rows", (R,), torch.int32, on)
+    config = _fp8_config(K, N, E, d_y.dtype, weight_dtype)
+
+    def call(s):
+        L, dev = lib(), d_y.device
+        need = ctypes.c_size_t()
+        _check(L.colibri_moe_fp8_experts_backward_workspace(config[1], n, R, ctypes.byref(need)),
+               "colibri_moe_fp8_experts_backward")
+        size = need.value
+        ws = _workspace(size, dev)
+        d_rows = torch.empty((R, K), dtype=d_y.dtype, device=dev) if w is not None else None
+        d_w = torch.empty((E, N, K), dtype=weight_dtype, device=dev) if x is not None else None
+        if R or d_w is not None:
+            of_w = (pw, ps, _at(d_rows)) if R else (None, None, None)
+            _check(L.colibri_moe_fp8_experts_backward(config[1], pd, ldd, px, ldx, n, pr, R, po, *of_w, _at(d_w), _at(ws),
+                                                      size, s), "colibri_moe_fp8_experts_backward")
+        return d_rows, d_w
+    return _run(call, d_y, on, stream)
+
+
+def fp8_status(device=None) -> int:
+    """As ``int8_status``, for the products of ``fp8_experts`` and ``fp8_experts_backward``."""
+    status = ctypes.c_int32()
+    with torch.cuda.device(device):
+        _check(lib().colibri_moe_fp8_status(ctypes.byref(status)), "colibri_moe_fp8_status")
+    return status.value
