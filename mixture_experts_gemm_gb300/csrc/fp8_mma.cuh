@@ -9,8 +9,9 @@
 //
 // One persistent CTA per SM on tiles of 128 x 128, or CTA pairs (cta_group::2) on tiles of 256 x 256 whose halves
 // of B each CTA loads once for both.  384 threads:
-//   warp 0      TMA producer of B, warp 2 of A (a ring of S stages, 128 rows x 128 bytes of each)
+//   warp 0      TMA producer (a ring of S stages, 128 rows x 128 bytes of A and of B)
 //   warp 1      issues the MMAs, four to a block, into the next of NB sums in TMEM
+//   warps 2, 3  bring the scales into shared memory (alternate blocks), multiplied where they go together
 //   warps 4-11  take the sums: a thread a row (TMEM lane) of half of the columns; then the epilogue
 // Operands whose contraction runs down the rows of memory (the weights in the rows' gradient, both operands in the
 // weights' gradient) are MN-major: the same 128 x 128 boxes under another descriptor, so nothing is transposed in
@@ -35,7 +36,7 @@ constexpr int kThreads = 384;
 constexpr int kTakers = 8, kTaker0 = 4;       // warps that take the sums
 constexpr int kTileBytes = 128 * 128;         // an operand's 128 rows (or columns) of a block
 constexpr int kBoxBytes = 32 * 128;           // the smallest box of rows
-constexpr int kStageCols = 16, kStageLd = 20; // epilogue staging: 32 rows of 16 floats a warp
+constexpr int kStageLd = 12;                  // epilogue staging: 32 rows of 8 words a warp, and 4 between
 constexpr Fp8Limit kDrain = {50000000, 63};   // 50 ms, far above the time of a copy or of a stage's MMAs
 
 template <bool PAIR>
@@ -45,8 +46,12 @@ struct Form {
   static constexpr int C = NT / 2;             // columns of a taker thread
   static constexpr int NB = 512 / NT;          // sums in TMEM
   static constexpr int S = 6;
+  // Blocks whose scales are in shared memory.  Those of block j are written once the MMAs of block j - S are done, which
+  // began when the sum of block j - S - NB had been taken: S + NB slots are never written while they are read.
+  static constexpr int SF = S + NB;
+  static constexpr int kScales = 128 + NT;  // of a slot: a row's (with the weights'), and a second one or the columns'
   static constexpr int kBars = 2 * S + 2 * NB + 3;
-  static constexpr int kSmem = 1024 + S * 2 * kTileBytes + kTakers * 32 * kStageLd * 4 + kBars * 8 + 32 +
+  static constexpr int kSmem = 1024 + S * 2 * kTileBytes + SF * kScales * 4 + kTakers * 32 * kStageLd * 4 + kBars * 8 + 32 +
                                4 * (3 * kFp8MaxExperts + 1);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -158,6 +163,18 @@ __device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t f) {
   return r;
 }
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // silu(v) u as it is stored: fast exp and quotient for bf16; for fp32 expf of what cannot overflow and the
 // approximate reciprocal, good to an ulp, of a sum between 1 and 2.
 template <typename O>
@@ -170,7 +187,7 @@ __device__ __forceinline__ float gated_value(float v, float u) {
 }
 
 struct Item {
-  int64_t i;           // item number
+  int i;               // item number
   int tile, part;
   int e, row, n;       // expert; first row of this CTA's 128 and how many of them there are
   int col;             // first column of the tile (of y)
@@ -190,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_a = smem;
   uint8_t* s_b = s_a + S * kTileBytes;
-  float* s_stage = reinterpret_cast<float*>(s_b + S * kTileBytes);
+  float* s_scale = reinterpret_cast<float*>(s_b + S * kTileBytes);
+  float* s_stage = s_scale + F::SF * F::kScales;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_stage + kTakers * 32 * kStageLd);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + F::kBars);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -209,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full0 + 8 * i, 2);  // A and B landed (PAIR: the leader's, both CTAs')
+      mbar_init(full0 + 8 * i, PAIR ? 3 : 2);  // A, B and the scales are there (PAIR: the leader's, both CTAs')
       mbar_init(empty0 + 8 * i, 1);
     }
     for (int i = 0; i < NB; ++i) {
@@ -237,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // The quantiser lets this kernel start once everything before it is done: offsets and weights may be read at once;
   // the warps that read its rows and scales wait for it.
-  if (warp == 3)
+  if (warp == 2)
     fp8_segments(a.offsets, a.E, a.R, lane, s_row0, s_rows, s_tiles,
                  [](int n) { return kWeights ? (n + kFp8Block - 1) / kFp8Block : (n + MT - 1) / MT; });
   tc_fence_before();
@@ -263,14 +281,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (cost < least) least = cost, parts = p;
     }
   }
-  const int64_t items = tiles * parts;
+  const int items = (int)(tiles * parts);  // y itself has more bytes
 
   // item -> its tile: row tiles of an expert fastest, so that CTAs at work share the other operand in L2
-  auto item_at = [&](int64_t i) {
+  auto item_at = [&](int i) {
     Item it;
     it.i = i;
-    it.tile = (int)(i / parts);
-    it.part = (int)(i - (int64_t)it.tile * parts);
+    it.tile = i / parts;
+    it.part = i - it.tile * parts;
     int blocks = kblocks;
     if constexpr (kWeights) {
       const int each = m_tiles * col_tiles;
@@ -306,55 +324,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   bool ok = true;
-  if (warp == 0 || warp == 2) {
-    // -------------------------------------------------------------- producers: B (warp 0) and A (warp 2)
-    const bool b_side = warp == 0;
-    if (!b_side || kWeights) pdl_wait();
+  // 384 threads hold 168 registers each at launch: 128 x 88 + 256 x 208 is as many.
+  if (warp < kTaker0) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
     const bool elected = elect_one();
-    const uint32_t base = smem_u32(b_side ? s_b : s_a);
+    const uint32_t a0 = smem_u32(s_a), b0 = smem_u32(s_b);
+    const int boxes_of = PAIR || kWeights ? 4 : 0;  // 0: as many as the tile's rows need
+    auto arm = [&](uint32_t st, int boxes) {
+      if (!PAIR || leader) mbar_arrive_expect_tx(full0 + 8 * st, (PAIR ? 2 : 1) * (kTileBytes + boxes * kBoxBytes));
+    };
+    auto load_b = [&](const Item& t, int kb, uint32_t st) {
+      const uint32_t full = PAIR ? mapa_shared(full0 + 8 * st, 0) : full0 + 8 * st, dst = b0 + st * kTileBytes;
+      const int k = kb * kFp8Block;
+      if constexpr (kWeights) {
+        load2<PAIR>(dst, &tm.b, full, t.col + rank * 128, (t.first + kb) * kFp8Block);
+      } else if constexpr (MODE == kFp8Rows) {
+        load3<PAIR>(dst, &tm.b, full, t.col + rank * 128, k, t.e);
+      } else if constexpr (GATED) {
+        // every taker thread's columns: C / 2 channels of w, then the same of w3
+        constexpr int kRuns = PAIR ? 1 : 2, kBytes = C / 2 * 128;
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) {
+          const int ch = t.col + (PAIR ? rank : r) * (C / 2);
+          load3<PAIR>(dst + 2 * r * kBytes, &tm.b, full, k, ch, t.e);
+          load3<PAIR>(dst + (2 * r + 1) * kBytes, &tm.b3, full, k, ch, t.e);
+        }
+      } else {
+        load3<PAIR>(dst, &tm.b, full, k, t.col + rank * 128, t.e);
+      }
+    };
+    auto load_a = [&](const Item& t, int kb, uint32_t st, int boxes) {
+      const uint32_t full = PAIR ? mapa_shared(full0 + 8 * st, 0) : full0 + 8 * st;
+      uint32_t dst = a0 + st * kTileBytes;
+      if constexpr (kWeights) {
+        load2<PAIR>(dst, &tm.a[2], full, t.row, (t.first + kb) * kFp8Block);
+      } else {
+        int row = t.row;
+#pragma unroll
+        for (int b = kFp8TokMaps - 1; b >= 0; --b)  // at most one copy of each box height
+          if (boxes >> b & 1) {
+            load2<PAIR>(dst, &tm.a[b], full, kb * kFp8Block, row);
+            dst += kBoxBytes << b, row += 32 << b;
+          }
+      }
+    };
+    // Weights do not hang on the quantiser: those of the first stages are on their way while it runs.
+    uint32_t early = 0;
+    if (kFromWeights && unit < items) {
+      const Item t = item_at(unit);
+      early = min(S, t.kb1 - t.kb0);
+      for (uint32_t st = 0; st < early; ++st) {
+        if (elected) {
+          arm(st, boxes_of ? boxes_of : (t.n + 31) / 32);
+          load_b(t, t.kb0 + st, st);
+        }
+        __syncwarp();
+      }
+    }
+    pdl_wait();
     uint32_t it = 0, st = 0, ph = 0;
-    for (int64_t i = unit; ok && i < items; i += units) {
+    for (int i = unit; ok && i < items; i += units) {
       const Item t = item_at(i);
-      const int boxes = PAIR || kWeights ? 4 : (t.n + 31) / 32;
+      const int boxes = boxes_of ? boxes_of : (t.n + 31) / 32;
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
         if (!__all_sync(~0u, wait_for(empty0 + 8 * st, ph ^ 1, s_abort, a.limit))) {
           ok = false;
           break;
         }
-        uint32_t full = full0 + 8 * st, dst = base + st * kTileBytes;
-        const int k = kb * kFp8Block;
         if (elected) {
-          const uint32_t bytes = (PAIR ? 2 : 1) * (b_side ? kTileBytes : boxes * kBoxBytes);
-          if (!PAIR || leader) mbar_arrive_expect_tx(full, bytes);
-          if constexpr (PAIR) full = mapa_shared(full, 0);
-          if (b_side) {
-            if constexpr (kWeights) {
-              load2<PAIR>(dst, &tm.b, full, t.col + rank * 128, (t.first + kb) * kFp8Block);
-            } else if constexpr (MODE == kFp8Rows) {
-              load3<PAIR>(dst, &tm.b, full, t.col + rank * 128, k, t.e);
-            } else if constexpr (GATED) {
-              // every taker thread's columns: C / 2 channels of w, then the same of w3
-              constexpr int kRuns = PAIR ? 1 : 2, kBytes = C / 2 * 128;
-#pragma unroll
-              for (int r = 0; r < kRuns; ++r) {
-                const int ch = t.col + (PAIR ? rank : r) * (C / 2);
-                load3<PAIR>(dst + 2 * r * kBytes, &tm.b, full, k, ch, t.e);
-                load3<PAIR>(dst + (2 * r + 1) * kBytes, &tm.b3, full, k, ch, t.e);
-              }
-            } else {
-              load3<PAIR>(dst, &tm.b, full, k, t.col + rank * 128, t.e);
-            }
-          } else if constexpr (kWeights) {
-            load2<PAIR>(dst, &tm.a[2], full, t.row, (t.first + kb) * kFp8Block);
-          } else {
-            int row = t.row;
-#pragma unroll
-            for (int b = kFp8TokMaps - 1; b >= 0; --b)  // at most one copy of each box height
-              if (boxes >> b & 1) {
-                load2<PAIR>(dst, &tm.a[b], full, k, row);
-                dst += kBoxBytes << b, row += 32 << b;
-              }
+          if (it >= early) {
+            arm(st, boxes);
+            load_b(t, kb, st);
           }
+          load_a(t, kb, st, boxes);
         }
         __syncwarp();
         if (++st == S) st = 0, ph ^= 1;
@@ -364,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Every copy has landed before the CTA can leave (PAIR: on the leader's barriers; the CTAs leave together).  After a
     // wait that gave up a stage may lack its other operand: the wait for it ends by kDrain.
     volatile int never = 0;
+    it = max(it, early);
     if (leader)
       for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_for(full0 + 8 * (j % S), j / S & 1, &never, kDrain);
     __syncwarp();
@@ -376,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t da0 = kWeights ? mn_desc(smem_u32(s_a)) : sw128_desc(smem_u32(s_a));
       const uint64_t db0 = MODE != kFp8Forward ? mn_desc(smem_u32(s_b)) : sw128_desc(smem_u32(s_b));
       uint32_t st = 0, ph = 0, buf = 0, bph = 0;
-      for (int64_t i = unit; ok && i < items; i += units) {
+      for (int i = unit; ok && i < items; i += units) {
         const Item t = item_at(i);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           bool got = wait_for<PAIR>(tempty0 + 8 * buf, bph ^ 1, s_abort, a.limit);
@@ -409,93 +454,168 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp >= kTaker0) {
+  } else {
+    // -------------------------------------------------------------- scales
+    pdl_wait();
+    const int kb_w = (a.K + kFp8Block - 1) / kFp8Block, nb_w = (a.N + kFp8Block - 1) / kFp8Block;  // the weights' blocks
+    uint32_t it = 0;  // block number over all items; this warp has those of its parity
+    for (int i = unit; ok && i < items; i += units) {
+      const Item t = item_at(i);
+      const int n = t.kb1 - t.kb0, last = max(t.n - 1, 0);
+      // four rows a lane; a tile past the last row or column takes the last one's
+      const float* sa = a.a_scale + (int64_t)(t.first + t.kb0) * a.lda + t.row;
+      int m[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = min(lane + 32 * j, last);
+      if (t.n == 0) sa = a.a_scale;  // nothing of it is used
+      const float *w0 = nullptr, *w1 = nullptr;  // of the tile's two halves, or of the two projections
+      int64_t w_step = 0;
+      if constexpr (kFromWeights) {
+        const int c0 = t.col / kFp8Block, c1 = GATED || !PAIR ? c0 : c0 + 1, most = (MODE == kFp8Forward ? nb_w : kb_w) - 1;
+        auto at = [&](int c) {
+          return MODE == kFp8Forward ? ((int64_t)t.e * nb_w + min(c, most)) * kb_w + t.kb0
+                                     : ((int64_t)t.e * nb_w + t.kb0) * kb_w + min(c, most);
+        };
+        w0 = a.w_scale + at(c0), w1 = (GATED ? a.w3_scale : a.w_scale) + at(c1);
+        w_step = MODE == kFp8Forward ? 1 : kb_w;
+      }
+      constexpr int kAhead = 4;  // of this warp's blocks whose loads are on their way
+      float fa[kAhead][4], f0[kAhead], f1[kAhead], fx[kAhead][kWeights ? NT / 32 : 1];
+      auto fetch = [&](int k, int kb) {
+        if (kb >= n) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fa[k][j] = sa[kb * a.lda + m[j]];
+        if constexpr (kFromWeights) f0[k] = w0[kb * w_step], f1[k] = w1[kb * w_step];
+        if constexpr (kWeights) {
+#pragma unroll
+          for (int j = 0; j < NT / 32; ++j)
+            fx[k][j] = a.x_scale[(int64_t)(t.first + t.kb0 + kb) * a.ldx + t.col + lane + 32 * j];
+        }
+      };
+      const int odd = (it ^ warp) & 1;  // the first of this warp's blocks in the item
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) fetch(k, odd + 2 * k);
+      for (int kb0 = odd; ok && kb0 < n; kb0 += 2 * kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int kb = kb0 + 2 * k;
+          if (kb >= n) break;
+          const uint32_t j = it + kb, st = j % S;
+          if (!__all_sync(~0u, wait_for(empty0 + 8 * st, (j / S & 1) ^ 1, s_abort, a.limit))) {
+            ok = false;
+            break;
+          }
+          float* slot = s_scale + j % F::SF * F::kScales;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            slot[lane + 32 * r] = kFromWeights ? fa[k][r] * f0[k] : fa[k][r];
+            if constexpr (kFromWeights && (GATED || PAIR)) slot[128 + lane + 32 * r] = fa[k][r] * f1[k];
+          }
+          if constexpr (kWeights) {
+#pragma unroll
+            for (int r = 0; r < NT / 32; ++r) slot[128 + lane + 32 * r] = fx[k][r];
+          }
+          __syncwarp();
+          if (lane == 0) {
+            if (!PAIR || leader)
+              mbar_arrive(full0 + 8 * st);
+            else
+              mbar_arrive_peer(mapa_shared(full0 + 8 * st, 0));
+          }
+          fetch(k, kb + 2 * kAhead);
+        }
+      }
+      it += n;
+    }
+    if (!ok && lane == 0) *s_abort = 1;
+    __syncwarp();
+  }
+  } else {
     // -------------------------------------------------------------- takers
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     pdl_wait();
     const int q = warp & 3, half = (warp - kTaker0) >> 2;  // TMEM lanes 32 q .. of columns half * C ..
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
-    const int kb_w = (a.K + kFp8Block - 1) / kFp8Block, nb_w = (a.N + kFp8Block - 1) / kFp8Block;  // the weights' blocks
-    float* stage = s_stage + (warp - kTaker0) * (32 * kStageLd);
-    uint32_t buf = 0, bph = 0, joins = 0;
-    for (int64_t i = unit; ok && i < items; i += units) {
-      const Item t = item_at(i);
-      const bool mine = q * 32 < t.n;  // whether any of this warp's rows exist
+    uint32_t* stage = reinterpret_cast<uint32_t*>(s_stage) + (warp - kTaker0) * (32 * kStageLd);
+    uint32_t buf = 0, bph = 0, sf = 0, joins = 0;
+    auto free_sum = [&](uint32_t bar) {
+      if (!PAIR || leader)
+        mbar_arrive(bar);
+      else
+        mbar_arrive_peer(mapa_shared(bar, 0));
+    };
+    for (int i = unit; ok && i < items; i += units) {
+      bool mine;  // whether any of this warp's rows exist
+      int left;   // blocks to go
+      {
+        const Item t = item_at(i);
+        mine = q * 32 < t.n, left = t.kb1 - t.kb0;
+      }
       uint64_t acc[C / 2];
 #pragma unroll
       for (int c = 0; c < C / 2; ++c) acc[c] = 0;
-      // scales: of the row, a stride apart from block to block; of the weights' block
-      const int m = min(q * 32 + lane, max(t.n - 1, 0));
-      const float* sa = a.a_scale + (kWeights ? (int64_t)t.first * a.lda : 0) + t.row + m;
-      const float *sw = nullptr, *sw3 = nullptr, *sx = nullptr;
-      int64_t w_step = 0;
-      if constexpr (kFromWeights) {
-        const int blk = (t.col + (GATED ? 0 : half * C)) / kFp8Block;  // a tile past the last column has no block
-        const int64_t at = MODE == kFp8Forward ? ((int64_t)t.e * nb_w + min(blk, nb_w - 1)) * kb_w
-                                               : (int64_t)t.e * nb_w * kb_w + min(blk, kb_w - 1);
-        sw = a.w_scale + at;
-        if constexpr (GATED) sw3 = a.w3_scale + at;
-        w_step = MODE == kFp8Forward ? 1 : kb_w;
-      } else {
-        sx = a.x_scale + (int64_t)t.first * a.ldx + t.col + half * C;
-      }
-      float fa = 0.f, fw = 0.f, fw3 = 0.f;  // the next block's
-      auto fetch = [&](int kb) {
-        fa = sa[kb * a.lda];
-        if constexpr (kFromWeights) fw = __ldg(sw + kb * w_step);
-        if constexpr (GATED) fw3 = __ldg(sw3 + kb * w_step);
-      };
-      if (mine && t.kb0 < t.kb1) fetch(t.kb0);
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        const float f0 = kFromWeights ? fa * fw : fa, f1 = GATED ? fa * fw3 : 0.f;
-        if (mine && kb + 1 < t.kb1) fetch(kb + 1);
-        if (!__all_sync(~0u, wait_for(tfull0 + 8 * buf, bph, s_abort, a.limit))) {
+      bool ready = false;  // the next sum was seen to be there
+#pragma unroll 1
+      for (; left > 0; --left) {
+        if (!ready && !__all_sync(~0u, wait_for(tfull0 + 8 * buf, bph, s_abort, a.limit))) {
           ok = false;
           break;
         }
+        tc_fence_after();
+        const uint32_t from = tmem_base + lanes + buf * NT + half * C, freed = tempty0 + 8 * buf;
+        const float* scale = s_scale + sf * F::kScales;
+        if (++buf == NB) buf = 0, bph ^= 1;
+        if (++sf == F::SF) sf = 0;
         if (mine) {
-          tc_fence_after();
-          const uint32_t from = tmem_base + lanes + buf * NT + half * C;
+          // the weights' block is the half's, or that of one of the projections
+          const float f0 = scale[(kFromWeights && PAIR && !GATED ? half * 128 : 0) + q * 32 + lane];
+          const float f1 = GATED ? scale[128 + q * 32 + lane] : 0.f;
 #pragma unroll
-          for (int c0 = 0; c0 < C; c0 += 16) {
-            uint32_t r[16];
-            tmem_ld16_sync(from + c0, r);
+          for (int c0 = 0; c0 < C; c0 += 32) {
+            uint32_t u[32];
+            tmem_ld32_sync(from + c0, u);
+            if (c0 + 32 == C) {  // this warp has its values: the sum may be overwritten
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0 && !kWeights) free_sum(freed);
+            }
             const float f = GATED && c0 >= C / 2 ? f1 : f0;
             const uint64_t ff = two(f, f);
-            if constexpr (kWeights) {
-              const float4* x4 = reinterpret_cast<const float4*>(sx + (int64_t)kb * a.ldx + c0);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float4 x = __ldg(x4 + c);
-                fma2(acc[c0 / 2 + 2 * c], mul2(two(r[4 * c], r[4 * c + 1]), two(x.x, x.y)), ff);
-                fma2(acc[c0 / 2 + 2 * c + 1], mul2(two(r[4 * c + 2], r[4 * c + 3]), two(x.z, x.w)), ff);
+            for (int c = 0; c < 32; c += 4) {
+              uint64_t lo = two(u[c], u[c + 1]), hi = two(u[c + 2], u[c + 3]);
+              if constexpr (kWeights) {
+                const float4 x = *reinterpret_cast<const float4*>(scale + 128 + half * C + c0 + c);
+                lo = mul2(lo, two(x.x, x.y)), hi = mul2(hi, two(x.z, x.w));
               }
-            } else {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) fma2(acc[c0 / 2 + c], two(r[2 * c], r[2 * c + 1]), ff);
+              fma2(acc[(c0 + c) / 2], lo, ff);
+              fma2(acc[(c0 + c) / 2 + 1], hi, ff);
             }
           }
-          tc_fence_before();
+          if (kWeights) {  // the columns' scales have been read, too
+            __syncwarp();
+            if (lane == 0) free_sum(freed);
+          }
+        } else {
+          __syncwarp();
+          if (lane == 0) free_sum(freed);
         }
-        __syncwarp();
-        if (lane == 0) {
-          if (!PAIR || leader)
-            mbar_arrive(tempty0 + 8 * buf);
-          else
-            mbar_arrive_peer(mapa_shared(tempty0 + 8 * buf, 0));
-        }
-        if (++buf == NB) buf = 0, bph ^= 1;
+        ready = left > 1 && __all_sync(~0u, mbar_test(tfull0 + 8 * buf, bph));
       }
       if (!ok) {
         if (lane == 0) *s_abort = 1;
         break;
       }
+      int again = i;
+      asm volatile("" : "+r"(again));  // its coordinates are computed again rather than held in registers above
+      const Item t = item_at(again);
       float v[C];
 #pragma unroll
       for (int c = 0; c < C / 2; ++c) one_each(acc[c], v[2 * c], v[2 * c + 1]);
       if (parts > 1) {
         const int64_t at = (int64_t)(half * C) * 128 + q * 32 + lane;
         if (mine) {
-          float* part = a.partial + t.i * (NT * 128) + at;
+          float* part = a.partial + (int64_t)t.i * (NT * 128) + at;
 #pragma unroll
           for (int c = 0; c < C; ++c) part[c * 128] = v[c];
         }
@@ -531,50 +651,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!mine) continue;
-      // 16 columns at a time through shared memory, so that stores cover whole sectors of a row
-      constexpr int kOut = GATED ? C / 2 : C, kVec = 16 / sizeof(O), kLanes = kStageCols / kVec;
+      // 32 bytes of every row at a time through shared memory, so that stores cover whole sectors of a row
+      constexpr int kOut = GATED ? C / 2 : C, kCols = 32 / sizeof(O);
       const int rows = min(t.n - q * 32, 32);
       const int64_t row0 = (kWeights ? (int64_t)t.e * a.N : 0) + t.row + q * 32;
       O* y = static_cast<O*>(a.y) + row0 * out_cols;
-      const bool wide = out_cols % kVec == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+      const bool wide = out_cols % (kCols / 2) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 #pragma unroll
-      for (int c0 = 0; c0 < kOut; c0 += kStageCols) {
+      for (int c0 = 0; c0 < kOut; c0 += kCols) {
         const int col = t.col + half * kOut + c0;
-        __syncwarp();  // the last columns have been read
+        uint32_t word[8];
 #pragma unroll
-        for (int c = 0; c < kStageCols; c += 4) {
-          float h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (GATED)
-              h[j] = gated_value<O>(v[c0 + c + j], v[kOut + c0 + c + j]);
-            else
-              h[j] = v[c0 + c + j];
-          }
-          *reinterpret_cast<float4*>(stage + lane * kStageLd + c) = make_float4(h[0], h[1], h[2], h[3]);
+        for (int j = 0; j < 8; ++j) {
+          auto value = [&](int c) {
+            if constexpr (GATED) return gated_value<O>(v[c], v[kOut + c]);
+            return v[c];
+          };
+          if constexpr (sizeof(O) == 2)
+            word[j] = pack_bf16(value(c0 + 2 * j), value(c0 + 2 * j + 1));
+          else
+            word[j] = __float_as_uint(value(c0 + j));
         }
+        __syncwarp();  // the last columns have been read
+        uint4* mine4 = reinterpret_cast<uint4*>(stage + lane * kStageLd);
+        mine4[0] = make_uint4(word[0], word[1], word[2], word[3]);
+        mine4[1] = make_uint4(word[4], word[5], word[6], word[7]);
         __syncwarp();
         if (wide) {
-          const int c = lane % kLanes * kVec;
+          const int c = (lane & 1) * (kCols / 2);
 #pragma unroll
-          for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
-            const float* from = stage + r * kStageLd + c;
-            if (r < rows && col + c < out_cols) {
-              O* to = y + (int64_t)r * out_cols + col + c;
-              if constexpr (sizeof(O) == 2) {
-                const float4 lo = *reinterpret_cast<const float4*>(from), hi = *reinterpret_cast<const float4*>(from + 4);
-                *reinterpret_cast<uint4*>(to) =
-                    make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
-              } else {
-                *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(from);
-              }
-            }
-          }
+          for (int r = lane >> 1; r < 32; r += 16)
+            if (r < rows && col + c < out_cols)
+              *reinterpret_cast<uint4*>(y + (int64_t)r * out_cols + col + c) =
+                  *reinterpret_cast<const uint4*>(stage + r * kStageLd + (lane & 1) * 4);
         } else {
-          const int c = lane % kStageCols;
+          const int c = lane % kCols;
           if (col + c < out_cols)
-            for (int r = lane / kStageCols; r < rows; r += 2)
-              y[(int64_t)r * out_cols + col + c] = from_float<O>(stage[r * kStageLd + c]);
+            for (int r = lane / kCols; r < rows; r += 32 / kCols)
+              y[(int64_t)r * out_cols + col + c] = reinterpret_cast<const O*>(stage + r * kStageLd)[c];
         }
       }
     }
