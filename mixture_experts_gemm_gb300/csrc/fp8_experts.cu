@@ -23,57 +23,126 @@ constexpr float kTop = 448.f;
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one of them is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-// A block's scale as every lane that shares `top` (the largest |x|, infinite after a NaN or an infinity) has it.
+// A block's scale from its largest |x| (NaN or infinite where a value is), and 1 / scale: 0 for a block whose values
+// are all 0 in e4m3 (a scale of 0 or NaN), negative where 1 / scale may overflow and every quotient is a division.
 struct Scale {
   float scale, inv;
-  bool live, exact;
+  __device__ __forceinline__ Scale() {}
   __device__ __forceinline__ explicit Scale(float top) {
     scale = top < INFINITY ? __fdiv_rn(top, kTop) : NAN;
-    live = scale > 0.f;
-    exact = scale < 1e-30f;  // 1 / scale may overflow there
-    inv = live ? __frcp_rn(scale) : 0.f;
+    inv = !(scale > 0.f) ? 0.f : scale < 1e-30f ? -1.f : __frcp_rn(scale);
   }
 };
 
-// e4m3(x / scale) of the IEEE quotient, eight at a time.  The product with 1 / scale is within 3 ulp of the quotient; it
-// rounds to the same e4m3 unless it is that near to the middle of two (20 bits below the three that are kept).
-// Only there, and below e4m3's normal range where the middles lie elsewhere, is the division done.
-__device__ __forceinline__ uint2 quantised8(const float (&x)[8], const Scale& s) {
-  if (!s.live) return make_uint2(0, 0);
-  float p[8];
-  bool doubt = s.exact;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    p[j] = x[j] * s.inv;
-    const uint32_t u = __float_as_uint(p[j]);
-    doubt |= ((u + 8 - 0x80000u) & 0xfffffu) <= 16u || (fabsf(p[j]) < 0.0156255f && p[j] != 0.f);
+// e4m3 of the IEEE quotients x0 / s0 and x1 / s1, two bytes.  x * inv is within 3 ulp of a quotient, so the quotient
+// lies between x * inv * (1 - 2^-21) and x * inv * (1 + 2^-21), and where both ends round to the same e4m3 so does
+// it.  `doubt` collects the bits in which they differ (about one value in 2^16): then the division decides.
+struct Ends {
+  float lo, hi;
+  __device__ __forceinline__ explicit Ends(float inv) : lo(inv * (1.f - 0x1p-21f)), hi(inv * (1.f + 0x1p-21f)) {}
+};
+__device__ __forceinline__ uint32_t quotients(float x0, float x1, const Ends& e0, const Ends& e1, uint32_t& doubt) {
+  const uint32_t lo = e4m3_pair(x0 * e0.lo, x1 * e1.lo), hi = e4m3_pair(x0 * e0.hi, x1 * e1.hi);
+  doubt |= lo ^ hi;
+  return lo;
+}
+__device__ __forceinline__ float quotient(float x, float scale) { return scale > 0.f ? __fdiv_rn(x, scale) : 0.f; }
+
+// Eight values of a row as loaded; zeros past its end.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float v[8];
+  __device__ __forceinline__ float get(int i) const { return v[i]; }
+  __device__ __forceinline__ void set(int i, float x) { v[i] = x; }
+  __device__ __forceinline__ void load(const float* p) { load8(p, v); }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+  __device__ __forceinline__ void set(int i, float x) {  // of zeros
+    w[i >> 1] |= i & 1 ? __float_as_uint(x) : __float_as_uint(x) >> 16;
   }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+};
+template <bool VEC, typename T>
+__device__ __forceinline__ Raw8<T> read8(const T* row, int col, int cols) {
+  Raw8<T> r = {};
+  if constexpr (VEC) {
+    if (col < cols) r.load(row + col);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (col + j < cols) r.set(j, to_float(row[col + j]));
+  }
+  return r;
+}
+
+// Largest |v| of eight columns, column by column or of all.
+template <typename T>
+struct Top8;
+template <>
+struct Top8<float> {
+  float v[8] = {};
+  __device__ __forceinline__ void take(const Raw8<float>& r) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = max_nan(v[i], fabsf(r.v[i]));
+  }
+  __device__ __forceinline__ float get(int i) const { return v[i]; }
+  __device__ __forceinline__ float all() const {
+    return max_nan(max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])), max_nan(max_nan(v[4], v[5]), max_nan(v[6], v[7])));
+  }
+  __device__ __forceinline__ void across(int lanes) {  // with the thread whose lane differs in this bit
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = max_nan(v[i], __shfl_xor_sync(~0u, v[i], lanes));
+  }
+};
+template <>
+struct Top8<__nv_bfloat16> {
+  uint32_t w[4] = {};
+  static __device__ __forceinline__ uint32_t two(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  __device__ __forceinline__ void take(const Raw8<__nv_bfloat16>& r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = two(w[i], r.w[i] & 0x7fff7fffu);
+  }
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+  __device__ __forceinline__ float all() const {
+    const uint32_t m = two(two(w[0], w[1]), two(w[2], w[3]));
+    return max_nan(bf16_lo(m), bf16_hi(m));
+  }
+  __device__ __forceinline__ void across(int lanes) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = two(w[i], __shfl_xor_sync(~0u, w[i], lanes));
+  }
+};
+
+// Eight values by one scale.
+template <typename T>
+__device__ __forceinline__ uint2 quantised8(const Raw8<T>& r, float scale, float inv) {
+  const Ends e(inv);
+  uint32_t q[4], doubt = inv < 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = quotients(r.get(2 * i), r.get(2 * i + 1), e, e, doubt);
   if (doubt) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = __fdiv_rn(x[j], s.scale);
+    for (int i = 0; i < 4; ++i) q[i] = e4m3_pair(quotient(r.get(2 * i), scale), quotient(r.get(2 * i + 1), scale));
   }
-  return make_uint2(e4m3_pair(p[0], p[1]) | e4m3_pair(p[2], p[3]) << 16,
-                    e4m3_pair(p[4], p[5]) | e4m3_pair(p[6], p[7]) << 16);
-}
-
-// Largest |v|, infinite once a NaN or an infinity is among them.
-__device__ __forceinline__ float top_of(float top, float v) {
-  const float m = fabsf(v);
-  return m < INFINITY ? fmaxf(top, m) : INFINITY;
-}
-
-// Columns col .. col + 7 of a row of `cols`; zeros past its end.
-template <typename T, bool VEC>
-__device__ __forceinline__ void read8(const T* row, int col, int cols, float (&v)[8]) {
-  if constexpr (VEC) {
-    if (col < cols) {
-      load8(row + col, v);
-      return;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = !VEC && col + j < cols ? to_float(row[col + j]) : 0.f;
+  if (inv == 0.f) return make_uint2(0, 0);  // 0 * infinity above
+  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
 // ------------------------------------------------------------------------------------- along rows
@@ -93,7 +162,8 @@ struct RowQuant {
 
 constexpr int kRowThreads = 256, kRowsAt = 32, kColsAt = 256;  // rows and columns of a thread block
 
-// Half a warp a block of 128, a warp four rows' 256 columns; all four are on their way before the first is used.
+// Half a warp a block of 128, a warp four rows' 256 columns; all four are on their way before the first is used.  The
+// warp's eight scales are computed at once, a lane one of them, and handed back.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(RowQuant a) {
   __shared__ float s_scale[kRowsAt][2];
@@ -104,26 +174,32 @@ __global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(RowQuant a) 
       a.ticket[i] = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = blockIdx.x * kRowsAt, col = blockIdx.y * kColsAt + lane * 8;
-  float v[4][8];
+  Raw8<T> v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = r0 + j * 8 + warp;
     int t = -1;
     if (r < a.n) t = a.rows ? a.rows[r] : r;
     const bool real = t >= 0 && t < a.n_tokens;
-    read8<T, VEC>(static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx, col, real ? a.cols : 0, v[j]);
+    v[j] = read8<VEC>(static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx, col, real ? a.cols : 0);
   }
+  float mine = 0.f;  // the largest |x| of row lane & 3
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    Top8<T> top;
+    top.take(v[j]);
+    float m = top.all();
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
+    if ((lane & 3) == j) mine = m;
+  }
+  const Scale own(mine);
+  if ((lane & 15) < 4) s_scale[(lane & 3) * 8 + warp][lane >> 4] = own.scale;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = r0 + j * 8 + warp;
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = top_of(top, v[j][i]);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    const Scale s(top);
-    if ((lane & 15) == 0) s_scale[j * 8 + warp][lane >> 4] = s.scale;
-    if (r < a.n && col < a.ldq) *reinterpret_cast<uint2*>(a.q + (int64_t)r * a.ldq + col) = quantised8(v[j], s);
+    const float scale = __shfl_sync(~0u, own.scale, (lane & 16) + j), inv = __shfl_sync(~0u, own.inv, (lane & 16) + j);
+    if (r < a.n && col < a.ldq) *reinterpret_cast<uint2*>(a.q + (int64_t)r * a.ldq + col) = quantised8(v[j], scale, inv);
   }
   __syncthreads();
   if (threadIdx.x < 2 * kRowsAt) {
@@ -157,11 +233,12 @@ struct TileQuant {
 
 constexpr int kTileThreads = 256;
 
-// A block of threads takes tiles of the same 128 rows: a thread eight columns of eight rows, 16 apart.
+// A block of threads takes tiles of the same 128 rows: a thread eight columns of eight rows, 16 apart.  The scales of
+// the columns (or of the square) are computed by a thread each and shared.
 template <typename T, bool VEC, int KIND>
-__global__ void __launch_bounds__(kTileThreads) quantise_tiles_kernel(TileQuant a) {
+__global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise_tiles_kernel(TileQuant a) {
   __shared__ int s_row0[kFp8MaxExperts], s_rows[kFp8MaxExperts], s_tiles[kFp8MaxExperts + 1];
-  __shared__ float s_top[8][kFp8Block];
+  __shared__ __align__(16) float s_top[8][kFp8Block], s_scale[kFp8Block], s_inv[kFp8Block];
   __shared__ float s_row_scale[kFp8Block];
   pdl_wait();
   pdl_trigger();
@@ -192,85 +269,101 @@ __global__ void __launch_bounds__(kTileThreads) quantise_tiles_kernel(TileQuant 
     first = (int64_t)m * a.matrix_rows + at;
     n = min(a.matrix_rows - at, kFp8Block);
   }
-  const int ty = threadIdx.x >> 4;
+  const int ty = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
   const int64_t out0 = KIND == kColumns ? (int64_t)blockIdx.x * kFp8Block : first;
-  const T* src[8];
+  int64_t src[8];  // of this thread's rows in x, or -1
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int i = ty + 16 * j;
     int64_t t = -1;
     if (i < n) t = a.rows ? a.rows[first + i] : first + i;
-    src[j] = t >= 0 && t < a.n_tokens ? static_cast<const T*>(a.x) + t * a.ldx : nullptr;
+    src[j] = t >= 0 && t < a.n_tokens ? t * a.ldx : -1;
   }
   for (int ct = blockIdx.y; ct * kFp8Block < a.ldq; ct += gridDim.y) {
-    const int c = (threadIdx.x & 15) * 8, col = ct * kFp8Block + c;
-    float v[8][8];
+    const int col = ct * kFp8Block + c;
+    Raw8<T> v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      read8<T, VEC>(src[j] ? src[j] : static_cast<const T*>(a.x), col, src[j] ? a.cols : 0, v[j]);
-    float top[8] = {};
+      v[j] = read8<VEC>(static_cast<const T*>(a.x) + max(src[j], (int64_t)0), col, src[j] >= 0 ? a.cols : 0);
+    Top8<T> top;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top[i] = top_of(top[i], v[j][i]);
+    for (int j = 0; j < 8; ++j) top.take(v[j]);
     if constexpr (KIND == kSquare) {
-#pragma unroll
-      for (int i = 1; i < 8; ++i) top[0] = fmaxf(top[0], top[i]);
-      top[0] = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top[0])));  // not negative: ordered as its bits
-      if (lane == 0) s_top[warp][0] = top[0];
+      const float m = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(top.all())));  // ordered as its bits, NaN above
+      if (lane == 0) s_top[warp][0] = m;
     } else {
+      top.across(16);
+      if (lane < 16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], 16));
-        if (lane < 16) s_top[warp][c + i] = top[i];
+        for (int i = 0; i < 8; ++i) s_top[warp][c + i] = top.get(i);
       }
     }
     if (KIND == kColumns && a.row_q) {
+      // along the rows, too: the half-warp's eight scales at once, a lane one of them
+      float mine = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        float m = 0.f;
+        Top8<T> row;
+        row.take(v[j]);
+        float m = row.all();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = top_of(m, v[j][i]);
+        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
+        if ((lane & 7) == j) mine = m;
+      }
+      const Scale own(mine);
+      if ((lane & 15) < 8) s_row_scale[ty + 16 * (lane & 7)] = own.scale;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        const Scale s(m);
+      for (int j = 0; j < 8; ++j) {
         const int i = ty + 16 * j;
-        if ((lane & 15) == 0) s_row_scale[i] = s.scale;
-        if (i < n && col < a.ldq) *reinterpret_cast<uint2*>(a.row_q + (first + i) * a.ldq + col) = quantised8(v[j], s);
+        const float scale = __shfl_sync(~0u, own.scale, (lane & 16) + j), inv = __shfl_sync(~0u, own.inv, (lane & 16) + j);
+        if (i < n && col < a.ldq)
+          *reinterpret_cast<uint2*>(a.row_q + (first + i) * a.ldq + col) = quantised8(v[j], scale, inv);
       }
     }
     __syncthreads();
     if constexpr (KIND == kSquare) {
       float m = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) m = fmaxf(m, s_top[w][0]);
+      for (int w = 0; w < 8; ++w) m = max_nan(m, s_top[w][0]);
       const Scale s(m);
       if (threadIdx.x == 0) a.scale[(int64_t)blockIdx.x * a.lds + ct] = s.scale;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (ty + 16 * j < n && col < a.ldq)
-          *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = quantised8(v[j], s);
+          *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = quantised8(v[j], s.scale, s.inv);
     } else {
       if (threadIdx.x < kFp8Block) {
         float m = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) m = fmaxf(m, s_top[w][threadIdx.x]);
-        s_top[0][threadIdx.x] = m;  // this thread alone reads and writes the column
-        a.scale[(int64_t)blockIdx.x * a.lds + ct * kFp8Block + threadIdx.x] = Scale(m).scale;
+        for (int w = 0; w < 8; ++w) m = max_nan(m, s_top[w][threadIdx.x]);
+        const Scale s(m);
+        s_scale[threadIdx.x] = s.scale, s_inv[threadIdx.x] = s.inv;
+        a.scale[(int64_t)blockIdx.x * a.lds + ct * kFp8Block + threadIdx.x] = s.scale;
         if (a.row_q && (int)threadIdx.x < n) a.row_scale[(int64_t)ct * a.R + first + threadIdx.x] = s_row_scale[threadIdx.x];
       }
       __syncthreads();
-      // column by column: eight rows' quotients by one scale
       uint32_t out[8][2] = {};
+      uint32_t doubt = 0, zero = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const Scale s(s_top[0][c + i]);
-        float x[8];
+      for (int i = 0; i < 8; i += 2) {
+        const float2 inv = *reinterpret_cast<const float2*>(s_inv + c + i);
+        const Ends e0(inv.x), e1(inv.y);
+        doubt |= inv.x < 0.f || inv.y < 0.f;
+        zero |= (inv.x == 0.f ? 1u << i : 0) | (inv.y == 0.f ? 2u << i : 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = v[j][i];
-        const uint2 q = quantised8(x, s);
+        for (int j = 0; j < 8; ++j)
+          out[j][i >> 2] |= quotients(v[j].get(i), v[j].get(i + 1), e0, e1, doubt) << (i & 2 ? 16 : 0);
+      }
+      if (doubt | zero) {  // with columns that are all 0 or hold what is not finite (0 * infinity above)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) out[j][i >> 2] |= ((j < 4 ? q.x : q.y) >> (8 * (j & 3)) & 0xff) << (8 * (i & 3));
+        for (int j = 0; j < 8; ++j) {
+          out[j][0] = out[j][1] = 0;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const uint32_t q = e4m3_pair(quotient(v[j].get(i), s_scale[c + i]), quotient(v[j].get(i + 1), s_scale[c + i + 1]));
+            out[j][i >> 2] |= q << (i & 2 ? 16 : 0);
+          }
+        }
       }
       if (col < a.ldq) {
 #pragma unroll
