@@ -561,7 +561,8 @@ COLIBRI_API int colibri_moe_fp8_experts_backward_workspace(const colibri_moe_fp8
 
 /* The gradients of colibri_moe_fp8_experts without w3, from d_y [R, N] (row stride ld_dy): d_rows [R, K] in dtype, one
  * row for each of y's (colibri_moe_dispatch_backward adds up a token's; rows from offsets[E] on are not written), or
- * NULL with w and w_scale; d_w [E, N, K] in out_dtype (zeros for an expert without rows), or NULL with x and rows. */
+ * NULL with w and w_scale; d_w [E, N, K] in out_dtype (16-byte aligned; zeros for an expert without rows), or NULL with x
+ * and rows. */
 COLIBRI_API int colibri_moe_fp8_experts_backward(const colibri_moe_fp8_config_t* cfg, const void* d_y, int64_t ld_dy,
                                                  const void* x, int64_t ldx, int32_t n_tokens, const int32_t* rows,
                                                  int32_t R, const int32_t* offsets, const uint8_t* w,

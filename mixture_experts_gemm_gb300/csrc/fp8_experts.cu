@@ -603,7 +603,7 @@ extern "C" int colibri_moe_fp8_experts_backward(const colibri_moe_fp8_config_t* 
   if ((d_rows != nullptr) != (w != nullptr) || (w != nullptr) != (w_scale != nullptr) || !ops_aligned16(w))
     return COLIBRI_ERR_INVALID_ARG;
   if (R > 0 && (!d_y || ld_dy < N || !offsets)) return COLIBRI_ERR_INVALID_ARG;
-  if (d_w && R > 0 && n_tokens > 0 && (!x || ldx < K)) return COLIBRI_ERR_INVALID_ARG;
+  if (!ops_aligned16(d_w) || (d_w && R > 0 && n_tokens > 0 && (!x || ldx < K))) return COLIBRI_ERR_INVALID_ARG;
   if (R > 0) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return COLIBRI_ERR_INVALID_ARG;
     if (workspace_bytes < workspace_of(cfg, R, 0, true).bytes) return COLIBRI_ERR_INVALID_ARG;

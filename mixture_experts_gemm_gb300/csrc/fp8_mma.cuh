@@ -182,6 +182,14 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
                : "r"(taddr)
                : "memory");
 }
+// 16 TMEM lanes x 32 columns, a thread two neighbouring columns of every eight, of two lanes: r[4 i] and r[4 i + 1] are
+// lane l / 4 of columns 8 i + 2 (l % 4) and the next, r[4 i + 2] and r[4 i + 3] those of lane l / 4 + 8.
+__device__ __forceinline__ void tmem_ld_spread(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // silu(v) u as it is stored: fast exp and quotient for bf16; for fp32 expf of what cannot overflow and the
@@ -522,7 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if constexpr (kWeights) {
 #pragma unroll
-            for (int r = 0; r < NT / 32; ++r) slot[128 + lane + 32 * r] = fx[k][r];
+            for (int r = 0; r < NT / 32; ++r) {  // in the order that the takers' threads read them
+              const int c = (lane + 32 * r) % C;
+              slot[128 + (lane + 32 * r - c) + (c % 8 / 2) * (C / 4) + c / 8 * 2 + c % 2] = fx[k][r];
+            }
           }
           __syncwarp();
           if (lane == 0) {
@@ -576,38 +587,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++buf == NB) buf = 0, bph ^= 1;
         if (++sf == F::SF) sf = 0;
         if (mine) {
-          // the weights' block is the half's, or that of one of the projections
-          const float f0 = scale[(kFromWeights && PAIR && !GATED ? half * 128 : 0) + q * 32 + lane];
-          const float f1 = GATED ? scale[128 + q * 32 + lane] : 0.f;
-          // 16 columns at a time: halves of 32 on their way behind one another took the registers' moves (8192 tokens of
-          // 14336 x 4096: 0.80 ms, 0.87 to 1.5 in larger pieces or with two in flight).  Everything up to the products is
-          // volatile, so that none of it moves above the wait.
+          if constexpr (kWeights) {
+            // A scale for every column as well.  With a row a thread each would have to read all of them, and reads of shared
+            // memory wait for the tensor cores' (2150 cycles a block against 500 without); with columns spread over four
+            // threads an eighth of the reads do.
+            uint64_t fr[4];  // of rows lane / 4 + 8 g
 #pragma unroll
-          for (int c0 = 0; c0 < C; c0 += 16) {
-            uint32_t u[16];
-            tmem_ld(from + c0, u);
-            tmem_wait();
-            if (c0 + 16 == C) {  // this warp has its values: the sum may be overwritten
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0 && !kWeights) free_sum(freed);
+            for (int g = 0; g < 4; ++g) {
+              const float f = scale[q * 32 + lane / 4 + 8 * g];
+              fr[g] = two(f, f);
             }
-            const float f = GATED && c0 >= C / 2 ? f1 : f0;
-            const uint64_t ff = two(f, f);
+            const float4* x4 = reinterpret_cast<const float4*>(scale + 128 + half * C + (lane & 3) * (C / 4));
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              uint64_t lo = two(u[c], u[c + 1]), hi = two(u[c + 2], u[c + 3]);
-              if constexpr (kWeights) {
-                const float4 x = *reinterpret_cast<const float4*>(scale + 128 + half * C + c0 + c);
-                lo = mul2(lo, two(x.x, x.y)), hi = mul2(hi, two(x.z, x.w));
+            for (int c0 = 0; c0 < C; c0 += 32) {
+              const float4 x[2] = {x4[c0 / 16], x4[c0 / 16 + 1]};
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {  // 16 rows
+                uint32_t u[16];
+                tmem_ld_spread(from + (static_cast<uint32_t>(16 * h) << 16) + c0, u);
+                tmem_wait();
+                if (c0 + 32 == C && h == 1) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) free_sum(freed);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float4 xi = x[i / 2];
+                  const uint64_t fx = i & 1 ? two(xi.z, xi.w) : two(xi.x, xi.y);
+#pragma unroll
+                  for (int g = 0; g < 2; ++g)
+                    fma2(acc[((2 * h + g) * C + c0 + 8 * i) / 8], mul2(two(u[4 * i + 2 * g], u[4 * i + 2 * g + 1]), fx),
+                         fr[2 * h + g]);
+                }
               }
-              fma2(acc[(c0 + c) / 2], lo, ff);
-              fma2(acc[(c0 + c) / 2 + 1], hi, ff);
             }
-          }
-          if (kWeights) {  // the columns' scales have been read, too
-            __syncwarp();
-            if (lane == 0) free_sum(freed);
+          } else {
+            // the weights' block is the half's, or that of one of the projections
+            const float f0 = scale[(kFromWeights && PAIR && !GATED ? half * 128 : 0) + q * 32 + lane];
+            const float f1 = GATED ? scale[128 + q * 32 + lane] : 0.f;
+            // 16 columns at a time: halves of 32 on their way behind one another took the registers' moves (8192 tokens of
+            // 14336 x 4096: 0.80 ms, 0.87 to 1.5 in larger pieces or with two in flight).  Everything up to the products is
+            // volatile, so that none of it moves above the wait.
+#pragma unroll
+            for (int c0 = 0; c0 < C; c0 += 16) {
+              uint32_t u[16];
+              tmem_ld(from + c0, u);
+              tmem_wait();
+              if (c0 + 16 == C) {  // this warp has its values: the sum may be overwritten
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) free_sum(freed);
+              }
+              const float f = GATED && c0 >= C / 2 ? f1 : f0;
+              const uint64_t ff = two(f, f);
+#pragma unroll
+              for (int c = 0; c < 16; c += 4) {
+                              fma2(acc[(c0 + c) / 2], two(u[c], u[c + 1]), ff);
+                fma2(acc[(c0 + c) / 2 + 1], two(u[c + 2], u[c + 3]), ff);
+              }
+            }
           }
         } else {
           __syncwarp();
@@ -664,6 +703,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!mine) continue;
+      if constexpr (kWeights) {
+        // Four threads hold eight columns of a row, two each.  They trade, so that each has 16 bytes of one row: in fp32 half of
+        // one of two runs of eight columns, in bf16 all of one of four (stores of 4 bytes: 16384 rows, 8 x 4096 x 14336
+        // in bf16, 1.57 ms).
+        const int64_t row = (int64_t)t.e * a.N + t.row + q * 32 + lane / 4;
+        const int rows = t.n - q * 32 - lane / 4;  // from this thread's first one on
+        O* y = static_cast<O*>(a.y) + row * out_cols;
+        constexpr int kRuns = 16 / (2 * sizeof(O));  // runs of eight columns traded at once
+        const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+          for (int j = 0; j < C / 8; j += kRuns) {
+            const float* from = v + 2 * (g * C / 8 + j);
+            uint4 out;
+            int col = t.col + half * C + 8 * j;
+            if constexpr (sizeof(O) == 4) {
+              const float a0 = __shfl_xor_sync(~0u, odd ? from[0] : from[2], 1), a1 = __shfl_xor_sync(~0u, odd ? from[1] : from[3], 1);
+              const float k0 = odd ? from[2] : from[0], k1 = odd ? from[3] : from[1];
+              out = make_uint4(__float_as_uint(odd ? a0 : k0), __float_as_uint(odd ? a1 : k1), __float_as_uint(odd ? k0 : a0),
+                               __float_as_uint(odd ? k1 : a1));
+              col += (odd ? 8 : 0) + (high ? 4 : 0);
+            } else {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] = pack_bf16(from[2 * i], from[2 * i + 1]);
+              const uint32_t r0 = __shfl_xor_sync(~0u, odd ? w[0] : w[1], 1), r2 = __shfl_xor_sync(~0u, odd ? w[2] : w[3], 1);
+              const uint32_t a0 = odd ? r0 : w[0], a1 = odd ? w[1] : r0, a2 = odd ? r2 : w[2], a3 = odd ? w[3] : r2;
+              const uint32_t s0 = __shfl_xor_sync(~0u, high ? a0 : a2, 2), s1 = __shfl_xor_sync(~0u, high ? a1 : a3, 2);
+              out = high ? make_uint4(s0, s1, a2, a3) : make_uint4(a0, a1, s0, s1);
+              col += 8 * (lane & 3);
+            }
+            if (8 * g < rows && col < out_cols)  // K is a multiple of 16: a thread's columns are inside together
+              *reinterpret_cast<uint4*>(y + (int64_t)(8 * g) * out_cols + col) = out;
+          }
+        }
+        continue;
+      }
       // 32 bytes of every row at a time through shared memory, so that stores cover whole sectors of a row
       constexpr int kOut = GATED ? C / 2 : C, kCols = 32 / sizeof(O);
       const int rows = min(t.n - q * 32, 32);
