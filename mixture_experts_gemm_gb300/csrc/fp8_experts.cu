@@ -29,30 +29,36 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if one of t
   return r;
 }
 
-// A block's scale from its largest |x| (NaN or infinite where a value is), and 1 / scale: 0 for a block whose values
-// are all 0 in e4m3 (a scale of 0 or NaN), negative where 1 / scale may overflow and every quotient is a division.
+// A block's scale from its largest |x| (NaN or infinite where a value is), and 1 / scale: 0 for a scale of 0 (whose
+// values are), negative where every quotient is to be a division: 1 / scale may overflow, or the scale is NaN.
 struct Scale {
   float scale, inv;
-  __device__ __forceinline__ Scale() {}
   __device__ __forceinline__ explicit Scale(float top) {
     scale = top < INFINITY ? __fdiv_rn(top, kTop) : NAN;
-    inv = !(scale > 0.f) ? 0.f : scale < 1e-30f ? -1.f : __frcp_rn(scale);
+    inv = scale == 0.f ? 0.f : scale >= 1e-30f ? __frcp_rn(scale) : -1.f;
   }
 };
 
 // e4m3 of the IEEE quotients x0 / s0 and x1 / s1, two bytes.  x * inv is within 3 ulp of a quotient, so the quotient
 // lies between x * inv * (1 - 2^-21) and x * inv * (1 + 2^-21), and where both ends round to the same e4m3 so does
-// it.  `doubt` collects the bits in which they differ (about one value in 2^16): then the division decides.
+// it.  Where they do not (of fp32 values one pair in 2^15; of bf16 values a few in a hundred, as quotients of few bits
+// often are the middle of two), a bit of `doubt` is set and the division decides, one pair after another.
 struct Ends {
   float lo, hi;
   __device__ __forceinline__ explicit Ends(float inv) : lo(inv * (1.f - 0x1p-21f)), hi(inv * (1.f + 0x1p-21f)) {}
 };
-__device__ __forceinline__ uint32_t quotients(float x0, float x1, const Ends& e0, const Ends& e1, uint32_t& doubt) {
+__device__ __forceinline__ uint32_t quotients(float x0, float x1, const Ends& e0, const Ends& e1, uint32_t& doubt, int bit) {
   const uint32_t lo = e4m3_pair(x0 * e0.lo, x1 * e1.lo), hi = e4m3_pair(x0 * e0.hi, x1 * e1.hi);
-  doubt |= lo ^ hi;
+  if (lo != hi) doubt |= 1u << bit;
   return lo;
 }
 __device__ __forceinline__ float quotient(float x, float scale) { return scale > 0.f ? __fdiv_rn(x, scale) : 0.f; }
+// Columns col and col + 1 of a row, by division.
+template <typename T>
+__device__ __forceinline__ void divide(const T* row, int col, int cols, float s0, float s1, uint8_t* q) {
+  const float x0 = row && col < cols ? to_float(row[col]) : 0.f, x1 = row && col + 1 < cols ? to_float(row[col + 1]) : 0.f;
+  *reinterpret_cast<uint16_t*>(q) = (uint16_t)e4m3_pair(quotient(x0, s0), quotient(x1, s1));
+}
 
 // Eight values of a row as loaded; zeros past its end.
 template <typename T>
@@ -130,18 +136,14 @@ struct Top8<__nv_bfloat16> {
   }
 };
 
-// Eight values by one scale.
+// Eight values by one scale; doubtful pairs as bits from `bit` on.
 template <typename T>
-__device__ __forceinline__ uint2 quantised8(const Raw8<T>& r, float scale, float inv) {
+__device__ __forceinline__ uint2 quantised8(const Raw8<T>& r, float inv, uint32_t& doubt, int bit) {
   const Ends e(inv);
-  uint32_t q[4], doubt = inv < 0.f;
+  uint32_t q[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = quotients(r.get(2 * i), r.get(2 * i + 1), e, e, doubt);
-  if (doubt) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = e4m3_pair(quotient(r.get(2 * i), scale), quotient(r.get(2 * i + 1), scale));
-  }
-  if (inv == 0.f) return make_uint2(0, 0);  // 0 * infinity above
+  for (int i = 0; i < 4; ++i) q[i] = quotients(r.get(2 * i), r.get(2 * i + 1), e, e, doubt, bit + i);
+  if (inv < 0.f) doubt |= 15u << bit;
   return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
@@ -195,13 +197,23 @@ __global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(RowQuant a) 
   }
   const Scale own(mine);
   if ((lane & 15) < 4) s_scale[(lane & 3) * 8 + warp][lane >> 4] = own.scale;
+  uint32_t doubt = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = r0 + j * 8 + warp;
-    const float scale = __shfl_sync(~0u, own.scale, (lane & 16) + j), inv = __shfl_sync(~0u, own.inv, (lane & 16) + j);
-    if (r < a.n && col < a.ldq) *reinterpret_cast<uint2*>(a.q + (int64_t)r * a.ldq + col) = quantised8(v[j], scale, inv);
+    const uint2 q = quantised8(v[j], __shfl_sync(~0u, own.inv, (lane & 16) + j), doubt, 4 * j);
+    if (r < a.n && col < a.ldq) *reinterpret_cast<uint2*>(a.q + (int64_t)r * a.ldq + col) = q;
   }
   __syncthreads();
+  if (col >= a.ldq) doubt = 0;
+  for (; doubt; doubt &= doubt - 1) {
+    const int bit = __ffs(doubt) - 1, j = bit >> 2, i = 2 * (bit & 3), r = r0 + j * 8 + warp;
+    if (r >= a.n) break;
+    const int t = a.rows ? a.rows[r] : r;
+    const float scale = s_scale[j * 8 + warp][lane >> 4];
+    divide(t >= 0 && t < a.n_tokens ? static_cast<const T*>(a.x) + t * a.ldx : nullptr, col + i, a.cols, scale, scale,
+           a.q + (int64_t)r * a.ldq + col + i);
+  }
   if (threadIdx.x < 2 * kRowsAt) {
     const int b = threadIdx.x / kRowsAt, r = threadIdx.x % kRowsAt, blk = blockIdx.y * 2 + b;
     if (r0 + r < a.n && blk * kFp8Block < a.cols)
@@ -271,20 +283,20 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
   }
   const int ty = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;
   const int64_t out0 = KIND == kColumns ? (int64_t)blockIdx.x * kFp8Block : first;
-  int64_t src[8];  // of this thread's rows in x, or -1
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int i = ty + 16 * j;
+  auto source = [&](int i) -> const T* {  // row i of the tile in x, or nullptr
     int64_t t = -1;
     if (i < n) t = a.rows ? a.rows[first + i] : first + i;
-    src[j] = t >= 0 && t < a.n_tokens ? t * a.ldx : -1;
-  }
+    return t >= 0 && t < a.n_tokens ? static_cast<const T*>(a.x) + t * a.ldx : nullptr;
+  };
+  const T* src[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) src[j] = source(ty + 16 * j);
   for (int ct = blockIdx.y; ct * kFp8Block < a.ldq; ct += gridDim.y) {
     const int col = ct * kFp8Block + c;
     Raw8<T> v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      v[j] = read8<VEC>(static_cast<const T*>(a.x) + max(src[j], (int64_t)0), col, src[j] >= 0 ? a.cols : 0);
+      v[j] = read8<VEC>(src[j], col, src[j] ? a.cols : 0);
     Top8<T> top;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top.take(v[j]);
@@ -298,6 +310,7 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
         for (int i = 0; i < 8; ++i) s_top[warp][c + i] = top.get(i);
       }
     }
+    uint32_t doubt_rows = 0;
     if (KIND == kColumns && a.row_q) {
       // along the rows, too: the half-warp's eight scales at once, a lane one of them
       float mine = 0.f;
@@ -315,12 +328,18 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int i = ty + 16 * j;
-        const float scale = __shfl_sync(~0u, own.scale, (lane & 16) + j), inv = __shfl_sync(~0u, own.inv, (lane & 16) + j);
-        if (i < n && col < a.ldq)
-          *reinterpret_cast<uint2*>(a.row_q + (first + i) * a.ldq + col) = quantised8(v[j], scale, inv);
+        const uint2 q = quantised8(v[j], __shfl_sync(~0u, own.inv, (lane & 16) + j), doubt_rows, 4 * j);
+        if (i < n && col < a.ldq) *reinterpret_cast<uint2*>(a.row_q + (first + i) * a.ldq + col) = q;
       }
     }
     __syncthreads();
+    if (col >= a.ldq) doubt_rows = 0;
+    for (; doubt_rows; doubt_rows &= doubt_rows - 1) {
+      const int bit = __ffs(doubt_rows) - 1, i = ty + 16 * (bit >> 2), k = 2 * (bit & 3);
+      if (i >= n) break;
+      divide(source(i), col + k, a.cols, s_row_scale[i], s_row_scale[i], a.row_q + (first + i) * a.ldq + col + k);
+    }
+    uint32_t doubt = 0;
     if constexpr (KIND == kSquare) {
       float m = 0.f;
 #pragma unroll
@@ -328,9 +347,16 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
       const Scale s(m);
       if (threadIdx.x == 0) a.scale[(int64_t)blockIdx.x * a.lds + ct] = s.scale;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (ty + 16 * j < n && col < a.ldq)
-          *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = quantised8(v[j], s.scale, s.inv);
+      for (int j = 0; j < 8; ++j) {
+        const uint2 q = quantised8(v[j], s.inv, doubt, 4 * j);
+        if (ty + 16 * j < n && col < a.ldq) *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = q;
+      }
+      if (col >= a.ldq) doubt = 0;
+      for (; doubt; doubt &= doubt - 1) {
+        const int bit = __ffs(doubt) - 1, i = ty + 16 * (bit >> 2), k = 2 * (bit & 3);
+        if (i >= n) break;
+        divide(source(i), col + k, a.cols, s.scale, s.scale, a.q + (out0 + i) * a.ldq + col + k);
+      }
     } else {
       if (threadIdx.x < kFp8Block) {
         float m = 0.f;
@@ -343,32 +369,23 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
       }
       __syncthreads();
       uint32_t out[8][2] = {};
-      uint32_t doubt = 0, zero = 0;
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
         const float2 inv = *reinterpret_cast<const float2*>(s_inv + c + i);
         const Ends e0(inv.x), e1(inv.y);
-        doubt |= inv.x < 0.f || inv.y < 0.f;
-        zero |= (inv.x == 0.f ? 1u << i : 0) | (inv.y == 0.f ? 2u << i : 0);
+        if (inv.x < 0.f || inv.y < 0.f) doubt |= 0xffu << 4 * i;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          out[j][i >> 2] |= quotients(v[j].get(i), v[j].get(i + 1), e0, e1, doubt) << (i & 2 ? 16 : 0);
-      }
-      if (doubt | zero) {  // with columns that are all 0 or hold what is not finite (0 * infinity above)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          out[j][0] = out[j][1] = 0;
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const uint32_t q = e4m3_pair(quotient(v[j].get(i), s_scale[c + i]), quotient(v[j].get(i + 1), s_scale[c + i + 1]));
-            out[j][i >> 2] |= q << (i & 2 ? 16 : 0);
-          }
-        }
+          out[j][i >> 2] |= quotients(v[j].get(i), v[j].get(i + 1), e0, e1, doubt, 4 * i + j) << (i & 2 ? 16 : 0);
       }
       if (col < a.ldq) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = make_uint2(out[j][0], out[j][1]);
+        for (; doubt; doubt &= doubt - 1) {
+          const int bit = __ffs(doubt) - 1, i = ty + 16 * (bit & 7), k = 2 * (bit >> 3);
+          divide(source(i), col + k, a.cols, s_scale[c + k], s_scale[c + k + 1], a.q + (out0 + i) * a.ldq + col + k);
+        }
       }
     }
     __syncthreads();  // the next tile's maxima
