@@ -186,7 +186,10 @@ struct BackArgs {
   int parts;  // warps that share a token
 };
 
-// A warp takes stretches of one token: W columns a lane, the token's rows one after another, two in flight.
+// Accesses of W columns that a lane has in flight.
+__host__ __device__ constexpr int back_units(int W) { return W == 8 ? 2 : 8; }
+
+// A warp takes stretches of one token: W columns a lane, the token's rows one after another.
 template <typename T, typename O, int W>
 __global__ void __launch_bounds__(kRowThreads) rows_back_kernel(BackArgs a) {
   pdl_wait();
@@ -199,24 +202,25 @@ __global__ void __launch_bounds__(kRowThreads) rows_back_kernel(BackArgs a) {
     const int part = (int)(i - t * a.parts);
     const int row = lane < a.k ? a.row_of[t * a.k + lane] : -1;
     const int own = row >= 0 && row < a.R ? row : -1;
-    for (int c0 = part * 32 * 2; c0 < n; c0 += a.parts * 32 * 2) {
-      float sum[2][W] = {};
+    constexpr int U = back_units(W);
+    for (int c0 = part * 32 * U; c0 < n; c0 += a.parts * 32 * U) {
+      float sum[U][W] = {};
       for (int s = 0; s < a.k; ++s) {
         const int r = __shfl_sync(~0u, own, s);
         if (r < 0) continue;
         const T* src = static_cast<const T*>(a.d_rows) + (int64_t)r * a.d;
-        float v[2][W] = {};
+        float v[U][W] = {};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < U; ++j)
           if (c0 + 32 * j + lane < n) load_w(src + (int64_t)(c0 + 32 * j + lane) * W, v[j]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < U; ++j)
 #pragma unroll
           for (int w = 0; w < W; ++w) sum[j][w] = __fadd_rn(sum[j][w], v[j][w]);
       }
       O* dst = static_cast<O*>(a.d_x) + t * a.d;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < U; ++j)
         if (c0 + 32 * j + lane < n) store_w(dst + (int64_t)(c0 + 32 * j + lane) * W, sum[j]);
     }
   }
@@ -492,7 +496,7 @@ extern "C" int colibri_moe_dispatch_backward(const void* d_rows, int32_t dtype, 
   BackArgs a = {d_rows, row_of, d_x, T, R, k, d, 1};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool vec = vectors_of_8(d, {d_rows, d_x}, {});
-  a.parts = shares(T, d / (vec ? 8 : 1), 64, sms);
+  a.parts = shares(T, d / (vec ? 8 : 1), 32 * back_units(vec ? 8 : 1), sms);
   const dim3 grid(warp_grid((int64_t)T * a.parts, sms)), block(kRowThreads);
   return status(with_type(dtype, [&](auto t) {
     return with_type(out_dtype, [&](auto o) {
