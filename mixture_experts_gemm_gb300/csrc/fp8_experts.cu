@@ -470,7 +470,12 @@ bool map_weights(CUtensorMap* m, const void* w, const colibri_moe_fp8_config_t* 
   return map_of(m, w, 3, dims, strides, box_rows);
 }
 
-// Tiles of 256 x 256 on CTA pairs where experts have more rows than a tile of 128.
+// Tiles of 256 x 256 on CTA pairs where an expert's rows, on average (the exact numbers are on the device), are more than a
+// single CTA's 128.  us of whole calls on a GB300, single CTAs / pairs, for eight experts of 2048 x 5632 x 2, eight of 4096
+// x 4096, and 64 of 2048 x 1408 (top-6, unevenly loaded), by that mean:
+//    64:  47 / 61,  38 / 45,  46 / 68      192:  81 /  63,  57 / 49,  65 / 75
+//    96:  48 / 62,  38 / 47,  52 / 68      256: 100 /  92,  69 / 67,  75 / 79
+//   128:  61 / 62,  46 / 48,  55 / 71      384: 129 / 112,  95 / 87,  94 / 97
 bool pair_rows(int R, int E) { return R / std::min(E, R) > 128; }
 
 struct Workspace {

@@ -428,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     it = max(it, early);
     if (leader)
       for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_for(full0 + 8 * (j % S), j / S & 1, &never, kDrain);
+    // A pair that stopped early may have issued different stages: nothing ever arrives on this barrier of a pair's.
+    if (PAIR && (!ok || *s_abort)) wait_for(joined, 0, &never, kDrain);
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer

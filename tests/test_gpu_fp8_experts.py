@@ -232,3 +232,258 @@ def test_gradients(ops, counts, N, K, dtype, weight_dtype):
     none, only = ops.fp8_experts_backward(d_y.cuda(), x.cuda(), None, None, off.cuda(), rows=rows.cuda(),
                                           weight_dtype=weight_dtype)
     assert none is None and torch.equal(only, d_w)
+
+
+@pytest.mark.parametrize("counts,N,K", [([3], 200, 8192), ([40, 0, 2], 64, 65536), ([3000], 64, 64), ([1500, 1], 96, 48),
+                                        ([130], 131, 144), ([1], 131072, 16)])
+def test_split_and_long_products(ops, counts, N, K):
+    """Few tiles and long sums (parts of the contraction added in order), few rows of many columns."""
+    test_product(ops, counts, N, K, F32, F32)
+    test_gradients(ops, counts, N, K, F32, F32)
+
+
+def exact_inputs(rows, cols, seed):
+    """Whole numbers whose blocks along rows and down columns all have the scale 1: 448 on the diagonal of every block of
+    128 x 128, small ones elsewhere (e4m3 has whole numbers up to 16)."""
+    x = torch.randint(-4, 5, (rows, cols), generator=gen(seed)).float()
+    r, c = torch.arange(rows)[:, None] % B, torch.arange(cols)[None] % B
+    return torch.where(r == c, 448.0, x)
+
+
+@pytest.mark.parametrize("counts,N,K", [([128, 256, 0, 384], 384, 256), ([1024, 512], 640, 384), ([4096], 256, 128)])
+def test_whole_numbers_are_exact(ops, counts, N, K):
+    """Where every scale is a power of two and every sum a whole number below 2^24, results are exact: the product, the
+    gradients, and these as differences of the product, which is linear in the weights and in x's values."""
+    E, R = len(counts), sum(counts)
+    off = segments(counts).cuda()
+    x, d_y = exact_inputs(R, K, 1).cuda(), exact_inputs(R, N, 2).cuda()
+    w = torch.randint(-8, 9, (E, N, K), generator=gen(3)).float().cuda()
+    s = (2.0 ** torch.randint(-2, 3, (E, -(-N // B), -(-K // B)), generator=gen(4))).cuda()
+    W = w.double() * s.double().repeat_interleave(B, 1)[:, :N].repeat_interleave(B, 2)[:, :, :K]
+    y = ops.fp8_experts(x, w.to(FP8), s, off)
+    d_rows, d_w = ops.fp8_experts_backward(d_y, x, w.to(FP8), s, off)
+    for e in range(E):
+        at = slice(int(off[e]), int(off[e + 1]))
+        assert torch.equal(y[at].double(), x[at].double() @ W[e].T)
+        assert torch.equal(d_rows[at].double(), d_y[at].double() @ W[e])
+        assert torch.equal(d_w[e].double(), d_y[at].double().T @ x[at].double())
+    other = torch.randint(-8, 9, (E, N, K), generator=gen(5)).float().cuda()
+    moved = (ops.fp8_experts(x, other.to(FP8), torch.ones_like(s), off).double()
+             - ops.fp8_experts(x, w.to(FP8), torch.ones_like(s), off).double())
+    assert (moved * d_y).sum() == (d_w.double() * (other - w).double()).sum()
+    there = x + torch.where(x.abs() < 448, torch.randint(0, 3, x.shape, generator=gen(6)).float().cuda(), 0.0)
+    moved = ops.fp8_experts(there, w.to(FP8), s, off).double() - y.double()
+    assert (moved * d_y).sum() == (d_rows.double() * (there - x).double()).sum()
+
+
+def c_forward(ops, x, ldx, n, rows, R, off, w, s, y, config, space):
+    L = ops.lib()
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    rc = L.colibri_moe_fp8_experts(ops.ctypes.byref(config), at(x), ldx, n, at(rows), R, at(off), at(w), at(s), None, None,
+                                   at(y), at(space), space.numel(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    torch.cuda.synchronize()
+
+
+def space_for(ops, config, n, R, backward=False):
+    size = ops.ctypes.c_size_t()
+    f = ops.lib().colibri_moe_fp8_experts_backward_workspace if backward else ops.lib().colibri_moe_fp8_experts_workspace
+    assert f(ops.ctypes.byref(config), n, R, ops.ctypes.byref(size)) == 0
+    return torch.empty(size.value, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("R,bounds", [(300, [0, 100, 40, 200, 250]), (300, [5, 290, 1000, 2000, -3]), (900, [0, 600, 600, 700, 850]),
+                                      (40, [0, 0, 0, 0, 0])])
+def test_segments_as_they_come(ops, R, bounds):
+    """Offsets outside 0..R are clamped, rows that an earlier segment holds stay with it, and rows of no segment, behind the
+    last one too, are left as they were."""
+    E, N, K = 4, 136, 160
+    x = torch.randn(R, K, generator=gen(R)).cuda()
+    w, s = weights(E, N, K, 7)
+    off = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    config = ops.Fp8Config(K, N, E, 0, 0, 0, 0)
+    y = torch.full((R, N), 7.0, device="cuda")
+    c_forward(ops, x, K, R, None, R, off, w.cuda(), s.cuda(), y, config, space_for(ops, config, R, R))
+    owner, reach = torch.full((R,), -1), 0
+    for e in range(E):
+        lo, hi = (min(max(b, 0), R) for b in bounds[e:e + 2])
+        owner[max(lo, reach):hi] = e
+        reach = max(reach, hi)
+    rows = torch.arange(R)
+    for e in range(E):
+        at = rows[owner == e]
+        if len(at):
+            # not the bits of a call on these rows alone: that may split its sums otherwise
+            args = x.cpu(), at, segments([len(at)]), w[e:e + 1], s[e:e + 1]
+            off_by = (y[at.cuda()].double().cpu() - product(*args)).abs()
+            assert worst(off_by - bound(product(*args, True), -(-K // B), F32)) <= 0
+    assert y[(owner < 0).cuda()].eq(7).all()
+
+
+@pytest.mark.parametrize("R", [70, 700])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_strides_and_tokens(ops, R, dtype):
+    """Rows of any stride and alignment, tokens outside x (rows of zeros), no row map: the bits of the plain call."""
+    E, N, K = 3, 100, 176
+    x, rows, off = inputs([R // 2, 0, R - R // 2], N, K, dtype, R)
+    w, s = (t.cuda() for t in weights(E, N, K, 9))
+    off, x = off.cuda(), x.cuda()
+    rows[::7], rows[3::11] = -1, len(x)
+    rows = rows.cuda()
+    there = torch.cat([x, torch.zeros(1, K, dtype=dtype, device="cuda")])[torch.where((rows < 0) | (rows >= len(x)), len(x), rows).long()]
+    want = ops.fp8_experts(there, w, s, off)
+    d_y = torch.randn(R, N, generator=gen(1)).to(dtype).cuda()
+    grads = ops.fp8_experts_backward(d_y, there, w, s, off)
+    for pad, first in ((0, 0), (8, 8), (5, 3)):
+        wide = torch.full((len(x), K + pad + first), math.nan, dtype=dtype, device="cuda")
+        wide[:, first:first + K] = x
+        deep = torch.full((R, N + pad + first), math.nan, dtype=dtype, device="cuda")
+        deep[:, first:first + N] = d_y
+        assert torch.equal(ops.fp8_experts(wide[:, first:first + K], w, s, off, rows=rows), want)
+        got = ops.fp8_experts_backward(deep[:, first:first + N], wide[:, first:first + K], w, s, off, rows=rows)
+        assert all(torch.equal(a, b) for a, b in zip(got, grads))
+
+
+@pytest.mark.parametrize("R", [90, 900])
+def test_what_is_not_finite_stays_where_it_enters(ops, R):
+    """A row with a NaN or an infinity has NaN in all its results; other rows, of the same tile too, and other experts'
+    gradients keep their bits.  So do experts beside one whose weights are NaN."""
+    E, N, K = 2, 136, 272
+    counts = [R // 3, R - R // 3]
+    x, rows, off = inputs(counts, N, K, F32, 3)
+    x, off = x.cuda()[:R], off.cuda()
+    w, s = (t.cuda() for t in weights(E, N, K, 11))
+    d_y = torch.randn(R, N, generator=gen(2)).cuda()
+    want, (d_rows, d_w) = ops.fp8_experts(x, w, s, off), ops.fp8_experts_backward(d_y, x, w, s, off)
+    bad, bad_dy = x.clone(), d_y.clone()
+    bad[1, 200], bad[5, 0], bad_dy[2, 100], bad_dy[7, 3] = math.nan, math.inf, -math.inf, math.nan
+    y = ops.fp8_experts(bad, w, s, off)
+    hit = torch.zeros(R, dtype=torch.bool, device="cuda")
+    hit[[1, 5]] = True
+    assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], want[~hit])
+    got_rows, got_w = ops.fp8_experts_backward(bad_dy, bad, w, s, off)
+    hit[:] = False
+    hit[[2, 7]] = True
+    assert torch.isnan(got_rows[hit]).all() and torch.equal(got_rows[~hit], d_rows[~hit])
+    assert torch.equal(got_w[1], d_w[1])
+    assert torch.isnan(got_w[0][[100, 3]]).all() and torch.isnan(got_w[0][:, [200, 0]]).all()
+    keep_n, keep_k = torch.ones(N, dtype=torch.bool), torch.ones(K, dtype=torch.bool)
+    keep_n[[100, 3]], keep_k[[200, 0]] = False, False
+    assert torch.equal(got_w[0][keep_n.cuda()][:, keep_k.cuda()], d_w[0][keep_n.cuda()][:, keep_k.cuda()])
+    nan_w = w.clone()
+    nan_w.view(torch.uint8)[1] = 0x7f
+    assert torch.equal(ops.fp8_experts(x, nan_w, s, off)[:counts[0]], want[:counts[0]])
+    assert torch.equal(ops.fp8_experts_backward(d_y, None, nan_w, s, off)[0][:counts[0]], d_rows[:counts[0]])
+
+
+def test_no_rows(ops):
+    w, s = (t.cuda() for t in weights(2, 24, 32, 1))
+    off, x, none = segments([0, 0]).cuda(), torch.ones(3, 32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    assert ops.fp8_experts(x, w, s, off, rows=none).shape == (0, 24)
+    d_rows, d_w = ops.fp8_experts_backward(torch.empty(0, 24, device="cuda"), x, w, s, off, rows=none)
+    assert d_rows.shape == (0, 32) and d_w.shape == (2, 24, 32) and d_w.eq(0).all()
+    # rows, but none of an expert: no gradient of a weight
+    d_rows, d_w = ops.fp8_experts_backward(torch.ones(3, 24, device="cuda"), x, w, s, off)
+    assert d_w.eq(0).all()
+    # no tokens: every row is zeros
+    y = ops.fp8_experts(x[:0], w, s, segments([2, 1]).cuda(), rows=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert y.eq(0).all()
+
+
+# ---- streams, graphs, waits
+@pytest.mark.parametrize("counts", [[3, 0, 1], [90, 40, 100], [400, 300, 500]], ids=str)
+def test_graphs_and_streams(ops, counts):
+    """The same bits from a captured and replayed call with other inputs, from two streams at once, and time after time."""
+    N, K = 392, 1040
+    data = [inputs(counts, N, K, BF16, i) for i in (1, 2)]
+    xs = [d[0][:sum(counts)].cuda() for d in data]
+    off = data[0][2].cuda()
+    w, s = (t.cuda() for t in weights(3, N, K, 5))
+    d_y = torch.randn(sum(counts), N, generator=gen(3)).bfloat16().cuda()
+
+    def step(x, stream=None):
+        return (ops.fp8_experts(x, w, s, off, w3=w, w3_scale=s, stream=stream),
+                *ops.fp8_experts_backward(d_y, x, w, s, off, stream=stream))
+
+    want = [step(x) for x in xs]
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(step(xs[0]), want[0]))
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[step(x, t) for x, t in zip(xs, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for p, q in zip(g, want) for a, b in zip(p, q))
+    x = xs[0].clone()
+    graphs, outs = [], []
+    for _ in range(2):  # two graphs, each with its own workspace
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(x))
+    for i in (1, 0):
+        x.copy_(xs[i])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 1], [128, 1, 97], [300, 257, 255]], ids=str)
+def test_a_wait_that_runs_out(ops, counts):
+    """Products told to wait for a microsecond at most (to within about 20) finish, or stop and say so; the next call, in
+    the same workspace, gives what a call without the limit gives."""
+    K, N, E, R = 4096, 520, len(counts), sum(counts)
+    x = torch.randn(R, K, generator=gen(R)).cuda()
+    w, s = (t.cuda() for t in weights(E, N, K, R))
+    off = segments(counts).cuda()
+    want = ops.fp8_experts(x, w, s, off)
+    d_y = torch.randn(R, N, generator=gen(1)).cuda()
+    grads = ops.fp8_experts_backward(d_y, x, w, s, off)
+    assert ops.fp8_status() == 0
+    config = lambda us: ops.Fp8Config(K, N, E, 0, 0, 0, us)  # noqa: E731
+    space = [space_for(ops, config(0), R, R, b) for b in (False, True)]
+
+    def call(us):
+        y, d_rows, d_w = torch.empty_like(want), torch.empty_like(grads[0]), torch.empty_like(grads[1])
+        c_forward(ops, x, K, R, None, R, off, w, s, y, config(us), space[0])
+        rc = ops.lib().colibri_moe_fp8_experts_backward(
+            ops.ctypes.byref(config(us)), d_y.data_ptr(), N, x.data_ptr(), K, R, None, R, off.data_ptr(), w.data_ptr(),
+            s.data_ptr(), d_rows.data_ptr(), d_w.data_ptr(), space[1].data_ptr(), space[1].numel(),
+            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        torch.cuda.synchronize()
+        return all(torch.equal(a, b) for a, b in zip((y, d_rows, d_w), (want, *grads)))
+
+    for _ in range(2):
+        same = call(1)
+        assert ops.fp8_status() == 1 or same
+        assert call(0) and ops.fp8_status() == 0
+    assert call(10_000_000) and ops.fp8_status() == 0
+
+
+@pytest.mark.parametrize("R", [10, 600])
+def test_a_wait_that_runs_out_is_reported(ops, R):
+    """The status word: set once by a call that gave up, from any stream, then clear.  65536 columns of 256 channels are at
+    least 64 blocks of each part, 20 us and more that the last tile's takers wait for the first copies and sums."""
+    K, N = 65536, 256
+    x = torch.randn(R, K, generator=gen(3)).cuda()
+    w, s = (t.cuda() for t in weights(1, N, K, 4))
+    off = segments([R]).cuda()
+    want = ops.fp8_experts(x, w, s, off)
+    assert ops.fp8_status() == 0
+    real = ops._fp8_config
+    config = ops.Fp8Config(K, N, 1, 0, 0, 1, 1)
+    for stream in (None, torch.cuda.Stream()):
+        ops._fp8_config = lambda *a: (config, ops.ctypes.addressof(config))
+        try:
+            y = ops.fp8_experts(x, w, s, off, stream=stream)
+        finally:
+            ops._fp8_config = real
+        gave_up = ops.fp8_status()  # waits for the device
+        assert gave_up == 1 or torch.equal(y, want)
+        y = ops.fp8_experts(x, w, s, off, stream=stream)
+        assert ops.fp8_status(0) == 0 and torch.equal(y, want)
