@@ -4,23 +4,21 @@
 
 namespace colibri {
 
-template <int MODE>
-static cudaError_t with_form(const Fp8Maps& m, const Fp8Args& a, bool pair, bool bf16_out, int device, int sms,
-                             cudaStream_t s) {
-  using B = __nv_bfloat16;
-  if (pair)
-    return bf16_out ? fp8::launch<MODE, true, false, B>(m, a, device, sms, s)
-                    : fp8::launch<MODE, true, false, float>(m, a, device, sms, s);
-  return bf16_out ? fp8::launch<MODE, false, false, B>(m, a, device, sms, s)
-                  : fp8::launch<MODE, false, false, float>(m, a, device, sms, s);
+template <int MODE, typename O>
+static cudaError_t with_form(const Fp8Maps& m, const Fp8Args& a, Fp8Form form, int device, int sms, cudaStream_t s) {
+  if (form == kFp8Wide) return fp8::launch<MODE, kFp8Wide, false, O>(m, a, device, sms, s);
+  return fp8::launch<MODE, kFp8Narrow, false, O>(m, a, device, sms, s);
 }
 
-cudaError_t launch_fp8_rows(const Fp8Maps& m, const Fp8Args& a, bool pair, bool bf16_out, int device, int sms, cudaStream_t s) {
-  return with_form<kFp8Rows>(m, a, pair, bf16_out, device, sms, s);
+cudaError_t launch_fp8_rows(const Fp8Maps& m, const Fp8Args& a, Fp8Form form, bool bf16_out, int device, int sms,
+                            cudaStream_t s) {
+  return bf16_out ? with_form<kFp8Rows, __nv_bfloat16>(m, a, form, device, sms, s)
+                  : with_form<kFp8Rows, float>(m, a, form, device, sms, s);
 }
-cudaError_t launch_fp8_weights(const Fp8Maps& m, const Fp8Args& a, bool pair, bool bf16_out, int device, int sms,
+cudaError_t launch_fp8_weights(const Fp8Maps& m, const Fp8Args& a, Fp8Form form, bool bf16_out, int device, int sms,
                                cudaStream_t s) {
-  return with_form<kFp8Weights>(m, a, pair, bf16_out, device, sms, s);
+  return bf16_out ? with_form<kFp8Weights, __nv_bfloat16>(m, a, form, device, sms, s)
+                  : with_form<kFp8Weights, float>(m, a, form, device, sms, s);
 }
 
 }  // namespace colibri

@@ -470,13 +470,25 @@ bool map_weights(CUtensorMap* m, const void* w, const colibri_moe_fp8_config_t* 
   return map_of(m, w, 3, dims, strides, box_rows);
 }
 
-// Tiles of 256 x 256 on CTA pairs where an expert's rows, on average (the exact numbers are on the device), are more than a
-// single CTA's 128.  us of whole calls on a GB300, single CTAs / pairs, for eight experts of 2048 x 5632 x 2, eight of 4096
-// x 4096, and 64 of 2048 x 1408 (top-6, unevenly loaded), by that mean:
-//    64:  47 / 61,  38 / 45,  46 / 68      192:  81 /  63,  57 / 49,  65 / 75
-//    96:  48 / 62,  38 / 47,  52 / 68      256: 100 /  92,  69 / 67,  75 / 79
-//   128:  61 / 62,  46 / 48,  55 / 71      384: 129 / 112,  95 / 87,  94 / 97
-bool pair_rows(int R, int E) { return R / std::min(E, R) > 128; }
+// Wide tiles where there are two or more an SM: a block's sum costs its takers much the same waits however wide it is, but
+// few tiles fill the SMs unevenly.  us on a GB300, narrow / wide:
+//   one token, two experts of 4096 x 14336 x 2 (224 wide tiles)  47 / 50     four tokens (672)  106 / 99
+//   rows of an expert   64 / 128 / 256, eight experts of 2048 x 5632 x 2     47 / 62 / 101   46 / 52 / 77
+//                                       eight of 4096 x 4096                 38 / 47 /  69   36 / 46 / 61
+//                                       64 of 2048 x 1408, unevenly loaded   46 / 54 /  74   44 / 48 / 64
+// (CTA pairs on tiles of 256 x 256 took 62, 48, 70 at 128 rows and 92, 67, 79 at 256; 8192 tokens, 14336 x 4096: 0.95 ms
+// in all against 0.87: what a block's sum waits for then comes from two SMs.)
+Fp8Form wide_from(int64_t tiles, int sms) { return tiles >= 2 * (int64_t)sms ? kFp8Wide : kFp8Narrow; }
+Fp8Form rows_form(int R, int E, int cols, int sms) {
+  const int used = std::min(E, R), mean = R / used;  // the exact numbers are on the device
+  return wide_from((int64_t)used * ((mean + 127) / 128) * ((cols + 255) / 256), sms);
+}
+// The weights' gradient sums over an expert's rows: of up to two blocks a wide tile is mostly its epilogue (256 rows, eight
+// experts of 1024 x 1408: 53 / 57; 512, 16 of 2048 x 1408: 181 / 168 with the rows' gradient).
+Fp8Form weights_form(int R, int E, int N, int K, int sms) {
+  if (R / std::min(E, R) <= 2 * kFp8Block) return kFp8Narrow;
+  return wide_from((int64_t)E * ((N + 127) / 128) * ((K + 255) / 256), sms);
+}
 
 struct Workspace {
   size_t q, scale, ticket, partial;          // rows' values and scales
@@ -497,7 +509,7 @@ Workspace workspace_of(const colibri_moe_fp8_config_t* c, int R, int sms, bool b
   w.q = take((size_t)R * cols);
   w.scale = take((size_t)R * blocks_of(cols) * sizeof(float));
   w.ticket = take(2 * w.items * sizeof(uint32_t));
-  w.partial = take((size_t)w.items * 128 * 128 * sizeof(float));
+  w.partial = take((size_t)w.items * 128 * 256 * sizeof(float));
   if (backward) {
     w.blocks = (int)((R + 127 * (int64_t)std::min(c->num_experts, R)) / 128);
     w.dq = take((size_t)w.blocks * 128 * cols);
@@ -585,12 +597,13 @@ extern "C" int colibri_moe_fp8_experts(const colibri_moe_fp8_config_t* cfg, cons
     return bad;
   int* word = status_word(device);
   if (!word) return COLIBRI_ERR_CUDA;
-  const bool pair = pair_rows(R, E), gated = w3 != nullptr;
+  const bool gated = w3 != nullptr;
+  const Fp8Form form = rows_form(R, E, gated ? 2 * N : N, sms);
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   Fp8Maps maps;
   bool ok = true;
   for (int i = 0; i < kFp8TokMaps; ++i) ok = ok && map_rows(&maps.a[i], ws + lay.q, R, K, 32 << i);
-  const int box = gated ? (pair ? 64 : 32) : 128;
+  const int box = !gated ? 128 : form == kFp8Narrow ? 32 : 64;
   ok = ok && map_weights(&maps.b, w, cfg, box) && map_weights(&maps.b3, gated ? w3 : w, cfg, box);
   if (!ok) return COLIBRI_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -602,7 +615,7 @@ extern "C" int colibri_moe_fp8_experts(const colibri_moe_fp8_config_t* cfg, cons
   const Fp8Args a = {offsets, scale, R, w_scale, w3_scale, nullptr, 0, y, reinterpret_cast<float*>(ws + lay.partial),
                      ticket, lay.items, R, E, N, K, limit_of(cfg), word};
   const cudaError_t e =
-      launch_fp8_forward(maps, a, pair, gated, cfg->out_dtype == COLIBRI_DTYPE_BF16, device, sms, s);
+      launch_fp8_forward(maps, a, form, gated, cfg->out_dtype == COLIBRI_DTYPE_BF16, device, sms, s);
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
 
@@ -686,14 +699,13 @@ extern "C" int colibri_moe_fp8_experts_backward(const colibri_moe_fp8_config_t* 
   if (d_rows) {
     const Fp8Args a = {offsets, scale, R, w_scale, nullptr, nullptr, 0, d_rows, partial, ticket, lay.items, R, E, N, K,
                        limit_of(cfg), word};
-    e = launch_fp8_rows(maps, a, pair_rows(R, E), cfg->dtype == COLIBRI_DTYPE_BF16, device, sms, s);
+    e = launch_fp8_rows(maps, a, rows_form(R, E, K, sms), cfg->dtype == COLIBRI_DTYPE_BF16, device, sms, s);
     if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
   }
   if (d_w) {
     const Fp8Args a = {offsets, dscale, up(N, 256), nullptr, nullptr, xscale, up(K, 256), d_w, partial,
                        ticket + lay.items, lay.items, R, E, N, K, limit_of(cfg), word};
-    const bool pair = (int64_t)E * ((N + 255) / 256) * ((K + 255) / 256) >= sms / 2;
-    e = launch_fp8_weights(wmaps, a, pair, cfg->out_dtype == COLIBRI_DTYPE_BF16, device, sms, s);
+    e = launch_fp8_weights(wmaps, a, weights_form(R, E, N, K, sms), cfg->out_dtype == COLIBRI_DTYPE_BF16, device, sms, s);
   }
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }

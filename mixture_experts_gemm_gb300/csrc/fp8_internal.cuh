@@ -91,11 +91,13 @@ __device__ __forceinline__ void fp8_segments(const int32_t* offsets, int E, int 
   }
 }
 
-// Form of the products: single CTAs on tiles of 128 x 128, or CTA pairs on 256 x 256.
-cudaError_t launch_fp8_forward(const Fp8Maps& m, const Fp8Args& a, bool pair, bool gated, bool bf16_out, int device, int sms,
+// Forms of the products: tiles of 128 rows x 128 or 256 columns.
+enum Fp8Form { kFp8Narrow, kFp8Wide };
+cudaError_t launch_fp8_forward(const Fp8Maps& m, const Fp8Args& a, Fp8Form form, bool gated, bool bf16_out, int device, int sms,
                                cudaStream_t s);
-cudaError_t launch_fp8_rows(const Fp8Maps& m, const Fp8Args& a, bool pair, bool bf16_out, int device, int sms, cudaStream_t s);
-cudaError_t launch_fp8_weights(const Fp8Maps& m, const Fp8Args& a, bool pair, bool bf16_out, int device, int sms,
+cudaError_t launch_fp8_rows(const Fp8Maps& m, const Fp8Args& a, Fp8Form form, bool bf16_out, int device, int sms,
+                            cudaStream_t s);
+cudaError_t launch_fp8_weights(const Fp8Maps& m, const Fp8Args& a, Fp8Form form, bool bf16_out, int device, int sms,
                                cudaStream_t s);
 
 }  // namespace colibri

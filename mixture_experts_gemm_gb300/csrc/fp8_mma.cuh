@@ -7,9 +7,8 @@
 // accumulators in registers.  That costs a fused multiply-add and a TMEM read for every 128 multiply-adds of the
 // tensor cores, on other units and by other warps, so it runs beside them: TMEM holds several blocks' sums.
 //
-// One persistent CTA per SM on tiles of 128 x 128, or CTA pairs (cta_group::2) on tiles of 256 x 256 whose halves
-// of B each CTA loads once for both.  384 threads:
-//   warp 0      TMA producer (a ring of S stages, 128 rows x 128 bytes of A and of B)
+// One persistent CTA per SM on tiles of 128 x 256, or of 128 x 128 where those are few.  384 threads:
+//   warp 0      TMA producer (a ring of S stages, 128 rows x 128 bytes of A, 128 or 256 of B)
 //   warp 1      issues the MMAs, four to a block, into the next of NB sums in TMEM
 //   warps 2, 3  bring the scales into shared memory (alternate blocks), multiplied where they go together
 //   warps 4-11  take the sums: a thread a row (TMEM lane) of half of the columns; then the epilogue
@@ -39,19 +38,21 @@ constexpr int kBoxBytes = 32 * 128;           // the smallest box of rows
 constexpr int kStageLd = 12;                  // epilogue staging: 32 rows of 8 words a warp, and 4 between
 constexpr Fp8Limit kDrain = {50000000, 63};   // 50 ms, far above the time of a copy or of a stage's MMAs
 
-template <bool PAIR>
+constexpr int MT = 128;                       // tile rows
+
+template <int FORM>
 struct Form {
-  static constexpr int NT = PAIR ? 256 : 128;  // tile columns
-  static constexpr int MT = PAIR ? 256 : 128;  // tile rows, 128 a CTA
+  static constexpr int NT = FORM == kFp8Narrow ? 128 : 256;  // tile columns
+  static constexpr int kB = NT * 128;                        // bytes of a block of theirs
   static constexpr int C = NT / 2;             // columns of a taker thread
   static constexpr int NB = 512 / NT;          // sums in TMEM
-  static constexpr int S = 6;
+  static constexpr int S = FORM == kFp8Wide ? 4 : 6;
   // Blocks whose scales are in shared memory.  Those of block j are written once the MMAs of block j - S are done, which
   // began when the sum of block j - S - NB had been taken: S + NB slots are never written while they are read.
   static constexpr int SF = S + NB;
   static constexpr int kScales = 128 + NT;  // of a slot: a row's (with the weights'), and a second one or the columns'
   static constexpr int kBars = 2 * S + 2 * NB + 3;
-  static constexpr int kSmem = 1024 + S * 2 * kTileBytes + SF * kScales * 4 + kTakers * 32 * kStageLd * 4 + kBars * 8 + 32 +
+  static constexpr int kSmem = 1024 + S * (kTileBytes + kB) + SF * kScales * 4 + kTakers * 32 * kStageLd * 4 + kBars * 8 + 32 +
                                4 * (3 * kFp8MaxExperts + 1);
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -62,13 +63,11 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// Waits for the phase of `bar` with parity `parity`, at most limit.ns or until *abort.  CLUSTER: arrivals come from
-// the pair's other CTA, too.
-template <bool CLUSTER = false>
+// Waits for the phase of `bar` with parity `parity`, at most limit.ns or until *abort.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, Fp8Limit limit) {
   uint64_t t0 = 0;
   for (uint32_t tries = 1;; ++tries) {
-    if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((tries & limit.clock_mask) == 0) {
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
@@ -77,28 +76,13 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   }
 }
 
-// Box of a matrix [rows, columns] (y, x) or of an expert's (z, y, x); PAIR: completing on the leader's barrier.
-template <bool PAIR>
-__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
-  if constexpr (PAIR)
-    tma_load_2d_pair(dst, m, bar, x, y);
-  else
-    tma_load_2d(dst, m, bar, x, y);
-}
-template <bool PAIR>
-__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
-  if constexpr (PAIR)
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
-        "%4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
+// Box of an expert's matrix (z, y, x).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 
 // MN-major operand of 128 rows of the contraction x 128 columns, as a box with the 128-byte swizzle leaves it: atoms of
@@ -117,27 +101,12 @@ constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
   return (1u << 4) | (a_mn ? 1u << 15 : 0) | (b_mn ? 1u << 16 : 0) | (static_cast<uint32_t>(n >> 3) << 17) |
          (static_cast<uint32_t>(m >> 4) << 24);
 }
-template <bool PAIR>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t more) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(more)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(more)
-        : "memory");
-}
-template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t bar) {
-  if constexpr (PAIR)
-    umma_commit_pair(bar, 0x3);
-  else
-    umma_commit(bar);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(more)
+      : "memory");
 }
 
 // Two fp32 in one register pair.
@@ -206,17 +175,17 @@ __device__ __forceinline__ float gated_value(float v, float u) {
 struct Item {
   int i;               // item number
   int tile, part;
-  int e, row, n;       // expert; first row of this CTA's 128 and how many of them there are
+  int e, row, n;       // expert, first row, rows of the tile
   int col;             // first column of the tile (of y)
   int kb0, kb1;        // blocks of the contraction
   int first;           // kFp8Weights: the expert's first block of rows
 };
 
-template <int MODE, bool PAIR, bool GATED, typename O>
+template <int MODE, int FORM, bool GATED, typename O>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_mma_kernel(const __grid_constant__ Fp8Maps tm, const __grid_constant__ Fp8Args a) {
-  using F = Form<PAIR>;
-  constexpr int S = F::S, NB = F::NB, NT = F::NT, MT = F::MT, C = F::C;
+  using F = Form<FORM>;
+  constexpr int S = F::S, NB = F::NB, NT = F::NT, C = F::C;
   constexpr bool kWeights = MODE == kFp8Weights, kFromWeights = !kWeights;  // whether B is the weights
   static_assert(!GATED || MODE == kFp8Forward);
   constexpr int kCh = GATED ? NT / 2 : NT;  // columns of y in a tile
@@ -224,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_a = smem;
   uint8_t* s_b = s_a + S * kTileBytes;
-  float* s_scale = reinterpret_cast<float*>(s_b + S * kTileBytes);
+  float* s_scale = reinterpret_cast<float*>(s_b + S * F::kB);
   float* s_stage = s_scale + F::SF * F::kScales;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_stage + kTakers * 32 * kStageLd);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + F::kBars);
@@ -238,18 +207,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tfull0 = empty0 + 8 * S, tempty0 = tfull0 + 8 * NB;
   const uint32_t drain = tempty0 + 8 * NB, joined = drain + 8, decided = joined + 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = PAIR ? (int)cluster_ctarank() : 0;
-  const bool leader = rank == 0;
 
   pdl_trigger();
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full0 + 8 * i, PAIR ? 3 : 2);  // A, B and the scales are there (PAIR: the leader's, both CTAs')
+      mbar_init(full0 + 8 * i, 2);  // A and B landed, the scales are there
       mbar_init(empty0 + 8 * i, 1);
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(tfull0 + 8 * i, 1);
-      mbar_init(tempty0 + 8 * i, PAIR ? 2 * kTakers : kTakers);
+      mbar_init(tempty0 + 8 * i, kTakers);
     }
     mbar_init(drain, 1);
     mbar_init(joined, kTakers);
@@ -262,13 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   if (warp == 1) {
-    if constexpr (PAIR) {
-      tmem_alloc_pair(smem_u32(tmem_slot), 512);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(smem_u32(tmem_slot), 512);
-      tmem_relinquish();
-    }
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
   }
   // The quantiser lets this kernel start once everything before it is done: offsets and weights may be read at once;
   // the warps that read its rows and scales wait for it.
@@ -277,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                  [](int n) { return kWeights ? (n + kFp8Block - 1) / kFp8Block : (n + MT - 1) / MT; });
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -286,10 +247,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int m_tiles = (a.N + MT - 1) / MT;               // kFp8Weights
   const int kblocks = ((MODE == kFp8Forward ? a.K : a.N) + kFp8Block - 1) / kFp8Block;  // not kFp8Weights
   const int64_t tiles = kWeights ? (int64_t)a.E * m_tiles * col_tiles : (int64_t)s_tiles[a.E] * col_tiles;
-  const int units = PAIR ? gridDim.x >> 1 : gridDim.x, unit = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int units = gridDim.x, unit = blockIdx.x;
   // Parts of the contraction: the number that leaves the SMs least idle in the last wave, a little against more parts.
   int parts = 1;
-  if (!PAIR && tiles < 2 * (int64_t)units) {
+  if (tiles < 2 * (int64_t)units) {
     const int most = kWeights ? max(1, (a.R + kFp8Block - 1) / kFp8Block) : kblocks;
     float least = 1e30f;
     for (int p = 1; p <= kFp8MaxSplits && p <= most && tiles * p <= a.max_items; ++p) {
@@ -312,8 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       it.e = it.tile / each;
       const int local = it.tile - it.e * each;
       it.col = local / m_tiles * kCh;
-      it.row = local % m_tiles * MT + rank * 128;  // of d_w's N rows
-      it.n = min(max(a.N - it.row, 0), 128);
+      it.row = local % m_tiles * MT;  // of d_w's N rows
+      it.n = min(a.N - it.row, MT);
       it.first = s_tiles[it.e];
       blocks = s_tiles[it.e + 1] - it.first;
     } else {
@@ -329,10 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tt = s_tiles[lo + 1] - s_tiles[lo], local = it.tile - s_tiles[lo] * col_tiles;
       it.col = local / tt * kCh;
       const int t = local % tt, n = s_rows[lo];
-      const int each = PAIR ? MT : ((n + tt - 1) / tt + 31) / 32 * 32;  // even tiles, whole boxes
-      const int at = t * each + rank * 128;
-      it.row = s_row0[lo] + at;
-      it.n = max(min(PAIR ? 128 : each, n - at), 0);
+      const int each = ((n + tt - 1) / tt + 31) / 32 * 32;  // even tiles, whole boxes
+      it.row = s_row0[lo] + t * each;
+      it.n = min(each, n - t * each);
       it.first = 0;
     }
     it.kb0 = (int)((int64_t)blocks * it.part / parts);
@@ -348,41 +308,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- producer
     const bool elected = elect_one();
     const uint32_t a0 = smem_u32(s_a), b0 = smem_u32(s_b);
-    const int boxes_of = PAIR || kWeights ? 4 : 0;  // 0: as many as the tile's rows need
+    auto boxes_of = [](const Item& t) { return kWeights ? 4 : (t.n + 31) / 32; };
     auto arm = [&](uint32_t st, int boxes) {
-      if (!PAIR || leader) mbar_arrive_expect_tx(full0 + 8 * st, (PAIR ? 2 : 1) * (kTileBytes + boxes * kBoxBytes));
+      mbar_arrive_expect_tx(full0 + 8 * st, F::kB + boxes * kBoxBytes);
     };
     auto load_b = [&](const Item& t, int kb, uint32_t st) {
-      const uint32_t full = PAIR ? mapa_shared(full0 + 8 * st, 0) : full0 + 8 * st, dst = b0 + st * kTileBytes;
+      const uint32_t full = full0 + 8 * st, dst = b0 + st * F::kB;
       const int k = kb * kFp8Block;
       if constexpr (kWeights) {
-        load2<PAIR>(dst, &tm.b, full, t.col + rank * 128, (t.first + kb) * kFp8Block);
+#pragma unroll
+        for (int r = 0; r < F::kB / kTileBytes; ++r)
+          tma_load_2d(dst + r * kTileBytes, &tm.b, full, t.col + r * 128, (t.first + kb) * kFp8Block);
       } else if constexpr (MODE == kFp8Rows) {
-        load3<PAIR>(dst, &tm.b, full, t.col + rank * 128, k, t.e);
+#pragma unroll
+        for (int r = 0; r < F::kB / kTileBytes; ++r)
+          tma_load_3d(dst + r * kTileBytes, &tm.b, full, t.col + r * 128, k, t.e);
       } else if constexpr (GATED) {
         // every taker thread's columns: C / 2 channels of w, then the same of w3
-        constexpr int kRuns = PAIR ? 1 : 2, kBytes = C / 2 * 128;
+        constexpr int kBytes = C / 2 * 128;
 #pragma unroll
-        for (int r = 0; r < kRuns; ++r) {
-          const int ch = t.col + (PAIR ? rank : r) * (C / 2);
-          load3<PAIR>(dst + 2 * r * kBytes, &tm.b, full, k, ch, t.e);
-          load3<PAIR>(dst + (2 * r + 1) * kBytes, &tm.b3, full, k, ch, t.e);
+        for (int r = 0; r < 2; ++r) {
+          const int ch = t.col + r * (C / 2);
+          tma_load_3d(dst + 2 * r * kBytes, &tm.b, full, k, ch, t.e);
+          tma_load_3d(dst + (2 * r + 1) * kBytes, &tm.b3, full, k, ch, t.e);
         }
       } else {
-        load3<PAIR>(dst, &tm.b, full, k, t.col + rank * 128, t.e);
+#pragma unroll
+        for (int r = 0; r < F::kB / kTileBytes; ++r)
+          tma_load_3d(dst + r * kTileBytes, &tm.b, full, k, t.col + r * 128, t.e);
       }
     };
     auto load_a = [&](const Item& t, int kb, uint32_t st, int boxes) {
-      const uint32_t full = PAIR ? mapa_shared(full0 + 8 * st, 0) : full0 + 8 * st;
+      const uint32_t full = full0 + 8 * st;
       uint32_t dst = a0 + st * kTileBytes;
       if constexpr (kWeights) {
-        load2<PAIR>(dst, &tm.a[2], full, t.row, (t.first + kb) * kFp8Block);
+        tma_load_2d(dst, &tm.a[2], full, t.row, (t.first + kb) * kFp8Block);
       } else {
         int row = t.row;
 #pragma unroll
         for (int b = kFp8TokMaps - 1; b >= 0; --b)  // at most one copy of each box height
           if (boxes >> b & 1) {
-            load2<PAIR>(dst, &tm.a[b], full, kb * kFp8Block, row);
+            tma_load_2d(dst, &tm.a[b], full, kb * kFp8Block, row);
             dst += kBoxBytes << b, row += 32 << b;
           }
       }
@@ -394,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       early = min(S, t.kb1 - t.kb0);
       for (uint32_t st = 0; st < early; ++st) {
         if (elected) {
-          arm(st, boxes_of ? boxes_of : (t.n + 31) / 32);
+          arm(st, boxes_of(t));
           load_b(t, t.kb0 + st, st);
         }
         __syncwarp();
@@ -404,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, st = 0, ph = 0;
     for (int i = unit; ok && i < items; i += units) {
       const Item t = item_at(i);
-      const int boxes = boxes_of ? boxes_of : (t.n + 31) / 32;
+      const int boxes = boxes_of(t);
       for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
         if (!__all_sync(~0u, wait_for(empty0 + 8 * st, ph ^ 1, s_abort, a.limit))) {
           ok = false;
@@ -422,57 +388,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) *s_abort = 1;
-    // Every copy has landed before the CTA can leave (PAIR: on the leader's barriers; the CTAs leave together).  After a
-    // wait that gave up a stage may lack its other operand: the wait for it ends by kDrain.
+    // Every copy has landed before the CTA can leave.  After a wait that gave up a stage may lack its other operand or its
+    // scales: the wait for it ends by kDrain.
     volatile int never = 0;
     it = max(it, early);
-    if (leader)
-      for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_for(full0 + 8 * (j % S), j / S & 1, &never, kDrain);
-    // A pair that stopped early may have issued different stages: nothing ever arrives on this barrier of a pair's.
-    if (PAIR && (!ok || *s_abort)) wait_for(joined, 0, &never, kDrain);
+    for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_for(full0 + 8 * (j % S), j / S & 1, &never, kDrain);
     __syncwarp();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer
-    if (leader) {
-      constexpr uint32_t id = idesc(MT, NT, kWeights, MODE != kFp8Forward);
-      constexpr int kStepA = kWeights ? 4096 >> 4 : 2, kStepB = MODE != kFp8Forward ? 4096 >> 4 : 2;  // 32 of the block
-      const bool elected = elect_one();
-      const uint64_t da0 = kWeights ? mn_desc(smem_u32(s_a)) : sw128_desc(smem_u32(s_a));
-      const uint64_t db0 = MODE != kFp8Forward ? mn_desc(smem_u32(s_b)) : sw128_desc(smem_u32(s_b));
-      uint32_t st = 0, ph = 0, buf = 0, bph = 0;
-      for (int i = unit; ok && i < items; i += units) {
-        const Item t = item_at(i);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          bool got = wait_for<PAIR>(tempty0 + 8 * buf, bph ^ 1, s_abort, a.limit);
-          got = got && wait_for(full0 + 8 * st, ph, s_abort, a.limit);
-          if (!__all_sync(~0u, got)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t da = da0 + st * (kTileBytes >> 4), db = db0 + st * (kTileBytes >> 4);
-          if (elected) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma<PAIR>(tmem_base + buf * NT, da + k * kStepA, db + k * kStepB, id, k != 0);
-            commit<PAIR>(empty0 + 8 * st);
-            commit<PAIR>(tfull0 + 8 * buf);
-          }
-          __syncwarp();
-          if (++st == S) st = 0, ph ^= 1;
-          if (++buf == NB) buf = 0, bph ^= 1;
+    constexpr uint32_t id = idesc(MT, NT, kWeights, MODE != kFp8Forward);
+    constexpr int kStepA = kWeights ? 4096 >> 4 : 2, kStepB = MODE != kFp8Forward ? 4096 >> 4 : 2;  // 32 of the block
+    const bool elected = elect_one();
+    const uint64_t da0 = kWeights ? mn_desc(smem_u32(s_a)) : sw128_desc(smem_u32(s_a));
+    const uint64_t db0 = MODE != kFp8Forward ? mn_desc(smem_u32(s_b)) : sw128_desc(smem_u32(s_b));
+    uint32_t st = 0, ph = 0, buf = 0, bph = 0;
+    for (int i = unit; ok && i < items; i += units) {
+      const Item t = item_at(i);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        bool got = wait_for(tempty0 + 8 * buf, bph ^ 1, s_abort, a.limit);
+        got = got && wait_for(full0 + 8 * st, ph, s_abort, a.limit);
+        if (!__all_sync(~0u, got)) {
+          ok = false;
+          break;
         }
+        tc_fence_after();
+        const uint64_t da = da0 + st * (kTileBytes >> 4), db = db0 + st * (F::kB >> 4);
+        if (elected) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma(tmem_base + buf * NT, da + k * kStepA, db + k * kStepB, id, k != 0);
+          umma_commit(empty0 + 8 * st);
+          umma_commit(tfull0 + 8 * buf);
+        }
+        __syncwarp();
+        if (++st == S) st = 0, ph ^= 1;
+        if (++buf == NB) buf = 0, bph ^= 1;
       }
-      if (!ok && lane == 0) *s_abort = 1;
-      if (elected) {
-        if constexpr (PAIR)
-          umma_commit_pair(drain, 0x1);
-        else
-          umma_commit(drain);  // completes when every MMA of this thread has
-        volatile int never = 0;
-        wait_for(drain, 0, &never, kDrain);
-      }
-      __syncwarp();
     }
+    if (!ok && lane == 0) *s_abort = 1;
+    if (elected) {
+      umma_commit(drain);  // completes when every MMA of this thread has
+      volatile int never = 0;
+      wait_for(drain, 0, &never, kDrain);
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------------------- scales
     pdl_wait();
@@ -490,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float *w0 = nullptr, *w1 = nullptr;  // of the tile's two halves, or of the two projections
       int64_t w_step = 0;
       if constexpr (kFromWeights) {
-        const int c0 = t.col / kFp8Block, c1 = GATED || !PAIR ? c0 : c0 + 1, most = (MODE == kFp8Forward ? nb_w : kb_w) - 1;
+        const int c0 = t.col / kFp8Block, c1 = GATED || NT == 128 ? c0 : c0 + 1, most = (MODE == kFp8Forward ? nb_w : kb_w) - 1;
         auto at = [&](int c) {
           return MODE == kFp8Forward ? ((int64_t)t.e * nb_w + min(c, most)) * kb_w + t.kb0
                                      : ((int64_t)t.e * nb_w + t.kb0) * kb_w + min(c, most);
@@ -528,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             slot[lane + 32 * r] = kFromWeights ? fa[k][r] * f0[k] : fa[k][r];
-            if constexpr (kFromWeights && (GATED || PAIR)) slot[128 + lane + 32 * r] = fa[k][r] * f1[k];
+            if constexpr (kFromWeights && (GATED || NT == 256)) slot[128 + lane + 32 * r] = fa[k][r] * f1[k];
           }
           if constexpr (kWeights) {
 #pragma unroll
@@ -538,12 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          if (lane == 0) {
-            if (!PAIR || leader)
-              mbar_arrive(full0 + 8 * st);
-            else
-              mbar_arrive_peer(mapa_shared(full0 + 8 * st, 0));
-          }
+          if (lane == 0) mbar_arrive(full0 + 8 * st);
           fetch(k, kb + 2 * kAhead);
         }
       }
@@ -560,12 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
     uint32_t* stage = reinterpret_cast<uint32_t*>(s_stage) + (warp - kTaker0) * (32 * kStageLd);
     uint32_t buf = 0, bph = 0, sf = 0, joins = 0;
-    auto free_sum = [&](uint32_t bar) {
-      if (!PAIR || leader)
-        mbar_arrive(bar);
-      else
-        mbar_arrive_peer(mapa_shared(bar, 0));
-    };
     for (int i = unit; ok && i < items; i += units) {
       bool mine;  // whether any of this warp's rows exist
       int left;   // blocks to go
@@ -611,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c0 + 32 == C && h == 1) {
                   tc_fence_before();
                   __syncwarp();
-                  if (lane == 0) free_sum(freed);
+                  if (lane == 0) mbar_arrive(freed);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -626,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else {
             // the weights' block is the half's, or that of one of the projections
-            const float f0 = scale[(kFromWeights && PAIR && !GATED ? half * 128 : 0) + q * 32 + lane];
+            const float f0 = scale[(kFromWeights && NT == 256 && !GATED ? half * 128 : 0) + q * 32 + lane];
             const float f1 = GATED ? scale[128 + q * 32 + lane] : 0.f;
             // 16 columns at a time: halves of 32 on their way behind one another took the registers' moves (8192 tokens of
             // 14336 x 4096: 0.80 ms, 0.87 to 1.5 in larger pieces or with two in flight).  Everything up to the products is
@@ -639,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c0 + 16 == C) {  // this warp has its values: the sum may be overwritten
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) free_sum(freed);
+                if (lane == 0) mbar_arrive(freed);
               }
               const float f = GATED && c0 >= C / 2 ? f1 : f0;
               const uint64_t ff = two(f, f);
@@ -652,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           __syncwarp();
-          if (lane == 0) free_sum(freed);
+          if (lane == 0) mbar_arrive(freed);
         }
         ready = left > 1 && __all_sync(~0u, mbar_test(tfull0 + 8 * buf, bph));
       }
@@ -788,45 +735,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // no CTA leaves while its peer may still signal its barriers
   if (warp == 1) {
     tc_fence_after();
-    if constexpr (PAIR)
-      tmem_dealloc_pair(tmem_base, 512);
-    else
-      tmem_dealloc(tmem_base, 512);
+    tmem_dealloc(tmem_base, 512);
   }
   if (threadIdx.x == 0 && *s_abort) atomicOr(a.status, COLIBRI_FP8_WAIT_EXPIRED);
 }
 
-template <int MODE, bool PAIR, bool GATED, typename O>
+template <int MODE, int FORM, bool GATED, typename O>
 cudaError_t launch(const Fp8Maps& maps, const Fp8Args& a, int device, int sms, cudaStream_t s) {
   static std::mutex mu;
   static bool ready[kOpsMaxDevices] = {};
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[device]) {
-      const cudaError_t e = cudaFuncSetAttribute(fp8_mma_kernel<MODE, PAIR, GATED, O>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Form<PAIR>::kSmem);
+      const cudaError_t e = cudaFuncSetAttribute(fp8_mma_kernel<MODE, FORM, GATED, O>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Form<FORM>::kSmem);
       if (e != cudaSuccess) return e;
       ready[device] = true;
     }
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(PAIR ? sms & ~1 : sms);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Form<PAIR>::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_mma_kernel<MODE, PAIR, GATED, O>, maps, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return pdl_launch(fp8_mma_kernel<MODE, FORM, GATED, O>, dim3(sms), dim3(kThreads), Form<FORM>::kSmem, s, maps, a);
 }
 
 }  // namespace fp8
