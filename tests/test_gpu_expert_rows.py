@@ -268,6 +268,20 @@ def test_gated_backward_is_gated_s_gradient(ops):
         assert float(((got - want).abs() - (far + size) * d_h.abs() - 1e-5).max()) <= 0
 
 
+@pytest.mark.parametrize("pad,first", [(8, 0), (8, 8), (5, 3)])
+def test_gated_of_strided_rows(ops, pad, first):
+    """Every operand with a stride and an alignment of its own: the bits of the contiguous call."""
+    R, f = 21, 264
+    u, v, g = (torch.randn(R, f, generator=gen(i)).bfloat16().cuda() for i in range(3))
+    wide = [torch.full((R, f + first + (i + 1) * pad), math.nan, dtype=BF16, device="cuda") for i in range(3)]
+    for w, t in zip(wide, (u, v, g)):
+        w[:, first:first + f] = t
+    a, b, c = (w[:, first:first + f] for w in wide)
+    assert torch.equal(ops.gated(a, b), ops.gated(u, v))
+    for got, want in zip(ops.gated_backward(c, a, b), ops.gated_backward(g, u, v)):
+        assert torch.equal(got, want)
+
+
 def test_gated_at_the_ends(ops):
     """Far from zero silu is 0 or u; nothing overflows on the way."""
     u = torch.tensor([[-3e38, -1e4, -104.0, -88.0, -0.0, 0.0, 88.0, 1e4, 3e38, math.nan]]).cuda()

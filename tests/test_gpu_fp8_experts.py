@@ -134,6 +134,20 @@ def test_quantize_what_is_not_finite(ops):
     assert q[0, :128].float().eq(0).all() and q[0, 128:].float().eq(448).all()
 
 
+def test_quantize_of_a_copy_on_another_stream(ops):
+    """Slices that cannot be viewed as rows, on a stream that does not wait for the current one."""
+    w = torch.randn(3, 40, 64, generator=gen(1)).cuda()
+    for x in (w[:, :33], w.transpose(1, 2)[:, :48, :32]):
+        for square in (False, True):
+            want = ops.fp8_quantize(x.contiguous(), square=square)
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            torch.cuda._sleep(10_000_000)  # what the call left to the current stream would come late
+            q, s = ops.fp8_quantize(x, square=square, stream=side)
+            side.synchronize()
+            assert torch.equal(q.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(s, want[1])
+
+
 def test_quantize_of_nothing(ops):
     q, s = ops.fp8_quantize(torch.empty(0, 256, device="cuda"))
     assert q.shape == (0, 256) and s.shape == (0, 2)
