@@ -53,11 +53,11 @@ __device__ __forceinline__ uint32_t quotients(float x0, float x1, const Ends& e0
   return lo;
 }
 __device__ __forceinline__ float quotient(float x, float scale) { return scale > 0.f ? __fdiv_rn(x, scale) : 0.f; }
-// Columns col and col + 1 of a row, by division.
+// Columns col and col + 1 of a row (zeros without one), by division.
 template <typename T>
-__device__ __forceinline__ void divide(const T* row, int col, int cols, float s0, float s1, uint8_t* q) {
+__device__ __forceinline__ uint16_t divided(const T* row, int col, int cols, float s0, float s1) {
   const float x0 = row && col < cols ? to_float(row[col]) : 0.f, x1 = row && col + 1 < cols ? to_float(row[col + 1]) : 0.f;
-  *reinterpret_cast<uint16_t*>(q) = (uint16_t)e4m3_pair(quotient(x0, s0), quotient(x1, s1));
+  return (uint16_t)e4m3_pair(quotient(x0, s0), quotient(x1, s1));
 }
 
 // Eight values of a row as loaded; zeros past its end.
@@ -154,23 +154,27 @@ struct RowQuant {
   int64_t ldx;
   int n_tokens;
   const int32_t* rows;  // token of each row, or nullptr: the row itself
-  int n, cols;          // rows to write; columns of x
+  int n, cols;          // rows to write (CHAINS: tokens); columns of x
   uint8_t* q;           // [n][ldq], zeros from cols on
   int ldq;
   float* scale;         // of row r, block b at b * block_step + r * row_step
   int64_t row_step, block_step;
   uint32_t* ticket;     // cleared for the product, or nullptr
   int n_ticket;
+  // CHAINS: rows of each token, head[t], then next[r] until it is negative, by the first `chained` blocks of threads; the
+  // *n_direct + 1 rows of `direct` by the others, each for itself
+  const int32_t *head, *next, *direct, *n_direct;
+  int chained;
 };
 
 constexpr int kRowThreads = 256, kRowsAt = 32, kColsAt = 256;  // rows and columns of a thread block
 
 // Half a warp a block of 128, a warp four rows' 256 columns; all four are on their way before the first is used.  The
 // warp's eight scales are computed at once, a lane one of them, and handed back.  16384 rows of 14336 from 8192 tokens:
-// 0.16 ms (0.10 ms of bytes), bound by issue slots (0.82 busy): 21 instructions a value, half of them the two products
-// and conversions.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(RowQuant a) {
+// 0.16 ms row by row, bound by issue slots (0.82 busy, 21 instructions a value, half of them the two products and
+// conversions), 0.12 ms token by token (0.07 ms of bytes; six blocks of threads an SM, with four 0.15).
+template <typename T, bool VEC, bool CHAINS>
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 2 ? 6 : 4) quantise_rows_kernel(RowQuant a) {
   __shared__ float s_scale[kRowsAt][2];
   pdl_wait();
   pdl_trigger();  // after the wait: what starts early may read what was there before this kernel
@@ -178,49 +182,85 @@ __global__ void __launch_bounds__(kRowThreads) quantise_rows_kernel(RowQuant a) 
     for (int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x; i < a.n_ticket; i += (int64_t)gridDim.x * kRowThreads)
       a.ticket[i] = 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = blockIdx.x * kRowsAt, col = blockIdx.y * kColsAt + lane * 8;
-  Raw8<T> v[4];
+  const int col = blockIdx.y * kColsAt + lane * 8;
+  const bool direct = CHAINS && (int)blockIdx.x >= a.chained;
+  const int n = direct ? *a.n_direct + 1 : a.n;
+  // f(row) for every row that i stands for
+  auto rows_of = [&](int i, auto f) {
+    if constexpr (CHAINS) {
+      if (direct)
+        f(a.direct[i]);
+      else
+        for (int r = a.head[i]; r >= 0; r = a.next[r]) f(r);
+    } else {
+      f(i);
+    }
+  };
+  auto source = [&](int i) -> const T* {  // nullptr: zeros
+    const int t = direct ? a.rows[a.direct[i]] : CHAINS || !a.rows ? i : a.rows[i];
+    return t >= 0 && t < a.n_tokens ? static_cast<const T*>(a.x) + t * a.ldx : nullptr;
+  };
+  const int64_t step = (int64_t)(direct ? gridDim.x - a.chained : gridDim.x) * kRowsAt;
+  for (int64_t at = (int64_t)(direct ? blockIdx.x - a.chained : blockIdx.x) * kRowsAt; at < n; at += step) {
+    const int r0 = (int)at;
+    Raw8<T> v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = r0 + j * 8 + warp;
-    int t = -1;
-    if (r < a.n) t = a.rows ? a.rows[r] : r;
-    const bool real = t >= 0 && t < a.n_tokens;
-    v[j] = read8<VEC>(static_cast<const T*>(a.x) + (real ? t : 0) * a.ldx, col, real ? a.cols : 0);
-  }
-  float mine = 0.f;  // the largest |x| of row lane & 3
+    for (int j = 0; j < 4; ++j) {
+      const int i = r0 + j * 8 + warp;
+      const T* x = i < n ? source(i) : nullptr;
+      v[j] = read8<VEC>(x, col, x ? a.cols : 0);
+    }
+    float mine = 0.f;  // the largest |x| of row lane & 3
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    Top8<T> top;
-    top.take(v[j]);
-    float m = top.all();
+    for (int j = 0; j < 4; ++j) {
+      Top8<T> top;
+      top.take(v[j]);
+      float m = top.all();
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
-    if ((lane & 3) == j) mine = m;
-  }
-  const Scale own(mine);
-  if ((lane & 15) < 4) s_scale[(lane & 3) * 8 + warp][lane >> 4] = own.scale;
-  uint32_t doubt = 0;
+      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
+      if ((lane & 3) == j) mine = m;
+    }
+    const Scale own(mine);
+    if ((lane & 15) < 4) s_scale[(lane & 3) * 8 + warp][lane >> 4] = own.scale;
+    uint32_t doubt = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = r0 + j * 8 + warp;
-    const uint2 q = quantised8(v[j], __shfl_sync(~0u, own.inv, (lane & 16) + j), doubt, 4 * j);
-    if (r < a.n && col < a.ldq) *reinterpret_cast<uint2*>(a.q + (int64_t)r * a.ldq + col) = q;
+    for (int j = 0; j < 4; ++j) {
+      const int i = r0 + j * 8 + warp;
+      const uint2 q = quantised8(v[j], __shfl_sync(~0u, own.inv, (lane & 16) + j), doubt, 4 * j);
+      if (i < n && col < a.ldq)
+        rows_of(i, [&](int r) { *reinterpret_cast<uint2*>(a.q + (int64_t)r * a.ldq + col) = q; });
+    }
+    __syncthreads();
+    if (col >= a.ldq) doubt = 0;
+    for (; doubt; doubt &= doubt - 1) {
+      const int bit = __ffs(doubt) - 1, j = bit >> 2, k = 2 * (bit & 3), i = r0 + j * 8 + warp;
+      if (i >= n) break;
+      const float scale = s_scale[j * 8 + warp][lane >> 4];
+      const uint16_t q = divided(source(i), col + k, a.cols, scale, scale);
+      rows_of(i, [&](int r) { *reinterpret_cast<uint16_t*>(a.q + (int64_t)r * a.ldq + col + k) = q; });
+    }
+    if (threadIdx.x < 2 * kRowsAt) {
+      const int b = threadIdx.x / kRowsAt, i = threadIdx.x % kRowsAt, blk = blockIdx.y * 2 + b;
+      if (r0 + i < n && blk * kFp8Block < a.cols)
+        rows_of(r0 + i, [&](int r) { a.scale[blk * a.block_step + r * a.row_step] = s_scale[i][b]; });
+    }
+    if (CHAINS) __syncthreads();  // the scales, before the next rows'
   }
-  __syncthreads();
-  if (col >= a.ldq) doubt = 0;
-  for (; doubt; doubt &= doubt - 1) {
-    const int bit = __ffs(doubt) - 1, j = bit >> 2, i = 2 * (bit & 3), r = r0 + j * 8 + warp;
-    if (r >= a.n) break;
-    const int t = a.rows ? a.rows[r] : r;
-    const float scale = s_scale[j * 8 + warp][lane >> 4];
-    divide(t >= 0 && t < a.n_tokens ? static_cast<const T*>(a.x) + t * a.ldx : nullptr, col + i, a.cols, scale, scale,
-           a.q + (int64_t)r * a.ldq + col + i);
-  }
-  if (threadIdx.x < 2 * kRowsAt) {
-    const int b = threadIdx.x / kRowsAt, r = threadIdx.x % kRowsAt, blk = blockIdx.y * 2 + b;
-    if (r0 + r < a.n && blk * kFp8Block < a.cols)
-      a.scale[blk * a.block_step + (r0 + r) * a.row_step] = s_scale[r][b];
+}
+
+// The rows of each token as chains, so that a token is quantised once; a chain's order is of no account.  Rows without a
+// token, and those behind a token's first kChainMost (a chain is walked row after row), are listed for themselves.
+// Everything that is counted begins at -1, as one fill leaves it.
+constexpr int kChainMost = 16;
+__global__ void __launch_bounds__(256) chain_rows_kernel(const int32_t* rows, int R, int n_tokens, int32_t* head, int32_t* count,
+                                                         int32_t* n_direct, int32_t* next, int32_t* direct) {
+  pdl_wait();
+  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < R; r += (int64_t)gridDim.x * 256) {
+    const int t = rows[r];
+    if (t >= 0 && t < n_tokens && atomicAdd(count + t, 1) + 1 < kChainMost)
+      next[r] = atomicExch(head + t, (int)r);
+    else
+      direct[atomicAdd(n_direct, 1) + 1] = (int)r;
   }
 }
 
@@ -342,7 +382,8 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
     for (; doubt_rows; doubt_rows &= doubt_rows - 1) {
       const int bit = __ffs(doubt_rows) - 1, i = ty + 16 * (bit >> 2), k = 2 * (bit & 3);
       if (i >= n) break;
-      divide(source(i), col + k, a.cols, s_row_scale[i], s_row_scale[i], a.row_q + (first + i) * a.ldq + col + k);
+      *reinterpret_cast<uint16_t*>(a.row_q + (first + i) * a.ldq + col + k) =
+          divided(source(i), col + k, a.cols, s_row_scale[i], s_row_scale[i]);
     }
     uint32_t doubt = 0;
     if constexpr (KIND == kSquare) {
@@ -360,7 +401,8 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
       for (; doubt; doubt &= doubt - 1) {
         const int bit = __ffs(doubt) - 1, i = ty + 16 * (bit >> 2), k = 2 * (bit & 3);
         if (i >= n) break;
-        divide(source(i), col + k, a.cols, s.scale, s.scale, a.q + (out0 + i) * a.ldq + col + k);
+        *reinterpret_cast<uint16_t*>(a.q + (out0 + i) * a.ldq + col + k) =
+            divided(source(i), col + k, a.cols, s.scale, s.scale);
       }
     } else {
       if (threadIdx.x < kFp8Block) {
@@ -389,7 +431,8 @@ __global__ void __launch_bounds__(kTileThreads, sizeof(T) == 2 ? 3 : 2) quantise
           *reinterpret_cast<uint2*>(a.q + (out0 + ty + 16 * j) * a.ldq + col) = make_uint2(out[j][0], out[j][1]);
         for (; doubt; doubt &= doubt - 1) {
           const int bit = __ffs(doubt) - 1, i = ty + 16 * (bit & 7), k = 2 * (bit >> 3);
-          divide(source(i), col + k, a.cols, s_scale[c + k], s_scale[c + k + 1], a.q + (out0 + i) * a.ldq + col + k);
+          *reinterpret_cast<uint16_t*>(a.q + (out0 + i) * a.ldq + col + k) =
+              divided(source(i), col + k, a.cols, s_scale[c + k], s_scale[c + k + 1]);
         }
       }
     }
@@ -437,12 +480,20 @@ cudaError_t with_type(int32_t t, F f) {
 }
 bool vectors(const void* x, int64_t ldx, int cols) { return ops_aligned16(x) && ldx % 8 == 0 && cols % 8 == 0; }
 
-cudaError_t quantise_rows(int dtype, const RowQuant& a, cudaStream_t s) {
-  const dim3 grid((unsigned)(((int64_t)a.n + kRowsAt - 1) / kRowsAt), (a.ldq + kColsAt - 1) / kColsAt), block(kRowThreads);
+template <bool CHAINS>
+cudaError_t quantise_rows(int dtype, const RowQuant& a, int direct_blocks, cudaStream_t s) {
+  const unsigned blocks = (unsigned)(((int64_t)a.n + kRowsAt - 1) / kRowsAt);
+  const dim3 grid(blocks + direct_blocks, (a.ldq + kColsAt - 1) / kColsAt), block(kRowThreads);
   return with_type(dtype, [&](auto t) {
-    return vectors(a.x, a.ldx, a.cols) ? pdl_launch(quantise_rows_kernel<decltype(t), true>, grid, block, 0, s, a)
-                                       : pdl_launch(quantise_rows_kernel<decltype(t), false>, grid, block, 0, s, a);
+    return vectors(a.x, a.ldx, a.cols) ? pdl_launch(quantise_rows_kernel<decltype(t), true, CHAINS>, grid, block, 0, s, a)
+                                       : pdl_launch(quantise_rows_kernel<decltype(t), false, CHAINS>, grid, block, 0, s, a);
   });
+}
+// Whether tokens are quantised once and written to each of their rows: where that saves more than the chains' two launches
+// cost.  Whole calls, us, without / with, by the values that are saved: 8 million 78 / 78, 476 / 475; 10 million 78 / 80; 42
+// million 211 / 196; 117 million (8192 tokens of 14336, two rows each) 889 / 829.
+bool chained(const int32_t* rows, int n_tokens, int R, int K) {
+  return rows && n_tokens > 0 && n_tokens < R && (int64_t)(R - n_tokens) * K >= (1 << 24);
 }
 template <int KIND>
 cudaError_t quantise_tiles(int dtype, const TileQuant& a, unsigned tiles, int sms, cudaStream_t s) {
@@ -496,7 +547,7 @@ Fp8Form weights_form(int R, int E, int N, int K, int sms) {
 }
 
 struct Workspace {
-  size_t q, scale, ticket, partial;          // rows' values and scales
+  size_t q, scale, ticket, partial, chain;   // rows' values and scales; forward: chains of tokens' rows
   size_t dq, dscale, xq, xscale;             // by columns, for the weights' gradient
   size_t bytes;
   int items, blocks;                         // of split tiles; blocks of 128 rows of one expert, at most
@@ -515,6 +566,7 @@ Workspace workspace_of(const colibri_moe_fp8_config_t* c, int R, int sms, bool b
   w.scale = take((size_t)R * blocks_of(cols) * sizeof(float));
   w.ticket = take(2 * w.items * sizeof(uint32_t));
   w.partial = take((size_t)w.items * 128 * 256 * sizeof(float));
+  if (!backward) w.chain = take((4 * (size_t)R + 1) * sizeof(int32_t));  // more than two of each token and two of each row
   if (backward) {
     w.blocks = (int)((R + 127 * (int64_t)std::min(c->num_experts, R)) / 128);
     w.dq = take((size_t)w.blocks * 128 * cols);
@@ -567,7 +619,7 @@ extern "C" int colibri_moe_fp8_quantize(const colibri_moe_fp8_config_t* cfg, con
     a.scale = scale, a.lds = blocks_of(K);
     e = quantise_tiles<kSquare>(cfg->dtype, a, (unsigned)cfg->num_experts * blocks_of(a.matrix_rows), sms, s);
   } else {
-    e = quantise_rows(cfg->dtype, {x, ldx, n, nullptr, n, K, q, K, scale, blocks_of(K), 1, nullptr, 0}, s);
+    e = quantise_rows<false>(cfg->dtype, {x, ldx, n, nullptr, n, K, q, K, scale, blocks_of(K), 1, nullptr, 0}, 0, s);
   }
   return e == cudaSuccess ? COLIBRI_OK : COLIBRI_ERR_CUDA;
 }
@@ -614,9 +666,21 @@ extern "C" int colibri_moe_fp8_experts(const colibri_moe_fp8_config_t* cfg, cons
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   float* scale = reinterpret_cast<float*>(ws + lay.scale);
   uint32_t* ticket = reinterpret_cast<uint32_t*>(ws + lay.ticket);
-  if (quantise_rows(cfg->dtype, {x, ldx, n_tokens, rows, R, K, ws + lay.q, K, scale, 1, R, ticket, lay.items}, s) !=
-      cudaSuccess)
+  RowQuant quant = {x, ldx, n_tokens, rows, R, K, ws + lay.q, K, scale, 1, R, ticket, lay.items};
+  if (chained(rows, n_tokens, R, K)) {  // n_tokens < R
+    int32_t* head = reinterpret_cast<int32_t*>(ws + lay.chain);
+    int32_t *count = head + n_tokens, *n_direct = count + n_tokens, *next = n_direct + 1, *direct = next + R;
+    if (cudaMemsetAsync(head, 0xff, (2 * (size_t)n_tokens + 1) * sizeof(int32_t), s) != cudaSuccess) return COLIBRI_ERR_CUDA;
+    const dim3 grid((unsigned)std::min<int64_t>(((int64_t)R + 255) / 256, (int64_t)sms * 8));
+    if (pdl_launch(chain_rows_kernel, grid, dim3(256), 0, s, rows, R, n_tokens, head, count, n_direct, next, direct) !=
+        cudaSuccess)
+      return COLIBRI_ERR_CUDA;
+    quant.head = head, quant.next = next, quant.direct = direct, quant.n_direct = n_direct, quant.n = n_tokens;
+    quant.chained = (n_tokens + kRowsAt - 1) / kRowsAt;
+    if (quantise_rows<true>(cfg->dtype, quant, 2 * sms, s) != cudaSuccess) return COLIBRI_ERR_CUDA;
+  } else if (quantise_rows<false>(cfg->dtype, quant, 0, s) != cudaSuccess) {
     return COLIBRI_ERR_CUDA;
+  }
   const Fp8Args a = {offsets, scale, R, w_scale, w3_scale, nullptr, 0, y, reinterpret_cast<float*>(ws + lay.partial),
                      ticket, lay.items, R, E, N, K, limit_of(cfg), word};
   const cudaError_t e =
@@ -698,7 +762,8 @@ extern "C" int colibri_moe_fp8_experts_backward(const colibri_moe_fp8_config_t* 
     t.q = ws + lay.xq, t.scale = xscale, t.lds = up(K, 256), t.row_q = nullptr, t.n_ticket = 0;
     e = quantise_tiles<kColumns>(cfg->dtype, t, lay.blocks, sms, s);
   } else {
-    e = quantise_rows(cfg->dtype, {d_y, ld_dy, R, nullptr, R, N, ws + lay.q, ldn, scale, 1, R, ticket, 2 * lay.items}, s);
+    e = quantise_rows<false>(
+        cfg->dtype, {d_y, ld_dy, R, nullptr, R, N, ws + lay.q, ldn, scale, 1, R, ticket, 2 * lay.items}, 0, s);
   }
   if (e != cudaSuccess) return COLIBRI_ERR_CUDA;
   if (d_rows) {

@@ -358,6 +358,25 @@ def test_strides_and_tokens(ops, R, dtype):
         assert all(torch.equal(a, b) for a, b in zip(got, grads))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("kind", ["random", "one token", "half without", "every token alike"])
+def test_tokens_of_many_rows(ops, dtype, kind):
+    """Enough repeated values that tokens are quantised once and written to all of their rows: the bits of the call on the
+    repeated rows themselves, whatever the map: a token of thousands of rows, rows without one, values by division."""
+    n, R, K, N, E = 700, 9100, 2064, 72, 3
+    x = special(n, K, 3, dtype).cuda()
+    g = gen(4)
+    rows = {"random": torch.randint(-1, n + 1, (R,), generator=g), "one token": torch.full((R,), 5),
+            "half without": torch.where(torch.rand(R, generator=g) < 0.5, torch.randint(0, n, (R,), generator=g), -1),
+            "every token alike": torch.arange(R) % n}[kind].int().cuda()
+    w, s = (t.cuda() for t in weights(E, N, K, 9))
+    off = segments([4000, 100, 5000]).cuda()
+    there = torch.cat([x, torch.zeros(1, K, dtype=dtype, device="cuda")])[torch.where((rows < 0) | (rows >= n), n, rows).long()]
+    want = ops.fp8_experts(there, w, s, off)
+    for _ in range(2):
+        assert torch.equal(ops.fp8_experts(x, w, s, off, rows=rows), want)
+
+
 @pytest.mark.parametrize("R", [90, 900])
 def test_what_is_not_finite_stays_where_it_enters(ops, R):
     """A row with a NaN or an infinity has NaN in all its results; other rows, of the same tile too, and other experts'
