@@ -377,6 +377,28 @@ def test_tokens_of_many_rows(ops, dtype, kind):
         assert torch.equal(ops.fp8_experts(x, w, s, off, rows=rows), want)
 
 
+def test_a_captured_call_follows_its_map(ops):
+    """Tokens of many rows in a graph: every replay goes by the map and the values that it finds, with nothing left of the
+    last one's."""
+    n, R, K, N, E = 700, 9100, 2064, 72, 3
+    g = gen(6)
+    x, rows = special(n, K, 3, BF16).cuda(), torch.full((R,), 5).int().cuda()
+    w, s = (t.cuda() for t in weights(E, N, K, 9))
+    off = segments([4000, 100, 5000]).cuda()
+    ops.fp8_experts(x, w, s, off, rows=rows)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = ops.fp8_experts(x, w, s, off, rows=rows)
+    for map_ in (torch.randint(-1, n + 1, (R,), generator=g), torch.full((R,), -1), torch.arange(R) % n, torch.full((R,), 5)):
+        rows.copy_(map_)
+        x.copy_(special(n, K, int(map_.sum()) % 97, BF16))
+        token = torch.where((rows < 0) | (rows >= n), n, rows).long()
+        want = ops.fp8_experts(torch.cat([x, torch.zeros_like(x[:1])])[token], w, s, off)
+        graph.replay()
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("R", [90, 900])
 def test_what_is_not_finite_stays_where_it_enters(ops, R):
     """A row with a NaN or an infinity has NaN in all its results; other rows, of the same tile too, and other experts'
